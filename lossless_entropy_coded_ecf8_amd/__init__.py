@@ -11,9 +11,11 @@ from .binding import (DecodePlan, alpha_hat, exponent_entropy_bound, DeviceEncod
                       encode_into, encode_workspace_bytes, histogram, histogram_device, lib, meta_from_freq, validate_meta,
                       workspace_bytes)
 
+from .adapters import AdapterPlan, GradClip, adapter_add, adapter_grads, clip_grad_norm, linear_fp8_input_grad
 from .pipeline import DecodePipeline, ECF8Linear, fp8_e4m3_bytes, linear_fp8
 
-__all__ = ["alpha_hat", "exponent_entropy_bound", "DecodePipeline", "ECF8Linear", "fp8_e4m3_bytes", "linear_fp8", "DecodePlan", "DeviceEncoded", "Ecf8Error", "Encoded", "build_codebook", "canonical_codes",
+__all__ = ["AdapterPlan", "GradClip", "adapter_add", "adapter_grads", "clip_grad_norm", "linear_fp8_input_grad",
+           "alpha_hat", "exponent_entropy_bound", "DecodePipeline", "ECF8Linear", "fp8_e4m3_bytes", "linear_fp8", "DecodePlan", "DeviceEncoded", "Ecf8Error", "Encoded", "build_codebook", "canonical_codes",
            "codebook_from_freq", "decode", "decode_batched", "encode", "encode_batched_into", "encode_device",
            "encode_into",
            "encode_workspace_bytes", "histogram", "histogram_device", "lib", "meta_from_freq", "validate_meta",
