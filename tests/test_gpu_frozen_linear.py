@@ -43,6 +43,7 @@ def make(T, N, K, dtype, d, seed=0, pad=0):
 
 
 SIZES = [(1, 16, 16), (1, 4096, 256), (2, 48, 32), (17, 16, 144), (31, 80, 400), (64, 512, 128), (100, 1040, 272),
+         (33, 4112, 48), (2048, 144, 6160),
          (127, 64, 1040), (129, 112, 128), (200, 3088, 64), (257, 256, 528), (513, 336, 656), (1025, 64, 1296)]
 
 
