@@ -35,46 +35,43 @@ __device__ __forceinline__ uint32_t widen2(uint32_t b)
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, UPPER));
 }
 
-// Four rows of four bytes turned: out[j] holds column j's four rows.
-__device__ __forceinline__ void transpose4(const uint32_t r[4], uint32_t out[4])
-{
-    const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
-    const uint32_t c = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), d = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
-    out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
-    out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
-    out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
-    out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
-}
-
 typedef __attribute__((address_space(1))) const void GlobalMem;
 typedef __attribute__((address_space(3))) void LdsMem;
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 LdsPair;
 
 // One workgroup: BM tokens by BN columns of dx, eight waves in WM rows of WN,
-// the reduction BK rows of the weight at a time through two LDS buffers.
+// the reduction BK rows of the weight at a time.
 //
-// dy goes from memory to LDS without passing registers, 16 bytes a lane.  The
-// weight passes registers once: a thread takes eight rows of four bytes, turns
-// them, widens them, and leaves one 16-byte operand for each of four columns, so
-// each byte is converted once for all eight waves.  Both tiles are rows of
-// 16-byte units along the reduction; unit u of row r sits at u ^ swizzle(r), and
-// sixteen lanes that read one unit of sixteen rows (or write it) meet different
-// banks.
+// Both tiles go from memory to LDS without passing registers, 16 bytes a lane,
+// into three buffers: while step s is multiplied, step s + 1 is on its way or
+// there and step s + 2 is sent for.  dy's tile is kept by token, 8 values of the
+// reduction in a unit, one matrix operand's share of a lane.  The weight's is
+// kept as it lies in memory, by row, and is turned by the transposing LDS read:
+// each group of 16 lanes reads 8 rows of 16 columns and each lane gets one
+// column's 8 rows, still E4M3, which four conversions widen.
 //
 // The weight is operand A and dy operand B, so a lane's results belong to one
-// token; the matrix instruction's rows are dealt to columns so that they are
-// 4 NF consecutive ones, stored 16 bytes at a time.
+// token, four consecutive columns of each operand.
+//
+// Banks.  Unit u of dy's row r sits at u ^ (r & 7), unit u of the weight's row r
+// at u ^ turn(r): the lanes that a read serves at once take one unit of 16
+// consecutive rows, and these cover the banks evenly.
 template <int TYPE, int BM, int BN, int BK, int WM, int WN>
 struct Tile {
-    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, CH = BK / 8;
-    static constexpr int kA = BM * CH, kB = BN * CH;           // 16-byte units of the two tiles
-    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (CH * BN / 4 + kThreads - 1) / kThreads;
-    static_assert(WM * WN == kThreads / 64 && MF >= 1 && NF >= 2, "eight waves");
-    static_assert(kA % 64 == 0 && (CH * BN / 4) % 64 == 0, "whole waves stage");
+    static constexpr int MF = BM / WM / 16, CH = BK / 8, BU = BN / 16;
+    static constexpr int kA = BM * CH, kB = BK * BU;           // 16-byte units of the two tiles
+    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (kB + kThreads - 1) / kThreads;
+    static constexpr int kLds = 3 * 16 * (kA + kB);
+    static constexpr int kAhead = kA / kThreads + kB / kThreads;  // loads every thread issues in one step
+    static_assert(WM * WN == kThreads / 64 && MF >= 1 && BN / WN == 64, "eight waves of 64 columns");
+    static_assert(kA % 64 == 0 && kB % 64 == 0 && (BU == 8 || BU == 16), "whole waves stage");
 
-    static __device__ __forceinline__ int swizzle_b(int col) { return (col ^ (col >> 3)) & 7; }
+    static __device__ __forceinline__ int turn(int row) { return BU == 16 ? row & 15 : (row ^ (row >> 3)) & 7; }
 
-    // dy's tile, straight to LDS.  Tokens past the last read the last one's row.
-    static __device__ __forceinline__ void stage_a(const GradArgs& A, int64_t t0, int n, u32x4* lds)
+    // Both tiles of one step, straight to LDS.  Tokens past the last read the last one's row, columns past the last the
+    // tile's first; neither reaches a result that is stored.
+    static __device__ __forceinline__ void stage(const GradArgs& A, int64_t t0, int k0, int n, u32x4* la, u32x4* lb)
     {
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
@@ -82,80 +79,99 @@ struct Tile {
             if (kA % kThreads && first >= kA) break;
             const int row = u / CH, ch = (u % CH) ^ (row & 7);
             const int64_t t = min(t0 + row, A.tokens - 1);
-            __builtin_amdgcn_global_load_lds((GlobalMem*)(A.dy + t * A.ld_dy + n + 8 * ch), (LdsMem*)(lds + first), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((GlobalMem*)(A.dy + t * A.ld_dy + n + 8 * ch), (LdsMem*)(la + first), 16, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsB; ++i) {
+            const int first = i * kThreads + (threadIdx.x & ~63), u = first + (threadIdx.x & 63);
+            if (kB % kThreads && first >= kB) break;
+            const int row = u / BU, col = k0 + 16 * ((u % BU) ^ turn(row));
+            __builtin_amdgcn_global_load_lds((GlobalMem*)(A.w + (int64_t)(n + row) * A.k + (col < A.k ? col : k0)), (LdsMem*)(lb + first), 16, 0, 0);
         }
     }
 
     // The same where the reduction ends inside the tile: zeros past n1.
-    static __device__ __forceinline__ void stage_a_tail(const GradArgs& A, int64_t t0, int n, int n1, u32x4* lds)
+    static __device__ __forceinline__ void stage_tail(const GradArgs& A, int64_t t0, int k0, int n, int n1, u32x4* la, u32x4* lb)
     {
         for (int u = threadIdx.x; u < kA; u += kThreads) {
             const int row = u / CH, ch = (u % CH) ^ (row & 7);
             const int64_t t = min(t0 + row, A.tokens - 1);
             u32x4 v{0, 0, 0, 0};
             if (n + 8 * ch < n1) v = *reinterpret_cast<const u32x4*>(A.dy + t * A.ld_dy + n + 8 * ch);
-            lds[u] = v;
+            la[u] = v;
+        }
+        for (int u = threadIdx.x; u < kB; u += kThreads) {
+            const int row = u / BU, col = k0 + 16 * ((u % BU) ^ turn(row));
+            u32x4 v{0, 0, 0, 0};
+            if (n + row < n1 && col < A.k) v = *reinterpret_cast<const u32x4*>(A.w + (int64_t)(n + row) * A.k + col);
+            lb[u] = v;
         }
     }
 
-    // The weight's bytes for this thread: rows n + 8 oct .. + 7, columns 4 quad .. + 3 (TAIL: zeros past n1; a whole
-    // tile is not looked at between its loads and its use, so that they stay in flight).
-    template <bool TAIL>
-    static __device__ __forceinline__ void load_b(const GradArgs& A, int k0, int n, int n1, uint32_t (*w)[8])
+    // Operands are read one group of products ahead of their use.
+    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[4])
     {
+        constexpr int KK = BK / 32, PER = MF < 2 ? 1 : 2, GROUPS = KK * MF / PER;
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, row0 = wm * (BM / WM) + c;
+        const int src = 8 * g + (c >> 1);                     // the weight's row that this lane reads for its group
+        u32x4 a[2][PER], b[4];
+        i32x2 raw[4];
+        const auto read_b = [&](int kk) {
 #pragma unroll
-        for (int i = 0; i < kUnitsB; ++i) {
-            const int u = i * kThreads + threadIdx.x, quad = u % (BN / 4), oct = u / (BN / 4);
-            const int col = k0 + 4 * quad < A.k ? k0 + 4 * quad : 0;
-            const bool in = oct < CH && (!TAIL || n + 8 * oct < n1);
-            const uint8_t* p = A.w + (int64_t)(in ? n + 8 * oct : 0) * A.k + col;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                w[i][q] = *reinterpret_cast<const uint32_t*>(p + (int64_t)q * A.k);
-                if (TAIL && !in) w[i][q] = 0;
+            for (int n = 0; n < 4; ++n) {
+                const int row = kk * 32 + src;
+                const char* p = reinterpret_cast<const char*>(lb + row * BU + ((wn * 4 + n) ^ turn(row))) + 8 * (c & 1);
+                raw[n] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LdsPair*)p);
             }
+        };
+        read_b(0);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) a[0][p] = la[(row0 + p * 16) * CH + (g ^ (c & 7))];
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const int m = i * PER % MF;
+            if (m == 0) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    b[n] = u32x4{widen2<TYPE, false>(raw[n][0]), widen2<TYPE, true>(raw[n][0]),
+                                 widen2<TYPE, false>(raw[n][1]), widen2<TYPE, true>(raw[n][1])};
+            }
+            if (i + 1 < GROUPS) {
+                const int k2 = (i + 1) * PER / MF, m2 = (i + 1) * PER % MF;
+                if (m2 == 0) read_b(k2);
+#pragma unroll
+                for (int p = 0; p < PER; ++p) a[(i + 1) & 1][p] = la[(row0 + (m2 + p) * 16) * CH + ((k2 * 4 + g) ^ (c & 7))];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int p = 0; p < PER; ++p)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[m + p][n] = mfma<TYPE>(b[n], a[i & 1][p], acc[m + p][n]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
-    static __device__ __forceinline__ void store_b(const uint32_t (*w)[8], u32x4* lds)
+    // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
+    static __device__ __forceinline__ void stage_and_multiply(const GradArgs& A, int64_t t0, int k0, int n,
+                                                              u32x4* __restrict__ to_a, u32x4* __restrict__ to_b,
+                                                              const u32x4* __restrict__ la, const u32x4* __restrict__ lb,
+                                                              int wm, int wn, f32x4 (*acc)[4])
     {
-#pragma unroll
-        for (int i = 0; i < kUnitsB; ++i) {
-            const int u = i * kThreads + threadIdx.x, quad = u % (BN / 4), oct = u / (BN / 4);
-            if ((CH * BN / 4) % kThreads && oct >= CH) break;
-            uint32_t lo[4], hi[4];
-            transpose4(w[i], lo);
-            transpose4(w[i] + 4, hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                lds[(4 * quad + j) * CH + (oct ^ swizzle_b(4 * quad + j))] =
-                    u32x4{widen2<TYPE, false>(lo[j]), widen2<TYPE, true>(lo[j]), widen2<TYPE, false>(hi[j]), widen2<TYPE, true>(hi[j])};
-        }
-    }
-
-    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[NF])
-    {
-        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            u32x4 a[MF], b[NF];
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const int row = wm * (BM / WM) + m * 16 + c;
-                a[m] = la[row * CH + ((kk * 4 + g) ^ (row & 7))];
-            }
-#pragma unroll
-            for (int n = 0; n < NF; ++n) {
-                const int col = wn * (BN / WN) + (c >> 2) * (4 * NF) + n * 4 + (c & 3);
-                b[n] = lb[col * CH + ((kk * 4 + g) ^ swizzle_b(col))];
-            }
-#pragma unroll
-            for (int m = 0; m < MF; ++m)
-#pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma<TYPE>(b[n], a[m], acc[m][n]);
-        }
+        stage(A, t0, k0, n, to_a, to_b);
+        __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
+        multiply(la, lb, wm, wn, acc);
     }
 };
+
+// All but the newest LOADS loads have arrived, and every LDS access is done, in
+// every wave of the workgroup.
+template <int LOADS>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 template <int TYPE, int BM, int BN, int BK, int WM, int WN>
 __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
@@ -163,7 +179,7 @@ __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
     typedef Tile<TYPE, BM, BN, BK, WM, WN> S;
     extern __shared__ u32x4 lds[];
     u32x4* const la = lds;
-    u32x4* const lb = lds + 2 * S::kA;
+    u32x4* const lb = lds + 3 * S::kA;
     const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
     // Workgroups go to the eight dies in turn; each die gets a run of tiles, in
     // columns of eight tiles down the tokens, so that its cache sees the same rows
@@ -175,57 +191,50 @@ __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
     const int tm = band * 8 + in_band % rows, tn = in_band / rows;
     const int64_t t0 = (int64_t)tm * BM;
     const int k0 = tn * BN;
-    const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = (n1 - n0) / BK;
-    f32x4 acc[S::MF][S::NF] = {};
-    uint32_t w[S::kUnitsB][8];
+    const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / BK : 0;
+    f32x4 acc[S::MF][4] = {};
+    // At the end of step s the tiles of step s + 1 have to be there, and only what
+    // this step sent for may be under way: kAhead loads (a wave that sent one more
+    // waits for it as well).  Steps past the last are replaced by the last, so that
+    // this count holds in every step.
     if (steps > 0) {
-        S::stage_a(A, t0, n0, la);
-        S::template load_b<false>(A, k0, n0, n1, w);
-        S::store_b(w, lb);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        S::stage(A, t0, k0, n0, la, lb);
+        S::stage(A, t0, k0, n0 + min(1, steps - 1) * BK, la + S::kA, lb + S::kB);
+        wait_and_meet<S::kAhead>();
     }
+    int use = 0, fill = 2;                                    // the buffers of steps s and s + 2
     for (int s = 0; s < steps; ++s) {
-        const int cur = s & 1;
-        if (s + 1 < steps) {
-            S::stage_a(A, t0, n0 + (s + 1) * BK, la + (cur ^ 1) * S::kA);
-            S::template load_b<false>(A, k0, n0 + (s + 1) * BK, n1, w);
-        }
-        S::multiply(la + cur * S::kA, lb + cur * S::kB, wm, wn, acc);
-        if (s + 1 < steps) S::store_b(w, lb + (cur ^ 1) * S::kB);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        S::stage_and_multiply(A, t0, k0, n0 + min(s + 2, steps - 1) * BK, la + fill * S::kA, lb + fill * S::kB,
+                              la + use * S::kA, lb + use * S::kB, wm, wn, acc);
+        wait_and_meet<S::kAhead>();
+        use = use == 2 ? 0 : use + 1;
+        fill = fill == 2 ? 0 : fill + 1;
     }
     if (n0 + steps * BK < n1) {
-        S::stage_a_tail(A, t0, n0 + steps * BK, n1, la);
-        S::template load_b<true>(A, k0, n0 + steps * BK, n1, w);
-        S::store_b(w, lb);
-        __syncthreads();
+        wait_and_meet<0>();
+        S::stage_tail(A, t0, k0, n0 + steps * BK, n1, la, lb);
+        wait_and_meet<0>();
         S::multiply(la, lb, wm, wn, acc);
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const int col = k0 + wn * (BN / WN) + g * (4 * S::NF);
-    if (col >= A.k) return;                                   // K and 4 NF: multiples of 8, so groups of eight are in or out
     const float scale = *A.w_scale;
 #pragma unroll
     for (int m = 0; m < S::MF; ++m) {
         const int64_t t = t0 + wm * (BM / WM) + m * 16 + c;
         if (t >= A.tokens) continue;
 #pragma unroll
-        for (int n = 0; n < S::NF; n += 2) {
-            if (col + 4 * n >= A.k) continue;
-            const f32x4 v0 = acc[m][n], v1 = acc[m][n + 1];
-            if (A.planes) {
-                float* p = A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.k + col + 4 * n;
-                *reinterpret_cast<f32x4*>(p) = v0;
-                *reinterpret_cast<f32x4*>(p + 4) = v1;
-            } else {
-                *reinterpret_cast<u32x4*>(A.dx + t * A.ld_dx + col + 4 * n) =
-                    u32x4{pack2<TYPE>(v0[0] * scale, v0[1] * scale), pack2<TYPE>(v0[2] * scale, v0[3] * scale),
-                          pack2<TYPE>(v1[0] * scale, v1[1] * scale), pack2<TYPE>(v1[2] * scale, v1[3] * scale)};
-            }
+        for (int n = 0; n < 4; ++n) {
+            const int col = k0 + wn * 64 + n * 16 + 4 * g;    // K is a multiple of 16: an operand's columns are in or out
+            if (col >= A.k) continue;
+            const f32x4 v = acc[m][n];
+            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.k + col) = v;
+            else
+                *reinterpret_cast<uint2*>(A.dx + t * A.ld_dx + col) =
+                    make_uint2(pack2<TYPE>(v[0] * scale, v[1] * scale), pack2<TYPE>(v[2] * scale, v[3] * scale));
         }
     }
+    // Loads to LDS that no step used are still under way: they land before the workgroup ends.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // Sums the shares in order, scales and rounds.
@@ -254,11 +263,11 @@ Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k)
 {
     const auto tiles = [&](uint64_t m, uint64_t c) { return ((tokens + m - 1) / m) * ((k + c - 1) / c); };
     if (tokens > 64 && tiles(256, 256) >= 192) return Shape{256, 256, 1};
-    const int bm = tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
-    const uint64_t t = tiles(bm, 128);
+    const int bm = tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128, bn = bm == 32 ? 256 : 128;
+    const uint64_t t = tiles(bm, bn);
     uint64_t s = t ? 512 / t : 1;
     if (s > n / 512) s = n / 512;
-    return Shape{bm, 128, (uint32_t)(s < 1 ? 1 : s > 32 ? 32 : s)};
+    return Shape{bm, bn, (uint32_t)(s < 1 ? 1 : s > 32 ? 32 : s)};
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
@@ -271,7 +280,7 @@ template <int TYPE, int BM, int BN, int BK, int WM, int WN>
 int launch(GradArgs A, uint32_t shares, hipStream_t st)
 {
     typedef Tile<TYPE, BM, BN, BK, WM, WN> S;
-    constexpr int bytes = 2 * (S::kA + S::kB) * 16;
+    constexpr int bytes = S::kLds;
     auto* kernel = input_grad_kernel<TYPE, BM, BN, BK, WM, WN>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
@@ -287,9 +296,9 @@ int run(const GradArgs& A, const Shape& s, hipStream_t st)
 {
     int rc;
     if (s.bm == 256) rc = launch<TYPE, 256, 256, 64, 2, 4>(A, 1, st);
-    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 128, 2, 4>(A, s.shares, st);
-    else if (s.bm == 64) rc = launch<TYPE, 64, 128, 128, 2, 4>(A, s.shares, st);
-    else rc = launch<TYPE, 32, 128, 128, 2, 4>(A, s.shares, st);
+    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 128, 4, 2>(A, s.shares, st);
+    else if (s.bm == 64) rc = launch<TYPE, 64, 128, 128, 4, 2>(A, s.shares, st);
+    else rc = launch<TYPE, 32, 256, 64, 2, 4>(A, s.shares, st);
     if (rc != ECF8_OK || s.shares < 2) return rc;
     const uint32_t join = (uint32_t)((A.tokens * A.k / 4 + kJoinThreads - 1) / kJoinThreads);
     grad_join_kernel<TYPE><<<join, kJoinThreads, 0, st>>>(A, (int)s.shares);
