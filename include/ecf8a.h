@@ -153,7 +153,7 @@ uint64_t ecf8a_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t
 
 /* dx = w_scale * dy w, the gradient that y = x (w * w_scale)^T passes to x.
  * dy: tokens rows of out_features values of `type` (ECF8A_BF16 or ECF8A_FP16),
- * ld_dy elements apart; w: out_features x in_features E4M3 bytes, contiguous
+ * ld_dy elements apart (at most 2^22); w: out_features x in_features E4M3 bytes, contiguous
  * and 16-byte aligned (a decoded weight); w_scale: device float; dx: tokens
  * rows of in_features values of the same type, ld_dx elements apart.  Both
  * feature counts are multiples of 16, as the FP8 product of the forward pass

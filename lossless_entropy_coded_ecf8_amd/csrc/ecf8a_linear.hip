@@ -35,10 +35,16 @@ __device__ __forceinline__ uint32_t widen2(uint32_t b)
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, UPPER));
 }
 
-typedef __attribute__((address_space(1))) const void GlobalMem;
+typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void LdsMem;
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2 LdsPair;
+
+// Every offset used with it is inside the operand, so the range is left open.
+__device__ __forceinline__ Rsrc buffer_of(const void* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
+}
 
 // One workgroup: BM tokens by BN columns of dx, eight waves in WM rows of WN,
 // the reduction BK rows of the weight at a time.
@@ -69,24 +75,45 @@ struct Tile {
 
     static __device__ __forceinline__ int turn(int row) { return BU == 16 ? row & 15 : (row ^ (row >> 3)) & 7; }
 
-    // Both tiles of one step, straight to LDS.  Tokens past the last read the last one's row, columns past the last the
-    // tile's first; neither reaches a result that is stored.
-    static __device__ __forceinline__ void stage(const GradArgs& A, int64_t t0, int k0, int n, u32x4* la, u32x4* lb)
+    // What a lane sends for lies at the same place of every step's tile: byte offsets from the tile's corner, found
+    // once.  Tokens past the last read the last one's row, columns past the last the tile's first; neither reaches a
+    // result that is stored.
+    struct Places {
+        uint32_t a[kUnitsA], b[kUnitsB];
+    };
+
+    static __device__ __forceinline__ Places places(const GradArgs& A, int64_t t0, int k0)
     {
+        Places at;
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
-            const int first = i * kThreads + (threadIdx.x & ~63), u = first + (threadIdx.x & 63);
-            if (kA % kThreads && first >= kA) break;
-            const int row = u / CH, ch = (u % CH) ^ (row & 7);
-            const int64_t t = min(t0 + row, A.tokens - 1);
-            __builtin_amdgcn_global_load_lds((GlobalMem*)(A.dy + t * A.ld_dy + n + 8 * ch), (LdsMem*)(la + first), 16, 0, 0);
+            const int u = i * kThreads + threadIdx.x, row = u / CH, ch = (u % CH) ^ (row & 7);
+            at.a[i] = 2 * ((uint32_t)min((int64_t)row, A.tokens - 1 - t0) * (uint32_t)A.ld_dy + 8 * ch);
         }
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
-            const int first = i * kThreads + (threadIdx.x & ~63), u = first + (threadIdx.x & 63);
+            const int u = i * kThreads + threadIdx.x, row = u / BU, col = 16 * ((u % BU) ^ turn(row));
+            at.b[i] = (uint32_t)row * A.k + (k0 + col < A.k ? col : 0);
+        }
+        return at;
+    }
+
+    // Both tiles of one step, straight to LDS.  Buffer loads: the compiler takes a global load to LDS for one that
+    // touches both memories and waits for all of them at every LDS read.
+    static __device__ __forceinline__ void stage(const GradArgs& A, const Places& at, int64_t t0, int k0, int n, u32x4* la, u32x4* lb)
+    {
+        const Rsrc ra = buffer_of(A.dy + t0 * A.ld_dy), rb = buffer_of(A.w + (int64_t)n * A.k + k0);
+#pragma unroll
+        for (int i = 0; i < kUnitsA; ++i) {
+            const int first = i * kThreads + (threadIdx.x & ~63);
+            if (kA % kThreads && first >= kA) break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + first), 16, at.a[i], 2 * n, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsB; ++i) {
+            const int first = i * kThreads + (threadIdx.x & ~63);
             if (kB % kThreads && first >= kB) break;
-            const int row = u / BU, col = k0 + 16 * ((u % BU) ^ turn(row));
-            __builtin_amdgcn_global_load_lds((GlobalMem*)(A.w + (int64_t)(n + row) * A.k + (col < A.k ? col : k0)), (LdsMem*)(lb + first), 16, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + first), 16, at.b[i], 0, 0, 0);
         }
     }
 
@@ -152,12 +179,12 @@ struct Tile {
     }
 
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
-    static __device__ __forceinline__ void stage_and_multiply(const GradArgs& A, int64_t t0, int k0, int n,
+    static __device__ __forceinline__ void stage_and_multiply(const GradArgs& A, const Places& at, int64_t t0, int k0, int n,
                                                               u32x4* __restrict__ to_a, u32x4* __restrict__ to_b,
                                                               const u32x4* __restrict__ la, const u32x4* __restrict__ lb,
                                                               int wm, int wn, f32x4 (*acc)[4])
     {
-        stage(A, t0, k0, n, to_a, to_b);
+        stage(A, at, t0, k0, n, to_a, to_b);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
         multiply(la, lb, wm, wn, acc);
     }
@@ -197,14 +224,15 @@ __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
     // this step sent for may be under way: kAhead loads (a wave that sent one more
     // waits for it as well).  Steps past the last are replaced by the last, so that
     // this count holds in every step.
+    const typename S::Places at = S::places(A, t0, k0);
     if (steps > 0) {
-        S::stage(A, t0, k0, n0, la, lb);
-        S::stage(A, t0, k0, n0 + min(1, steps - 1) * BK, la + S::kA, lb + S::kB);
+        S::stage(A, at, t0, k0, n0, la, lb);
+        S::stage(A, at, t0, k0, n0 + min(1, steps - 1) * BK, la + S::kA, lb + S::kB);
         wait_and_meet<S::kAhead>();
     }
     int use = 0, fill = 2;                                    // the buffers of steps s and s + 2
     for (int s = 0; s < steps; ++s) {
-        S::stage_and_multiply(A, t0, k0, n0 + min(s + 2, steps - 1) * BK, la + fill * S::kA, lb + fill * S::kB,
+        S::stage_and_multiply(A, at, t0, k0, n0 + min(s + 2, steps - 1) * BK, la + fill * S::kA, lb + fill * S::kB,
                               la + use * S::kA, lb + use * S::kB, wm, wn, acc);
         wait_and_meet<S::kAhead>();
         use = use == 2 ? 0 : use + 1;
@@ -324,7 +352,7 @@ extern "C" int ecf8a_input_grad(const void* dy, uint64_t ld_dy, uint64_t tokens,
     if (!dy || !w || !w_scale || !dx || !aligned(dy, 16) || !aligned(w, 16) || !aligned(w_scale, 4) || !aligned(dx, 16) ||
         (tokens > 1 && (ld_dy % 8 || ld_dx % 8)))
         return ECF8_ERR_ARG;
-    if (ld_dy < out_features || ld_dx < in_features) return ECF8_ERR_SIZE;
+    if (ld_dy < out_features || ld_dx < in_features || ld_dy > (1u << 22)) return ECF8_ERR_SIZE;  // a tile's rows: 32-bit offsets
     const uint64_t need = ecf8a_input_grad_bytes(tokens, out_features, in_features);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
     const Shape s = shape_of(tokens, out_features, in_features);
