@@ -22,7 +22,7 @@ struct GradArgs {
     int64_t ld_dx;
     float* planes;           // [share][tokens][in_features]; nullptr: one share, written to dx
     int64_t tokens;
-    int n, k, share;         // share: reduction length of one of gridDim.y shares, a multiple of 128
+    int n, k, share;         // share: reduction length of one of gridDim.y shares, a multiple of 64
     int tiles_m, tiles_n;
 };
 
@@ -50,8 +50,9 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p)
 // the reduction BK rows of the weight at a time.
 //
 // Both tiles go from memory to LDS without passing registers, 16 bytes a lane,
-// into three buffers: while step s is multiplied, step s + 1 is on its way or
-// there and step s + 2 is sent for.  dy's tile is kept by token, 8 values of the
+// into STAGES buffers: while step s is multiplied, step s + STAGES - 1 is sent
+// for and those between are on their way (about 1.5 us for a tile of 128 by 128,
+// three times what its products take).  dy's tile is kept by token, 8 values of the
 // reduction in a unit, one matrix operand's share of a lane.  The weight's is
 // kept as it lies in memory, by row, and is turned by the transposing LDS read:
 // each group of 16 lanes reads 8 rows of 16 columns and each lane gets one
@@ -63,13 +64,15 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p)
 // Banks.  Unit u of dy's row r sits at u ^ (r & 7), unit u of the weight's row r
 // at u ^ turn(r): the lanes that a read serves at once take one unit of 16
 // consecutive rows, and these cover the banks evenly.
-template <int TYPE, int BM, int BN, int BK, int WM, int WN>
+template <int TYPE, int BM, int BN, int BK, int WM, int WN, int STAGES>
 struct Tile {
     static constexpr int MF = BM / WM / 16, CH = BK / 8, BU = BN / 16;
     static constexpr int kA = BM * CH, kB = BK * BU;           // 16-byte units of the two tiles
     static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (kB + kThreads - 1) / kThreads;
-    static constexpr int kLds = 3 * 16 * (kA + kB);
-    static constexpr int kAhead = kA / kThreads + kB / kThreads;  // loads every thread issues in one step
+    static constexpr int kLds = STAGES * 16 * (kA + kB);
+    // Loads that may be under way at the end of a step: those of all stages but the next one's.
+    static constexpr int kAhead = (STAGES - 2) * (kA / kThreads + kB / kThreads);
+    static_assert(STAGES >= 3 && kLds <= 160 * 1024 && kAhead < 64, "LDS and the load counter");
     static_assert(WM * WN == kThreads / 64 && MF >= 1 && BN / WN == 64, "eight waves of 64 columns");
     static_assert(kA % 64 == 0 && kB % 64 == 0 && (BU == 8 || BU == 16), "whole waves stage");
 
@@ -200,13 +203,13 @@ __device__ __forceinline__ void wait_and_meet()
     asm volatile("" ::: "memory");
 }
 
-template <int TYPE, int BM, int BN, int BK, int WM, int WN>
+template <int TYPE, int BM, int BN, int BK, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
 {
-    typedef Tile<TYPE, BM, BN, BK, WM, WN> S;
+    typedef Tile<TYPE, BM, BN, BK, WM, WN, STAGES> S;
     extern __shared__ u32x4 lds[];
     u32x4* const la = lds;
-    u32x4* const lb = lds + 3 * S::kA;
+    u32x4* const lb = lds + STAGES * S::kA;
     const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
     // Workgroups go to the eight dies in turn; each die gets a run of tiles, in
     // columns of eight tiles down the tokens, so that its cache sees the same rows
@@ -220,23 +223,23 @@ __global__ __launch_bounds__(kThreads) void input_grad_kernel(GradArgs A)
     const int k0 = tn * BN;
     const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / BK : 0;
     f32x4 acc[S::MF][4] = {};
-    // At the end of step s the tiles of step s + 1 have to be there, and only what
-    // this step sent for may be under way: kAhead loads (a wave that sent one more
-    // waits for it as well).  Steps past the last are replaced by the last, so that
-    // this count holds in every step.
+    // At the end of step s the tiles of step s + 1 have to be there, and only those
+    // of the steps behind it may be under way: kAhead loads (a wave that sent one
+    // more waits for it as well).  Steps past the last are replaced by the last, so
+    // that this count holds in every step.
     const typename S::Places at = S::places(A, t0, k0);
     if (steps > 0) {
-        S::stage(A, at, t0, k0, n0, la, lb);
-        S::stage(A, at, t0, k0, n0 + min(1, steps - 1) * BK, la + S::kA, lb + S::kB);
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, k0, n0 + min(s, steps - 1) * BK, la + s * S::kA, lb + s * S::kB);
         wait_and_meet<S::kAhead>();
     }
-    int use = 0, fill = 2;                                    // the buffers of steps s and s + 2
+    int use = 0, fill = STAGES - 1;                           // the buffers of steps s and s + STAGES - 1
     for (int s = 0; s < steps; ++s) {
-        S::stage_and_multiply(A, at, t0, k0, n0 + min(s + 2, steps - 1) * BK, la + fill * S::kA, lb + fill * S::kB,
+        S::stage_and_multiply(A, at, t0, k0, n0 + min(s + STAGES - 1, steps - 1) * BK, la + fill * S::kA, lb + fill * S::kB,
                               la + use * S::kA, lb + use * S::kB, wm, wn, acc);
         wait_and_meet<S::kAhead>();
-        use = use == 2 ? 0 : use + 1;
-        fill = fill == 2 ? 0 : fill + 1;
+        use = use == STAGES - 1 ? 0 : use + 1;
+        fill = fill == STAGES - 1 ? 0 : fill + 1;
     }
     if (n0 + steps * BK < n1) {
         wait_and_meet<0>();
@@ -271,8 +274,15 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(GradArgs A, int
 {
     const int64_t plane = A.tokens * A.k, i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
     if (i >= plane) return;
-    f32x4 s = *reinterpret_cast<const f32x4*>(A.planes + i);
-    for (int p = 1; p < shares; ++p) s += *reinterpret_cast<const f32x4*>(A.planes + p * plane + i);
+    f32x4 s{0, 0, 0, 0};
+    for (int p = 0; p < shares; p += 8) {                     // eight loads in flight, added in order
+        f32x4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4*>(A.planes + min(p + j, shares - 1) * plane + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (p + j < shares) s += v[j];
+    }
     const float scale = *A.w_scale;
     const int64_t t = i / A.k;
     uint32_t* p = reinterpret_cast<uint32_t*>(A.dx + t * A.ld_dx + (i - t * A.k));
@@ -281,21 +291,47 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(GradArgs A, int
 }
 
 // The tile for a size, and the shares that the reduction is cut into where too
-// few tiles are left to fill the card.
+// few tiles are left to fill the card: whichever of them the step times below
+// make shortest.
 struct Shape {
     int bm, bn;
     uint32_t shares;
 };
 
+// Measured on MI355X (bfloat16): microseconds of one step (64 rows of the weight)
+// of a workgroup alone on its compute unit, and of two side by side (the largest
+// two tiles leave no LDS for a second one).  Larger tiles take less from LDS and
+// memory for each product; smaller ones fill 256 compute units from fewer tokens.
+// 2048 x 4096 x 4096: 66 us in tiles of 128 x 256, 72 in 128 x 128, 96 in 256 x
+// 256, which win at 4096 tokens with 109 against 124.  Joining shares costs a
+// launch and their traffic: 1001 x 4096 x 4096 takes 45 us unsplit in 128 x 128,
+// 48 in 128 x 256 with two shares.  24 x 14336 x 4096: 18 us with 16 shares, 21
+// with 8, 22 with 28.
+struct Cost {
+    int bm, bn;
+    double one, two;
+};
+constexpr Cost kCosts[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}, {64, 256, 0.7, 1.1}, {32, 256, 0.8, 1.6}};
+
 Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k)
 {
-    const auto tiles = [&](uint64_t m, uint64_t c) { return ((tokens + m - 1) / m) * ((k + c - 1) / c); };
-    if (tokens > 64 && tiles(256, 256) >= 192) return Shape{256, 256, 1};
-    const int bm = tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128, bn = bm == 32 ? 256 : 128;
-    const uint64_t t = tiles(bm, bn);
-    uint64_t s = t ? 512 / t : 1;
-    if (s > n / 512) s = n / 512;
-    return Shape{bm, bn, (uint32_t)(s < 1 ? 1 : s > 32 ? 32 : s)};
+    Shape best{32, 256, 1};
+    double least = -1.0;
+    for (const Cost& c : kCosts) {
+        if (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens) continue;      // over half of the rows would be padding
+        const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
+        for (uint32_t s = 1; s <= 16 && (s == 1 || n / s >= 256); ++s) {
+            const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
+            const double full = c.two > 0.0 ? c.two : c.one;
+            const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
+            const double us = turns * ((n + s - 1) / s + 63) / 64 + (s > 1 ? 4.0 + 8.0 * s * tokens * k / 5e6 : 0.0);
+            if (least < 0.0 || us < least) {
+                least = us;
+                best = Shape{c.bm, c.bn, s};
+            }
+        }
+    }
+    return best;
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
@@ -304,12 +340,12 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
            k <= ECF8A_MAX_FEATURES && k % 16 == 0;
 }
 
-template <int TYPE, int BM, int BN, int BK, int WM, int WN>
+template <int TYPE, int BM, int BN, int BK, int WM, int WN, int STAGES>
 int launch(GradArgs A, uint32_t shares, hipStream_t st)
 {
-    typedef Tile<TYPE, BM, BN, BK, WM, WN> S;
+    typedef Tile<TYPE, BM, BN, BK, WM, WN, STAGES> S;
     constexpr int bytes = S::kLds;
-    auto* kernel = input_grad_kernel<TYPE, BM, BN, BK, WM, WN>;
+    auto* kernel = input_grad_kernel<TYPE, BM, BN, BK, WM, WN, STAGES>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
@@ -323,10 +359,11 @@ template <int TYPE>
 int run(const GradArgs& A, const Shape& s, hipStream_t st)
 {
     int rc;
-    if (s.bm == 256) rc = launch<TYPE, 256, 256, 64, 2, 4>(A, 1, st);
-    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 128, 4, 2>(A, s.shares, st);
-    else if (s.bm == 64) rc = launch<TYPE, 64, 128, 128, 4, 2>(A, s.shares, st);
-    else rc = launch<TYPE, 32, 256, 64, 2, 4>(A, s.shares, st);
+    if (s.bm == 256) rc = launch<TYPE, 256, 256, 64, 2, 4, 3>(A, s.shares, st);
+    else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 64, 2, 4, 3>(A, s.shares, st);
+    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 64, 4, 2, 3>(A, s.shares, st);
+    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 64, 2, 4, 3>(A, s.shares, st);
+    else rc = launch<TYPE, 32, 256, 64, 2, 4, 3>(A, s.shares, st);
     if (rc != ECF8_OK || s.shares < 2) return rc;
     const uint32_t join = (uint32_t)((A.tokens * A.k / 4 + kJoinThreads - 1) / kJoinThreads);
     grad_join_kernel<TYPE><<<join, kJoinThreads, 0, st>>>(A, (int)s.shares);
@@ -358,7 +395,7 @@ extern "C" int ecf8a_input_grad(const void* dy, uint64_t ld_dy, uint64_t tokens,
     const Shape s = shape_of(tokens, out_features, in_features);
     const GradArgs A{static_cast<const uint16_t*>(dy), (int64_t)ld_dy, w, w_scale, static_cast<uint16_t*>(dx), (int64_t)ld_dx,
                      s.shares > 1 ? static_cast<float*>(workspace) : nullptr, (int64_t)tokens, (int)out_features,
-                     (int)in_features, (int)round_up((out_features + s.shares - 1) / s.shares, 128), 0, 0};
+                     (int)in_features, (int)round_up((out_features + s.shares - 1) / s.shares, 64), 0, 0};
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     return type == ECF8A_BF16 ? run<kBf16>(A, s, st) : run<kFp16>(A, s, st);
 }
