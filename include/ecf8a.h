@@ -6,7 +6,7 @@
  * low-rank factors for each request or task, and this header holds the
  * operators that such a layer needs on AMD Instinct MI355X (gfx950):
  *   - the adapters of many requests added to the shared projection's output,
- *     from one token to long prompts (ecf8a_plan_prepare, ecf8a_add);
+ *     from one token to long prompts (ecf8a_plan_prepare, ecf8a_add; ecf8a_add_few);
  *   - their gradients (ecf8a_grads);
  *   - the gradient the frozen E4M3 weight passes to its input
  *     (ecf8a_input_grad);
@@ -62,6 +62,7 @@ extern "C" {
 #define ECF8A_MAX_ADAPTERS 2048
 #define ECF8A_MAX_RANK 256
 #define ECF8A_MAX_TOKENS 16777216       /* 2^24 */
+#define ECF8A_FEW_TOKENS 512            /* of ecf8a_add_few */
 #define ECF8A_MAX_FEATURES 1048576      /* 2^20 */
 
 /* ------------------------------ adapters ------------------------------- */
@@ -132,6 +133,17 @@ uint64_t ecf8a_grads_bytes(const ecf8a_plan* plan, const ecf8a_bank* bank);
 int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* x, uint64_t ldx, uint32_t x_type,
               const float* x_scale, const void* base, uint64_t ld_base, void* out, uint64_t ld_out,
               void* hidden, void* workspace, uint64_t workspace_bytes, void* hip_stream);
+
+/* Whether ecf8a_add_few is the faster way for this many tokens and this bank (1)
+ * or a plan and ecf8a_add (0). */
+int ecf8a_few(uint64_t tokens, const ecf8a_bank* bank);
+
+/* ecf8a_add for at most ECF8A_FEW_TOKENS tokens and rank 64, from the index
+ * itself (as in ecf8a_plan_prepare): one launch, no plan and no workspace.
+ * Errors as ecf8a_plan_prepare and ecf8a_add. */
+int ecf8a_add_few(const void* index, uint32_t index_bytes, uint64_t tokens, const ecf8a_bank* bank, const void* x,
+                  uint64_t ldx, uint32_t x_type, const float* x_scale, const void* base, uint64_t ld_base,
+                  void* out, uint64_t ld_out, void* hip_stream);
 
 /* The gradients of ecf8a_add for dy, the gradient of out (which is base's own
  * gradient too).  dy, x, dx_base and dx: rows of the bank's type; hidden: what

@@ -49,7 +49,7 @@ class ClipPlanA(ctypes.Structure):
 
 
 EXPORTS_A = ["ecf8a_plan_bytes", "ecf8a_plan_prepare", "ecf8a_hidden_bytes", "ecf8a_add_bytes", "ecf8a_grads_bytes",
-             "ecf8a_add", "ecf8a_grads", "ecf8a_input_grad_bytes", "ecf8a_input_grad", "ecf8a_clip_bytes",
+             "ecf8a_add", "ecf8a_few", "ecf8a_add_few", "ecf8a_grads", "ecf8a_input_grad_bytes", "ecf8a_input_grad", "ecf8a_clip_bytes",
              "ecf8a_clip_prepare", "ecf8a_clip_run"]
 
 _ready = None
@@ -69,6 +69,8 @@ def _lib() -> ctypes.CDLL:
         "ecf8a_add_bytes": (u64, [plan, bank]),
         "ecf8a_grads_bytes": (u64, [plan, bank]),
         "ecf8a_add": (i, [plan, bank, vp, u64, u32, vp, vp, u64, vp, u64, vp, vp, u64, vp]),
+        "ecf8a_few": (i, [u64, bank]),
+        "ecf8a_add_few": (i, [vp, u32, u64, bank, vp, u64, u32, vp, vp, u64, vp, u64, vp]),
         "ecf8a_grads": (i, [plan, bank, vp, u64, vp, u64, vp, vp, u64, vp, u64, vp, vp, vp, u64, vp]),
         "ecf8a_input_grad_bytes": (u64, [u64, u64, u64]),
         "ecf8a_input_grad": (i, [vp, u64, u64, u64, vp, u64, vp, u32, vp, u64, vp, u64, vp]),
@@ -157,6 +159,13 @@ def _apart(out, others, what: str):
         raise ValueError("%s overlaps %s" % (what, name))
 
 
+def _index_ok(index):
+    if index.dim() != 1 or index.dtype not in _INDEX_BYTES or not index.is_contiguous():
+        raise ValueError("index must be a contiguous int32 or int64 vector")
+    if not index.is_cuda:
+        raise ValueError("index must be on the GPU, got %s" % index.device)
+
+
 class AdapterPlan:
     """The tokens of a batch grouped by adapter (ecf8a_plan_prepare): one launch, shared by every projection that
     the batch passes through.
@@ -167,10 +176,7 @@ class AdapterPlan:
     """
 
     def __init__(self, index: torch.Tensor, n_adapters: int, workspace: Optional[torch.Tensor] = None, stream=None):
-        if index.dim() != 1 or index.dtype not in _INDEX_BYTES or not index.is_contiguous():
-            raise ValueError("index must be a contiguous int32 or int64 vector")
-        if not index.is_cuda:
-            raise ValueError("index must be on the GPU, got %s" % index.device)
+        _index_ok(index)
         L = _lib()
         self.tokens, self.adapters, self.device = index.numel(), int(n_adapters), index.device
         need = L.ecf8a_plan_bytes(self.tokens, self.adapters) if self.adapters > 0 else 0
@@ -205,8 +211,7 @@ class AdapterPlan:
         return _empty(max(n, 16), torch.uint8, self.device, stream)
 
 
-def _bank(down, up, scaling, ranks, plan) -> BankA:
-    dev = plan.device
+def _bank(down, up, scaling, ranks, dev) -> BankA:
     if down.dim() != 3 or up.dim() != 3 or down.shape[:2] != up.shape[:2]:
         raise ValueError("down must be (L, R, K) and up (L, R, N), got %s and %s" % (tuple(down.shape), tuple(up.shape)))
     if down.dtype not in (torch.bfloat16, torch.float16) or up.dtype != down.dtype:
@@ -214,8 +219,6 @@ def _bank(down, up, scaling, ranks, plan) -> BankA:
     if not (down.is_contiguous() and up.is_contiguous()):
         raise ValueError("down and up must be contiguous")
     L, R, K = down.shape
-    if L != plan.adapters:
-        raise ValueError("a plan of %d adapters with a bank of %d" % (plan.adapters, L))
     if scaling.dtype != torch.float32 or scaling.shape != (L,) or not scaling.is_contiguous():
         raise ValueError("scaling must be %d contiguous float32 values" % L)
     if ranks is not None and (ranks.dtype != torch.int32 or ranks.shape != (L,) or not ranks.is_contiguous()):
@@ -252,9 +255,14 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     the result goes (default: a new tensor); out=base adds in place and leaves tokens without an adapter untouched.
     hidden: a plan.hidden(R) buffer that keeps h for adapter_grads.  Not differentiable by itself: see ECF8Linear.
     """
-    plan = index if isinstance(index, AdapterPlan) else AdapterPlan(index, down.shape[0], stream=stream)
-    bank = _bank(down, up, scaling, ranks, plan)
-    T, K, N, dev = plan.tokens, bank.in_features, bank.out_features, plan.device
+    plan = index if isinstance(index, AdapterPlan) else None
+    if plan is None:
+        _index_ok(index)
+        if hidden is not None:
+            raise ValueError("hidden goes with an AdapterPlan")
+    dev, T = index.device, index.tokens if plan is not None else index.numel()
+    bank = _bank(down, up, scaling, ranks, dev)
+    K, N = bank.in_features, bank.out_features
     ldx = _rows(x, "x", T, K, (down.dtype, torch.float8_e4m3fn), dev)
     if x_scale is not None:
         if x.dtype != torch.float8_e4m3fn:
@@ -270,16 +278,25 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
         same = base is not None and out.data_ptr() == base.data_ptr() and ld_out == ld_base
         _apart(out, [("x", x), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks), ("x_scale", x_scale),
                      ("hidden", hidden), ("base", None if same else base)], "out")
+    L = _lib()
+    if plan is None:
+        if L.ecf8a_few(T, ctypes.byref(bank)):
+            with _Launch(dev, stream) as st:
+                _check(L.ecf8a_add_few(index.data_ptr(), _INDEX_BYTES[index.dtype], T, ctypes.byref(bank), x.data_ptr(), ldx,
+                                       _TYPES[x.dtype], _ptr(x_scale), _ptr(base), ld_base, out.data_ptr(), ld_out,
+                                       st.cuda_stream), "ecf8a_add_few")
+            return out
+        plan = AdapterPlan(index, bank.adapters, stream=stream)
+    if plan.adapters != bank.adapters:
+        raise ValueError("a plan of %d adapters with a bank of %d" % (plan.adapters, bank.adapters))
     if hidden is not None:
         _hidden_ok(hidden, plan, bank.rank)
-    L = _lib()
     with _Launch(dev, stream) as st:
         plan._order(st)
         ws = _scratch(L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream)
         _check(L.ecf8a_add(ctypes.byref(plan.c), ctypes.byref(bank), x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(x_scale),
                            _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), ws.data_ptr(), ws.numel(),
-                           st.cuda_stream),
-               "ecf8a_add")
+                           st.cuda_stream), "ecf8a_add")
     return out
 
 
@@ -295,8 +312,11 @@ def adapter_grads(dy: torch.Tensor, x: Optional[torch.Tensor], down: torch.Tenso
     same batch (None: h is computed again from x).  want: whether dx, and the factors' gradients, are wanted; what is
     not comes back as None.  x must be in the factors' type; it may be None if only dx is wanted.
     """
-    bank = _bank(down, up, scaling, ranks, plan)
-    T, K, N, dev = plan.tokens, bank.in_features, bank.out_features, plan.device
+    T, dev = plan.tokens, plan.device
+    bank = _bank(down, up, scaling, ranks, dev)
+    K, N = bank.in_features, bank.out_features
+    if plan.adapters != bank.adapters:
+        raise ValueError("a plan of %d adapters with a bank of %d" % (plan.adapters, bank.adapters))
     ty = (down.dtype,)
     ld_dy = _rows(dy, "dy", T, N, ty, dev)
     want_dx, want_factors = want

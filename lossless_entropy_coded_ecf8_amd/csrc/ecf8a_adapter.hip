@@ -10,14 +10,17 @@
 // tokens' rows once (and, for single tokens, by reading the factors), so the
 // matrix instructions only have to keep out of the way.
 //
-// Z stays in float32 between the kernels.  Where it is an operand of a matrix
-// instruction it goes in as two bfloat16 (split8), which costs a second
-// instruction on a unit that waits for memory anyway and keeps 16 bits of it;
-// the float16 factors and rows go in as two bfloat16 as well (exact), since a
-// float16 cannot hold Z's range.
+// Z is summed in float32 and handed on as two bfloat16 (split2), the form in which
+// the matrix instructions take it: 16 bits of it are kept for a second
+// instruction on a unit that waits for memory anyway.  It is written once in the
+// layout of each reader: by slot for `wide` (a lane takes eight rank rows of a
+// token), by rank row for `factor` (eight tokens of a rank row), so that both load
+// their operands 16 bytes at a time and compute nothing.  The float16 factors and
+// rows go in as two bfloat16 as well (exact), since a float16 cannot hold Z's range.
 //
 // Tokens are taken in the plan's order: sorted by adapter, each group padded
-// to 16 slots, cut into chunks of at most 64 slots that share one adapter.
+// to 16 slots, cut into chunks of at most 64 slots that share one adapter.  Few
+// tokens take one kernel that does `low` and `wide` for 16 of them (few_kernel).
 #include "ecf8a_common.h"
 
 namespace {
@@ -28,6 +31,7 @@ constexpr int kTile = 16;                 // slots a group is padded to: one mat
 constexpr int kChunk = 64;                // slots of one chunk at most
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanLds = 15 * 1024;       // ints of LDS for the grouping
+constexpr int kBatch = 8;
 constexpr int kThreads = 256;
 constexpr int kStrip = 128;               // columns of one wave: 16 lanes of 8
 
@@ -113,7 +117,24 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
     __syncthreads();
     const int run = ((tokens + waves - 1) / waves + 63) / 64 * 64;
     const int t0 = min(tokens, wave * run), t1 = wave < waves ? min(tokens, t0 + run) : t0;
-    for (int t = t0 + lane; t < t1; t += 64) atomicAdd(&hist[wave * groups + read_index(index, index_bytes, t, adapters)], 1);
+    int mine[kBatch];                                       // the adapters of kBatch tokens, -1 past the end: loads in flight
+    const auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) mine[i] = t + i * 64 + lane < t1 ? read_index(index, index_bytes, t + i * 64 + lane, adapters) : -1;
+    };
+    for (int t = t0; t < t1; t += 64 * kBatch) {
+        fetch(t);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int first = __builtin_amdgcn_readfirstlane(mine[i]);
+            const uint64_t real = __ballot(mine[i] >= 0);
+            if (__ballot(mine[i] == first || mine[i] < 0) == ~0ull) {     // one request's tokens: one addition
+                if (lane == 0 && first >= 0) atomicAdd(&hist[wave * groups + first], (int)__popcll(real));
+            } else if (mine[i] >= 0) {
+                atomicAdd(&hist[wave * groups + mine[i]], 1);
+            }
+        }
+    }
     __syncthreads();
     // Per thread a run of groups, so that one scan over threads covers all.
     const int per = (groups + kPlanThreads - 1) / kPlanThreads;
@@ -166,27 +187,30 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
         const int at = (c - chunk0[lo]) * kChunk;
         p.chunks[c] = i32x4{lo, slot0[lo] + at, min(kChunk, count[lo] - at), 0};
     }
-    for (int tb = t0; tb < t1; tb += 64) {
-        const int t = tb + lane;
-        const int a = t < t1 ? read_index(index, index_bytes, t, adapters) : -1;
-        const int first = __builtin_amdgcn_readfirstlane(a);
-        int rank = 0, same = 0;
-        if (__ballot(a == first || a < 0) == ~0ull) {        // one request's tokens: the usual case of a prompt
-            rank = lane;
-            same = (int)__popcll(__ballot(a >= 0));
-        } else {
+    for (int tb = t0; tb < t1; tb += 64 * kBatch) {
+        if (run > 64 * kBatch) fetch(tb);                   // else they are still there
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                const int o = __builtin_amdgcn_readlane(a, j);
-                same += o == a;
-                rank += o == a && j < lane;
+        for (int i = 0; i < kBatch; ++i) {
+            const int a = mine[i];
+            const int first = __builtin_amdgcn_readfirstlane(a);
+            if (first < 0) continue;                        // valid lanes are a prefix
+            int rank = 0, same = 0;
+            if (__ballot(a == first || a < 0) == ~0ull) {
+                rank = lane;
+                same = (int)__popcll(__ballot(a >= 0));
+            } else {
+                for (int j = 0; j < 64; ++j) {
+                    const int o = __builtin_amdgcn_readlane(a, j);
+                    same += o == a;
+                    rank += o == a && j < lane;
+                }
             }
-        }
-        if (a >= 0) {
-            volatile int* next = &hist[wave * groups + a];
-            const int at = *next;
-            p.slot_token[at + rank] = t;
-            if (rank == same - 1) *next = at + same;          // one lane of each adapter, after every lane's read
+            if (a >= 0) {
+                volatile int* next = &hist[wave * groups + a];
+                const int at = *next;
+                p.slot_token[at + rank] = tb + i * 64 + lane;
+                if (rank == same - 1) *next = at + same;    // one lane of each adapter, after every lane's read
+            }
         }
     }
 }
@@ -235,6 +259,37 @@ __device__ __forceinline__ void load_row16(const void* row, int k, int limit, u3
     }
 }
 
+// Where a Z goes: by slot and by rank row, each as the upper and then the lower
+// bfloat16; either may be absent.
+struct Forms {
+    uint16_t* slot;          // [2][max_slots][zr]
+    uint16_t* row;           // [2][zr][max_slots]
+    int64_t plane;           // max_slots * zr
+    int slots, zr;
+};
+
+// Four consecutive rank rows of one slot.
+__device__ __forceinline__ void write_forms(const Forms& f, int slot, int row, f32x4 v)
+{
+    uint32_t h0, l0, h1, l1;
+    split2(v[0], v[1], h0, l0);
+    split2(v[2], v[3], h1, l1);
+    if (f.slot) {
+        uint16_t* p = f.slot + (int64_t)slot * f.zr + row;
+        *reinterpret_cast<uint2*>(p) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(p + f.plane) = make_uint2(l0, l1);
+    }
+    if (f.row) {
+        const uint32_t h[2] = {h0, h1}, l[2] = {l0, l1};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint16_t* p = f.row + (int64_t)(row + i) * f.slots + slot;
+            p[0] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
+            p[f.plane] = (uint16_t)(l[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
 struct LowArgs {
     PlanView plan;
     const void* v;           // tokens' rows
@@ -243,106 +298,156 @@ struct LowArgs {
     const float* scaling;
     const int32_t* ranks;
     const float* v_scale;
-    float* z;                // [plane][max_slots][zr]
-    int64_t plane;           // floats of one plane
-    int width, rank, zr, adapters;
+    float* planes;           // [share][max_slots][zr] where the width is split, else nullptr
+    Forms forms;
+    int width, rank, adapters;
+    int per;                 // workgroups per chunk
 };
 
-// One workgroup: one chunk, 16 RT rank rows, one of gridDim.y shares of the
-// width.  Its four waves take 64-column blocks in turn, so that a wave's two
-// loads of a row cover whole 128-byte lines, and meet in LDS.
-template <int TYPE, int VT, int RT, int NT, bool VEC>
-__device__ __forceinline__ void low_body(const LowArgs& A, const i32x4 chunk, f32x4* red)
+__device__ __forceinline__ int rank_of(const int32_t* ranks, int a, int rank)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int a = chunk[0], r0 = blockIdx.z * 64;
-    const int rank = A.ranks ? min(max(A.ranks[a], 0), A.rank) : A.rank;
-    const void* vrow[NT];
-    bool real[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {                          // padding reads row 0; its result is set to 0 below
-        const int t = n * kTile < chunk[2] ? A.plan.slot_token[chunk[1] + n * kTile + c] : -1;
-        real[n] = t >= 0;
-        vrow[n] = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(t, 0) * A.ldv;
-    }
+    return ranks ? min(max(ranks[a], 0), rank) : rank;
+}
+
+// The products of RT times 16 rank rows from r0 on with NT times 16 tokens over
+// the 64-column blocks first, first + step, ...  A wave's two loads of a row cover
+// whole 128-byte lines.
+template <int TYPE, int VT, int RT, int NT, bool VEC>
+__device__ __forceinline__ void low_products(const void* const* vrow, const uint16_t* f, int64_t f_row, int r0, int rank,
+                                             int width, int first, int step, f32x4 (*acc)[NT])
+{
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const uint16_t* frow[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-        frow[r] = A.f + ((int64_t)a * A.rank + max(0, min(r0 + r * 16 + c, rank - 1))) * A.width;
-    f32x4 acc[RT][NT] = {};
-    const int blocks = (A.width + 63) / 64, whole = A.width / 64;
-    for (int b = blockIdx.y * 4 + wave; b < blocks; b += gridDim.y * 4) {
-        const int k = b * 64 + 16 * g;
-        u32x4 fv[RT][2], vv[NT][2];
-        if (b < whole) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, false>(vrow[n], k, A.width, vv[n]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, false>(frow[r], k, A.width, fv[r]);
-        } else {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, true>(vrow[n], k, A.width, vv[n]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, true>(frow[r], k, A.width, fv[r]);
-        }
+    for (int r = 0; r < RT; ++r) frow[r] = f + (f_row + max(0, min(r0 + r * 16 + c, rank - 1))) * width;
+    const int blocks = (width + 63) / 64, whole = width / 64;
+    const auto products = [&](const u32x4 (*fv)[2], const u32x4 (*vv)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[r][n] = mfma<TYPE>(fv[r][h], vv[n][h], acc[r][n]);
+    };
+    int b = first;
+    for (; b < whole; b += step) {
+        const int k = b * 64 + 16 * g;
+        u32x4 fv[RT][2], vv[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, false>(vrow[n], k, width, vv[n]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, false>(frow[r], k, width, fv[r]);
+        products(fv, vv);
     }
+    if (b < blocks) {                                       // the last block, not whole: zeros past the width
+        const int k = b * 64 + 16 * g;
+        u32x4 fv[RT][2], vv[NT][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, true>(vrow[n], k, width, vv[n]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) red[(wave * RT * NT + r * NT + n) * 64 + lane] = acc[r][n];
-    __syncthreads();
-    float scale = A.scaling[a];
-    if (A.v_scale) scale *= *A.v_scale;
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if ((r * NT + n) % 4 != wave || n * kTile >= chunk[2]) continue;   // tiles past the chunk are another's
-            f32x4 s = red[(r * NT + n) * 64 + lane];
-            for (int w = 1; w < 4; ++w) s += red[(w * RT * NT + r * NT + n) * 64 + lane];
-            const int row = r0 + r * 16 + 4 * g;
-            if (row >= A.zr) continue;
-            f32x4 o;
-            for (int i = 0; i < 4; ++i) o[i] = real[n] && row + i < rank ? s[i] * scale : 0.0f;
-            float* z = A.z + blockIdx.y * A.plane + (int64_t)(chunk[1] + n * kTile + c) * A.zr + row;
-            *reinterpret_cast<f32x4*>(z) = o;
-        }
+        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, true>(frow[r], k, width, fv[r]);
+        products(fv, vv);
+    }
 }
 
-template <int TYPE, int VT, int RT, bool VEC>
-__global__ __launch_bounds__(kThreads) void low_kernel(LowArgs A)
+// Sums TILES results over the WAVES waves of a workgroup, in a fixed order; wave w
+// gives tiles w, w + WAVES, ... to done(tile, sum).  red: WAVES / 2 * TILES * 64.
+template <int WAVES, int TILES, typename F>
+__device__ __forceinline__ void sum_waves(const f32x4* acc, f32x4* red, F done)
 {
-    __shared__ f32x4 red[4 * RT * 4 * 64];
-    if ((int)blockIdx.x >= A.plan.head[0]) return;
-    const i32x4 chunk = A.plan.chunks[blockIdx.x];
-    if (chunk[0] >= A.adapters) return;
-    if (chunk[2] <= 16) low_body<TYPE, VT, RT, 1, VEC>(A, chunk, red);
-    else if (chunk[2] <= 32) low_body<TYPE, VT, RT, 2, VEC>(A, chunk, red);
-    else low_body<TYPE, VT, RT, 4, VEC>(A, chunk, red);
+    constexpr int HALF = WAVES / 2;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (wave >= HALF)
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) red[((wave - HALF) * TILES + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    if (wave < HALF)
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) red[(wave * TILES + i) * 64 + lane] += acc[i];
+    __syncthreads();
+    for (int i = wave; i < TILES; i += WAVES) {
+        f32x4 s = red[i * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < HALF; ++w) s += red[(w * TILES + i) * 64 + lane];
+        done(i, s);
+    }
+}
+
+// One workgroup: up to NT tiles of one chunk, 16 RT rank rows, one of gridDim.y
+// shares of the width.  Its eight waves take 64-column blocks in turn and meet in
+// LDS.  NT and the shares are chosen so that 256 workgroups or more read the rows:
+// measured at 4096 x 4096, rank 16, bfloat16: 12 us + 5 us to join with chunks of 64
+// in 15 shares, see the table of the design notes for the present figure.
+template <int TYPE, int VT, int RT, int NT, bool VEC>
+__device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int tokens, f32x4* red)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4, r0 = blockIdx.z * 64;
+    const int rank = rank_of(A.ranks, a, A.rank);
+    const void* vrow[NT];
+    bool real[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {                          // padding reads row 0; its result is set to 0 below
+        const int t = n * kTile < tokens ? A.plan.slot_token[slot0 + n * kTile + c] : -1;
+        real[n] = t >= 0;
+        vrow[n] = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(t, 0) * A.ldv;
+    }
+    f32x4 acc[RT][NT] = {};
+    low_products<TYPE, VT, RT, NT, VEC>(vrow, A.f, (int64_t)a * A.rank, r0, rank, A.width, blockIdx.y * 8 + wave, gridDim.y * 8, acc);
+    float scale = A.scaling[a];
+    if (A.v_scale) scale *= *A.v_scale;
+    sum_waves<8, RT * NT>(&acc[0][0], red, [&](int tile, f32x4 s) {
+        const int n = tile % NT, row = r0 + tile / NT * 16 + 4 * g;
+        if (n * kTile >= tokens || row >= A.forms.zr) return;   // tiles past the chunk are another's
+        bool have = false;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) have = i == n ? real[i] : have;
+        f32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = have && row + i < rank ? s[i] * scale : 0.0f;
+        const int slot = slot0 + n * kTile + c;
+        if (A.planes) *reinterpret_cast<f32x4*>(A.planes + blockIdx.y * A.forms.plane + (int64_t)slot * A.forms.zr + row) = o;
+        else write_forms(A.forms, slot, row, o);
+    });
+}
+
+template <int TYPE, int VT, int RT, int NT, bool VEC>
+__global__ __launch_bounds__(512) void low_kernel(LowArgs A)
+{
+    __shared__ f32x4 red[4 * RT * NT * 64];
+    const int id = blockIdx.x / A.per, at = (blockIdx.x - id * A.per) * NT * kTile;
+    if (id >= A.plan.head[0]) return;
+    const i32x4 chunk = A.plan.chunks[id];
+    if (chunk[0] >= A.adapters || at >= chunk[2]) return;
+    const int tokens = min(chunk[2] - at, NT * kTile);
+    if (NT >= 2 && tokens <= kTile) low_body<TYPE, VT, RT, 1, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
+    else low_body<TYPE, VT, RT, NT, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
 }
 
 // Sums the planes of a split width, in plane order.
-__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ planes, int64_t plane, int count,
-                                                        const int* __restrict__ head, int zr, float* __restrict__ z)
+__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ planes, int count,
+                                                        const int* __restrict__ head, Forms f)
 {
     const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-    if (i >= (int64_t)head[1] * zr) return;
-    f32x4 s = *reinterpret_cast<const f32x4*>(planes + i);
-    for (int p = 1; p < count; ++p) s += *reinterpret_cast<const f32x4*>(planes + p * plane + i);
-    *reinterpret_cast<f32x4*>(z + i) = s;
+    if (i >= (int64_t)head[1] * f.zr) return;
+    f32x4 s{0, 0, 0, 0};
+    for (int p = 0; p < count; p += 8) {                    // eight loads in flight
+        f32x4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4*>(planes + min(p + j, count - 1) * f.plane + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (p + j < count) s += v[j];
+    }
+    const int slot = (int)(i / f.zr);
+    write_forms(f, slot, (int)(i - (int64_t)slot * f.zr), s);
 }
 
 // ------------------------------------------------------------- wide: O = B + Z F
 
 struct WideArgs {
     PlanView plan;
-    const float* z;
+    const uint16_t* z;       // by slot
+    int64_t plane;
     const uint16_t* f;
     const int32_t* ranks;
     const uint16_t* base;
@@ -380,12 +485,65 @@ __device__ __forceinline__ void load_factor(const uint16_t* f, int width, int r,
     }
 }
 
+// Eight columns of a row, 0 past the width.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load_cols(const uint16_t* row, int col, int width)
+{
+    u32x4 v{0, 0, 0, 0};
+    if constexpr (VEC) {
+        if (col < width) v = *reinterpret_cast<const u32x4*>(row + col);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col + j < width) v[j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
+    }
+    return v;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_cols(uint16_t* row, int col, int width, u32x4 v)
+{
+    if constexpr (VEC) {
+        if (col < width) *reinterpret_cast<u32x4*>(row + col) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col + j < width) row[col + j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// One row's eight columns: base plus the results of its token, rounded once.
+template <int TYPE>
+__device__ __forceinline__ u32x4 add_row(u32x4 base, const f32x4* acc, int i)
+{
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const f32x2 b = unpack2<TYPE>(base[j]);
+        o[j] = pack2<TYPE>(b[0] + acc[2 * j][i], b[1] + acc[2 * j + 1][i]);
+    }
+    return o;
+}
+
+// The products of 16 tokens with BLOCKS blocks of 32 rank rows at this lane's eight
+// columns.  HALF: up to 16 rank rows, whose lower bfloat16 take the upper half of
+// the reduction slots, so that one instruction does both.
+template <int TYPE, bool HALF>
+__device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* hi, const u32x4* lo, f32x4* acc)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        acc[j] = mfma_bf16(zh, hi[j], acc[j]);
+        if constexpr (!HALF) acc[j] = mfma_bf16(zl, hi[j], acc[j]);
+        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(zh, lo[j], acc[j]);
+    }
+}
+
 // One wave: 128 columns of one chunk.  A lane's eight columns are consecutive
 // (column 8c + j goes to the j-th instruction), so that the factor's rows are
 // read, and the result's rows read and written, 16 bytes at a time, and no LDS
 // is used.  RB: blocks of 32 rank rows kept in registers for the whole chunk
-// (0: up to 16 rows, the upper half of the slots taking lo; -1: any number,
-// read again for each 16 tokens).
+// (0: up to 16 rows; -1: any number, read again for each 16 tokens).
 template <int TYPE, int RB, bool VEC>
 __global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
 {
@@ -397,8 +555,30 @@ __global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
     if (col - 8 * c >= A.width) return;
     const bool bare = a >= A.adapters;
     if (bare && A.base == A.out) return;
-    const int rank = bare ? 0 : A.ranks ? min(max(A.ranks[a], 0), A.rank) : A.rank;
-    const uint16_t* f = A.f + (int64_t)(bare ? 0 : a) * A.rank * A.width;
+    const int tiles = (chunk[2] + kTile - 1) / kTile;
+    i32x4 tok[4];
+    u32x4 base[4][4];
+    const auto fetch = [&](int tile) {                      // all rows of the chunk are sent for before the first is used
+        tok[tile] = i32x4{-1, -1, -1, -1};
+        if (tile < tiles) tok[tile] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + chunk[1] + tile * kTile + 4 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            base[tile][i] = u32x4{0, 0, 0, 0};
+            if (A.base && tok[tile][i] >= 0) base[tile][i] = load_cols<VEC>(A.base + tok[tile][i] * A.ld_base, col, A.width);
+        }
+    };
+#pragma unroll
+    for (int tile = 0; tile < 4; ++tile) fetch(tile);
+    if (bare) {
+#pragma unroll
+        for (int tile = 0; tile < 4; ++tile)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tok[tile][i] >= 0) store_cols<VEC>(A.out + tok[tile][i] * A.ld_out, col, A.width, base[tile][i]);
+        return;
+    }
+    const int rank = rank_of(A.ranks, a, A.rank);
+    const uint16_t* f = A.f + (int64_t)a * A.rank * A.width;
     constexpr int KEEP = RB <= 0 ? 1 : RB;
     u32x4 hi[KEEP][8], lo[KEEP][8];
     if constexpr (RB == 0) load_factor<TYPE, VEC>(f, A.width, 8 * (g & 1), rank, col, hi[0], lo[0]);
@@ -406,92 +586,200 @@ __global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
 #pragma unroll
         for (int b = 0; b < KEEP; ++b) load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi[b], lo[b]);
     }
-    const int tiles = (chunk[2] + kTile - 1) / kTile;
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int slot = chunk[1] + tile * kTile;
-        const i32x4 tok = *reinterpret_cast<const i32x4*>(A.plan.slot_token + slot + 4 * g);
+#pragma unroll
+    for (int tile = 0; tile < 4; ++tile) {
+        if (tile >= tiles) break;
+        const uint16_t* z = A.z + (int64_t)(chunk[1] + tile * kTile + c) * A.zr;
+        f32x4 acc[8] = {};
+        if constexpr (RB == 0) {
+            const u32x4 both = *reinterpret_cast<const u32x4*>(z + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
+            wide_products<TYPE, true>(both, both, hi[0], lo[0], acc);
+        } else {
+            const auto block = [&](int b, int at) {
+                const uint16_t* p = z + 32 * b + 8 * g;
+                wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + A.plane), hi[at], lo[at], acc);
+            };
+            if constexpr (RB > 0) {
+#pragma unroll
+                for (int b = 0; b < RB; ++b) block(b, b);
+            } else {
+                for (int b = 0; b < (A.zr + 31) / 32; ++b) {
+                    load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi[0], lo[0]);
+                    block(b, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (tok[tile][i] >= 0)
+                store_cols<VEC>(A.out + tok[tile][i] * A.ld_out, col, A.width, add_row<TYPE>(base[tile][i], acc, i));
+    }
+}
+
+// ------------------------------------------------------------- few tokens: both at once
+
+struct FewArgs {
+    PlanView plan;           // used where index is nullptr
+    const void* index;
+    int index_bytes, tokens;
+    const void* v;
+    int64_t ldv;
+    const uint16_t* f;       // (adapters, rank, in)
+    const uint16_t* f2;      // (adapters, rank, out)
+    const float* scaling;
+    const int32_t* ranks;
+    const float* v_scale;
+    const uint16_t* base;
+    int64_t ld_base;
+    uint16_t* out;           // nullptr: only the forms are wanted
+    int64_t ld_out;
+    Forms forms;             // by rank row, for the gradients; row nullptr: not wanted
+    int in, width, rank, adapters;
+};
+
+// One workgroup: 16 tokens of one adapter, from their rows to the result.  Its
+// waves split the input width for `low`, leave h in LDS, and split the output width
+// for `wide`.  One launch, no workspace and no grouping beforehand: without a plan,
+// workgroup b looks token b's adapter up among all tokens and goes on if b is its
+// first token, or the 17th, ...  What bounds it is how fast one compute unit reads
+// both factors of its adapter (about 100 GB/s): it is taken where that is short.
+constexpr int few_waves(int rt) { return rt == 4 ? 8 : 16; }      // rank 64 needs the registers of eight
+
+template <int TYPE, int VT, int RT, bool VEC>
+__global__ __launch_bounds__(64 * few_waves(RT)) void few_kernel(FewArgs A)
+{
+    constexpr int ZR = 16 * RT, WAVES = few_waves(RT);
+    __shared__ f32x4 red[WAVES / 2 * RT * 64];
+    __shared__ __attribute__((aligned(16))) uint16_t zs[2][16][ZR + 8];   // 8 more: rows meet different banks
+    __shared__ uint64_t found[WAVES];
+    __shared__ __attribute__((aligned(16))) int list[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+    int a, slot0 = 0;
+    if (A.index) {
+        const int b = blockIdx.x;
+        a = read_index(A.index, A.index_bytes, b, A.adapters);
+        if (a >= A.adapters) {                              // no adapter: the row itself
+            if (!A.out || A.base == A.out) return;
+            for (int col = 8 * tid; col < A.width; col += 8 * 64 * WAVES) {
+                u32x4 v{0, 0, 0, 0};
+                if (A.base) v = load_cols<VEC>(A.base + b * A.ld_base, col, A.width);
+                store_cols<VEC>(A.out + b * A.ld_out, col, A.width, v);
+            }
+            return;
+        }
+        const bool same = tid < A.tokens && read_index(A.index, A.index_bytes, tid, A.adapters) == a;
+        const uint64_t ballot = __ballot(same);
+        if (lane == 0) found[wave] = ballot;
+        if (tid < 16) list[tid] = -1;
+        __syncthreads();
+        int before = 0, mine = 0;                           // how many of the adapter's tokens lie before b, and before this one
+        for (int w = 0; w < WAVES; ++w) {
+            const int n = (int)__popcll(found[w]);
+            before += w < (b >> 6) ? n : w == (b >> 6) ? (int)__popcll(found[w] & ((1ull << (b & 63)) - 1)) : 0;
+            mine += w < wave ? n : 0;
+        }
+        if (before % 16) return;
+        mine += (int)__popcll(ballot & ((1ull << lane) - 1)) - before;
+        if (same && mine >= 0 && mine < 16) list[mine] = tid;
+    } else {
+        const int id = blockIdx.x / 4, at = (blockIdx.x & 3) * kTile;
+        if (id >= A.plan.head[0]) return;
+        const i32x4 chunk = A.plan.chunks[id];
+        if (at >= chunk[2]) return;
+        a = chunk[0];
+        slot0 = chunk[1] + at;
+        if (tid < 16) list[tid] = A.plan.slot_token[slot0 + tid];
+        if (a >= A.adapters) {
+            if (!A.out || A.base == A.out) return;
+            __syncthreads();
+            for (int i = wave; i < 16; i += WAVES) {
+                const int t = list[i];
+                if (t < 0) continue;
+                for (int col = 8 * lane; col < A.width; col += 8 * 64) {
+                    u32x4 v{0, 0, 0, 0};
+                    if (A.base) v = load_cols<VEC>(A.base + t * A.ld_base, col, A.width);
+                    store_cols<VEC>(A.out + t * A.ld_out, col, A.width, v);
+                }
+            }
+            return;
+        }
+    }
+    __syncthreads();
+    const int rank = rank_of(A.ranks, a, A.rank);
+    const bool real = list[c] >= 0;
+    const void* vrow = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(list[c], 0) * A.ldv;
+    f32x4 acc[RT][1] = {};
+    low_products<TYPE, VT, RT, 1, VEC>(&vrow, A.f, (int64_t)a * A.rank, 0, rank, A.in, wave, WAVES, acc);
+    float scale = A.scaling[a];
+    if (A.v_scale) scale *= *A.v_scale;
+    sum_waves<WAVES, RT>(&acc[0][0], red, [&](int tile, f32x4 s) {
+        const int row = tile * 16 + 4 * g;
+        f32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = real && row + i < rank ? s[i] * scale : 0.0f;
+        uint32_t h0, l0, h1, l1;
+        split2(o[0], o[1], h0, l0);
+        split2(o[2], o[3], h1, l1);
+        *reinterpret_cast<uint2*>(&zs[0][c][row]) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(&zs[1][c][row]) = make_uint2(l0, l1);
+        if (A.forms.row && row < A.forms.zr) write_forms(A.forms, slot0 + c, row, o);
+    });
+    __syncthreads();
+    if (!A.out) return;
+    const i32x4 tok = *reinterpret_cast<const i32x4*>(&list[4 * g]);
+    const uint16_t* f = A.f2 + (int64_t)a * A.rank * A.width;
+    for (int strip = wave * kStrip; strip < A.width; strip += WAVES * kStrip) {
+        const int col = strip + 8 * c;
         u32x4 base[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             base[i] = u32x4{0, 0, 0, 0};
-            if (!A.base || tok[i] < 0) continue;
-            const uint16_t* p = A.base + tok[i] * A.ld_base + col;
-            if constexpr (VEC) {
-                if (col < A.width) base[i] = *reinterpret_cast<const u32x4*>(p);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j < A.width) base[i][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-            }
+            if (A.base && tok[i] >= 0) base[i] = load_cols<VEC>(A.base + tok[i] * A.ld_base, col, A.width);
         }
-        f32x4 acc[8] = {};
-        if (!bare) {
-            const float* z = A.z + (int64_t)(slot + c) * A.zr;
-            if constexpr (RB == 0) {
-                u32x4 zh, zl;
-                const float* p = z + 8 * (g & 1);
-                split8(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4), zh, zl);
-                const u32x4 both = g < 2 ? zh : zl;
+        f32x4 sum[8] = {};
+        u32x4 hi[8], lo[8];
+        if constexpr (RT == 1) {
+            load_factor<TYPE, VEC>(f, A.width, 8 * (g & 1), rank, col, hi, lo);
+            const u32x4 both = *reinterpret_cast<const u32x4*>(&zs[g >> 1][c][8 * (g & 1)]);
+            wide_products<TYPE, true>(both, both, hi, lo, sum);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc[j] = mfma_bf16(both, hi[0][j], acc[j]);
-                    if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(both, lo[0][j], acc[j]);
-                }
-            } else {
-                const int blocks = RB > 0 ? RB : (A.zr + 31) / 32;
-                for (int b = 0; b < blocks; ++b) {
-                    const int at = RB > 0 ? b : 0;
-                    if constexpr (RB < 0) load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi[0], lo[0]);
-                    u32x4 zh, zl;
-                    const float* p = z + 32 * b + 8 * g;
-                    split8(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4), zh, zl);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        acc[j] = mfma_bf16(zh, hi[at][j], acc[j]);
-                        acc[j] = mfma_bf16(zl, hi[at][j], acc[j]);
-                        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(zh, lo[at][j], acc[j]);
-                    }
-                }
+            for (int b = 0; b < RT / 2; ++b) {
+                load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi, lo);
+                wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(&zs[0][c][32 * b + 8 * g]),
+                                           *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, sum);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (tok[i] < 0) continue;
-            u32x4 o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x2 b = unpack2<TYPE>(base[i][j]);
-                o[j] = bare ? base[i][j] : pack2<TYPE>(b[0] + acc[2 * j][i], b[1] + acc[2 * j + 1][i]);
-            }
-            uint16_t* p = A.out + tok[i] * A.ld_out + col;
-            if constexpr (VEC) {
-                if (col < A.width) *reinterpret_cast<u32x4*>(p) = o;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j < A.width) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
-            }
-        }
+        for (int i = 0; i < 4; ++i)
+            if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, add_row<TYPE>(base[i], sum, i));
     }
 }
 
 // ------------------------------------------------------------- factor: G = Z^T V
 
-struct FactorArgs {
-    PlanView plan;
-    const float* z;
+struct FactorSide {
+    const uint16_t* z;       // by rank row
     const uint16_t* v;
     int64_t ldv;
-    const int32_t* ranks;
     uint16_t* grad;          // (adapters, rank, width)
     float* part;             // [unit][zr][stride]
-    int width, stride, rank, zr, adapters;
+    int width, stride;
 };
 
-// One workgroup: one unit of one adapter's slots, 128 columns, 16 RT rank rows.
-// Its four waves take 32 slots in turn; a lane reads eight tokens' 16 bytes and
-// turns them, as load_factor does, so that the sum over tokens runs in the
-// matrix instructions' reduction slots.  An adapter of one unit is written at
+struct FactorArgs {
+    PlanView plan;
+    FactorSide side[2];      // d_down from z and x, d_up from h and dy
+    const int32_t* ranks;
+    int64_t plane;
+    int rank, zr, slots, adapters;
+    int strips;              // of side 0
+};
+
+// One workgroup: one unit of one adapter's slots, 128 columns of one side, 16 RT
+// rank rows.  Its four waves take 32 slots in turn; a lane reads eight tokens' 16
+// bytes and turns them, as load_factor does, so that the sum over tokens runs in
+// the matrix instructions' reduction slots.  An adapter of one unit is written at
 // once, others leave float32 partial sums that sum_kernel joins in order.
 template <int TYPE, int RT, bool VEC>
 __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
@@ -499,48 +787,41 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
     __shared__ f32x4 red[2 * RT * 8 * 64];
     if ((int)blockIdx.y >= A.plan.head[2]) return;
     const i32x4 unit = A.plan.units[blockIdx.y];
+    const bool second = (int)blockIdx.x >= A.strips;
+    const FactorSide& S = A.side[second];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int col = blockIdx.x * kStrip + 8 * c, r0 = blockIdx.z * 64;
-    const bool inside = col < A.width;
-    const int safe = inside ? col : 0;
+    const int col = (blockIdx.x - (second ? A.strips : 0)) * kStrip + 8 * c, r0 = blockIdx.z * 64;
+    const bool inside = col < S.width;
     f32x4 acc[RT][8] = {};
-    for (int s = wave * 32; s < unit[2]; s += 128) {
-        const int slot = unit[1] + s + 8 * g;
-        const bool have = s + 8 * g < unit[2];                // units are whole tiles of 16: eight slots are in or out
-        i32x4 tok[2] = {{-1, -1, -1, -1}, {-1, -1, -1, -1}};
-        if (have) {
-            tok[0] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + slot);
-            tok[1] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + slot + 4);
+    i32x4 tok[2];
+    const auto tokens_of = [&](int s) {
+        tok[0] = tok[1] = i32x4{-1, -1, -1, -1};
+        if (s + 8 * g < unit[2]) {                            // units are whole tiles of 16: eight slots are in or out
+            tok[0] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + unit[1] + s + 8 * g);
+            tok[1] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + unit[1] + s + 8 * g + 4);
         }
+    };
+    tokens_of(wave * 32);
+    for (int s = wave * 32; s < unit[2]; s += 128) {
+        const bool have = s + 8 * g < unit[2];
         u32x4 w[8], t[8], tl[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const int tq = tok[q >> 2][q & 3];
             w[q] = u32x4{0, 0, 0, 0};
-            if (tq >= 0) {
-                const uint16_t* p = A.v + tq * A.ldv + safe;
-                if constexpr (VEC) w[q] = *reinterpret_cast<const u32x4*>(p);
-                else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + j < A.width) w[q][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-                }
-            }
+            if (tq >= 0) w[q] = load_cols<VEC>(S.v + tq * S.ldv, col, S.width);
         }
+        tokens_of(s + 128);
         u32x4 zh[RT], zl[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = r0 + r * 16 + c;
-            f32x4 lo4{0, 0, 0, 0}, hi4{0, 0, 0, 0};
+            zh[r] = zl[r] = u32x4{0, 0, 0, 0};
             if (have && row < A.zr) {
-                const float* z = A.z + (int64_t)slot * A.zr + row;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    lo4[q] = z[q * A.zr];
-                    hi4[q] = z[(q + 4) * A.zr];
-                }
+                const uint16_t* z = S.z + (int64_t)row * A.slots + unit[1] + s + 8 * g;
+                zh[r] = *reinterpret_cast<const u32x4*>(z);
+                zl[r] = *reinterpret_cast<const u32x4*>(z + A.plane);
             }
-            split8(lo4, hi4, zh[r], zl[r]);
         }
         transpose8(w, t);
         if constexpr (TYPE == kFp16) {
@@ -572,8 +853,7 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
         __syncthreads();
     }
     if (wave != 0 || !inside) return;
-    const int a = unit[0];
-    const int rank = A.ranks ? min(max(A.ranks[a], 0), A.rank) : A.rank;
+    const int a = unit[0], rank = rank_of(A.ranks, a, A.rank);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -584,17 +864,11 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
             for (int j = 0; j < 8; ++j) v[j] = row < rank ? acc[r][j][i] : 0.0f;
             if (unit[3]) {
                 if (row >= A.rank) continue;
-                uint16_t* p = A.grad + ((int64_t)a * A.rank + row) * A.width + col;
-                if constexpr (VEC)
-                    *reinterpret_cast<u32x4*>(p) = u32x4{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]),
-                                                         pack2<TYPE>(v[4], v[5]), pack2<TYPE>(v[6], v[7])};
-                else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + j < A.width) p[j] = round1<TYPE>(v[j]);
-                }
+                store_cols<VEC>(S.grad + ((int64_t)a * A.rank + row) * S.width, col, S.width,
+                                u32x4{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]), pack2<TYPE>(v[4], v[5]),
+                                      pack2<TYPE>(v[6], v[7])});
             } else if (row < A.zr) {
-                float* p = A.part + ((int64_t)blockIdx.y * A.zr + row) * A.stride + col;
+                float* p = S.part + ((int64_t)blockIdx.y * A.zr + row) * S.stride + col;
                 *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
@@ -603,39 +877,56 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
 
 // The gradients of adapters with no unit (0) or several (their partial sums).
 template <int TYPE>
-__global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A)
+__global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A, int first)
 {
     const int a = blockIdx.z, row = blockIdx.y;
     const int u0 = A.plan.unit_start[a], u1 = A.plan.unit_start[a + 1];
     if (u1 - u0 == 1) return;
-    for (int col = blockIdx.x * kThreads + threadIdx.x; col < A.width; col += gridDim.x * kThreads) {
-        float s = 0.0f;
-        for (int u = u0; u < u1; ++u) s += A.part[((int64_t)u * A.zr + row) * A.stride + col];
-        A.grad[((int64_t)a * A.rank + row) * A.width + col] = round1<TYPE>(s);
+    const bool second = (int)blockIdx.x >= first;
+    const FactorSide& S = A.side[second];
+    const int col = (blockIdx.x - (second ? first : 0)) * kThreads + threadIdx.x;
+    if (col >= S.width) return;
+    float s = 0.0f;
+    for (int u = u0; u < u1; u += 8) {                      // eight loads in flight, added in order
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = S.part[((int64_t)min(u + j, u1 - 1) * A.zr + row) * S.stride + col];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (u + j < u1) s += v[j];
     }
+    S.grad[((int64_t)a * A.rank + row) * S.width + col] = round1<TYPE>(s);
 }
 
 // ------------------------------------------------------------- host side
 
 uint32_t z_rows(uint32_t rank) { return rank <= 16 ? 16 : (uint32_t)round_up(rank, 32); }
 
-// Shares of the width that a `low` call is cut into: enough workgroups for the
-// card from few chunks, each wave keeping at least one block of 64 columns.
-uint32_t shares_of(const ecf8a_plan& p, uint64_t width)
+// How a `low` call covers the chunks: tiles of one workgroup, and the shares of
+// the width where that leaves fewer than 256 workgroups, each wave of eight keeping
+// at least one block of 64 columns.
+struct LowShape {
+    uint32_t tiles, shares;
+};
+
+LowShape low_shape(const ecf8a_plan& p, uint64_t width)
 {
-    const uint64_t chunks = p.tokens / kChunk + (p.adapters < p.tokens ? p.adapters : p.tokens);
-    uint64_t s = chunks ? 1024 / chunks : 1;
-    const uint64_t most = (width + 255) / 256;
-    if (s > most) s = most;
-    return (uint32_t)(s < 1 ? 1 : s > 16 ? 16 : s);
+    const uint64_t used = p.adapters < p.tokens ? p.adapters : p.tokens;
+    LowShape s{p.tokens >= 16384 ? 4u : p.tokens >= 8192 ? 2u : 1u, 1};
+    const uint64_t groups = p.tokens / (kTile * s.tiles) + used;
+    uint64_t shares = groups ? 256 / groups : 1;
+    const uint64_t most = (width + 511) / 512;
+    if (shares > most) shares = most;
+    s.shares = (uint32_t)(shares < 1 ? 1 : shares > 16 ? 16 : shares);
+    return s;
 }
 
-uint64_t z_bytes(const ecf8a_plan& p, uint32_t rank) { return round_up(4ull * p.max_slots * z_rows(rank), 256); }
+uint64_t form_bytes(const ecf8a_plan& p, uint32_t rank) { return round_up(4ull * p.max_slots * z_rows(rank), 256); }
 
 uint64_t low_bytes(const ecf8a_plan& p, uint32_t rank, uint64_t width)
 {
-    const uint64_t s = shares_of(p, width);
-    return s > 1 ? s * z_bytes(p, rank) : 0;
+    const uint64_t s = low_shape(p, width).shares;
+    return s > 1 ? round_up(s * 4ull * p.max_slots * z_rows(rank), 256) : 0;
 }
 
 uint64_t part_bytes(const ecf8a_plan& p, uint32_t rank, uint64_t width)
@@ -648,13 +939,13 @@ bool plan_ok(const ecf8a_plan* p)
     return p && p->tokens <= ECF8A_MAX_TOKENS && p->adapters >= 1 && p->adapters <= ECF8A_MAX_ADAPTERS;
 }
 
-int check_bank(const ecf8a_plan* plan, const ecf8a_bank* b)
+int check_bank(const ecf8a_bank* b)
 {
-    if (!plan_ok(plan) || !b) return ECF8_ERR_ARG;
+    if (!b) return ECF8_ERR_ARG;
     if (b->type != ECF8A_BF16 && b->type != ECF8A_FP16) return ECF8_ERR_UNSUPPORTED;
-    if (b->adapters != plan->adapters) return ECF8_ERR_ARG;
-    if (b->rank < 1 || b->rank > ECF8A_MAX_RANK || b->in_features < 1 || b->in_features > ECF8A_MAX_FEATURES ||
-        b->out_features < 1 || b->out_features > ECF8A_MAX_FEATURES)
+    if (b->adapters < 1 || b->adapters > ECF8A_MAX_ADAPTERS || b->rank < 1 || b->rank > ECF8A_MAX_RANK ||
+        b->in_features < 1 || b->in_features > ECF8A_MAX_FEATURES || b->out_features < 1 ||
+        b->out_features > ECF8A_MAX_FEATURES)
         return ECF8_ERR_SIZE;
     if (!b->down || !b->up || !b->scaling || !aligned(b->down, 2) || !aligned(b->up, 2) || !aligned(b->scaling, 4) ||
         !aligned(b->ranks, 4))
@@ -664,37 +955,103 @@ int check_bank(const ecf8a_plan* plan, const ecf8a_bank* b)
 
 bool vec16(const void* p, uint64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
-template <int TYPE, int VT, bool VEC>
-void launch_low(const LowArgs& A, dim3 grid, hipStream_t st)
+// One direction of the pair: rows v of width `in` through factor f, and through
+// factor f2 onto base rows of width `out_width`.
+struct Pass {
+    const void* v;
+    uint64_t ldv;
+    uint32_t vt;
+    const float* v_scale;
+    const void* f;
+    uint64_t in;
+    const void* f2;
+    uint64_t width;
+    const void* base;
+    uint64_t ld_base;
+    void* out;               // nullptr: only the forms
+    uint64_t ld_out;
+};
+
+bool vec_low(const Pass& s)
 {
-    if (A.zr <= 16) low_kernel<TYPE, VT, 1, VEC><<<grid, kThreads, 0, st>>>(A);
-    else if (A.zr <= 32) low_kernel<TYPE, VT, 2, VEC><<<grid, kThreads, 0, st>>>(A);
-    else low_kernel<TYPE, VT, 4, VEC><<<grid, kThreads, 0, st>>>(A);
+    return s.vt == ECF8A_E4M3 ? aligned(s.v, 16) && s.ldv % 16 == 0 && s.in % 16 == 0 && aligned(s.f, 16)
+                              : vec16(s.v, s.ldv) && vec16(s.f, s.in);
 }
 
-// Z of one side into `z`; `planes` holds the shares of a split width.
-int run_low(const ecf8a_plan& p, const ecf8a_bank& b, const void* v, uint64_t ldv, uint32_t vt, const float* v_scale,
-            const void* f, uint64_t width, float* z, float* planes, hipStream_t st)
+bool vec_wide(const Pass& s)
 {
-    const uint32_t shares = shares_of(p, width);
-    LowArgs A{view_of(p), v, (int64_t)ldv, static_cast<const uint16_t*>(f), b.scaling, b.ranks, v_scale,
-              shares > 1 ? planes : z, (int64_t)(z_bytes(p, b.rank) / 4), (int)width, (int)b.rank, (int)z_rows(b.rank),
-              (int)b.adapters};
-    const dim3 grid(p.max_chunks, shares, (A.zr + 63) / 64);
-    const bool e4m3 = vt == ECF8A_E4M3;
-    const bool vec = e4m3 ? aligned(v, 16) && ldv % 16 == 0 && width % 16 == 0 && aligned(f, 16)
-                          : vec16(v, ldv) && vec16(f, width);
+    return vec16(s.f2, s.width) && vec16(s.out, s.ld_out) && (!s.base || vec16(s.base, s.ld_base));
+}
+
+// Whether one kernel does both halves: few tokens, and factors that one compute
+// unit reads in a few microseconds.
+bool few(uint64_t tokens, const ecf8a_bank& b)
+{
+    return tokens <= ECF8A_FEW_TOKENS && b.rank <= 64 && 2ull * b.rank * (b.in_features + b.out_features) <= 2u << 20;
+}
+
+template <int TYPE, int VT, bool VEC>
+void launch_few(const FewArgs& A, uint32_t grid, hipStream_t st)
+{
+    if (A.rank <= 16) few_kernel<TYPE, VT, 1, VEC><<<grid, 64 * few_waves(1), 0, st>>>(A);
+    else if (A.rank <= 32) few_kernel<TYPE, VT, 2, VEC><<<grid, 64 * few_waves(2), 0, st>>>(A);
+    else few_kernel<TYPE, VT, 4, VEC><<<grid, 64 * few_waves(4), 0, st>>>(A);
+}
+
+int run_few(const PlanView& view, uint32_t grid, const void* index, uint32_t index_bytes, uint64_t tokens,
+            const ecf8a_bank& b, const Pass& s, const Forms& forms, hipStream_t st)
+{
+    const FewArgs A{view, index, (int)index_bytes, (int)tokens, s.v, (int64_t)s.ldv, static_cast<const uint16_t*>(s.f),
+                    static_cast<const uint16_t*>(s.f2), b.scaling, b.ranks, s.v_scale,
+                    static_cast<const uint16_t*>(s.base), (int64_t)s.ld_base, static_cast<uint16_t*>(s.out),
+                    (int64_t)s.ld_out, forms, (int)s.in, (int)s.width, (int)b.rank, (int)b.adapters};
+    const bool vec = vec_low(s) && (!s.out || vec_wide(s)), e4m3 = s.vt == ECF8A_E4M3;
     if (b.type == ECF8A_BF16) {
-        if (e4m3) vec ? launch_low<kBf16, kE4m3, true>(A, grid, st) : launch_low<kBf16, kE4m3, false>(A, grid, st);
-        else vec ? launch_low<kBf16, kBf16, true>(A, grid, st) : launch_low<kBf16, kBf16, false>(A, grid, st);
+        if (e4m3) vec ? launch_few<kBf16, kE4m3, true>(A, grid, st) : launch_few<kBf16, kE4m3, false>(A, grid, st);
+        else vec ? launch_few<kBf16, kBf16, true>(A, grid, st) : launch_few<kBf16, kBf16, false>(A, grid, st);
     } else {
-        if (e4m3) vec ? launch_low<kFp16, kE4m3, true>(A, grid, st) : launch_low<kFp16, kE4m3, false>(A, grid, st);
-        else vec ? launch_low<kFp16, kFp16, true>(A, grid, st) : launch_low<kFp16, kFp16, false>(A, grid, st);
+        if (e4m3) vec ? launch_few<kFp16, kE4m3, true>(A, grid, st) : launch_few<kFp16, kE4m3, false>(A, grid, st);
+        else vec ? launch_few<kFp16, kFp16, true>(A, grid, st) : launch_few<kFp16, kFp16, false>(A, grid, st);
     }
-    if (shares > 1) {
-        const uint64_t quads = (uint64_t)p.max_slots * A.zr / 4;
-        join_kernel<<<dim3((uint32_t)((quads + kThreads - 1) / kThreads)), kThreads, 0, st>>>(
-            planes, A.plane, (int)shares, A.plan.head, A.zr, z);
+    return launch_status();
+}
+
+template <int TYPE, int VT, int RT, bool VEC>
+void launch_low_tiles(const LowArgs& A, dim3 grid, uint32_t tiles, hipStream_t st)
+{
+    if (tiles == 1) low_kernel<TYPE, VT, RT, 1, VEC><<<grid, 512, 0, st>>>(A);
+    else if (tiles == 2) low_kernel<TYPE, VT, RT, 2, VEC><<<grid, 512, 0, st>>>(A);
+    else low_kernel<TYPE, VT, RT, 4, VEC><<<grid, 512, 0, st>>>(A);
+}
+
+template <int TYPE, int VT, bool VEC>
+void launch_low(const LowArgs& A, dim3 grid, uint32_t tiles, hipStream_t st)
+{
+    if (A.forms.zr <= 16) launch_low_tiles<TYPE, VT, 1, VEC>(A, grid, tiles, st);
+    else if (A.forms.zr <= 32) launch_low_tiles<TYPE, VT, 2, VEC>(A, grid, tiles, st);
+    else launch_low_tiles<TYPE, VT, 4, VEC>(A, grid, tiles, st);
+}
+
+int run_low(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, float* planes, hipStream_t st)
+{
+    const LowShape shape = low_shape(p, s.in);
+    const LowArgs A{view_of(p), s.v, (int64_t)s.ldv, static_cast<const uint16_t*>(s.f), b.scaling, b.ranks, s.v_scale,
+                    shape.shares > 1 ? planes : nullptr, forms, (int)s.in, (int)b.rank, (int)b.adapters,
+                    (int)(4 / shape.tiles)};
+    const dim3 grid(p.max_chunks * (4 / shape.tiles), shape.shares, (forms.zr + 63) / 64);
+    const bool e4m3 = s.vt == ECF8A_E4M3, vec = vec_low(s);
+    const uint32_t n = shape.tiles;
+    if (b.type == ECF8A_BF16) {
+        if (e4m3) vec ? launch_low<kBf16, kE4m3, true>(A, grid, n, st) : launch_low<kBf16, kE4m3, false>(A, grid, n, st);
+        else vec ? launch_low<kBf16, kBf16, true>(A, grid, n, st) : launch_low<kBf16, kBf16, false>(A, grid, n, st);
+    } else {
+        if (e4m3) vec ? launch_low<kFp16, kE4m3, true>(A, grid, n, st) : launch_low<kFp16, kE4m3, false>(A, grid, n, st);
+        else vec ? launch_low<kFp16, kFp16, true>(A, grid, n, st) : launch_low<kFp16, kFp16, false>(A, grid, n, st);
+    }
+    if (shape.shares > 1) {
+        const uint64_t quads = (uint64_t)p.max_slots * forms.zr / 4;
+        join_kernel<<<dim3((uint32_t)((quads + kThreads - 1) / kThreads)), kThreads, 0, st>>>(planes, (int)shape.shares,
+                                                                                            A.plan.head, forms);
     }
     return launch_status();
 }
@@ -708,17 +1065,26 @@ void launch_wide(const WideArgs& A, dim3 grid, hipStream_t st)
     else wide_kernel<TYPE, -1, VEC><<<grid, kThreads, 0, st>>>(A);
 }
 
-int run_wide(const ecf8a_plan& p, const ecf8a_bank& b, const float* z, const void* f, uint64_t width, const void* base,
-             uint64_t ld_base, void* out, uint64_t ld_out, hipStream_t st)
+int run_wide(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, hipStream_t st)
 {
-    WideArgs A{view_of(p), z, static_cast<const uint16_t*>(f), b.ranks, static_cast<const uint16_t*>(base),
-               (int64_t)ld_base, static_cast<uint16_t*>(out), (int64_t)ld_out, (int)width, (int)b.rank,
-               (int)z_rows(b.rank), (int)b.adapters, (int)((width + 4 * kStrip - 1) / (4 * kStrip))};
+    const WideArgs A{view_of(p), forms.slot, forms.plane, static_cast<const uint16_t*>(s.f2), b.ranks,
+                     static_cast<const uint16_t*>(s.base), (int64_t)s.ld_base, static_cast<uint16_t*>(s.out),
+                     (int64_t)s.ld_out, (int)s.width, (int)b.rank, forms.zr, (int)b.adapters,
+                     (int)((s.width + 4 * kStrip - 1) / (4 * kStrip))};
     const dim3 grid((uint32_t)A.groups * p.max_chunks);
-    const bool vec = vec16(f, width) && vec16(out, ld_out) && (!base || vec16(base, ld_base));
+    const bool vec = vec_wide(s);
     if (b.type == ECF8A_BF16) vec ? launch_wide<kBf16, true>(A, grid, st) : launch_wide<kBf16, false>(A, grid, st);
     else vec ? launch_wide<kFp16, true>(A, grid, st) : launch_wide<kFp16, false>(A, grid, st);
     return launch_status();
+}
+
+// One direction, whichever way.  `forms.row` is written if it is given.
+int run_pass(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, Forms forms, float* planes, hipStream_t st)
+{
+    if (few(p.tokens, b)) return run_few(view_of(p), 4 * p.max_chunks, nullptr, 0, p.tokens, b, s, Forms{nullptr, forms.row, forms.plane, forms.slots, forms.zr}, st);
+    if (!s.out) forms.slot = nullptr;
+    const int rc = run_low(p, b, s, forms, planes, st);
+    return rc == ECF8_OK && s.out ? run_wide(p, b, s, forms, st) : rc;
 }
 
 template <int TYPE, bool VEC>
@@ -729,22 +1095,27 @@ void launch_factor(const FactorArgs& A, dim3 grid, hipStream_t st)
     else factor_kernel<TYPE, 4, VEC><<<grid, kThreads, 0, st>>>(A);
 }
 
-int run_factor(const ecf8a_plan& p, const ecf8a_bank& b, const float* z, const void* v, uint64_t ldv, uint64_t width,
-               void* grad, float* part, hipStream_t st)
+int run_factor(const ecf8a_plan& p, const ecf8a_bank& b, const FactorArgs& A, hipStream_t st)
 {
-    const uint64_t stride = round_up(width, kStrip);
-    FactorArgs A{view_of(p), z, static_cast<const uint16_t*>(v), (int64_t)ldv, b.ranks, static_cast<uint16_t*>(grad),
-                 part, (int)width, (int)stride, (int)b.rank, (int)z_rows(b.rank), (int)b.adapters};
-    const bool vec = vec16(v, ldv) && vec16(grad, width);
+    bool vec = true;
+    for (const FactorSide& s : A.side) vec = vec && vec16(s.v, s.ldv) && vec16(s.grad, s.width);
+    const uint32_t strips = (uint32_t)((A.side[0].stride + A.side[1].stride) / kStrip);
     if (p.tokens) {
-        const dim3 grid((uint32_t)(stride / kStrip), p.max_units, (A.zr + 63) / 64);
+        const dim3 grid(strips, p.max_units, (A.zr + 63) / 64);
         if (b.type == ECF8A_BF16) vec ? launch_factor<kBf16, true>(A, grid, st) : launch_factor<kBf16, false>(A, grid, st);
         else vec ? launch_factor<kFp16, true>(A, grid, st) : launch_factor<kFp16, false>(A, grid, st);
     }
-    const dim3 grid((uint32_t)((width + kThreads - 1) / kThreads), b.rank, b.adapters);
-    if (b.type == ECF8A_BF16) sum_kernel<kBf16><<<grid, kThreads, 0, st>>>(A);
-    else sum_kernel<kFp16><<<grid, kThreads, 0, st>>>(A);
+    const uint32_t first = (A.side[0].width + kThreads - 1) / kThreads, rest = (A.side[1].width + kThreads - 1) / kThreads;
+    const dim3 grid(first + rest, b.rank, b.adapters);
+    if (b.type == ECF8A_BF16) sum_kernel<kBf16><<<grid, kThreads, 0, st>>>(A, (int)first);
+    else sum_kernel<kFp16><<<grid, kThreads, 0, st>>>(A, (int)first);
     return launch_status();
+}
+
+Forms forms_of(const ecf8a_plan& p, uint32_t rank, void* slot, void* row)
+{
+    const int zr = (int)z_rows(rank);
+    return Forms{static_cast<uint16_t*>(slot), static_cast<uint16_t*>(row), (int64_t)p.max_slots * zr, (int)p.max_slots, zr};
 }
 
 bool sizes_ok(uint64_t tokens, uint32_t adapters)
@@ -803,48 +1174,76 @@ extern "C" int ecf8a_plan_prepare(const void* index, uint32_t index_bytes, uint6
 extern "C" uint64_t ecf8a_hidden_bytes(const ecf8a_plan* plan, uint32_t rank)
 {
     if (!plan_ok(plan) || rank < 1 || rank > ECF8A_MAX_RANK) return 0;
-    return z_bytes(*plan, rank);
+    return form_bytes(*plan, rank);
 }
 
 extern "C" uint64_t ecf8a_add_bytes(const ecf8a_plan* plan, const ecf8a_bank* b)
 {
     if (!plan_ok(plan) || !b || b->rank < 1 || b->rank > ECF8A_MAX_RANK) return 0;
-    return z_bytes(*plan, b->rank) + low_bytes(*plan, b->rank, b->in_features) + 256;
+    if (few(plan->tokens, *b)) return 256;
+    return form_bytes(*plan, b->rank) + low_bytes(*plan, b->rank, b->in_features) + 256;
 }
 
 extern "C" uint64_t ecf8a_grads_bytes(const ecf8a_plan* plan, const ecf8a_bank* b)
 {
     if (!plan_ok(plan) || !b || b->rank < 1 || b->rank > ECF8A_MAX_RANK) return 0;
     const uint64_t lk = low_bytes(*plan, b->rank, b->in_features), ln = low_bytes(*plan, b->rank, b->out_features);
-    const uint64_t pk = part_bytes(*plan, b->rank, b->in_features), pn = part_bytes(*plan, b->rank, b->out_features);
-    uint64_t most = lk > ln ? lk : ln;
-    if (pk > most) most = pk;
-    if (pn > most) most = pn;
-    return 2 * z_bytes(*plan, b->rank) + most + 256;
+    const uint64_t parts = part_bytes(*plan, b->rank, b->in_features) + part_bytes(*plan, b->rank, b->out_features);
+    const uint64_t low = lk > ln ? lk : ln;
+    return 3 * form_bytes(*plan, b->rank) + (low > parts ? low : parts) + 256;
+}
+
+extern "C" int ecf8a_few(uint64_t tokens, const ecf8a_bank* bank)
+{
+    return bank && few(tokens, *bank) ? 1 : 0;
+}
+
+// The checks of x, base and out that both ways of adding share.
+static int check_add(const ecf8a_bank* bank, const void* x, uint64_t ldx, uint32_t x_type, const float* x_scale,
+                     const void* base, uint64_t ld_base, const void* out, uint64_t ld_out)
+{
+    if (!x || !out || !aligned(x, x_type == ECF8A_E4M3 ? 1 : 2) || !aligned(out, 2) || !aligned(base, 2) ||
+        !aligned(x_scale, 4) || (base == out && ld_base != ld_out))
+        return ECF8_ERR_ARG;
+    if (ldx < bank->in_features || ld_out < bank->out_features || (base && ld_base < bank->out_features))
+        return ECF8_ERR_SIZE;
+    return ECF8_OK;
+}
+
+extern "C" int ecf8a_add_few(const void* index, uint32_t index_bytes, uint64_t tokens, const ecf8a_bank* bank, const void* x,
+                             uint64_t ldx, uint32_t x_type, const float* x_scale, const void* base, uint64_t ld_base,
+                             void* out, uint64_t ld_out, void* hip_stream)
+{
+    int rc = check_bank(bank);
+    if (rc != ECF8_OK) return rc;
+    if (x_type != bank->type && x_type != ECF8A_E4M3) return ECF8_ERR_UNSUPPORTED;
+    if ((index_bytes != 4 && index_bytes != 8) || (tokens && !index) || !aligned(index, index_bytes)) return ECF8_ERR_ARG;
+    if (tokens > ECF8A_FEW_TOKENS || bank->rank > 64) return ECF8_ERR_SIZE;
+    if (tokens == 0) return ECF8_OK;
+    rc = check_add(bank, x, ldx, x_type, x_scale, base, ld_base, out, ld_out);
+    if (rc != ECF8_OK) return rc;
+    const Pass s{x, ldx, x_type, x_scale, bank->down, bank->in_features, bank->up, bank->out_features, base, ld_base, out, ld_out};
+    return run_few(PlanView{}, (uint32_t)tokens, index, index_bytes, tokens, *bank, s, Forms{}, static_cast<hipStream_t>(hip_stream));
 }
 
 extern "C" int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* x, uint64_t ldx, uint32_t x_type,
                          const float* x_scale, const void* base, uint64_t ld_base, void* out, uint64_t ld_out,
                          void* hidden, void* workspace, uint64_t workspace_bytes, void* hip_stream)
 {
-    const int rc = check_bank(plan, bank);
+    if (!plan_ok(plan)) return ECF8_ERR_ARG;
+    int rc = check_bank(bank);
     if (rc != ECF8_OK) return rc;
     if (x_type != bank->type && x_type != ECF8A_E4M3) return ECF8_ERR_UNSUPPORTED;
+    if (bank->adapters != plan->adapters || !aligned(hidden, 16)) return ECF8_ERR_ARG;
     if (plan->tokens == 0) return ECF8_OK;
-    if (!x || !out || !aligned(x, x_type == ECF8A_E4M3 ? 1 : 2) || !aligned(out, 2) || !aligned(base, 2) ||
-        !aligned(x_scale, 4) || !aligned(hidden, 16) || (base == out && ld_base != ld_out))
-        return ECF8_ERR_ARG;
-    if (ldx < bank->in_features || ld_out < bank->out_features || (base && ld_base < bank->out_features))
-        return ECF8_ERR_SIZE;
+    rc = check_add(bank, x, ldx, x_type, x_scale, base, ld_base, out, ld_out);
+    if (rc != ECF8_OK) return rc;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < ecf8a_add_bytes(plan, bank))
         return ECF8_ERR_WORKSPACE;
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
     char* w = static_cast<char*>(workspace);
-    float* z = hidden ? static_cast<float*>(hidden) : reinterpret_cast<float*>(w);
-    const int e = run_low(*plan, *bank, x, ldx, x_type, x_scale, bank->down, bank->in_features, z,
-                          reinterpret_cast<float*>(w + z_bytes(*plan, bank->rank)), st);
-    if (e != ECF8_OK) return e;
-    return run_wide(*plan, *bank, z, bank->up, bank->out_features, base, ld_base, out, ld_out, st);
+    const Pass s{x, ldx, x_type, x_scale, bank->down, bank->in_features, bank->up, bank->out_features, base, ld_base, out, ld_out};
+    return run_pass(*plan, *bank, s, forms_of(*plan, bank->rank, w, hidden),
+                    reinterpret_cast<float*>(w + form_bytes(*plan, bank->rank)), static_cast<hipStream_t>(hip_stream));
 }
 
 extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* dy, uint64_t ld_dy, const void* x,
@@ -852,9 +1251,11 @@ extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const
                            uint64_t ld_dx, void* d_down, void* d_up, void* workspace, uint64_t workspace_bytes,
                            void* hip_stream)
 {
-    int rc = check_bank(plan, bank);
+    if (!plan_ok(plan)) return ECF8_ERR_ARG;
+    int rc = check_bank(bank);
     if (rc != ECF8_OK) return rc;
-    if (!d_down != !d_up || !aligned(d_down, 2) || !aligned(d_up, 2)) return ECF8_ERR_ARG;
+    if (bank->adapters != plan->adapters || !d_down != !d_up || !aligned(d_down, 2) || !aligned(d_up, 2))
+        return ECF8_ERR_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < ecf8a_grads_bytes(plan, bank))
         return ECF8_ERR_WORKSPACE;
     const uint64_t K = bank->in_features, N = bank->out_features;
@@ -867,18 +1268,25 @@ extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const
     }
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     char* w = static_cast<char*>(workspace);
-    const uint64_t zb = z_bytes(*plan, bank->rank);
-    float* z = reinterpret_cast<float*>(w);
-    float* h = reinterpret_cast<float*>(w + zb);
-    float* scratch = reinterpret_cast<float*>(w + 2 * zb);
-    if (plan->tokens) {
-        rc = run_low(*plan, *bank, dy, ld_dy, bank->type, nullptr, bank->up, N, z, scratch, st);
-        if (rc == ECF8_OK && dx) rc = run_wide(*plan, *bank, z, bank->down, K, dx_base, ld_dx_base, dx, ld_dx, st);
-        if (rc == ECF8_OK && d_down && !hidden)
-            rc = run_low(*plan, *bank, x, ldx, bank->type, nullptr, bank->down, K, h, scratch, st);
+    const uint64_t fb = form_bytes(*plan, bank->rank);
+    void* const z_row = d_down ? w + fb : nullptr;
+    float* const scratch = reinterpret_cast<float*>(w + 3 * fb);
+    if (plan->tokens && (dx || d_down)) {
+        const Pass s{dy, ld_dy, bank->type, nullptr, bank->up, N, bank->down, K, dx_base, ld_dx_base, dx, ld_dx};
+        rc = run_pass(*plan, *bank, s, forms_of(*plan, bank->rank, w, z_row), scratch, st);
+        if (rc == ECF8_OK && d_down && !hidden) {
+            const Pass h{x, ldx, bank->type, nullptr, bank->down, K, bank->up, N, nullptr, 0, nullptr, 0};
+            rc = run_pass(*plan, *bank, h, forms_of(*plan, bank->rank, nullptr, w + 2 * fb), scratch, st);
+        }
     }
     if (rc != ECF8_OK || !d_down) return rc;
-    rc = run_factor(*plan, *bank, z, x, ldx, K, d_down, scratch, st);
-    if (rc != ECF8_OK) return rc;
-    return run_factor(*plan, *bank, hidden ? static_cast<const float*>(hidden) : h, dy, ld_dy, N, d_up, scratch, st);
+    const Forms z = forms_of(*plan, bank->rank, nullptr, z_row);
+    const uint64_t sk = round_up(K, kStrip), sn = round_up(N, kStrip);
+    const uint16_t* h = static_cast<const uint16_t*>(hidden ? hidden : w + 2 * fb);
+    float* const part_up = scratch + part_bytes(*plan, bank->rank, K) / 4;
+    const FactorArgs A{view_of(*plan),
+                       {{z.row, static_cast<const uint16_t*>(x), (int64_t)ldx, static_cast<uint16_t*>(d_down), scratch, (int)K, (int)sk},
+                        {h, static_cast<const uint16_t*>(dy), (int64_t)ld_dy, static_cast<uint16_t*>(d_up), part_up, (int)N, (int)sn}},
+                       bank->ranks, z.plane, (int)bank->rank, z.zr, z.slots, (int)bank->adapters, (int)(sk / kStrip)};
+    return run_factor(*plan, *bank, A, st);
 }
