@@ -30,8 +30,9 @@ using namespace ecf8a;
 constexpr int kTile = 16;                 // slots a group is padded to: one matrix instruction's rows
 constexpr int kChunk = 64;                // slots of one chunk at most
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanLds = 15 * 1024;       // ints of LDS for the grouping
-constexpr int kBatch = 8;
+constexpr int kPlanLds = 10000;           // ints of LDS for the grouping
+constexpr int kPlanKept = 12288;          // tokens whose adapters fit beside them
+constexpr int kBatch = 4;
 constexpr int kThreads = 256;
 constexpr int kStrip = 128;               // columns of one wave: 16 lanes of 8
 
@@ -106,6 +107,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
                                                             PlanView p)
 {
     __shared__ int lds[kPlanLds];
+    __shared__ uint16_t kept[kPlanKept];
     __shared__ int scan[kPlanThreads / 64][3];
     const int groups = adapters + 1;                        // the last: no adapter
     int* const hist = lds;                                  // [waves][groups]: next slot of each wave in each group
@@ -117,13 +119,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
     __syncthreads();
     const int run = ((tokens + waves - 1) / waves + 63) / 64 * 64;
     const int t0 = min(tokens, wave * run), t1 = wave < waves ? min(tokens, t0 + run) : t0;
-    int mine[kBatch];                                       // the adapters of kBatch tokens, -1 past the end: loads in flight
-    const auto fetch = [&](int t) {
+    const bool keep = tokens <= kPlanKept;                  // the adapters stay in LDS for the second look
+    for (int t = t0; t < t1; t += 64 * kBatch) {
+        int mine[kBatch];                                   // loads in flight; -1 past the end
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) mine[i] = t + i * 64 + lane < t1 ? read_index(index, index_bytes, t + i * 64 + lane, adapters) : -1;
-    };
-    for (int t = t0; t < t1; t += 64 * kBatch) {
-        fetch(t);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int first = __builtin_amdgcn_readfirstlane(mine[i]);
@@ -133,6 +133,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
             } else if (mine[i] >= 0) {
                 atomicAdd(&hist[wave * groups + mine[i]], 1);
             }
+            if (keep && mine[i] >= 0) kept[t + i * 64 + lane] = (uint16_t)mine[i];
         }
     }
     __syncthreads();
@@ -187,47 +188,48 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
         const int at = (c - chunk0[lo]) * kChunk;
         p.chunks[c] = i32x4{lo, slot0[lo] + at, min(kChunk, count[lo] - at), 0};
     }
-    for (int tb = t0; tb < t1; tb += 64 * kBatch) {
-        if (run > 64 * kBatch) fetch(tb);                   // else they are still there
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int a = mine[i];
-            const int first = __builtin_amdgcn_readfirstlane(a);
-            if (first < 0) continue;                        // valid lanes are a prefix
-            int rank = 0, same = 0;
-            if (__ballot(a == first || a < 0) == ~0ull) {
-                rank = lane;
-                same = (int)__popcll(__ballot(a >= 0));
-            } else {
-                for (int j = 0; j < 64; ++j) {
-                    const int o = __builtin_amdgcn_readlane(a, j);
-                    same += o == a;
-                    rank += o == a && j < lane;
-                }
+#pragma unroll 1
+    for (int tb = t0; tb < t1; tb += 64) {
+        const int t = tb + lane;
+        const int a = t >= t1 ? -1 : keep ? (int)kept[t] : read_index(index, index_bytes, t, adapters);
+        const int first = __builtin_amdgcn_readfirstlane(a);
+        int rank = 0, same = 0;
+        if (__ballot(a == first || a < 0) == ~0ull) {        // valid lanes are a prefix
+            rank = lane;
+            same = (int)__popcll(__ballot(a >= 0));
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < 64; ++j) {
+                const int o = __builtin_amdgcn_readlane(a, j);
+                same += o == a;
+                rank += o == a && j < lane;
             }
-            if (a >= 0) {
-                volatile int* next = &hist[wave * groups + a];
-                const int at = *next;
-                p.slot_token[at + rank] = tb + i * 64 + lane;
-                if (rank == same - 1) *next = at + same;    // one lane of each adapter, after every lane's read
-            }
+        }
+        if (a >= 0) {
+            volatile int* next = &hist[wave * groups + a];
+            const int at = *next;
+            p.slot_token[at + rank] = t;
+            if (rank == same - 1) *next = at + same;          // one lane of each adapter, after every lane's read
         }
     }
 }
 
 // ------------------------------------------------------------- low: Z = c V F^T
 
-// Sixteen consecutive values of a row from k on, as the operands of two matrix
-// instructions.  VEC: 16-byte loads; values at or past `limit` are 0.
-template <int TYPE, int VT, bool VEC, bool TAIL>
+// A lane's values of a 64-column block, as the operands of two matrix instructions:
+// eight from k on and eight from k + GAP on.  Values at or past `limit` are 0 (looked
+// at only with TAIL).  VEC: rows of whole, aligned 16-byte units; else the same loads
+// at any address, and value by value where a row ends.  16-bit rows have GAP 32, so
+// that the four lanes of a row read 64 consecutive bytes; an E4M3 row's 16 bytes
+// are one load (GAP 8), and the factor that goes with it follows.
+template <int TYPE, int VT, int GAP, bool VEC, bool TAIL>
 __device__ __forceinline__ void load_row16(const void* row, int k, int limit, u32x4 v[2])
 {
     if constexpr (VT == kE4m3) {
         const uint8_t* p = static_cast<const uint8_t*>(row) + k;
         u32x4 b{0, 0, 0, 0};
-        if constexpr (VEC) {
-            if (!TAIL || k < limit) b = *reinterpret_cast<const u32x4*>(p);
-        } else {
+        if (!TAIL || k + 16 <= limit) b = load16<VEC>(p);
+        else if constexpr (!VEC) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (k + i < limit) b[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
@@ -246,14 +248,12 @@ __device__ __forceinline__ void load_row16(const void* row, int k, int limit, u3
         const uint16_t* p = static_cast<const uint16_t*>(row) + k;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if constexpr (VEC) {
-                if (!TAIL || k + 8 * h < limit) v[h] = *reinterpret_cast<const u32x4*>(p + 8 * h);
-                else v[h] = u32x4{0, 0, 0, 0};
-            } else {
-                v[h] = u32x4{0, 0, 0, 0};
+            v[h] = u32x4{0, 0, 0, 0};
+            if (!TAIL || k + GAP * h + 8 <= limit) v[h] = load16<VEC>(p + GAP * h);
+            else if constexpr (!VEC) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (k + 8 * h + i < limit) v[h][i >> 1] |= (uint32_t)p[8 * h + i] << (16 * (i & 1));
+                    if (k + GAP * h + i < limit) v[h][i >> 1] |= (uint32_t)p[GAP * h + i] << (16 * (i & 1));
             }
         }
     }
@@ -263,9 +263,10 @@ __device__ __forceinline__ void load_row16(const void* row, int k, int limit, u3
 // bfloat16; either may be absent.
 struct Forms {
     uint16_t* slot;          // [2][max_slots][zr]
-    uint16_t* row;           // [2][zr][max_slots]
+    uint16_t* row;           // [2][max_slots / 16][zr][16]: rows of a tile lie together (a pitch of max_slots put the
+                             // rows of one load on one memory channel and took 273 us for 16384 x 18944 at rank 64)
     int64_t plane;           // max_slots * zr
-    int slots, zr;
+    int zr;
 };
 
 // Four consecutive rank rows of one slot.
@@ -283,7 +284,7 @@ __device__ __forceinline__ void write_forms(const Forms& f, int slot, int row, f
         const uint32_t h[2] = {h0, h1}, l[2] = {l0, l1};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint16_t* p = f.row + (int64_t)(row + i) * f.slots + slot;
+            uint16_t* p = f.row + ((int64_t)(slot / kTile) * f.zr + row + i) * kTile + slot % kTile;
             p[0] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
             p[f.plane] = (uint16_t)(l[i >> 1] >> (16 * (i & 1)));
         }
@@ -312,7 +313,7 @@ __device__ __forceinline__ int rank_of(const int32_t* ranks, int a, int rank)
 // The products of RT times 16 rank rows from r0 on with NT times 16 tokens over
 // the 64-column blocks first, first + step, ...  A wave's two loads of a row cover
 // whole 128-byte lines.
-template <int TYPE, int VT, int RT, int NT, bool VEC>
+template <int TYPE, int VT, int RT, int NT, int AHEAD, bool VEC>
 __device__ __forceinline__ void low_products(const void* const* vrow, const uint16_t* f, int64_t f_row, int r0, int rank,
                                              int width, int first, int step, f32x4 (*acc)[NT])
 {
@@ -320,7 +321,8 @@ __device__ __forceinline__ void low_products(const void* const* vrow, const uint
     const uint16_t* frow[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) frow[r] = f + (f_row + max(0, min(r0 + r * 16 + c, rank - 1))) * width;
-    const int blocks = (width + 63) / 64, whole = width / 64;
+    constexpr int GAP = VT == kE4m3 ? 8 : 32;
+    const int blocks = (width + 63) / 64, whole = width / 64, k0 = (VT == kE4m3 ? 16 : 8) * g;
     const auto products = [&](const u32x4 (*fv)[2], const u32x4 (*vv)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -329,23 +331,49 @@ __device__ __forceinline__ void low_products(const void* const* vrow, const uint
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[r][n] = mfma<TYPE>(fv[r][h], vv[n][h], acc[r][n]);
     };
+    const auto fetch = [&](int b, u32x4 (*fv)[2], u32x4 (*vv)[2]) {
+        const int k = b * 64 + k0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, GAP, VEC, false>(vrow[n], k, width, vv[n]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, GAP, VEC, false>(frow[r], k, width, fv[r]);
+    };
+    // The loads of AHEAD blocks are in flight together, or (1) those of the next one.
     int b = first;
-    for (; b < whole; b += step) {
-        const int k = b * 64 + 16 * g;
-        u32x4 fv[RT][2], vv[NT][2];
+    if constexpr (AHEAD > 1) {
+        for (; b + (AHEAD - 1) * step < whole; b += AHEAD * step) {
+            u32x4 fv[AHEAD][RT][2], vv[AHEAD][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, false>(vrow[n], k, width, vv[n]);
+            for (int i = 0; i < AHEAD; ++i) fetch(b + i * step, fv[i], vv[i]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, false>(frow[r], k, width, fv[r]);
-        products(fv, vv);
+            for (int i = 0; i < AHEAD; ++i) products(fv[i], vv[i]);
+        }
+        for (; b < whole; b += step) {
+            u32x4 fv[RT][2], vv[NT][2];
+            fetch(b, fv, vv);
+            products(fv, vv);
+        }
+    } else if (b < whole) {
+        u32x4 fv[2][RT][2], vv[2][NT][2];
+        fetch(b, fv[0], vv[0]);
+        while (true) {
+            if (b + step < whole) fetch(b + step, fv[1], vv[1]);
+            products(fv[0], vv[0]);
+            b += step;
+            if (b >= whole) break;
+            if (b + step < whole) fetch(b + step, fv[0], vv[0]);
+            products(fv[1], vv[1]);
+            b += step;
+            if (b >= whole) break;
+        }
     }
     if (b < blocks) {                                       // the last block, not whole: zeros past the width
-        const int k = b * 64 + 16 * g;
+        const int k = b * 64 + k0;
         u32x4 fv[RT][2], vv[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, VEC, true>(vrow[n], k, width, vv[n]);
+        for (int n = 0; n < NT; ++n) load_row16<TYPE, VT, GAP, VEC, true>(vrow[n], k, width, vv[n]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, VEC, true>(frow[r], k, width, fv[r]);
+        for (int r = 0; r < RT; ++r) load_row16<TYPE, TYPE, GAP, VEC, true>(frow[r], k, width, fv[r]);
         products(fv, vv);
     }
 }
@@ -374,11 +402,14 @@ __device__ __forceinline__ void sum_waves(const f32x4* acc, f32x4* red, F done)
 }
 
 // One workgroup: up to NT tiles of one chunk, 16 RT rank rows, one of gridDim.y
-// shares of the width.  Its eight waves take 64-column blocks in turn and meet in
+// shares of the width.  Its waves take 64-column blocks in turn and meet in
 // LDS.  NT and the shares are chosen so that 256 workgroups or more read the rows:
 // measured at 4096 x 4096, rank 16, bfloat16: 12 us + 5 us to join with chunks of 64
 // in 15 shares, see the table of the design notes for the present figure.
-template <int TYPE, int VT, int RT, int NT, bool VEC>
+// 16 waves where 128 registers hold their loads in flight.
+constexpr int low_waves(int rt, int nt) { return rt <= 2 && nt <= 2 ? 16 : 8; }
+
+template <int TYPE, int VT, int RT, int NT, int WAVES, bool VEC>
 __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int tokens, f32x4* red)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4, r0 = blockIdx.z * 64;
@@ -392,10 +423,10 @@ __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int
         vrow[n] = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(t, 0) * A.ldv;
     }
     f32x4 acc[RT][NT] = {};
-    low_products<TYPE, VT, RT, NT, VEC>(vrow, A.f, (int64_t)a * A.rank, r0, rank, A.width, blockIdx.y * 8 + wave, gridDim.y * 8, acc);
+    low_products<TYPE, VT, RT, NT, RT + NT <= 2 ? 4 : RT + NT <= 4 ? 2 : 1, VEC>(vrow, A.f, (int64_t)a * A.rank, r0, rank, A.width, blockIdx.y * WAVES + wave, gridDim.y * WAVES, acc);
     float scale = A.scaling[a];
     if (A.v_scale) scale *= *A.v_scale;
-    sum_waves<8, RT * NT>(&acc[0][0], red, [&](int tile, f32x4 s) {
+    sum_waves<WAVES, RT * NT>(&acc[0][0], red, [&](int tile, f32x4 s) {
         const int n = tile % NT, row = r0 + tile / NT * 16 + 4 * g;
         if (n * kTile >= tokens || row >= A.forms.zr) return;   // tiles past the chunk are another's
         bool have = false;
@@ -411,16 +442,17 @@ __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int
 }
 
 template <int TYPE, int VT, int RT, int NT, bool VEC>
-__global__ __launch_bounds__(512) void low_kernel(LowArgs A)
+__global__ __launch_bounds__(64 * low_waves(RT, NT)) void low_kernel(LowArgs A)
 {
-    __shared__ f32x4 red[4 * RT * NT * 64];
+    constexpr int WAVES = low_waves(RT, NT);
+    __shared__ f32x4 red[WAVES / 2 * RT * NT * 64];
     const int id = blockIdx.x / A.per, at = (blockIdx.x - id * A.per) * NT * kTile;
     if (id >= A.plan.head[0]) return;
     const i32x4 chunk = A.plan.chunks[id];
     if (chunk[0] >= A.adapters || at >= chunk[2]) return;
     const int tokens = min(chunk[2] - at, NT * kTile);
-    if (NT >= 2 && tokens <= kTile) low_body<TYPE, VT, RT, 1, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
-    else low_body<TYPE, VT, RT, NT, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
+    if (NT >= 2 && tokens <= kTile) low_body<TYPE, VT, RT, 1, WAVES, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
+    else low_body<TYPE, VT, RT, NT, WAVES, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
 }
 
 // Sums the planes of a split width, in plane order.
@@ -458,41 +490,13 @@ struct WideArgs {
     int groups;              // workgroups across the width
 };
 
-// Rows r .. r + 7 of the factor at this lane's eight columns, turned into one
-// operand per column.  Rows that take no part are 0, whatever is stored there.
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void load_factor(const uint16_t* f, int width, int r, int rank, int col, u32x4 hi[8], u32x4 lo[8])
-{
-    u32x4 w[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        w[q] = u32x4{0, 0, 0, 0};
-        if (r + q < rank) {
-            const uint16_t* p = f + (int64_t)(r + q) * width + col;
-            if constexpr (VEC) {
-                if (col < width) w[q] = *reinterpret_cast<const u32x4*>(p);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j < width) w[q][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-            }
-        }
-    }
-    transpose8(w, hi);
-    if constexpr (TYPE == kFp16) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split8_f16(hi[j], hi[j], lo[j]);
-    }
-}
-
 // Eight columns of a row, 0 past the width.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load_cols(const uint16_t* row, int col, int width)
 {
     u32x4 v{0, 0, 0, 0};
-    if constexpr (VEC) {
-        if (col < width) v = *reinterpret_cast<const u32x4*>(row + col);
-    } else {
+    if (VEC ? col < width : col + 8 <= width) v = load16<VEC>(row + col);
+    else if constexpr (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (col + j < width) v[j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
@@ -503,12 +507,34 @@ __device__ __forceinline__ u32x4 load_cols(const uint16_t* row, int col, int wid
 template <bool VEC>
 __device__ __forceinline__ void store_cols(uint16_t* row, int col, int width, u32x4 v)
 {
-    if constexpr (VEC) {
-        if (col < width) *reinterpret_cast<u32x4*>(row + col) = v;
-    } else {
+    if (VEC ? col < width : col + 8 <= width) store16<VEC>(row + col, v);
+    else if constexpr (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (col + j < width) row[col + j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// Rows r .. r + 7 of the factor at this lane's eight columns.  Rows that take no
+// part are 0, whatever is stored there.
+template <bool VEC>
+__device__ __forceinline__ void load_factor(const uint16_t* f, int width, int r, int rank, int col, u32x4 w[8])
+{
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        w[q] = u32x4{0, 0, 0, 0};
+        if (r + q < rank) w[q] = load_cols<VEC>(f + (int64_t)(r + q) * width, col, width);
+    }
+}
+
+// ... turned into one operand per column (lo: of a float16, the rest of it).
+template <int TYPE>
+__device__ __forceinline__ void turn_factor(const u32x4 w[8], u32x4 hi[8], u32x4 lo[8])
+{
+    transpose8(w, hi);
+    if constexpr (TYPE == kFp16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split8_f16(hi[j], hi[j], lo[j]);
     }
 }
 
@@ -544,8 +570,15 @@ __device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* h
 // read, and the result's rows read and written, 16 bytes at a time, and no LDS
 // is used.  RB: blocks of 32 rank rows kept in registers for the whole chunk
 // (0: up to 16 rows; -1: any number, read again for each 16 tokens).
+//
+// Bound by the rows' way in and out.  What keeps that busy is many waves rather
+// than many loads of each: with the rows of all four tiles sent for at once a wave
+// holds 158 to 255 registers, and 8192 tokens x 14336 columns at rank 32 take 108
+// us, 16384 x 13824 at rank 64 take 338; tile by tile 93 and 222 (5.1 and 4.1
+// TB/s).  The result is stored past the caches, which are left to the base rows
+// (2048 x 8192 at rank 16: 17 -> 13 us).
 template <int TYPE, int RB, bool VEC>
-__global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
+__global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 : 3) : 2) void wide_kernel(WideArgs A)
 {
     const int id = blockIdx.x / A.groups;                   // neighbouring workgroups: the same rows, next columns
     if (id >= A.plan.head[0]) return;
@@ -556,40 +589,34 @@ __global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
     const bool bare = a >= A.adapters;
     if (bare && A.base == A.out) return;
     const int tiles = (chunk[2] + kTile - 1) / kTile;
-    i32x4 tok[4];
-    u32x4 base[4][4];
-    const auto fetch = [&](int tile) {                      // all rows of the chunk are sent for before the first is used
-        tok[tile] = i32x4{-1, -1, -1, -1};
-        if (tile < tiles) tok[tile] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + chunk[1] + tile * kTile + 4 * g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            base[tile][i] = u32x4{0, 0, 0, 0};
-            if (A.base && tok[tile][i] >= 0) base[tile][i] = load_cols<VEC>(A.base + tok[tile][i] * A.ld_base, col, A.width);
-        }
-    };
-#pragma unroll
-    for (int tile = 0; tile < 4; ++tile) fetch(tile);
-    if (bare) {
-#pragma unroll
-        for (int tile = 0; tile < 4; ++tile)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (tok[tile][i] >= 0) store_cols<VEC>(A.out + tok[tile][i] * A.ld_out, col, A.width, base[tile][i]);
-        return;
-    }
-    const int rank = rank_of(A.ranks, a, A.rank);
-    const uint16_t* f = A.f + (int64_t)a * A.rank * A.width;
+    const int rank = bare ? 0 : rank_of(A.ranks, a, A.rank);
+    const uint16_t* f = A.f + (int64_t)(bare ? 0 : a) * A.rank * A.width;
     constexpr int KEEP = RB <= 0 ? 1 : RB;
     u32x4 hi[KEEP][8], lo[KEEP][8];
-    if constexpr (RB == 0) load_factor<TYPE, VEC>(f, A.width, 8 * (g & 1), rank, col, hi[0], lo[0]);
-    if constexpr (RB > 0) {
+    if constexpr (RB >= 0) {
 #pragma unroll
-        for (int b = 0; b < KEEP; ++b) load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi[b], lo[b]);
+        for (int b = 0; b < KEEP; ++b) {
+            u32x4 w[8];
+            load_factor<VEC>(f, A.width, RB == 0 ? 8 * (g & 1) : 32 * b + 8 * g, rank, col, w);
+            turn_factor<TYPE>(w, hi[b], lo[b]);
+        }
     }
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int slot = chunk[1] + tile * kTile;
+        const i32x4 tok = *reinterpret_cast<const i32x4*>(A.plan.slot_token + slot + 4 * g);
+        u32x4 base[4];
 #pragma unroll
-    for (int tile = 0; tile < 4; ++tile) {
-        if (tile >= tiles) break;
-        const uint16_t* z = A.z + (int64_t)(chunk[1] + tile * kTile + c) * A.zr;
+        for (int i = 0; i < 4; ++i) {
+            base[i] = u32x4{0, 0, 0, 0};
+            if (A.base && tok[i] >= 0) base[i] = load_cols<VEC>(A.base + tok[i] * A.ld_base, col, A.width);
+        }
+        if (bare) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, base[i]);
+            continue;
+        }
+        const uint16_t* z = A.z + (int64_t)(slot + c) * A.zr;
         f32x4 acc[8] = {};
         if constexpr (RB == 0) {
             const u32x4 both = *reinterpret_cast<const u32x4*>(z + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
@@ -604,15 +631,16 @@ __global__ __launch_bounds__(kThreads) void wide_kernel(WideArgs A)
                 for (int b = 0; b < RB; ++b) block(b, b);
             } else {
                 for (int b = 0; b < (A.zr + 31) / 32; ++b) {
-                    load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi[0], lo[0]);
+                    u32x4 w[8];
+                    load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, w);
+                    turn_factor<TYPE>(w, hi[0], lo[0]);
                     block(b, 0);
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (tok[tile][i] >= 0)
-                store_cols<VEC>(A.out + tok[tile][i] * A.ld_out, col, A.width, add_row<TYPE>(base[tile][i], acc, i));
+            if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, add_row<TYPE>(base[i], acc, i));
     }
 }
 
@@ -643,12 +671,12 @@ struct FewArgs {
 // workgroup b looks token b's adapter up among all tokens and goes on if b is its
 // first token, or the 17th, ...  What bounds it is how fast one compute unit reads
 // both factors of its adapter (about 100 GB/s): it is taken where that is short.
-constexpr int few_waves(int rt) { return rt == 4 ? 8 : 16; }      // rank 64 needs the registers of eight
+constexpr int kFewWaves = 8;              // few enough to have 256 registers each, for loads in flight
 
 template <int TYPE, int VT, int RT, bool VEC>
-__global__ __launch_bounds__(64 * few_waves(RT)) void few_kernel(FewArgs A)
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(FewArgs A)
 {
-    constexpr int ZR = 16 * RT, WAVES = few_waves(RT);
+    constexpr int ZR = 16 * RT, WAVES = kFewWaves;
     __shared__ f32x4 red[WAVES / 2 * RT * 64];
     __shared__ __attribute__((aligned(16))) uint16_t zs[2][16][ZR + 8];   // 8 more: rows meet different banks
     __shared__ uint64_t found[WAVES];
@@ -708,8 +736,21 @@ __global__ __launch_bounds__(64 * few_waves(RT)) void few_kernel(FewArgs A)
     const int rank = rank_of(A.ranks, a, A.rank);
     const bool real = list[c] >= 0;
     const void* vrow = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(list[c], 0) * A.ldv;
+    // The first strip's rows and the first block of its factor do not wait for h.
+    const i32x4 tok = *reinterpret_cast<const i32x4*>(&list[4 * g]);
+    const uint16_t* f = A.f2 + (int64_t)a * A.rank * A.width;
+    u32x4 base[4], w[8];
+    const auto fetch = [&](int col) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            base[i] = u32x4{0, 0, 0, 0};
+            if (A.base && tok[i] >= 0) base[i] = load_cols<VEC>(A.base + tok[i] * A.ld_base, col, A.width);
+        }
+        load_factor<VEC>(f, A.width, RT == 1 ? 8 * (g & 1) : 8 * g, rank, col, w);
+    };
+    if (A.out && wave * kStrip < A.width) fetch(wave * kStrip + 8 * c);
     f32x4 acc[RT][1] = {};
-    low_products<TYPE, VT, RT, 1, VEC>(&vrow, A.f, (int64_t)a * A.rank, 0, rank, A.in, wave, WAVES, acc);
+    low_products<TYPE, VT, RT, 1, RT == 1 ? 8 : RT == 2 ? 4 : 2, VEC>(&vrow, A.f, (int64_t)a * A.rank, 0, rank, A.in, wave, WAVES, acc);
     float scale = A.scaling[a];
     if (A.v_scale) scale *= *A.v_scale;
     sum_waves<WAVES, RT>(&acc[0][0], red, [&](int tile, f32x4 s) {
@@ -726,33 +767,30 @@ __global__ __launch_bounds__(64 * few_waves(RT)) void few_kernel(FewArgs A)
     });
     __syncthreads();
     if (!A.out) return;
-    const i32x4 tok = *reinterpret_cast<const i32x4*>(&list[4 * g]);
-    const uint16_t* f = A.f2 + (int64_t)a * A.rank * A.width;
     for (int strip = wave * kStrip; strip < A.width; strip += WAVES * kStrip) {
         const int col = strip + 8 * c;
-        u32x4 base[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            base[i] = u32x4{0, 0, 0, 0};
-            if (A.base && tok[i] >= 0) base[i] = load_cols<VEC>(A.base + tok[i] * A.ld_base, col, A.width);
-        }
         f32x4 sum[8] = {};
-        u32x4 hi[8], lo[8];
+        u32x4 hi[8], lo[8], row[4] = {base[0], base[1], base[2], base[3]};
+        turn_factor<TYPE>(w, hi, lo);
+        if (strip + WAVES * kStrip < A.width) fetch(col + WAVES * kStrip);
         if constexpr (RT == 1) {
-            load_factor<TYPE, VEC>(f, A.width, 8 * (g & 1), rank, col, hi, lo);
             const u32x4 both = *reinterpret_cast<const u32x4*>(&zs[g >> 1][c][8 * (g & 1)]);
             wide_products<TYPE, true>(both, both, hi, lo, sum);
         } else {
 #pragma unroll
             for (int b = 0; b < RT / 2; ++b) {
-                load_factor<TYPE, VEC>(f, A.width, 32 * b + 8 * g, rank, col, hi, lo);
+                if (b) {
+                    u32x4 more[8];
+                    load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, more);
+                    turn_factor<TYPE>(more, hi, lo);
+                }
                 wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(&zs[0][c][32 * b + 8 * g]),
                                            *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, sum);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, add_row<TYPE>(base[i], sum, i));
+            if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, add_row<TYPE>(row[i], sum, i));
     }
 }
 
@@ -772,28 +810,33 @@ struct FactorArgs {
     FactorSide side[2];      // d_down from z and x, d_up from h and dy
     const int32_t* ranks;
     int64_t plane;
-    int rank, zr, slots, adapters;
-    int strips;              // of side 0
+    int rank, zr, adapters;
+    int groups;              // workgroups across side 0
 };
 
-// One workgroup: one unit of one adapter's slots, 128 columns of one side, 16 RT
-// rank rows.  Its four waves take 32 slots in turn; a lane reads eight tokens' 16
-// bytes and turns them, as load_factor does, so that the sum over tokens runs in
-// the matrix instructions' reduction slots.  An adapter of one unit is written at
-// once, others leave float32 partial sums that sum_kernel joins in order.
-template <int TYPE, int RT, bool VEC>
-__global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
+// One wave: one unit of one adapter's slots, 128 columns of one side, 16 RT rank
+// rows.  The four waves of a workgroup take neighbouring columns of the same slots
+// (HALVES 2: two strips of columns, and for each two halves of 64 rank rows), so
+// that a wave's Z or V comes from the first-level cache for another.  64 rank rows
+// in one wave hold 276 registers, one wave per SIMD: 267 us for 16384 x 18944.  A lane reads
+// eight tokens' 16 bytes and turns them, as the factor is turned in `wide`, so that
+// the sum over tokens runs in the matrix instructions' reduction slots.  An
+// adapter of one unit is written at once, others leave float32 partial sums that
+// sum_kernel joins in order.
+template <int TYPE, int RT, int HALVES, bool VEC>
+__global__ __launch_bounds__(kThreads, RT == 1 ? 4 : 3) void factor_kernel(FactorArgs A)
 {
-    __shared__ f32x4 red[2 * RT * 8 * 64];
     if ((int)blockIdx.y >= A.plan.head[2]) return;
     const i32x4 unit = A.plan.units[blockIdx.y];
-    const bool second = (int)blockIdx.x >= A.strips;
+    const bool second = (int)blockIdx.x >= A.groups;
     const FactorSide& S = A.side[second];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.x - (second ? A.strips : 0)) * kStrip + 8 * c, r0 = blockIdx.z * 64;
-    const bool inside = col < S.width;
+    const int strip = (blockIdx.x - (second ? A.groups : 0)) * (4 / HALVES) + wave / HALVES;
+    const int col = strip * kStrip + 8 * c, r0 = blockIdx.z * 64 + wave % HALVES * 32;
+    if (strip * kStrip >= S.width || r0 >= A.zr) return;
     f32x4 acc[RT][8] = {};
     i32x4 tok[2];
+    u32x4 w[8];
     const auto tokens_of = [&](int s) {
         tok[0] = tok[1] = i32x4{-1, -1, -1, -1};
         if (s + 8 * g < unit[2]) {                            // units are whole tiles of 16: eight slots are in or out
@@ -801,24 +844,29 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
             tok[1] = *reinterpret_cast<const i32x4*>(A.plan.slot_token + unit[1] + s + 8 * g + 4);
         }
     };
-    tokens_of(wave * 32);
-    for (int s = wave * 32; s < unit[2]; s += 128) {
-        const bool have = s + 8 * g < unit[2];
-        u32x4 w[8], t[8], tl[8];
+    const auto rows_of = [&]() {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const int tq = tok[q >> 2][q & 3];
             w[q] = u32x4{0, 0, 0, 0};
             if (tq >= 0) w[q] = load_cols<VEC>(S.v + tq * S.ldv, col, S.width);
         }
-        tokens_of(s + 128);
-        u32x4 zh[RT], zl[RT];
+    };
+    // The rows are not sent for ahead of their turn: that takes 32 registers, and a
+    // third wave per SIMD hides more (8192 x 18432 at rank 32: 92 -> 62 us).
+    tokens_of(0);
+    for (int s = 0; s < unit[2]; s += 32) {
+        rows_of();
+        tokens_of(s + 32);
+        const bool have = s + 8 * g < unit[2];
+        u32x4 zh[RT], zl[RT], t[8], tl[8];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = r0 + r * 16 + c;
             zh[r] = zl[r] = u32x4{0, 0, 0, 0};
             if (have && row < A.zr) {
-                const uint16_t* z = S.z + (int64_t)row * A.slots + unit[1] + s + 8 * g;
+                const int slot = unit[1] + s + 8 * g;
+                const uint16_t* z = S.z + ((int64_t)(slot / kTile) * A.zr + row) * kTile + slot % kTile;
                 zh[r] = *reinterpret_cast<const u32x4*>(z);
                 zl[r] = *reinterpret_cast<const u32x4*>(z + A.plane);
             }
@@ -837,22 +885,7 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
                 if constexpr (TYPE == kFp16) acc[r][j] = mfma_bf16(zh[r], tl[j], acc[r][j]);
             }
     }
-    // Waves 2 and 3 hand over to 0 and 1, and 1 to 0.
-    for (int half = 2; half >= 1; half >>= 1) {
-        if (wave >= half && wave < 2 * half)
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) red[(((wave - half) * RT + r) * 8 + j) * 64 + lane] = acc[r][j];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[r][j] += red[((wave * RT + r) * 8 + j) * 64 + lane];
-        __syncthreads();
-    }
-    if (wave != 0 || !inside) return;
+    if (col >= S.width) return;
     const int a = unit[0], rank = rank_of(A.ranks, a, A.rank);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -876,7 +909,7 @@ __global__ __launch_bounds__(kThreads) void factor_kernel(FactorArgs A)
 }
 
 // The gradients of adapters with no unit (0) or several (their partial sums).
-template <int TYPE>
+template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A, int first)
 {
     const int a = blockIdx.z, row = blockIdx.y;
@@ -884,18 +917,25 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A, int first)
     if (u1 - u0 == 1) return;
     const bool second = (int)blockIdx.x >= first;
     const FactorSide& S = A.side[second];
-    const int col = (blockIdx.x - (second ? first : 0)) * kThreads + threadIdx.x;
+    const int col = ((blockIdx.x - (second ? first : 0)) * kThreads + threadIdx.x) * 4;
     if (col >= S.width) return;
-    float s = 0.0f;
-    for (int u = u0; u < u1; u += 8) {                      // eight loads in flight, added in order
-        float v[8];
+    f32x4 s{0, 0, 0, 0};
+    for (int u = u0; u < u1; u += 4) {                      // four loads in flight, added in order
+        f32x4 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = S.part[((int64_t)min(u + j, u1 - 1) * A.zr + row) * S.stride + col];
+        for (int j = 0; j < 4; ++j)
+            v[j] = *reinterpret_cast<const f32x4*>(S.part + ((int64_t)min(u + j, u1 - 1) * A.zr + row) * S.stride + col);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
             if (u + j < u1) s += v[j];
     }
-    S.grad[((int64_t)a * A.rank + row) * S.width + col] = round1<TYPE>(s);
+    uint16_t* p = S.grad + ((int64_t)a * A.rank + row) * S.width + col;
+    if (VEC) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<TYPE>(s[0], s[1]), pack2<TYPE>(s[2], s[3]));
+    else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < S.width) p[i] = round1<TYPE>(s[i]);
+    }
 }
 
 // ------------------------------------------------------------- host side
@@ -993,9 +1033,9 @@ bool few(uint64_t tokens, const ecf8a_bank& b)
 template <int TYPE, int VT, bool VEC>
 void launch_few(const FewArgs& A, uint32_t grid, hipStream_t st)
 {
-    if (A.rank <= 16) few_kernel<TYPE, VT, 1, VEC><<<grid, 64 * few_waves(1), 0, st>>>(A);
-    else if (A.rank <= 32) few_kernel<TYPE, VT, 2, VEC><<<grid, 64 * few_waves(2), 0, st>>>(A);
-    else few_kernel<TYPE, VT, 4, VEC><<<grid, 64 * few_waves(4), 0, st>>>(A);
+    if (A.rank <= 16) few_kernel<TYPE, VT, 1, VEC><<<grid, 64 * kFewWaves, 0, st>>>(A);
+    else if (A.rank <= 32) few_kernel<TYPE, VT, 2, VEC><<<grid, 64 * kFewWaves, 0, st>>>(A);
+    else few_kernel<TYPE, VT, 4, VEC><<<grid, 64 * kFewWaves, 0, st>>>(A);
 }
 
 int run_few(const PlanView& view, uint32_t grid, const void* index, uint32_t index_bytes, uint64_t tokens,
@@ -1019,9 +1059,9 @@ int run_few(const PlanView& view, uint32_t grid, const void* index, uint32_t ind
 template <int TYPE, int VT, int RT, bool VEC>
 void launch_low_tiles(const LowArgs& A, dim3 grid, uint32_t tiles, hipStream_t st)
 {
-    if (tiles == 1) low_kernel<TYPE, VT, RT, 1, VEC><<<grid, 512, 0, st>>>(A);
-    else if (tiles == 2) low_kernel<TYPE, VT, RT, 2, VEC><<<grid, 512, 0, st>>>(A);
-    else low_kernel<TYPE, VT, RT, 4, VEC><<<grid, 512, 0, st>>>(A);
+    if (tiles == 1) low_kernel<TYPE, VT, RT, 1, VEC><<<grid, 64 * low_waves(RT, 1), 0, st>>>(A);
+    else if (tiles == 2) low_kernel<TYPE, VT, RT, 2, VEC><<<grid, 64 * low_waves(RT, 2), 0, st>>>(A);
+    else low_kernel<TYPE, VT, RT, 4, VEC><<<grid, 64 * low_waves(RT, 4), 0, st>>>(A);
 }
 
 template <int TYPE, int VT, bool VEC>
@@ -1081,7 +1121,7 @@ int run_wide(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Form
 // One direction, whichever way.  `forms.row` is written if it is given.
 int run_pass(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, Forms forms, float* planes, hipStream_t st)
 {
-    if (few(p.tokens, b)) return run_few(view_of(p), 4 * p.max_chunks, nullptr, 0, p.tokens, b, s, Forms{nullptr, forms.row, forms.plane, forms.slots, forms.zr}, st);
+    if (few(p.tokens, b)) return run_few(view_of(p), 4 * p.max_chunks, nullptr, 0, p.tokens, b, s, Forms{nullptr, forms.row, forms.plane, forms.zr}, st);
     if (!s.out) forms.slot = nullptr;
     const int rc = run_low(p, b, s, forms, planes, st);
     return rc == ECF8_OK && s.out ? run_wide(p, b, s, forms, st) : rc;
@@ -1090,32 +1130,37 @@ int run_pass(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, Forms form
 template <int TYPE, bool VEC>
 void launch_factor(const FactorArgs& A, dim3 grid, hipStream_t st)
 {
-    if (A.zr <= 16) factor_kernel<TYPE, 1, VEC><<<grid, kThreads, 0, st>>>(A);
-    else if (A.zr <= 32) factor_kernel<TYPE, 2, VEC><<<grid, kThreads, 0, st>>>(A);
-    else factor_kernel<TYPE, 4, VEC><<<grid, kThreads, 0, st>>>(A);
+    if (A.zr <= 16) factor_kernel<TYPE, 1, 1, VEC><<<grid, kThreads, 0, st>>>(A);
+    else if (A.zr <= 32) factor_kernel<TYPE, 2, 1, VEC><<<grid, kThreads, 0, st>>>(A);
+    else factor_kernel<TYPE, 2, 2, VEC><<<grid, kThreads, 0, st>>>(A);
 }
+
+// Columns of a factor_kernel workgroup.
+uint32_t factor_columns(int zr) { return zr <= 32 ? 4 * kStrip : 2 * kStrip; }
 
 int run_factor(const ecf8a_plan& p, const ecf8a_bank& b, const FactorArgs& A, hipStream_t st)
 {
     bool vec = true;
     for (const FactorSide& s : A.side) vec = vec && vec16(s.v, s.ldv) && vec16(s.grad, s.width);
-    const uint32_t strips = (uint32_t)((A.side[0].stride + A.side[1].stride) / kStrip);
+    const uint32_t columns = factor_columns(A.zr), groups = A.groups + (A.side[1].stride + columns - 1) / columns;
     if (p.tokens) {
-        const dim3 grid(strips, p.max_units, (A.zr + 63) / 64);
+        const dim3 grid(groups, p.max_units, (A.zr + 63) / 64);
         if (b.type == ECF8A_BF16) vec ? launch_factor<kBf16, true>(A, grid, st) : launch_factor<kBf16, false>(A, grid, st);
         else vec ? launch_factor<kFp16, true>(A, grid, st) : launch_factor<kFp16, false>(A, grid, st);
     }
-    const uint32_t first = (A.side[0].width + kThreads - 1) / kThreads, rest = (A.side[1].width + kThreads - 1) / kThreads;
+    const uint32_t four = 4 * kThreads, first = (A.side[0].width + four - 1) / four, rest = (A.side[1].width + four - 1) / four;
     const dim3 grid(first + rest, b.rank, b.adapters);
-    if (b.type == ECF8A_BF16) sum_kernel<kBf16><<<grid, kThreads, 0, st>>>(A, (int)first);
-    else sum_kernel<kFp16><<<grid, kThreads, 0, st>>>(A, (int)first);
+    if (b.type == ECF8A_BF16)
+        vec ? sum_kernel<kBf16, true><<<grid, kThreads, 0, st>>>(A, (int)first) : sum_kernel<kBf16, false><<<grid, kThreads, 0, st>>>(A, (int)first);
+    else
+        vec ? sum_kernel<kFp16, true><<<grid, kThreads, 0, st>>>(A, (int)first) : sum_kernel<kFp16, false><<<grid, kThreads, 0, st>>>(A, (int)first);
     return launch_status();
 }
 
 Forms forms_of(const ecf8a_plan& p, uint32_t rank, void* slot, void* row)
 {
     const int zr = (int)z_rows(rank);
-    return Forms{static_cast<uint16_t*>(slot), static_cast<uint16_t*>(row), (int64_t)p.max_slots * zr, (int)p.max_slots, zr};
+    return Forms{static_cast<uint16_t*>(slot), static_cast<uint16_t*>(row), (int64_t)p.max_slots * zr, zr};
 }
 
 bool sizes_ok(uint64_t tokens, uint32_t adapters)
@@ -1284,9 +1329,10 @@ extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const
     const uint64_t sk = round_up(K, kStrip), sn = round_up(N, kStrip);
     const uint16_t* h = static_cast<const uint16_t*>(hidden ? hidden : w + 2 * fb);
     float* const part_up = scratch + part_bytes(*plan, bank->rank, K) / 4;
+    const uint64_t columns = factor_columns(z.zr);
     const FactorArgs A{view_of(*plan),
                        {{z.row, static_cast<const uint16_t*>(x), (int64_t)ldx, static_cast<uint16_t*>(d_down), scratch, (int)K, (int)sk},
                         {h, static_cast<const uint16_t*>(dy), (int64_t)ld_dy, static_cast<uint16_t*>(d_up), part_up, (int)N, (int)sn}},
-                       bank->ranks, z.plane, (int)bank->rank, z.zr, z.slots, (int)bank->adapters, (int)(sk / kStrip)};
+                       bank->ranks, z.plane, (int)bank->rank, z.zr, (int)bank->adapters, (int)((sk + columns - 1) / columns)};
     return run_factor(*plan, *bank, A, st);
 }

@@ -41,6 +41,25 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// 16 bytes.  ALIGNED: on a 16-byte border; else anywhere (the card takes 16-byte
+// accesses at any address, lines apart at the cost of a second line).
+typedef u32x4 __attribute__((aligned(1))) u32x4_any;
+
+template <bool ALIGNED>
+__device__ __forceinline__ u32x4 load16(const void* p)
+{
+    if constexpr (ALIGNED) return *static_cast<const u32x4*>(p);
+    return *static_cast<const u32x4_any*>(p);
+}
+
+// Aligned: past the caches, for results that this library does not read again.
+template <bool ALIGNED>
+__device__ __forceinline__ void store16(void* p, u32x4 v)
+{
+    if constexpr (ALIGNED) __builtin_nontemporal_store(v, static_cast<u32x4*>(p));
+    else *static_cast<u32x4_any*>(p) = v;
+}
+
 // The two values of a dword of 16-bit type.
 template <int TYPE>
 __device__ __forceinline__ f32x2 unpack2(uint32_t v)
