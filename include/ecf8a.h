@@ -134,16 +134,19 @@ int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* x, uin
               const float* x_scale, const void* base, uint64_t ld_base, void* out, uint64_t ld_out,
               void* hidden, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
-/* Whether ecf8a_add_few is the faster way for this many tokens and this bank (1)
- * or a plan and ecf8a_add (0). */
+/* Whether ecf8a_add_few takes this many tokens and this bank (1: at most
+ * ECF8A_FEW_TOKENS tokens and rank 64) or a plan and ecf8a_add are needed (0). */
 int ecf8a_few(uint64_t tokens, const ecf8a_bank* bank);
 
-/* ecf8a_add for at most ECF8A_FEW_TOKENS tokens and rank 64, from the index
- * itself (as in ecf8a_plan_prepare): one launch, no plan and no workspace.
- * Errors as ecf8a_plan_prepare and ecf8a_add. */
+/* Workspace bytes of ecf8a_add_few (256-byte aligned; 0: none is used). */
+uint64_t ecf8a_add_few_bytes(uint64_t tokens, const ecf8a_bank* bank);
+
+/* ecf8a_add for few tokens, from the index itself (as in ecf8a_plan_prepare)
+ * without a plan: one or two launches.  Errors as ecf8a_plan_prepare and
+ * ecf8a_add. */
 int ecf8a_add_few(const void* index, uint32_t index_bytes, uint64_t tokens, const ecf8a_bank* bank, const void* x,
                   uint64_t ldx, uint32_t x_type, const float* x_scale, const void* base, uint64_t ld_base,
-                  void* out, uint64_t ld_out, void* hip_stream);
+                  void* out, uint64_t ld_out, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
 /* The gradients of ecf8a_add for dy, the gradient of out (which is base's own
  * gradient too).  dy, x, dx_base and dx: rows of the bank's type; hidden: what

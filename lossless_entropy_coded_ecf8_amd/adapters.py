@@ -49,7 +49,7 @@ class ClipPlanA(ctypes.Structure):
 
 
 EXPORTS_A = ["ecf8a_plan_bytes", "ecf8a_plan_prepare", "ecf8a_hidden_bytes", "ecf8a_add_bytes", "ecf8a_grads_bytes",
-             "ecf8a_add", "ecf8a_few", "ecf8a_add_few", "ecf8a_grads", "ecf8a_input_grad_bytes", "ecf8a_input_grad", "ecf8a_clip_bytes",
+             "ecf8a_add", "ecf8a_few", "ecf8a_add_few_bytes", "ecf8a_add_few", "ecf8a_grads", "ecf8a_input_grad_bytes", "ecf8a_input_grad", "ecf8a_clip_bytes",
              "ecf8a_clip_prepare", "ecf8a_clip_run"]
 
 _ready = None
@@ -70,7 +70,8 @@ def _lib() -> ctypes.CDLL:
         "ecf8a_grads_bytes": (u64, [plan, bank]),
         "ecf8a_add": (i, [plan, bank, vp, u64, u32, vp, vp, u64, vp, u64, vp, vp, u64, vp]),
         "ecf8a_few": (i, [u64, bank]),
-        "ecf8a_add_few": (i, [vp, u32, u64, bank, vp, u64, u32, vp, vp, u64, vp, u64, vp]),
+        "ecf8a_add_few_bytes": (u64, [u64, bank]),
+        "ecf8a_add_few": (i, [vp, u32, u64, bank, vp, u64, u32, vp, vp, u64, vp, u64, vp, u64, vp]),
         "ecf8a_grads": (i, [plan, bank, vp, u64, vp, u64, vp, vp, u64, vp, u64, vp, vp, vp, u64, vp]),
         "ecf8a_input_grad_bytes": (u64, [u64, u64, u64]),
         "ecf8a_input_grad": (i, [vp, u64, u64, u64, vp, u64, vp, u32, vp, u64, vp, u64, vp]),
@@ -91,7 +92,7 @@ def _ptr(t) -> Optional[int]:
 
 
 class _Launch:
-    """The device of the operands made current for the launches; gives the stream to launch on."""
+    """The device of the operands made current for the launches; gives the handle of the stream to launch on."""
 
     def __init__(self, device, stream):
         if stream is not None and stream.device != device:
@@ -102,11 +103,17 @@ class _Launch:
         self.before = torch.cuda.current_device()
         if self.before != self.device.index:
             torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.before != self.device.index:
             torch.cuda.set_device(self.before)
+
+
+def _stream_of(device, stream):
+    return torch.cuda.current_stream(device) if stream is None else stream
 
 
 def _empty(bytes_or_shape, dtype, device, stream):
@@ -189,19 +196,19 @@ class AdapterPlan:
                 binding._check_buffer(workspace, self.device, "workspace")
             self.workspace, self.c = workspace, PlanA()
             _check(L.ecf8a_plan_prepare(index.data_ptr(), _INDEX_BYTES[index.dtype], self.tokens, self.adapters,
-                                        workspace.data_ptr(), workspace.numel(), st.cuda_stream, ctypes.byref(self.c)),
+                                        workspace.data_ptr(), workspace.numel(), st, ctypes.byref(self.c)),
                    "ecf8a_plan_prepare")
-            self._made_on = st
+            self._made_on, self._handle = _stream_of(self.device, stream), st
         self._event = None
 
-    def _order(self, stream):
+    def _order(self, handle, stream):
         """Makes a launch on another stream than the plan's own wait for the grouping."""
-        if stream.cuda_stream == self._made_on.cuda_stream or torch.cuda.is_current_stream_capturing():
+        if handle == self._handle or torch.cuda.is_current_stream_capturing():
             return
         if self._event is None:
             self._event = torch.cuda.Event()
             self._event.record(self._made_on)
-        stream.wait_event(self._event)
+        _stream_of(self.device, stream).wait_event(self._event)
 
     def hidden(self, rank: int, stream=None) -> torch.Tensor:
         """A buffer that carries h from adapter_add to adapter_grads (opaque bytes)."""
@@ -282,9 +289,11 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     if plan is None:
         if L.ecf8a_few(T, ctypes.byref(bank)):
             with _Launch(dev, stream) as st:
+                need = L.ecf8a_add_few_bytes(T, ctypes.byref(bank))
+                ws = _scratch(need, workspace, dev, stream) if need else None
                 _check(L.ecf8a_add_few(index.data_ptr(), _INDEX_BYTES[index.dtype], T, ctypes.byref(bank), x.data_ptr(), ldx,
                                        _TYPES[x.dtype], _ptr(x_scale), _ptr(base), ld_base, out.data_ptr(), ld_out,
-                                       st.cuda_stream), "ecf8a_add_few")
+                                       _ptr(ws), 0 if ws is None else ws.numel(), st), "ecf8a_add_few")
             return out
         plan = AdapterPlan(index, bank.adapters, stream=stream)
     if plan.adapters != bank.adapters:
@@ -292,11 +301,11 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     if hidden is not None:
         _hidden_ok(hidden, plan, bank.rank)
     with _Launch(dev, stream) as st:
-        plan._order(st)
+        plan._order(st, stream)
         ws = _scratch(L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream)
         _check(L.ecf8a_add(ctypes.byref(plan.c), ctypes.byref(bank), x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(x_scale),
                            _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), ws.data_ptr(), ws.numel(),
-                           st.cuda_stream), "ecf8a_add")
+                           st), "ecf8a_add")
     return out
 
 
@@ -343,11 +352,11 @@ def adapter_grads(dy: torch.Tensor, x: Optional[torch.Tensor], down: torch.Tenso
     d_up = _empty(up.shape, up.dtype, dev, stream) if want_factors else None
     L = _lib()
     with _Launch(dev, stream) as st:
-        plan._order(st)
+        plan._order(st, stream)
         ws = _scratch(L.ecf8a_grads_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream)
         _check(L.ecf8a_grads(ctypes.byref(plan.c), ctypes.byref(bank), dy.data_ptr(), ld_dy,
                              _ptr(x) if want_factors else None, ldx, _ptr(hidden), _ptr(dx_base), ld_b, _ptr(dx), ld_dx,
-                             _ptr(d_down), _ptr(d_up), ws.data_ptr(), ws.numel(), st.cuda_stream), "ecf8a_grads")
+                             _ptr(d_down), _ptr(d_up), ws.data_ptr(), ws.numel(), st), "ecf8a_grads")
     return dx, d_down, d_up
 
 
@@ -379,7 +388,7 @@ def linear_fp8_input_grad(dy: torch.Tensor, w_u8: torch.Tensor, w_scale: torch.T
         need = L.ecf8a_input_grad_bytes(T, N, K)
         ws = _scratch(need, workspace, dev, stream) if need else None
         _check(L.ecf8a_input_grad(dy.data_ptr(), ld_dy, T, N, w_u8.data_ptr(), K, w_scale.data_ptr(), _TYPES[dy.dtype],
-                                  out.data_ptr(), ld_dx, _ptr(ws), 0 if ws is None else ws.numel(), st.cuda_stream),
+                                  out.data_ptr(), ld_dx, _ptr(ws), 0 if ws is None else ws.numel(), st),
                "ecf8a_input_grad")
     return out
 
@@ -417,18 +426,18 @@ class GradClip:
             self.workspace = _empty(max(need, 256), torch.uint8, self.device, stream)
             self.c = ClipPlanA()
             _check(L.ecf8a_clip_prepare(arr, len(self.grads), _TYPES[first.dtype], self.workspace.data_ptr(),
-                                        self.workspace.numel(), st.cuda_stream, ctypes.byref(self.c)),
+                                        self.workspace.numel(), st, ctypes.byref(self.c)),
                    "ecf8a_clip_prepare")
-            self._made_on, self._event = st, torch.cuda.Event()
-            self._event.record(st)
+            self._handle, self._event = st, torch.cuda.Event()
+            self._event.record(_stream_of(self.device, stream))
 
     def run(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scales every gradient by min(1, max_norm / (norm + 1e-6)) and returns the norm before (0-d float32)."""
         with _Launch(self.device, stream) as st:
-            if st.cuda_stream != self._made_on.cuda_stream and not torch.cuda.is_current_stream_capturing():
-                st.wait_event(self._event)
+            if st != self._handle and not torch.cuda.is_current_stream_capturing():
+                _stream_of(self.device, stream).wait_event(self._event)
             norm = _empty((), torch.float32, self.device, stream)
-            _check(_lib().ecf8a_clip_run(ctypes.byref(self.c), float(max_norm), norm.data_ptr(), st.cuda_stream),
+            _check(_lib().ecf8a_clip_run(ctypes.byref(self.c), float(max_norm), norm.data_ptr(), st),
                    "ecf8a_clip_run")
         return norm
 

@@ -291,6 +291,38 @@ __device__ __forceinline__ void write_forms(const Forms& f, int slot, int row, f
     }
 }
 
+// Few tokens without a plan: workgroup b looks token b's adapter up among all tokens
+// (one a thread) and goes on if b is its first token, its 17th, ...  Returns the
+// adapter, `adapters` for none, -1 if another workgroup has this token; list: the up
+// to 16 tokens, -1 behind them.
+template <int WAVES>
+__device__ __forceinline__ int find_group(const void* index, int bytes, int tokens, int adapters, uint64_t* found, int* list)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
+    const int a = read_index(index, bytes, b, adapters), own = tid < tokens ? read_index(index, bytes, tid, adapters) : -1;
+    if (tid < 16) list[tid] = a >= adapters && tid == 0 ? b : -1;
+    if (a >= adapters) {
+        __syncthreads();
+        return a;
+    }
+    const bool same = own == a;
+    const uint64_t ballot = __ballot(same);
+    if (lane == 0) found[wave] = ballot;
+    __syncthreads();
+    int before = 0, mine = 0;                               // of the adapter's tokens, those before b, and before this one
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const uint64_t m = found[w];
+        before += (int)__popcll(w < (b >> 6) ? m : w == (b >> 6) ? m & ((1ull << (b & 63)) - 1) : 0);
+        mine += w < wave ? (int)__popcll(m) : 0;
+    }
+    if (before % 16) return -1;
+    mine += (int)__popcll(ballot & ((1ull << lane) - 1)) - before;
+    if (same && mine >= 0 && mine < 16) list[mine] = tid;
+    __syncthreads();
+    return a;
+}
+
 struct LowArgs {
     PlanView plan;
     const void* v;           // tokens' rows
@@ -303,6 +335,8 @@ struct LowArgs {
     Forms forms;
     int width, rank, adapters;
     int per;                 // workgroups per chunk
+    const void* index;       // few tokens: the index itself, nullptr with a plan
+    int index_bytes, tokens;
 };
 
 __device__ __forceinline__ int rank_of(const int32_t* ranks, int a, int rank)
@@ -402,15 +436,10 @@ __device__ __forceinline__ void sum_waves(const f32x4* acc, f32x4* red, F done)
 }
 
 // One workgroup: up to NT tiles of one chunk, 16 RT rank rows, one of gridDim.y
-// shares of the width.  Its waves take 64-column blocks in turn and meet in
-// LDS.  NT and the shares are chosen so that 256 workgroups or more read the rows:
-// measured at 4096 x 4096, rank 16, bfloat16: 12 us + 5 us to join with chunks of 64
-// in 15 shares, see the table of the design notes for the present figure.
-// 16 waves where 128 registers hold their loads in flight.
-constexpr int low_waves(int rt, int nt) { return rt <= 2 && nt <= 2 ? 16 : 8; }
-
-template <int TYPE, int VT, int RT, int NT, int WAVES, bool VEC>
-__device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int tokens, f32x4* red)
+// shares of the width.  Its waves take 64-column blocks in turn and meet in LDS.
+// tokens_of(n): this lane's token of tile n.
+template <int TYPE, int VT, int RT, int NT, int WAVES, bool VEC, typename F>
+__device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int tokens, f32x4* red, F token_of)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4, r0 = blockIdx.z * 64;
     const int rank = rank_of(A.ranks, a, A.rank);
@@ -418,14 +447,14 @@ __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int
     bool real[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {                          // padding reads row 0; its result is set to 0 below
-        const int t = n * kTile < tokens ? A.plan.slot_token[slot0 + n * kTile + c] : -1;
+        const int t = n * kTile < tokens ? token_of(n * kTile + c) : -1;
         real[n] = t >= 0;
         vrow[n] = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(t, 0) * A.ldv;
     }
-    f32x4 acc[RT][NT] = {};
-    low_products<TYPE, VT, RT, NT, RT + NT <= 2 ? 4 : RT + NT <= 4 ? 2 : 1, VEC>(vrow, A.f, (int64_t)a * A.rank, r0, rank, A.width, blockIdx.y * WAVES + wave, gridDim.y * WAVES, acc);
     float scale = A.scaling[a];
     if (A.v_scale) scale *= *A.v_scale;
+    f32x4 acc[RT][NT] = {};
+    low_products<TYPE, VT, RT, NT, RT + NT <= 2 ? 4 : RT + NT <= 4 ? 2 : 1, VEC>(vrow, A.f, (int64_t)a * A.rank, r0, rank, A.width, blockIdx.y * WAVES + wave, gridDim.y * WAVES, acc);
     sum_waves<WAVES, RT * NT>(&acc[0][0], red, [&](int tile, f32x4 s) {
         const int n = tile % NT, row = r0 + tile / NT * 16 + 4 * g;
         if (n * kTile >= tokens || row >= A.forms.zr) return;   // tiles past the chunk are another's
@@ -441,18 +470,41 @@ __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int
     });
 }
 
-template <int TYPE, int VT, int RT, int NT, bool VEC>
+// 16 waves where 128 registers hold their loads in flight.
+constexpr int low_waves(int rt, int nt) { return rt <= 2 && nt <= 2 ? 16 : 8; }
+
+// With a plan: NT and the shares are chosen so that 256 workgroups or more read the
+// rows.  INDEX: few tokens without a plan; the groups found are written down as
+// chunks of one tile, slots 16 b on, for wide_kernel to read as it reads a plan.
+template <int TYPE, int VT, int RT, int NT, bool VEC, bool INDEX>
 __global__ __launch_bounds__(64 * low_waves(RT, NT)) void low_kernel(LowArgs A)
 {
     constexpr int WAVES = low_waves(RT, NT);
     __shared__ f32x4 red[WAVES / 2 * RT * NT * 64];
-    const int id = blockIdx.x / A.per, at = (blockIdx.x - id * A.per) * NT * kTile;
-    if (id >= A.plan.head[0]) return;
-    const i32x4 chunk = A.plan.chunks[id];
-    if (chunk[0] >= A.adapters || at >= chunk[2]) return;
-    const int tokens = min(chunk[2] - at, NT * kTile);
-    if (NT >= 2 && tokens <= kTile) low_body<TYPE, VT, RT, 1, WAVES, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
-    else low_body<TYPE, VT, RT, NT, WAVES, VEC>(A, chunk[0], chunk[1] + at, tokens, red);
+    if constexpr (INDEX) {
+        __shared__ uint64_t found[WAVES];
+        __shared__ int list[16];
+        const int b = blockIdx.x, a = find_group<WAVES>(A.index, A.index_bytes, A.tokens, A.adapters, found, list);
+        if (blockIdx.y == 0 && threadIdx.x < 16) {
+            if (threadIdx.x == 0) {
+                int n = 0;
+                for (int i = 0; i < 16; ++i) n += a >= 0 && list[i] >= 0;
+                A.plan.chunks[b] = i32x4{a < 0 ? A.adapters : a, b * kTile, n, 0};
+                if (b == 0) A.plan.head[0] = A.tokens;
+            }
+            A.plan.slot_token[b * kTile + threadIdx.x] = a < 0 ? -1 : list[threadIdx.x];
+        }
+        if (a < 0 || a >= A.adapters) return;
+        low_body<TYPE, VT, RT, 1, WAVES, VEC>(A, a, b * kTile, kTile, red, [&](int i) { return list[i]; });
+    } else {
+        const int id = blockIdx.x / A.per, at = (blockIdx.x - id * A.per) * NT * kTile;
+        const i32x4 chunk = A.plan.chunks[id];
+        if (id >= A.plan.head[0] || chunk[0] >= A.adapters || at >= chunk[2]) return;
+        const int tokens = min(chunk[2] - at, NT * kTile), slot = chunk[1] + at;
+        const auto token_of = [&](int i) { return A.plan.slot_token[slot + i]; };
+        if (NT >= 2 && tokens <= kTile) low_body<TYPE, VT, RT, 1, WAVES, VEC>(A, chunk[0], slot, tokens, red, token_of);
+        else low_body<TYPE, VT, RT, NT, WAVES, VEC>(A, chunk[0], slot, tokens, red, token_of);
+    }
 }
 
 // Sums the planes of a split width, in plane order.
@@ -479,7 +531,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict_
 struct WideArgs {
     PlanView plan;
     const uint16_t* z;       // by slot
+    const float* planes;     // PLANES: the shares' sums instead, [shares][slot][zr]
     int64_t plane;
+    int shares;
     const uint16_t* f;
     const int32_t* ranks;
     const uint16_t* base;
@@ -577,12 +631,34 @@ __device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* h
 // us, 16384 x 13824 at rank 64 take 338; tile by tile 93 and 222 (5.1 and 4.1
 // TB/s).  The result is stored past the caches, which are left to the base rows
 // (2048 x 8192 at rank 16: 17 -> 13 us).
-template <int TYPE, int RB, bool VEC>
+// Eight rank rows of one slot from the shares' sums, added in order.
+__device__ __forceinline__ void sum_planes(const float* z, int64_t plane, int shares, u32x4& zh, u32x4& zl)
+{
+    f32x4 s0{0, 0, 0, 0}, s1{0, 0, 0, 0};
+    for (int p = 0; p < shares; p += 4) {                   // eight loads in flight
+        f32x4 v0[4], v1[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float* q = z + min(p + j, shares - 1) * plane;
+            v0[j] = *reinterpret_cast<const f32x4*>(q);
+            v1[j] = *reinterpret_cast<const f32x4*>(q + 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p + j < shares) {
+                s0 += v0[j];
+                s1 += v1[j];
+            }
+    }
+    split8(s0, s1, zh, zl);
+}
+
+template <int TYPE, int RB, bool VEC, bool PLANES>
 __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 : 3) : 2) void wide_kernel(WideArgs A)
 {
     const int id = blockIdx.x / A.groups;                   // neighbouring workgroups: the same rows, next columns
+    const i32x4 chunk = A.plan.chunks[id];                  // there for every id, and sent for with the count
     if (id >= A.plan.head[0]) return;
-    const i32x4 chunk = A.plan.chunks[id];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const int a = chunk[0], col = ((blockIdx.x - id * A.groups) * 4 + wave) * kStrip + 8 * c;
     if (col - 8 * c >= A.width) return;
@@ -616,15 +692,26 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 :
                 if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, base[i]);
             continue;
         }
-        const uint16_t* z = A.z + (int64_t)(slot + c) * A.zr;
+        const int64_t at = (int64_t)(slot + c) * A.zr;
         f32x4 acc[8] = {};
         if constexpr (RB == 0) {
-            const u32x4 both = *reinterpret_cast<const u32x4*>(z + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
+            u32x4 both, rest;
+            if constexpr (PLANES) {
+                sum_planes(A.planes + at + 8 * (g & 1), A.plane, A.shares, both, rest);
+                both = g < 2 ? both : rest;
+            } else {
+                both = *reinterpret_cast<const u32x4*>(A.z + at + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
+            }
             wide_products<TYPE, true>(both, both, hi[0], lo[0], acc);
         } else {
-            const auto block = [&](int b, int at) {
-                const uint16_t* p = z + 32 * b + 8 * g;
-                wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + A.plane), hi[at], lo[at], acc);
+            const auto block = [&](int b, int keep) {
+                u32x4 zh, zl;
+                if constexpr (PLANES) sum_planes(A.planes + at + 32 * b + 8 * g, A.plane, A.shares, zh, zl);
+                else {
+                    zh = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g);
+                    zl = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g + A.plane);
+                }
+                wide_products<TYPE, false>(zh, zl, hi[keep], lo[keep], acc);
             };
             if constexpr (RB > 0) {
 #pragma unroll
@@ -667,10 +754,10 @@ struct FewArgs {
 
 // One workgroup: 16 tokens of one adapter, from their rows to the result.  Its
 // waves split the input width for `low`, leave h in LDS, and split the output width
-// for `wide`.  One launch, no workspace and no grouping beforehand: without a plan,
-// workgroup b looks token b's adapter up among all tokens and goes on if b is its
-// first token, or the 17th, ...  What bounds it is how fast one compute unit reads
-// both factors of its adapter (about 100 GB/s): it is taken where that is short.
+// for `wide`.  One launch, no workspace and no grouping beforehand.  What bounds it
+// is how fast one compute unit reads both factors of its adapter, about 30 GB/s
+// however many loads are in flight (256 KB: 4 us for each half): it is taken for
+// small factors only.
 constexpr int kFewWaves = 8;              // few enough to have 256 registers each, for loads in flight
 
 template <int TYPE, int VT, int RT, bool VEC>
@@ -684,55 +771,30 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(FewArgs A)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
     int a, slot0 = 0;
     if (A.index) {
-        const int b = blockIdx.x;
-        a = read_index(A.index, A.index_bytes, b, A.adapters);
-        if (a >= A.adapters) {                              // no adapter: the row itself
-            if (!A.out || A.base == A.out) return;
-            for (int col = 8 * tid; col < A.width; col += 8 * 64 * WAVES) {
-                u32x4 v{0, 0, 0, 0};
-                if (A.base) v = load_cols<VEC>(A.base + b * A.ld_base, col, A.width);
-                store_cols<VEC>(A.out + b * A.ld_out, col, A.width, v);
-            }
-            return;
-        }
-        const bool same = tid < A.tokens && read_index(A.index, A.index_bytes, tid, A.adapters) == a;
-        const uint64_t ballot = __ballot(same);
-        if (lane == 0) found[wave] = ballot;
-        if (tid < 16) list[tid] = -1;
-        __syncthreads();
-        int before = 0, mine = 0;                           // how many of the adapter's tokens lie before b, and before this one
-        for (int w = 0; w < WAVES; ++w) {
-            const int n = (int)__popcll(found[w]);
-            before += w < (b >> 6) ? n : w == (b >> 6) ? (int)__popcll(found[w] & ((1ull << (b & 63)) - 1)) : 0;
-            mine += w < wave ? n : 0;
-        }
-        if (before % 16) return;
-        mine += (int)__popcll(ballot & ((1ull << lane) - 1)) - before;
-        if (same && mine >= 0 && mine < 16) list[mine] = tid;
+        a = find_group<WAVES>(A.index, A.index_bytes, A.tokens, A.adapters, found, list);
+        if (a < 0) return;
     } else {
         const int id = blockIdx.x / 4, at = (blockIdx.x & 3) * kTile;
-        if (id >= A.plan.head[0]) return;
         const i32x4 chunk = A.plan.chunks[id];
-        if (at >= chunk[2]) return;
+        if (id >= A.plan.head[0] || at >= chunk[2]) return;
         a = chunk[0];
         slot0 = chunk[1] + at;
         if (tid < 16) list[tid] = A.plan.slot_token[slot0 + tid];
-        if (a >= A.adapters) {
-            if (!A.out || A.base == A.out) return;
-            __syncthreads();
-            for (int i = wave; i < 16; i += WAVES) {
-                const int t = list[i];
-                if (t < 0) continue;
-                for (int col = 8 * lane; col < A.width; col += 8 * 64) {
-                    u32x4 v{0, 0, 0, 0};
-                    if (A.base) v = load_cols<VEC>(A.base + t * A.ld_base, col, A.width);
-                    store_cols<VEC>(A.out + t * A.ld_out, col, A.width, v);
-                }
-            }
-            return;
-        }
+        __syncthreads();
     }
-    __syncthreads();
+    if (a >= A.adapters) {                                  // no adapter: the rows themselves
+        if (!A.out || A.base == A.out) return;
+        for (int i = wave; i < 16; i += WAVES) {
+            const int t = list[i];
+            if (t < 0) continue;
+            for (int col = 8 * lane; col < A.width; col += 8 * 64) {
+                u32x4 v{0, 0, 0, 0};
+                if (A.base) v = load_cols<VEC>(A.base + t * A.ld_base, col, A.width);
+                store_cols<VEC>(A.out + t * A.ld_out, col, A.width, v);
+            }
+        }
+        return;
+    }
     const int rank = rank_of(A.ranks, a, A.rank);
     const bool real = list[c] >= 0;
     const void* vrow = static_cast<const char*>(A.v) + (VT == kE4m3 ? 1 : 2) * (int64_t)max(list[c], 0) * A.ldv;
@@ -826,8 +888,8 @@ struct FactorArgs {
 template <int TYPE, int RT, int HALVES, bool VEC>
 __global__ __launch_bounds__(kThreads, RT == 1 ? 4 : 3) void factor_kernel(FactorArgs A)
 {
-    if ((int)blockIdx.y >= A.plan.head[2]) return;
     const i32x4 unit = A.plan.units[blockIdx.y];
+    if ((int)blockIdx.y >= A.plan.head[2]) return;
     const bool second = (int)blockIdx.x >= A.groups;
     const FactorSide& S = A.side[second];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -1023,12 +1085,38 @@ bool vec_wide(const Pass& s)
     return vec16(s.f2, s.width) && vec16(s.out, s.ld_out) && (!s.base || vec16(s.base, s.ld_base));
 }
 
-// Whether one kernel does both halves: few tokens, and factors that one compute
-// unit reads in a few microseconds.
-bool few(uint64_t tokens, const ecf8a_bank& b)
+// Few tokens: from the index itself, without a plan.
+bool few(uint64_t tokens, const ecf8a_bank& b) { return tokens <= ECF8A_FEW_TOKENS && b.rank <= 64; }
+
+// Whether few_kernel does both halves at once: factors of up to 256 KB, which one
+// compute unit reads in about as long as a second launch takes.  One token, 4096 x
+// 4096 at rank 16 (256 KB): 11.2 us in one kernel, 5.7 + 5.6 in two; 64 tokens, 8192
+// x 8192 at rank 16 (512 KB): 22.5 us in one, 7.9 + 7.7 in two.
+bool one_kernel(uint64_t tokens, const ecf8a_bank& b)
 {
-    return tokens <= ECF8A_FEW_TOKENS && b.rank <= 64 && 2ull * b.rank * (b.in_features + b.out_features) <= 2u << 20;
+    return few(tokens, b) && 2ull * b.rank * (b.in_features + b.out_features) <= 256u << 10;
 }
+
+// Shares of the width for few tokens: every token may have an adapter of its own, or
+// all of them one.
+uint32_t few_shares(uint64_t tokens, uint64_t width)
+{
+    uint64_t s = 512 / (tokens ? tokens : 1);
+    const uint64_t most = (width + 511) / 512;
+    if (s < 4) s = 4;
+    if (s > most) s = most;
+    return (uint32_t)(s < 1 ? 1 : s > 8 ? 8 : s);
+}
+
+// The workspace of ecf8a_add_few: the groups as wide_kernel reads a plan's, then the
+// shares' sums.
+PlanView few_view(void* workspace, uint64_t tokens)
+{
+    char* w = static_cast<char*>(workspace);
+    return PlanView{reinterpret_cast<int*>(w), reinterpret_cast<i32x4*>(w + 256), nullptr, nullptr,
+                    reinterpret_cast<int*>(w + 256 + 16 * tokens)};
+}
+uint64_t few_planes_at(uint64_t tokens) { return round_up(256 + 16 * tokens + 4 * kTile * tokens, 256); }
 
 template <int TYPE, int VT, bool VEC>
 void launch_few(const FewArgs& A, uint32_t grid, hipStream_t st)
@@ -1059,9 +1147,10 @@ int run_few(const PlanView& view, uint32_t grid, const void* index, uint32_t ind
 template <int TYPE, int VT, int RT, bool VEC>
 void launch_low_tiles(const LowArgs& A, dim3 grid, uint32_t tiles, hipStream_t st)
 {
-    if (tiles == 1) low_kernel<TYPE, VT, RT, 1, VEC><<<grid, 64 * low_waves(RT, 1), 0, st>>>(A);
-    else if (tiles == 2) low_kernel<TYPE, VT, RT, 2, VEC><<<grid, 64 * low_waves(RT, 2), 0, st>>>(A);
-    else low_kernel<TYPE, VT, RT, 4, VEC><<<grid, 64 * low_waves(RT, 4), 0, st>>>(A);
+    if (A.index) low_kernel<TYPE, VT, RT, 1, VEC, true><<<grid, 64 * low_waves(RT, 1), 0, st>>>(A);
+    else if (tiles == 1) low_kernel<TYPE, VT, RT, 1, VEC, false><<<grid, 64 * low_waves(RT, 1), 0, st>>>(A);
+    else if (tiles == 2) low_kernel<TYPE, VT, RT, 2, VEC, false><<<grid, 64 * low_waves(RT, 2), 0, st>>>(A);
+    else low_kernel<TYPE, VT, RT, 4, VEC, false><<<grid, 64 * low_waves(RT, 4), 0, st>>>(A);
 }
 
 template <int TYPE, int VT, bool VEC>
@@ -1072,15 +1161,9 @@ void launch_low(const LowArgs& A, dim3 grid, uint32_t tiles, hipStream_t st)
     else launch_low_tiles<TYPE, VT, 4, VEC>(A, grid, tiles, st);
 }
 
-int run_low(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, float* planes, hipStream_t st)
+void launch_low_pass(const LowArgs& A, const ecf8a_bank& b, const Pass& s, dim3 grid, uint32_t n, hipStream_t st)
 {
-    const LowShape shape = low_shape(p, s.in);
-    const LowArgs A{view_of(p), s.v, (int64_t)s.ldv, static_cast<const uint16_t*>(s.f), b.scaling, b.ranks, s.v_scale,
-                    shape.shares > 1 ? planes : nullptr, forms, (int)s.in, (int)b.rank, (int)b.adapters,
-                    (int)(4 / shape.tiles)};
-    const dim3 grid(p.max_chunks * (4 / shape.tiles), shape.shares, (forms.zr + 63) / 64);
     const bool e4m3 = s.vt == ECF8A_E4M3, vec = vec_low(s);
-    const uint32_t n = shape.tiles;
     if (b.type == ECF8A_BF16) {
         if (e4m3) vec ? launch_low<kBf16, kE4m3, true>(A, grid, n, st) : launch_low<kBf16, kE4m3, false>(A, grid, n, st);
         else vec ? launch_low<kBf16, kBf16, true>(A, grid, n, st) : launch_low<kBf16, kBf16, false>(A, grid, n, st);
@@ -1088,43 +1171,71 @@ int run_low(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms
         if (e4m3) vec ? launch_low<kFp16, kE4m3, true>(A, grid, n, st) : launch_low<kFp16, kE4m3, false>(A, grid, n, st);
         else vec ? launch_low<kFp16, kFp16, true>(A, grid, n, st) : launch_low<kFp16, kFp16, false>(A, grid, n, st);
     }
-    if (shape.shares > 1) {
+}
+
+LowArgs low_args(const PlanView& view, const ecf8a_bank& b, const Pass& s, const Forms& forms, float* planes, int per)
+{
+    return LowArgs{view, s.v, (int64_t)s.ldv, static_cast<const uint16_t*>(s.f), b.scaling, b.ranks, s.v_scale, planes, forms,
+                   (int)s.in, (int)b.rank, (int)b.adapters, per, nullptr, 0, 0};
+}
+
+// Z of one side in the forms wanted; shares of a split width go to `planes` and are
+// joined, or left there for wide_kernel to add up where no form by rank row is wanted.
+void run_low(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, float* planes, hipStream_t st)
+{
+    const LowShape shape = low_shape(p, s.in);
+    const LowArgs A = low_args(view_of(p), b, s, forms, shape.shares > 1 ? planes : nullptr, (int)(4 / shape.tiles));
+    launch_low_pass(A, b, s, dim3(p.max_chunks * (4 / shape.tiles), shape.shares, (forms.zr + 63) / 64), shape.tiles, st);
+    if (shape.shares > 1 && forms.row) {
         const uint64_t quads = (uint64_t)p.max_slots * forms.zr / 4;
         join_kernel<<<dim3((uint32_t)((quads + kThreads - 1) / kThreads)), kThreads, 0, st>>>(planes, (int)shape.shares,
                                                                                             A.plan.head, forms);
     }
-    return launch_status();
+}
+
+template <int TYPE, bool VEC, bool PLANES>
+void launch_wide_z(const WideArgs& A, dim3 grid, hipStream_t st)
+{
+    if (A.zr <= 16) wide_kernel<TYPE, 0, VEC, PLANES><<<grid, kThreads, 0, st>>>(A);
+    else if (A.zr <= 32) wide_kernel<TYPE, 1, VEC, PLANES><<<grid, kThreads, 0, st>>>(A);
+    else if (A.zr <= 64) wide_kernel<TYPE, 2, VEC, PLANES><<<grid, kThreads, 0, st>>>(A);
+    else wide_kernel<TYPE, -1, VEC, PLANES><<<grid, kThreads, 0, st>>>(A);
 }
 
 template <int TYPE, bool VEC>
 void launch_wide(const WideArgs& A, dim3 grid, hipStream_t st)
 {
-    if (A.zr <= 16) wide_kernel<TYPE, 0, VEC><<<grid, kThreads, 0, st>>>(A);
-    else if (A.zr <= 32) wide_kernel<TYPE, 1, VEC><<<grid, kThreads, 0, st>>>(A);
-    else if (A.zr <= 64) wide_kernel<TYPE, 2, VEC><<<grid, kThreads, 0, st>>>(A);
-    else wide_kernel<TYPE, -1, VEC><<<grid, kThreads, 0, st>>>(A);
+    if (A.planes) launch_wide_z<TYPE, VEC, true>(A, grid, st);
+    else launch_wide_z<TYPE, VEC, false>(A, grid, st);
 }
 
-int run_wide(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, hipStream_t st)
+void launch_wide_pass(const PlanView& view, const ecf8a_bank& b, const Pass& s, const Forms& forms, const float* planes,
+                      uint32_t shares, uint32_t chunks, hipStream_t st)
 {
-    const WideArgs A{view_of(p), forms.slot, forms.plane, static_cast<const uint16_t*>(s.f2), b.ranks,
+    const WideArgs A{view, forms.slot, planes, forms.plane, (int)shares, static_cast<const uint16_t*>(s.f2), b.ranks,
                      static_cast<const uint16_t*>(s.base), (int64_t)s.ld_base, static_cast<uint16_t*>(s.out),
                      (int64_t)s.ld_out, (int)s.width, (int)b.rank, forms.zr, (int)b.adapters,
                      (int)((s.width + 4 * kStrip - 1) / (4 * kStrip))};
-    const dim3 grid((uint32_t)A.groups * p.max_chunks);
+    const dim3 grid((uint32_t)A.groups * chunks);
     const bool vec = vec_wide(s);
     if (b.type == ECF8A_BF16) vec ? launch_wide<kBf16, true>(A, grid, st) : launch_wide<kBf16, false>(A, grid, st);
     else vec ? launch_wide<kFp16, true>(A, grid, st) : launch_wide<kFp16, false>(A, grid, st);
-    return launch_status();
 }
 
 // One direction, whichever way.  `forms.row` is written if it is given.
 int run_pass(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, Forms forms, float* planes, hipStream_t st)
 {
-    if (few(p.tokens, b)) return run_few(view_of(p), 4 * p.max_chunks, nullptr, 0, p.tokens, b, s, Forms{nullptr, forms.row, forms.plane, forms.zr}, st);
+    if (one_kernel(p.tokens, b)) {
+        forms.slot = nullptr;
+        return run_few(view_of(p), 4 * p.max_chunks, nullptr, 0, p.tokens, b, s, forms, st);
+    }
     if (!s.out) forms.slot = nullptr;
-    const int rc = run_low(p, b, s, forms, planes, st);
-    return rc == ECF8_OK && s.out ? run_wide(p, b, s, forms, st) : rc;
+    run_low(p, b, s, forms, planes, st);
+    if (s.out) {
+        const uint32_t shares = low_shape(p, s.in).shares;
+        launch_wide_pass(view_of(p), b, s, forms, shares > 1 && !forms.row ? planes : nullptr, shares, p.max_chunks, st);
+    }
+    return launch_status();
 }
 
 template <int TYPE, bool VEC>
@@ -1225,7 +1336,7 @@ extern "C" uint64_t ecf8a_hidden_bytes(const ecf8a_plan* plan, uint32_t rank)
 extern "C" uint64_t ecf8a_add_bytes(const ecf8a_plan* plan, const ecf8a_bank* b)
 {
     if (!plan_ok(plan) || !b || b->rank < 1 || b->rank > ECF8A_MAX_RANK) return 0;
-    if (few(plan->tokens, *b)) return 256;
+    if (one_kernel(plan->tokens, *b)) return 256;
     return form_bytes(*plan, b->rank) + low_bytes(*plan, b->rank, b->in_features) + 256;
 }
 
@@ -1255,20 +1366,42 @@ static int check_add(const ecf8a_bank* bank, const void* x, uint64_t ldx, uint32
     return ECF8_OK;
 }
 
+extern "C" uint64_t ecf8a_add_few_bytes(uint64_t tokens, const ecf8a_bank* b)
+{
+    if (!b || !few(tokens, *b) || one_kernel(tokens, *b)) return 0;
+    return round_up(few_planes_at(tokens) + 4ull * few_shares(tokens, b->in_features) * kTile * tokens * z_rows(b->rank), 256);
+}
+
 extern "C" int ecf8a_add_few(const void* index, uint32_t index_bytes, uint64_t tokens, const ecf8a_bank* bank, const void* x,
                              uint64_t ldx, uint32_t x_type, const float* x_scale, const void* base, uint64_t ld_base,
-                             void* out, uint64_t ld_out, void* hip_stream)
+                             void* out, uint64_t ld_out, void* workspace, uint64_t workspace_bytes, void* hip_stream)
 {
     int rc = check_bank(bank);
     if (rc != ECF8_OK) return rc;
     if (x_type != bank->type && x_type != ECF8A_E4M3) return ECF8_ERR_UNSUPPORTED;
     if ((index_bytes != 4 && index_bytes != 8) || (tokens && !index) || !aligned(index, index_bytes)) return ECF8_ERR_ARG;
-    if (tokens > ECF8A_FEW_TOKENS || bank->rank > 64) return ECF8_ERR_SIZE;
+    if (!few(tokens, *bank)) return ECF8_ERR_SIZE;
     if (tokens == 0) return ECF8_OK;
     rc = check_add(bank, x, ldx, x_type, x_scale, base, ld_base, out, ld_out);
     if (rc != ECF8_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const Pass s{x, ldx, x_type, x_scale, bank->down, bank->in_features, bank->up, bank->out_features, base, ld_base, out, ld_out};
-    return run_few(PlanView{}, (uint32_t)tokens, index, index_bytes, tokens, *bank, s, Forms{}, static_cast<hipStream_t>(hip_stream));
+    if (one_kernel(tokens, *bank))
+        return run_few(PlanView{}, (uint32_t)tokens, index, index_bytes, tokens, *bank, s, Forms{}, st);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < ecf8a_add_few_bytes(tokens, bank))
+        return ECF8_ERR_WORKSPACE;
+    const int zr = (int)z_rows(bank->rank);
+    const Forms forms{nullptr, nullptr, (int64_t)kTile * (int64_t)tokens * zr, zr};
+    const PlanView view = few_view(workspace, tokens);
+    float* planes = reinterpret_cast<float*>(static_cast<char*>(workspace) + few_planes_at(tokens));
+    const uint32_t shares = few_shares(tokens, s.in);
+    LowArgs A = low_args(view, *bank, s, forms, planes, 1);
+    A.index = index;
+    A.index_bytes = (int)index_bytes;
+    A.tokens = (int)tokens;
+    launch_low_pass(A, *bank, s, dim3((uint32_t)tokens, shares), 1, st);
+    launch_wide_pass(view, *bank, s, forms, planes, shares, (uint32_t)tokens, st);
+    return launch_status();
 }
 
 extern "C" int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* x, uint64_t ldx, uint32_t x_type,
