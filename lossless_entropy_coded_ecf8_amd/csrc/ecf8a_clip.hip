@@ -23,7 +23,8 @@ using namespace ecf8a;
 
 constexpr int kThreads = 256;
 constexpr int kStep = 16 * kThreads;          // bytes a workgroup loads at once
-constexpr uint32_t kMaxGrid = 1024;
+constexpr int kFlight = 4;                    // 16-byte loads of a lane in flight
+constexpr uint32_t kMaxGrid = 2048;
 
 struct Piece {
     const void* grad;
@@ -103,7 +104,15 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const Piece* __restrict_
         const T* g = static_cast<const T*>(p.grad);
         const uint64_t head = head_of<TYPE>(p), units = (p.n - head) / per, tail = head + units * per;
         const u32x4* body = reinterpret_cast<const u32x4*>(g + head);
-        for (uint64_t u = threadIdx.x; u < units; u += kThreads) s += squares<TYPE>(body[u]);
+        uint64_t u = threadIdx.x;
+        for (; u + (kFlight - 1) * kThreads < units; u += kFlight * kThreads) {
+            u32x4 v[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) v[i] = body[u + i * kThreads];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) s += squares<TYPE>(v[i]);
+        }
+        for (; u < units; u += kThreads) s += squares<TYPE>(body[u]);
         if (threadIdx.x < head) {
             const double d = value_of<TYPE>(g[threadIdx.x]);
             s += d * d;
@@ -139,8 +148,7 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(const Piece* __restrict
         T* o = static_cast<T*>(p.out);
         const uint64_t head = head_of<TYPE>(p), units = (p.n - head) / per, tail = head + units * per;
         const bool wide = (reinterpret_cast<uintptr_t>(o + head) & 15) == 0;
-        for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
-            u32x4 v = *reinterpret_cast<const u32x4*>(g + head + u * per);
+        const auto put = [&](uint64_t u, u32x4 v) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if constexpr (TYPE == ECF8A_FP32) v[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, (uint32_t)v[k]) * by);
@@ -150,15 +158,19 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(const Piece* __restrict
                 }
             }
             T* q = o + head + u * per;
-            if (wide) *reinterpret_cast<u32x4*>(q) = v;
-            else {
+            if (wide) store16<true>(q, v);
+            else store16<false>(q, v);
+        };
+        const u32x4* body = reinterpret_cast<const u32x4*>(g + head);
+        uint64_t u = threadIdx.x;
+        for (; u + (kFlight - 1) * kThreads < units; u += kFlight * kThreads) {
+            u32x4 v[kFlight];
 #pragma unroll
-                for (int k = 0; k < per; ++k) {
-                    if constexpr (TYPE == ECF8A_FP32) q[k] = __builtin_bit_cast(float, (uint32_t)v[k]);
-                    else q[k] = (T)(v[k >> 1] >> (16 * (k & 1)));
-                }
-            }
+            for (int i = 0; i < kFlight; ++i) v[i] = __builtin_nontemporal_load(body + u + i * kThreads);
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) put(u + i * kThreads, v[i]);
         }
+        for (; u < units; u += kThreads) put(u, body[u]);
         if (threadIdx.x < head) o[threadIdx.x] = scaled<TYPE>(g[threadIdx.x], by);
         if (tail + threadIdx.x < p.n) o[tail + threadIdx.x] = scaled<TYPE>(g[tail + threadIdx.x], by);
     }
