@@ -446,3 +446,49 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
                    stream=None) -> torch.Tensor:
     """GradClip(grads, out).run(max_norm): for lists whose tensors change from step to step."""
     return GradClip(grads, out, stream).run(max_norm, stream)
+
+
+FEW_TOKENS = 512            # up to here a batch needs no AdapterPlan (ECF8A_FEW_TOKENS)
+
+
+class AdapterBank(torch.nn.Module):
+    """The low-rank adapters of one projection: ``n_adapters`` pairs of up to ``rank`` rows, as trainable parameters
+    ``down`` (L, R, K) and ``up`` (L, R, N), with a float32 ``scaling`` (L,) and, where ranks differ, int32 ``ranks``.
+
+    Adapter a adds scaling[a] * up[a].T @ down[a] to the weight of the tokens that name it.  ``up`` starts at 0, so a
+    new adapter changes nothing.
+    """
+
+    def __init__(self, n_adapters: int, rank: int, in_features: int, out_features: int, scaling=1.0, ranks=None,
+                 dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("adapters are bfloat16 or float16, got %s" % dtype)
+        if n_adapters < 1 or rank < 1:
+            raise ValueError("need at least one adapter of rank 1 or more")
+        self.down = torch.nn.Parameter((torch.randn(n_adapters, rank, in_features, device=device) / in_features ** 0.5).to(dtype))
+        self.up = torch.nn.Parameter(torch.zeros(n_adapters, rank, out_features, dtype=dtype, device=device))
+        scaling = torch.as_tensor(scaling, dtype=torch.float32, device=device).expand(n_adapters).contiguous()
+        self.register_buffer("scaling", scaling)
+        if ranks is not None:
+            ranks = torch.as_tensor(ranks, dtype=torch.int32, device=device).expand(n_adapters).contiguous()
+        self.register_buffer("ranks", ranks)
+
+    @property
+    def n_adapters(self) -> int:
+        return self.down.shape[0]
+
+    @property
+    def rank(self) -> int:
+        return self.down.shape[1]
+
+    def add_(self, y: torch.Tensor, x: torch.Tensor, index, x_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """adapter_add into y, the shared projection's output; no gradients are kept."""
+        return adapter_add(y, x, self.down.detach(), self.up.detach(), self.scaling, index, ranks=self.ranks,
+                           x_scale=x_scale, out=y)
+
+
+def clip_adapter_grads(banks, max_norm: float, stream=None) -> torch.Tensor:
+    """clip_grad_norm over the gradients of these banks' parameters, in place; returns the norm before."""
+    grads = [p.grad for b in banks for p in (b.down, b.up) if p.grad is not None]
+    return clip_grad_norm(grads, max_norm, stream=stream)

@@ -23,6 +23,8 @@
 // tokens take one kernel that does `low` and `wide` for 16 of them (few_kernel).
 #include "ecf8a_common.h"
 
+#include <type_traits>
+
 namespace {
 
 using namespace ecf8a;
@@ -581,15 +583,22 @@ __device__ __forceinline__ void load_factor(const uint16_t* f, int width, int r,
     }
 }
 
-// ... turned into one operand per column (lo: of a float16, the rest of it).
-template <int TYPE>
-__device__ __forceinline__ void turn_factor(const u32x4 w[8], u32x4 hi[8], u32x4 lo[8])
+// ... turned into one operand per column (lo: of a float16, the rest of it).  True if
+// one is not finite.  HALF: see wide_products.
+template <int TYPE, bool HALF>
+__device__ __forceinline__ bool turn_factor(const u32x4 w[8], u32x4 hi[8], u32x4 lo[8])
 {
     transpose8(w, hi);
     if constexpr (TYPE == kFp16) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) split8_f16(hi[j], hi[j], lo[j]);
     }
+    const bool odd = any_not_finite(hi);
+    if (HALF && odd && (threadIdx.x & 32)) {                // these lanes hold the slots of the lower halves
+#pragma unroll
+        for (int j = 0; j < 8; ++j) hi[j] = finite(hi[j]);
+    }
+    return odd;
 }
 
 // One row's eight columns: base plus the results of its token, rounded once.
@@ -605,17 +614,29 @@ __device__ __forceinline__ u32x4 add_row(u32x4 base, const f32x4* acc, int i)
     return o;
 }
 
-// The products of 16 tokens with BLOCKS blocks of 32 rank rows at this lane's eight
-// columns.  HALF: up to 16 rank rows, whose lower bfloat16 take the upper half of
-// the reduction slots, so that one instruction does both.
+// The products of 16 tokens with 32 rank rows at this lane's eight columns.  HALF: up
+// to 16 rank rows, whose lower bfloat16 take the upper half of the reduction slots,
+// so that one instruction does both.  odd: a factor value is not finite.
 template <int TYPE, bool HALF>
-__device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* hi, const u32x4* lo, f32x4* acc)
+__device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* hi, const u32x4* lo, bool odd, f32x4* acc)
 {
+    const u32x4 zf = TYPE == kFp16 ? finite(zh) : zh;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         acc[j] = mfma_bf16(zh, hi[j], acc[j]);
-        if constexpr (!HALF) acc[j] = mfma_bf16(zl, hi[j], acc[j]);
-        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(zh, lo[j], acc[j]);
+        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(zf, lo[j], acc[j]);
+    }
+    if constexpr (HALF) return;
+    if (!odd) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(zl, hi[j], acc[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u32x4 one = hi[j];                              // rare: not to be kept in registers for the next tile
+            asm volatile("" : "+v"(one));
+            acc[j] = mfma_bf16(zl, finite(one), acc[j]);
+        }
     }
 }
 
@@ -654,7 +675,7 @@ __device__ __forceinline__ void sum_planes(const float* z, int64_t plane, int sh
 }
 
 template <int TYPE, int RB, bool VEC, bool PLANES>
-__global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 : 3) : 2) void wide_kernel(WideArgs A)
+__global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !PLANES) ? 4 : 3) : 2) void wide_kernel(WideArgs A)
 {
     const int id = blockIdx.x / A.groups;                   // neighbouring workgroups: the same rows, next columns
     const i32x4 chunk = A.plan.chunks[id];                  // there for every id, and sent for with the count
@@ -669,12 +690,13 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 :
     const uint16_t* f = A.f + (int64_t)(bare ? 0 : a) * A.rank * A.width;
     constexpr int KEEP = RB <= 0 ? 1 : RB;
     u32x4 hi[KEEP][8], lo[KEEP][8];
+    bool odd[KEEP] = {};
     if constexpr (RB >= 0) {
 #pragma unroll
         for (int b = 0; b < KEEP; ++b) {
             u32x4 w[8];
             load_factor<VEC>(f, A.width, RB == 0 ? 8 * (g & 1) : 32 * b + 8 * g, rank, col, w);
-            turn_factor<TYPE>(w, hi[b], lo[b]);
+            odd[b] = turn_factor<TYPE, RB == 0>(w, hi[b], lo[b]);
         }
     }
     for (int tile = 0; tile < tiles; ++tile) {
@@ -702,7 +724,7 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 :
             } else {
                 both = *reinterpret_cast<const u32x4*>(A.z + at + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
             }
-            wide_products<TYPE, true>(both, both, hi[0], lo[0], acc);
+            wide_products<TYPE, true>(both, both, hi[0], lo[0], odd[0], acc);
         } else {
             const auto block = [&](int b, int keep) {
                 u32x4 zh, zl;
@@ -711,7 +733,7 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 :
                     zh = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g);
                     zl = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g + A.plane);
                 }
-                wide_products<TYPE, false>(zh, zl, hi[keep], lo[keep], acc);
+                wide_products<TYPE, false>(zh, zl, hi[keep], lo[keep], odd[keep], acc);
             };
             if constexpr (RB > 0) {
 #pragma unroll
@@ -720,7 +742,7 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || RB == 1 ? 4 :
                 for (int b = 0; b < (A.zr + 31) / 32; ++b) {
                     u32x4 w[8];
                     load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, w);
-                    turn_factor<TYPE>(w, hi[0], lo[0]);
+                    odd[0] = turn_factor<TYPE, false>(w, hi[0], lo[0]);
                     block(b, 0);
                 }
             }
@@ -812,7 +834,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(FewArgs A)
     };
     if (A.out && wave * kStrip < A.width) fetch(wave * kStrip + 8 * c);
     f32x4 acc[RT][1] = {};
-    low_products<TYPE, VT, RT, 1, RT == 1 ? 8 : RT == 2 ? 4 : 2, VEC>(&vrow, A.f, (int64_t)a * A.rank, 0, rank, A.in, wave, WAVES, acc);
+    low_products<TYPE, VT, RT, 1, RT == 1 && TYPE == kBf16 ? 8 : RT <= 2 ? 4 : 2, VEC>(&vrow, A.f, (int64_t)a * A.rank, 0, rank, A.in, wave, WAVES, acc);
     float scale = A.scaling[a];
     if (A.v_scale) scale *= *A.v_scale;
     sum_waves<WAVES, RT>(&acc[0][0], red, [&](int tile, f32x4 s) {
@@ -833,21 +855,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(FewArgs A)
         const int col = strip + 8 * c;
         f32x4 sum[8] = {};
         u32x4 hi[8], lo[8], row[4] = {base[0], base[1], base[2], base[3]};
-        turn_factor<TYPE>(w, hi, lo);
+        bool odd = turn_factor<TYPE, RT == 1>(w, hi, lo);
         if (strip + WAVES * kStrip < A.width) fetch(col + WAVES * kStrip);
         if constexpr (RT == 1) {
             const u32x4 both = *reinterpret_cast<const u32x4*>(&zs[g >> 1][c][8 * (g & 1)]);
-            wide_products<TYPE, true>(both, both, hi, lo, sum);
+            wide_products<TYPE, true>(both, both, hi, lo, odd, sum);
         } else {
 #pragma unroll
             for (int b = 0; b < RT / 2; ++b) {
                 if (b) {
                     u32x4 more[8];
                     load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, more);
-                    turn_factor<TYPE>(more, hi, lo);
+                    odd = turn_factor<TYPE, false>(more, hi, lo);
                 }
                 wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(&zs[0][c][32 * b + 8 * g]),
-                                           *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, sum);
+                                           *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, odd, sum);
             }
         }
 #pragma unroll
@@ -886,7 +908,7 @@ struct FactorArgs {
 // adapter of one unit is written at once, others leave float32 partial sums that
 // sum_kernel joins in order.
 template <int TYPE, int RT, int HALVES, bool VEC>
-__global__ __launch_bounds__(kThreads, RT == 1 ? 4 : 3) void factor_kernel(FactorArgs A)
+__global__ __launch_bounds__(kThreads, (RT == 1 ? 4 : 3) - (TYPE == kFp16)) void factor_kernel(FactorArgs A)
 {
     const i32x4 unit = A.plan.units[blockIdx.y];
     if ((int)blockIdx.y >= A.plan.head[2]) return;
@@ -916,36 +938,73 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? 4 : 3) void factor_kernel(Facto
     };
     // The rows are not sent for ahead of their turn: that takes 32 registers, and a
     // third wave per SIMD hides more (8192 x 18432 at rank 32: 92 -> 62 us).
-    tokens_of(0);
-    for (int s = 0; s < unit[2]; s += 32) {
-        rows_of();
-        tokens_of(s + 32);
-        const bool have = s + 8 * g < unit[2];
-        u32x4 zh[RT], zl[RT], t[8], tl[8];
+    const auto unit_sum = [&](auto careful) {
+        tokens_of(0);
+        for (int s = 0; s < unit[2]; s += 32) {
+            rows_of();
+            tokens_of(s + 32);
+            const bool have = s + 8 * g < unit[2];
+            u32x4 zh[RT], zl[RT], t[8], tl[8];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int row = r0 + r * 16 + c;
-            zh[r] = zl[r] = u32x4{0, 0, 0, 0};
-            if (have && row < A.zr) {
-                const int slot = unit[1] + s + 8 * g;
-                const uint16_t* z = S.z + ((int64_t)(slot / kTile) * A.zr + row) * kTile + slot % kTile;
-                zh[r] = *reinterpret_cast<const u32x4*>(z);
-                zl[r] = *reinterpret_cast<const u32x4*>(z + A.plane);
+            for (int r = 0; r < RT; ++r) {
+                const int row = r0 + r * 16 + c;
+                zh[r] = zl[r] = u32x4{0, 0, 0, 0};
+                if (have && row < A.zr) {
+                    const int slot = unit[1] + s + 8 * g;
+                    const uint16_t* z = S.z + ((int64_t)(slot / kTile) * A.zr + row) * kTile + slot % kTile;
+                    zh[r] = *reinterpret_cast<const u32x4*>(z);
+                    zl[r] = *reinterpret_cast<const u32x4*>(z + A.plane);
+                }
+            }
+            transpose8(w, t);
+            if constexpr (TYPE == kFp16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) split8_f16(t[j], t[j], tl[j]);
+            }
+            if constexpr (!careful) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        acc[r][j] = mfma_bf16(zh[r], t[j], acc[r][j]);
+                        acc[r][j] = mfma_bf16(zl[r], t[j], acc[r][j]);
+                        if constexpr (TYPE == kFp16) acc[r][j] = mfma_bf16(zh[r], tl[j], acc[r][j]);
+                    }
+            } else {                                          // in place, in an order that needs no copies
+                const auto products = [&](const u32x4* z, const u32x4* v) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[r][j] = mfma_bf16(z[r], v[j], acc[r][j]);
+                };
+                products(zh, t);
+                if constexpr (TYPE == kFp16) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) zh[r] = finite(zh[r]);
+                    products(zh, tl);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] = finite(t[j]);
+                products(zl, t);
             }
         }
-        transpose8(w, t);
-        if constexpr (TYPE == kFp16) {
+    };
+    unit_sum(std::false_type{});
+    // An infinity among the rows or Z has met lower halves of 0: only then once more,
+    // keeping those products finite.
+    float test = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) split8_f16(t[j], t[j], tl[j]);
-        }
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) test = __builtin_fmaf(acc[r][j][i], 0.0f, test);
+    if (__ballot(test != test)) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc[r][j] = mfma_bf16(zh[r], t[j], acc[r][j]);
-                acc[r][j] = mfma_bf16(zl[r], t[j], acc[r][j]);
-                if constexpr (TYPE == kFp16) acc[r][j] = mfma_bf16(zh[r], tl[j], acc[r][j]);
-            }
+            for (int j = 0; j < 8; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+        unit_sum(std::true_type{});
     }
     if (col >= S.width) return;
     const int a = unit[0], rank = rank_of(A.ranks, a, A.rank);

@@ -122,6 +122,31 @@ __device__ __forceinline__ void split8_f16(u32x4 v, u32x4& hi, u32x4& lo)
     split8(f32x4{a[0], a[1], b[0], b[1]}, f32x4{c[0], c[1], d[0], d[1]}, hi, lo);
 }
 
+// A bfloat16 operand with 0 in place of infinities and NaN: for the product with a
+// lower half, which may be 0 or of the other sign and would make a NaN of what the
+// upper half's product says rightly.
+__device__ __forceinline__ u32x4 finite(u32x4 v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((v[i] & 0x7F80u) == 0x7F80u) v[i] &= 0xFFFF0000u;
+        if ((v[i] & 0x7F800000u) == 0x7F800000u) v[i] &= 0xFFFFu;
+    }
+    return v;
+}
+
+// Whether any lane of the wave has an infinity or a NaN in its eight operands.
+__device__ __forceinline__ bool any_not_finite(const u32x4 v[8])
+{
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= (v[j][i] & 0x7F80u) == 0x7F80u || (v[j][i] & 0x7F800000u) == 0x7F800000u;
+    __builtin_amdgcn_sched_barrier(0);
+    return __ballot(odd) != 0;
+}
+
 // Eight rows of eight 16-bit columns, one row in each w[q], turned into one
 // operand for each column: t[j] holds column j of rows 0 .. 7.
 __device__ __forceinline__ void transpose8(const u32x4 w[8], u32x4 t[8])

@@ -15,6 +15,11 @@ Every decode is the library's HIP kernel (``DecodePlan``) and every product is
 a library GEMM (``torch._scaled_mm`` on FP8 operands, i.e. hipBLASLt); this
 module only allocates the pool once and orders launches on two HIP streams
 with events.
+
+A compressed weight is frozen.  What varies per request, or is trained, is a bank
+of low-rank adapters beside it (adapters.py): ``ECF8Linear.forward`` and
+``DecodePipeline.run`` add them when serving, ``ECF8Linear.adapted`` is the
+differentiable layer for training them.
 """
 from __future__ import annotations
 
@@ -23,6 +28,7 @@ from typing import List, Optional, Sequence
 import torch
 
 from . import binding
+from .adapters import FEW_TOKENS, AdapterBank, AdapterPlan, adapter_add, adapter_grads, linear_fp8_input_grad
 
 E4M3_MAX = 448.0
 
@@ -142,10 +148,71 @@ class ECF8Linear(torch.nn.Module):
             check_decode(self._own_plan, stream)
         return self._own.view(self.out_features, self.in_features)
 
-    def forward(self, x_fp8: torch.Tensor, x_scale: torch.Tensor,
-                weight_u8: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, x_fp8: torch.Tensor, x_scale: torch.Tensor, weight_u8: Optional[torch.Tensor] = None,
+                adapters: Optional[AdapterBank] = None, index=None) -> torch.Tensor:
+        """adapters, index: low-rank adapters added to the output, and the adapter of each token (a vector on the GPU,
+        -1 for none, or an AdapterPlan of it).  The output then has the adapters' type."""
         w = self.decoded_weight() if weight_u8 is None else weight_u8.view(self.out_features, self.in_features)
-        return linear_fp8(x_fp8, x_scale, w, self.w_scale, self.bias)
+        if adapters is None:
+            return linear_fp8(x_fp8, x_scale, w, self.w_scale, self.bias)
+        if index is None:
+            raise ValueError("adapters need the index of each token's adapter")
+        y = linear_fp8(x_fp8, x_scale, w, self.w_scale, self.bias, out_dtype=adapters.down.dtype)
+        return adapters.add_(y, x_fp8, index, x_scale)
+
+    def adapted(self, x: torch.Tensor, adapters: AdapterBank, index, x_scale: Optional[torch.Tensor] = None,
+                weight_u8: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer with adapters for training: differentiable in x and in the adapters' parameters.
+
+        x: (T, in_features) in the adapters' type.  The frozen product takes x in E4M3 with x_scale (default: the
+        largest magnitude of x over 448), which its gradient passes through as if it were exact; the adapters take x
+        itself.  The weight is decoded for the forward pass and again for the backward pass (weight_u8: a decoded weight
+        that is kept instead).  The weight and the bias get no gradient.  index as in forward.
+        """
+        plan = index if isinstance(index, AdapterPlan) else AdapterPlan(index, adapters.n_adapters)
+        return _Adapted.apply(x, adapters.down, adapters.up, self, adapters, plan, x_scale, weight_u8)
+
+
+def quantize_e4m3(x: torch.Tensor, scale: Optional[torch.Tensor] = None) -> "tuple[torch.Tensor, torch.Tensor]":
+    """x as float8_e4m3fn and its float32 scale, on the device and without a synchronisation (scale None: the largest
+    magnitude over 448, 1 for an all-zero x)."""
+    v = x.detach().float()
+    if scale is None:
+        amax = v.abs().amax() if v.numel() else v.new_zeros(())
+        scale = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    return (v / scale).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn), scale
+
+
+class _Adapted(torch.autograd.Function):
+    """ECF8Linear.adapted: y = frozen(x) + adapters(x)."""
+
+    @staticmethod
+    def forward(ctx, x, down, up, layer, bank, plan, x_scale, weight_u8):
+        xq, scale = quantize_e4m3(x, x_scale)
+        w = layer.decoded_weight() if weight_u8 is None else weight_u8.view(layer.out_features, layer.in_features)
+        y = linear_fp8(xq, scale, w, layer.w_scale, layer.bias, out_dtype=down.dtype)
+        hidden = plan.hidden(bank.rank) if ctx.needs_input_grad[1] or ctx.needs_input_grad[2] else None
+        adapter_add(y, x, down, up, bank.scaling, plan, ranks=bank.ranks, out=y, hidden=hidden)
+        ctx.save_for_backward(x, down, up, bank.scaling, bank.ranks, hidden)
+        ctx.layer, ctx.plan, ctx.weight_u8 = layer, plan, weight_u8
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, down, up, scaling, ranks, hidden = ctx.saved_tensors
+        layer, w = ctx.layer, ctx.weight_u8
+        dy = dy.contiguous()                                  # a sum's gradient is one value, expanded
+        if dy.data_ptr() % 16:
+            dy = dy.clone()
+        want_x, want_factors = ctx.needs_input_grad[0], ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+        dx = None
+        if want_x:
+            w = layer.decoded_weight() if w is None else w.view(layer.out_features, layer.in_features)
+            dx = linear_fp8_input_grad(dy, w, layer.w_scale)
+        dx, d_down, d_up = adapter_grads(dy, x, down, up, scaling, ctx.plan, hidden=hidden, ranks=ranks, dx_base=dx, dx=dx,
+                                         want=(want_x, want_factors))
+        return dx, d_down, d_up, None, None, None, None, None
 
 
 class DecodePipeline:
@@ -192,15 +259,28 @@ class DecodePipeline:
     def pool_bytes(self) -> int:
         return self.pool.numel()
 
-    def run(self, xs: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor]) -> List[torch.Tensor]:
-        """Layer i computes on xs[i]; returns the outputs (caller's stream order)."""
+    def run(self, xs: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor],
+            adapters: Optional[Sequence[Optional[AdapterBank]]] = None, index=None) -> List[torch.Tensor]:
+        """Layer i computes on xs[i]; returns the outputs (caller's stream order).
+
+        adapters: a bank (or None) for each layer, all of the same number of adapters, added to the layer's output as
+        ECF8Linear.forward does; index: the adapter of each token, the same for all layers (it is grouped once)."""
         L = len(self.layers)
         main = torch.cuda.current_stream(self.layers[0].device)
         outs = []
+        banks = list(adapters) if adapters is not None else [None] * L
+        if len(banks) != L:
+            raise ValueError("%d adapter banks for %d layers" % (len(banks), L))
+        first = next((b for b in banks if b is not None), None)
+        if first is not None:
+            if index is None:
+                raise ValueError("adapters need the index of each token's adapter")
+            if not isinstance(index, AdapterPlan) and index.numel() > FEW_TOKENS:
+                index = AdapterPlan(index, first.n_adapters)
         if self.ahead == 0:
             for i in range(L):
                 self.plans[i].run(main)
-                outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i)))
+                outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
             self._check(main)
             return outs
         side = self.side
@@ -216,7 +296,7 @@ class DecodePipeline:
                 self.plans[j].run(side)
                 self.decoded[j].record(side)
             main.wait_event(self.decoded[i])
-            outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i)))
+            outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
             self.used[i].record(main)
         main.wait_stream(side)
         self._check(main)
