@@ -391,3 +391,23 @@ def test_refusals():
         E.AdapterPlan(s["index"], 2049)
     only = E.adapter_grads(s["dy"], None, s["down"], s["up"], s["scaling"], plan, want=(True, False))
     assert only[1] is None and only[2] is None and only[0].shape == (12, 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_infinite_rows_give_infinite_gradients(dtype):
+    """An infinity in a token's own row reaches its adapter's gradient as an infinity in that column, and nothing else
+    becomes a NaN where the formula has none (h and z are positive here)."""
+    d = dev()
+    for T in (20, 700):
+        x, down = torch.ones(T, 80, dtype=dtype, device=d), torch.full((2, 3, 80), 0.125, dtype=dtype, device=d)
+        dy, up = torch.ones(T, 88, dtype=dtype, device=d), torch.full((2, 3, 88), 0.25, dtype=dtype, device=d)
+        index = (torch.arange(T, device=d) % 2).int()
+        plan = E.AdapterPlan(index, 2)
+        one = torch.ones(2, device=d)
+        hidden = plan.hidden(3)
+        E.adapter_add(None, x, down, up, one, plan, hidden=hidden)
+        x[4, 7] = float("inf")                                   # token 4: adapter 0
+        _, dd, du = E.adapter_grads(dy, x, down, up, one, plan, hidden=hidden)
+        assert bool((dd[0, :, 7] == float("inf")).all())
+        rest = torch.arange(80, device=d) != 7
+        assert bool(torch.isfinite(dd[0][:, rest]).all()) and bool(torch.isfinite(dd[1]).all()) and bool(torch.isfinite(du).all())
