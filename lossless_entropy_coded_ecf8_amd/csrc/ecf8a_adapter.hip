@@ -32,8 +32,8 @@ using namespace ecf8a;
 constexpr int kTile = 16;                 // slots a group is padded to: one matrix instruction's rows
 constexpr int kChunk = 64;                // slots of one chunk at most
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanLds = 10000;           // ints of LDS for the grouping
-constexpr int kPlanKept = 12288;          // tokens whose adapters fit beside them
+constexpr int kPlanLds = 30000;           // ints of LDS for the grouping: 16 waves up to 1577 adapters, 11 for 2048
+constexpr int kPlanKept = 20480;          // tokens whose adapters fit beside them
 constexpr int kBatch = 4;
 constexpr int kThreads = 256;
 constexpr int kStrip = 128;               // columns of one wave: 16 lanes of 8
@@ -75,23 +75,29 @@ __device__ __forceinline__ int read_index(const void* index, int bytes, int64_t 
 }
 
 // Exclusive prefix over the workgroup of three values at once.
-__device__ __forceinline__ void block_scan3(int v[3], int total[3], int (*lds)[3])
+__device__ __forceinline__ void block_scan3(int v[3], int total[3], i32x4* lds)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int inc[3] = {v[0], v[1], v[2]};
+#pragma unroll
     for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
         for (int i = 0; i < 3; ++i) {
             const int o = __shfl_up(inc[i], d);
             if (lane >= d) inc[i] += o;
         }
-    if (lane == 63)
-        for (int i = 0; i < 3; ++i) lds[wave][i] = inc[i];
+    if (lane == 63) lds[wave] = i32x4{inc[0], inc[1], inc[2], 0};
     __syncthreads();
+    i32x4 part[kPlanThreads / 64];
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) part[w] = lds[w];
+#pragma unroll
     for (int i = 0; i < 3; ++i) {
         int before = 0, all = 0;
+#pragma unroll
         for (int w = 0; w < kPlanThreads / 64; ++w) {
-            if (w < wave) before += lds[w][i];
-            all += lds[w][i];
+            if (w < wave) before += part[w][i];
+            all += part[w][i];
         }
         v[i] = before + inc[i] - v[i];
         total[i] = all;
@@ -110,9 +116,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
 {
     __shared__ int lds[kPlanLds];
     __shared__ uint16_t kept[kPlanKept];
-    __shared__ int scan[kPlanThreads / 64][3];
+    __shared__ i32x4 scan[kPlanThreads / 64];
     const int groups = adapters + 1;                        // the last: no adapter
-    int* const hist = lds;                                  // [waves][groups]: next slot of each wave in each group
+    int* const hist = lds;                                  // [waves][groups]: counts, then where in each group each wave goes on
     int* const count = lds + waves * groups;                // [groups]
     int* const chunk0 = count + groups;                     // [groups]
     int* const slot0 = chunk0 + groups;                     // [groups]
@@ -144,12 +150,15 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
     const int a0 = min(groups, tid * per), a1 = min(groups, a0 + per);
     int v[3] = {0, 0, 0}, total[3];
     for (int a = a0; a < a1; ++a) {
-        int c = 0;
-        for (int w = 0; w < waves; ++w) {
-            const int h = hist[w * groups + a];
-            hist[w * groups + a] = c;
-            c += h;
-        }
+        int h[kPlanThreads / 64], c = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 64; ++w) h[w] = w < waves ? hist[w * groups + a] : 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 64; ++w)
+            if (w < waves) {
+                hist[w * groups + a] = c;
+                c += h[w];
+            }
         count[a] = c;
         const int s = (c + kTile - 1) / kTile * kTile;
         v[0] += s;
@@ -161,7 +170,6 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
         const int c = count[a], s = (c + kTile - 1) / kTile * kTile;
         slot0[a] = v[0];
         chunk0[a] = v[1];
-        for (int w = 0; w < waves; ++w) hist[w * groups + a] += v[0];
         for (int i = c; i < s; ++i) p.slot_token[v[0] + i] = -1;
         if (a < adapters) {
             const int units = (s + unit_slots - 1) / unit_slots;
@@ -190,27 +198,40 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
         const int at = (c - chunk0[lo]) * kChunk;
         p.chunks[c] = i32x4{lo, slot0[lo] + at, min(kChunk, count[lo] - at), 0};
     }
+    const auto adapter_at = [&](int t) { return t >= t1 ? -1 : keep ? (int)kept[t] : read_index(index, index_bytes, t, adapters); };
+    int ahead = adapter_at(t0 + lane);
 #pragma unroll 1
     for (int tb = t0; tb < t1; tb += 64) {
-        const int t = tb + lane;
-        const int a = t >= t1 ? -1 : keep ? (int)kept[t] : read_index(index, index_bytes, t, adapters);
-        const int first = __builtin_amdgcn_readfirstlane(a);
+        const int t = tb + lane, a = ahead;
+        ahead = adapter_at(t + 64);
         int rank = 0, same = 0;
-        if (__ballot(a == first || a < 0) == ~0ull) {        // valid lanes are a prefix
-            rank = lane;
-            same = (int)__popcll(__ballot(a >= 0));
-        } else {
-#pragma unroll 4
+        uint64_t left = __ballot(a >= 0);
+        for (int tries = 0; left && tries < 8; ++tries) {     // one adapter of these 64 tokens after the other
+            const int first = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
+            const uint64_t mine = __ballot(a == first);
+            if (a == first) {
+                rank = (int)__popcll(mine & ((1ull << lane) - 1));
+                same = (int)__popcll(mine);
+            }
+            left &= ~mine;
+        }
+        if (left) {                                           // many adapters: each token with every one before it
+            int before = 0, all = 0;
+#pragma unroll 16
             for (int j = 0; j < 64; ++j) {
-                const int o = __builtin_amdgcn_readlane(a, j);
-                same += o == a;
-                rank += o == a && j < lane;
+                const bool equal = a == __builtin_amdgcn_readlane(a, j);
+                all += equal;
+                before += equal && j < lane;
+            }
+            if (left >> lane & 1) {
+                rank = before;
+                same = all;
             }
         }
         if (a >= 0) {
             volatile int* next = &hist[wave * groups + a];
             const int at = *next;
-            p.slot_token[at + rank] = t;
+            p.slot_token[slot0[a] + at + rank] = t;
             if (rank == same - 1) *next = at + same;          // one lane of each adapter, after every lane's read
         }
     }
