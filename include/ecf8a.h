@@ -115,7 +115,8 @@ typedef struct {
  * 16-byte aligned) that carries h from a forward call to its gradients. */
 uint64_t ecf8a_hidden_bytes(const ecf8a_plan* plan, uint32_t rank);
 
-/* Workspace bytes of ecf8a_add, and of ecf8a_grads (256-byte aligned). */
+/* Workspace bytes of ecf8a_add (0: none is used), and of ecf8a_grads (256-byte
+ * aligned). */
 uint64_t ecf8a_add_bytes(const ecf8a_plan* plan, const ecf8a_bank* bank);
 uint64_t ecf8a_grads_bytes(const ecf8a_plan* plan, const ecf8a_bank* bank);
 

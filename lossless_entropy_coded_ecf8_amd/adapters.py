@@ -198,8 +198,7 @@ class AdapterPlan:
             _check(L.ecf8a_plan_prepare(index.data_ptr(), _INDEX_BYTES[index.dtype], self.tokens, self.adapters,
                                         workspace.data_ptr(), workspace.numel(), st, ctypes.byref(self.c)),
                    "ecf8a_plan_prepare")
-            self._made_on, self._handle = _stream_of(self.device, stream), st
-        self._event = None
+            self._made_on, self._handle, self._event = stream, st, None
 
     def _order(self, handle, stream):
         """Makes a launch on another stream than the plan's own wait for the grouping."""
@@ -207,7 +206,7 @@ class AdapterPlan:
             return
         if self._event is None:
             self._event = torch.cuda.Event()
-            self._event.record(self._made_on)
+            self._event.record(self._made_on or torch.cuda.ExternalStream(self._handle, device=self.device))
         _stream_of(self.device, stream).wait_event(self._event)
 
     def hidden(self, rank: int, stream=None) -> torch.Tensor:
@@ -237,7 +236,8 @@ def _bank(down, up, scaling, ranks, dev) -> BankA:
 
 
 def _hidden_ok(hidden, plan, rank):
-    binding._check_buffer(hidden, plan.device, "hidden")
+    if hidden.dtype != torch.uint8 or not hidden.is_contiguous() or hidden.device != plan.device:
+        raise ValueError("hidden must be a plan.hidden() buffer on %s" % plan.device)
     if hidden.numel() < _lib().ecf8a_hidden_bytes(ctypes.byref(plan.c), rank):
         raise ValueError("hidden is smaller than plan.hidden(%d)" % rank)
 
@@ -302,10 +302,11 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
         _hidden_ok(hidden, plan, bank.rank)
     with _Launch(dev, stream) as st:
         plan._order(st, stream)
-        ws = _scratch(L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream)
+        need = L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank))
+        ws = _scratch(need, workspace, dev, stream) if need else None
         _check(L.ecf8a_add(ctypes.byref(plan.c), ctypes.byref(bank), x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(x_scale),
-                           _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), ws.data_ptr(), ws.numel(),
-                           st), "ecf8a_add")
+                           _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), _ptr(ws),
+                           0 if ws is None else ws.numel(), st), "ecf8a_add")
     return out
 
 

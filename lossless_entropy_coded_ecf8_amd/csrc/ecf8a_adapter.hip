@@ -1085,16 +1085,19 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A, int first)
 uint32_t z_rows(uint32_t rank) { return rank <= 16 ? 16 : (uint32_t)round_up(rank, 32); }
 
 // How a `low` call covers the chunks: tiles of one workgroup, and the shares of
-// the width where that leaves fewer than 256 workgroups, each wave of eight keeping
-// at least one block of 64 columns.
+// the width where that leaves fewer than 256 workgroups.  More tiles read the factor
+// less often, fewer fill the card from fewer tokens.  Measured (bfloat16): 16384 x
+// 13824, rank 64: 111 us with four tiles, 153 with two, 254 with one; 8192 x 4096,
+// rank 32: 26, 35, 27, rank 64: 33, 28, 41; 4096 x 4096, rank 16: four tiles in three
+// shares 11.6 and a join, one tile unsplit 11.1.
 struct LowShape {
     uint32_t tiles, shares;
 };
 
-LowShape low_shape(const ecf8a_plan& p, uint64_t width)
+LowShape low_shape(const ecf8a_plan& p, uint32_t rank, uint64_t width)
 {
     const uint64_t used = p.adapters < p.tokens ? p.adapters : p.tokens;
-    LowShape s{p.tokens >= 16384 ? 4u : p.tokens >= 8192 ? 2u : 1u, 1};
+    LowShape s{p.tokens < 8192 ? 1u : p.tokens >= 16384 || rank <= 32 ? 4u : 2u, 1};
     const uint64_t groups = p.tokens / (kTile * s.tiles) + used;
     uint64_t shares = groups ? 256 / groups : 1;
     const uint64_t most = (width + 511) / 512;
@@ -1107,7 +1110,7 @@ uint64_t form_bytes(const ecf8a_plan& p, uint32_t rank) { return round_up(4ull *
 
 uint64_t low_bytes(const ecf8a_plan& p, uint32_t rank, uint64_t width)
 {
-    const uint64_t s = low_shape(p, width).shares;
+    const uint64_t s = low_shape(p, rank, width).shares;
     return s > 1 ? round_up(s * 4ull * p.max_slots * z_rows(rank), 256) : 0;
 }
 
@@ -1263,7 +1266,7 @@ LowArgs low_args(const PlanView& view, const ecf8a_bank& b, const Pass& s, const
 // joined, or left there for wide_kernel to add up where no form by rank row is wanted.
 void run_low(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, const Forms& forms, float* planes, hipStream_t st)
 {
-    const LowShape shape = low_shape(p, s.in);
+    const LowShape shape = low_shape(p, b.rank, s.in);
     const LowArgs A = low_args(view_of(p), b, s, forms, shape.shares > 1 ? planes : nullptr, (int)(4 / shape.tiles));
     launch_low_pass(A, b, s, dim3(p.max_chunks * (4 / shape.tiles), shape.shares, (forms.zr + 63) / 64), shape.tiles, st);
     if (shape.shares > 1 && forms.row) {
@@ -1312,7 +1315,7 @@ int run_pass(const ecf8a_plan& p, const ecf8a_bank& b, const Pass& s, Forms form
     if (!s.out) forms.slot = nullptr;
     run_low(p, b, s, forms, planes, st);
     if (s.out) {
-        const uint32_t shares = low_shape(p, s.in).shares;
+        const uint32_t shares = low_shape(p, b.rank, s.in).shares;
         launch_wide_pass(view_of(p), b, s, forms, shares > 1 && !forms.row ? planes : nullptr, shares, p.max_chunks, st);
     }
     return launch_status();
@@ -1416,7 +1419,7 @@ extern "C" uint64_t ecf8a_hidden_bytes(const ecf8a_plan* plan, uint32_t rank)
 extern "C" uint64_t ecf8a_add_bytes(const ecf8a_plan* plan, const ecf8a_bank* b)
 {
     if (!plan_ok(plan) || !b || b->rank < 1 || b->rank > ECF8A_MAX_RANK) return 0;
-    if (one_kernel(plan->tokens, *b)) return 256;
+    if (one_kernel(plan->tokens, *b)) return 0;
     return form_bytes(*plan, b->rank) + low_bytes(*plan, b->rank, b->in_features) + 256;
 }
 
@@ -1496,12 +1499,13 @@ extern "C" int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const v
     if (plan->tokens == 0) return ECF8_OK;
     rc = check_add(bank, x, ldx, x_type, x_scale, base, ld_base, out, ld_out);
     if (rc != ECF8_OK) return rc;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < ecf8a_add_bytes(plan, bank))
-        return ECF8_ERR_WORKSPACE;
+    const uint64_t need = ecf8a_add_bytes(plan, bank);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
     char* w = static_cast<char*>(workspace);
     const Pass s{x, ldx, x_type, x_scale, bank->down, bank->in_features, bank->up, bank->out_features, base, ld_base, out, ld_out};
     return run_pass(*plan, *bank, s, forms_of(*plan, bank->rank, w, hidden),
-                    reinterpret_cast<float*>(w + form_bytes(*plan, bank->rank)), static_cast<hipStream_t>(hip_stream));
+                    need ? reinterpret_cast<float*>(w + form_bytes(*plan, bank->rank)) : nullptr,
+                    static_cast<hipStream_t>(hip_stream));
 }
 
 extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* dy, uint64_t ld_dy, const void* x,

@@ -69,7 +69,7 @@ def test_add_refusals(few):
                   (ARG, dict(x=P + 1)), (ARG, dict(base=P + 1)), (ARG, dict(xs=P + 2)), (ARG, dict(base=P, out=P, ldo=50)),
                   (SIZE, dict(ldx=63)), (SIZE, dict(ldb=47)), (SIZE, dict(ldo=47)),
                   (WORKSPACE, dict(ws=None, ldx=65536, **big)), (WORKSPACE, dict(ws=P + 8, ldx=65536, **big)),
-                  (WORKSPACE, dict(n=300, ldx=65536, **big))):
+                  (WORKSPACE, dict(n=300, ldx=65536, **big))):  # 300 bytes: below any need
         assert call(**k) == rc, k
     if few:
         assert call(rank=65) == SIZE
