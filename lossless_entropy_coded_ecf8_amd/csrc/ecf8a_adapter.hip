@@ -604,22 +604,15 @@ __device__ __forceinline__ void load_factor(const uint16_t* f, int width, int r,
     }
 }
 
-// ... turned into one operand per column (lo: of a float16, the rest of it).  True if
-// one is not finite.  HALF: see wide_products.
-template <int TYPE, bool HALF>
-__device__ __forceinline__ bool turn_factor(const u32x4 w[8], u32x4 hi[8], u32x4 lo[8])
+// ... turned into one operand per column (lo: of a float16, the rest of it).
+template <int TYPE>
+__device__ __forceinline__ void turn_factor(const u32x4 w[8], u32x4 hi[8], u32x4 lo[8])
 {
     transpose8(w, hi);
     if constexpr (TYPE == kFp16) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) split8_f16(hi[j], hi[j], lo[j]);
     }
-    const bool odd = any_not_finite(hi);
-    if (HALF && odd && (threadIdx.x & 32)) {                // these lanes hold the slots of the lower halves
-#pragma unroll
-        for (int j = 0; j < 8; ++j) hi[j] = finite(hi[j]);
-    }
-    return odd;
 }
 
 // One row's eight columns: base plus the results of its token, rounded once.
@@ -637,27 +630,20 @@ __device__ __forceinline__ u32x4 add_row(u32x4 base, const f32x4* acc, int i)
 
 // The products of 16 tokens with 32 rank rows at this lane's eight columns.  HALF: up
 // to 16 rank rows, whose lower bfloat16 take the upper half of the reduction slots,
-// so that one instruction does both.  odd: a factor value is not finite.
-template <int TYPE, bool HALF>
-__device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* hi, const u32x4* lo, bool odd, f32x4* acc)
+// so that one instruction does both.  CAREFUL: see any_not_finite.
+template <int TYPE, bool HALF, bool CAREFUL>
+__device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* hi, const u32x4* lo, f32x4* acc)
 {
-    const u32x4 zf = TYPE == kFp16 ? finite(zh) : zh;
+    const auto kept_finite = [](u32x4 v) {
+        asm volatile("" : "+v"(v));                         // not to be found once and kept in registers
+        return finite(v);
+    };
+    const bool lower = HALF && (threadIdx.x & 32);          // lanes that hold the lower halves' slots
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        acc[j] = mfma_bf16(zh, hi[j], acc[j]);
-        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(zf, lo[j], acc[j]);
-    }
-    if constexpr (HALF) return;
-    if (!odd) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(zl, hi[j], acc[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            u32x4 one = hi[j];                              // rare: not to be kept in registers for the next tile
-            asm volatile("" : "+v"(one));
-            acc[j] = mfma_bf16(zl, finite(one), acc[j]);
-        }
+        acc[j] = mfma_bf16(zh, CAREFUL && lower ? kept_finite(hi[j]) : hi[j], acc[j]);
+        if constexpr (!HALF) acc[j] = mfma_bf16(zl, CAREFUL ? kept_finite(hi[j]) : hi[j], acc[j]);
+        if constexpr (TYPE == kFp16) acc[j] = mfma_bf16(CAREFUL ? kept_finite(zh) : zh, lo[j], acc[j]);
     }
 }
 
@@ -711,13 +697,12 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !
     const uint16_t* f = A.f + (int64_t)(bare ? 0 : a) * A.rank * A.width;
     constexpr int KEEP = RB <= 0 ? 1 : RB;
     u32x4 hi[KEEP][8], lo[KEEP][8];
-    bool odd[KEEP] = {};
     if constexpr (RB >= 0) {
 #pragma unroll
         for (int b = 0; b < KEEP; ++b) {
             u32x4 w[8];
             load_factor<VEC>(f, A.width, RB == 0 ? 8 * (g & 1) : 32 * b + 8 * g, rank, col, w);
-            odd[b] = turn_factor<TYPE, RB == 0>(w, hi[b], lo[b]);
+            turn_factor<TYPE>(w, hi[b], lo[b]);
         }
     }
     for (int tile = 0; tile < tiles; ++tile) {
@@ -737,36 +722,44 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !
         }
         const int64_t at = (int64_t)(slot + c) * A.zr;
         f32x4 acc[8] = {};
-        if constexpr (RB == 0) {
-            u32x4 both, rest;
-            if constexpr (PLANES) {
-                sum_planes(A.planes + at + 8 * (g & 1), A.plane, A.shares, both, rest);
-                both = g < 2 ? both : rest;
-            } else {
-                both = *reinterpret_cast<const u32x4*>(A.z + at + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
-            }
-            wide_products<TYPE, true>(both, both, hi[0], lo[0], odd[0], acc);
-        } else {
-            const auto block = [&](int b, int keep) {
-                u32x4 zh, zl;
-                if constexpr (PLANES) sum_planes(A.planes + at + 32 * b + 8 * g, A.plane, A.shares, zh, zl);
-                else {
-                    zh = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g);
-                    zl = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g + A.plane);
+        const auto tile_products = [&](auto careful) {
+            if constexpr (RB == 0) {
+                u32x4 both, rest;
+                if constexpr (PLANES) {
+                    sum_planes(A.planes + at + 8 * (g & 1), A.plane, A.shares, both, rest);
+                    both = g < 2 ? both : rest;
+                } else {
+                    both = *reinterpret_cast<const u32x4*>(A.z + at + 8 * (g & 1) + (g < 2 ? 0 : A.plane));
                 }
-                wide_products<TYPE, false>(zh, zl, hi[keep], lo[keep], odd[keep], acc);
-            };
-            if constexpr (RB > 0) {
+                wide_products<TYPE, true, careful>(both, both, hi[0], lo[0], acc);
+            } else {
+                const auto block = [&](int b, int keep) {
+                    u32x4 zh, zl;
+                    if constexpr (PLANES) sum_planes(A.planes + at + 32 * b + 8 * g, A.plane, A.shares, zh, zl);
+                    else {
+                        zh = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g);
+                        zl = *reinterpret_cast<const u32x4*>(A.z + at + 32 * b + 8 * g + A.plane);
+                    }
+                    wide_products<TYPE, false, careful>(zh, zl, hi[keep], lo[keep], acc);
+                };
+                if constexpr (RB > 0) {
 #pragma unroll
-                for (int b = 0; b < RB; ++b) block(b, b);
-            } else {
-                for (int b = 0; b < (A.zr + 31) / 32; ++b) {
-                    u32x4 w[8];
-                    load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, w);
-                    odd[0] = turn_factor<TYPE, false>(w, hi[0], lo[0]);
-                    block(b, 0);
+                    for (int b = 0; b < RB; ++b) block(b, b);
+                } else {
+                    for (int b = 0; b < (A.zr + 31) / 32; ++b) {
+                        u32x4 w[8];
+                        load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, w);
+                        turn_factor<TYPE>(w, hi[0], lo[0]);
+                        block(b, 0);
+                    }
                 }
             }
+        };
+        tile_products(std::false_type{});
+        if (any_not_finite<8>(acc)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
+            tile_products(std::true_type{});
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -876,22 +869,30 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(FewArgs A)
         const int col = strip + 8 * c;
         f32x4 sum[8] = {};
         u32x4 hi[8], lo[8], row[4] = {base[0], base[1], base[2], base[3]};
-        bool odd = turn_factor<TYPE, RT == 1>(w, hi, lo);
+        turn_factor<TYPE>(w, hi, lo);
         if (strip + WAVES * kStrip < A.width) fetch(col + WAVES * kStrip);
-        if constexpr (RT == 1) {
-            const u32x4 both = *reinterpret_cast<const u32x4*>(&zs[g >> 1][c][8 * (g & 1)]);
-            wide_products<TYPE, true>(both, both, hi, lo, odd, sum);
-        } else {
+        const auto strip_products = [&](auto careful) {
+            if constexpr (RT == 1) {
+                const u32x4 both = *reinterpret_cast<const u32x4*>(&zs[g >> 1][c][8 * (g & 1)]);
+                wide_products<TYPE, true, careful>(both, both, hi, lo, sum);
+            } else {
 #pragma unroll
-            for (int b = 0; b < RT / 2; ++b) {
-                if (b) {
-                    u32x4 more[8];
-                    load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, more);
-                    odd = turn_factor<TYPE, false>(more, hi, lo);
+                for (int b = 0; b < RT / 2; ++b) {
+                    if (b || (careful && RT > 2)) {
+                        u32x4 more[8];
+                        load_factor<VEC>(f, A.width, 32 * b + 8 * g, rank, col, more);
+                        turn_factor<TYPE>(more, hi, lo);
+                    }
+                    wide_products<TYPE, false, careful>(*reinterpret_cast<const u32x4*>(&zs[0][c][32 * b + 8 * g]),
+                                                        *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, sum);
                 }
-                wide_products<TYPE, false>(*reinterpret_cast<const u32x4*>(&zs[0][c][32 * b + 8 * g]),
-                                           *reinterpret_cast<const u32x4*>(&zs[1][c][32 * b + 8 * g]), hi, lo, odd, sum);
             }
+        };
+        strip_products(std::false_type{});
+        if (any_not_finite<8>(sum)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = f32x4{0, 0, 0, 0};
+            strip_products(std::true_type{});
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1011,16 +1012,7 @@ __global__ __launch_bounds__(kThreads, (RT == 1 ? 4 : 3) - (TYPE == kFp16)) void
         }
     };
     unit_sum(std::false_type{});
-    // An infinity among the rows or Z has met lower halves of 0: only then once more,
-    // keeping those products finite.
-    float test = 0.0f;
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) test = __builtin_fmaf(acc[r][j][i], 0.0f, test);
-    if (__ballot(test != test)) {
+    if (any_not_finite<8 * RT>(&acc[0][0])) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll

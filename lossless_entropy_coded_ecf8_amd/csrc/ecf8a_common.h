@@ -135,16 +135,17 @@ __device__ __forceinline__ u32x4 finite(u32x4 v)
     return v;
 }
 
-// Whether any lane of the wave has an infinity or a NaN in its eight operands.
-__device__ __forceinline__ bool any_not_finite(const u32x4 v[8])
+// Whether a result of the wave is not finite: then, and only then, infinities may
+// have met lower halves, and the products are done again with `finite` in place.
+template <int N>
+__device__ __forceinline__ bool any_not_finite(const f32x4* acc)
 {
-    bool odd = false;
+    float test = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) odd |= (v[j][i] & 0x7F80u) == 0x7F80u || (v[j][i] & 0x7F800000u) == 0x7F800000u;
-    __builtin_amdgcn_sched_barrier(0);
-    return __ballot(odd) != 0;
+        for (int i = 0; i < 4; ++i) test = __builtin_fmaf(acc[j][i], 0.0f, test);
+    return __ballot(test != test) != 0;
 }
 
 // Eight rows of eight 16-bit columns, one row in each w[q], turned into one
