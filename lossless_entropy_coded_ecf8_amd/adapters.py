@@ -134,7 +134,7 @@ def _rows(t, what: str, rows: int, cols: int, dtypes, device) -> int:
         raise ValueError("%s is on %s, the index on %s" % (what, t.device, device))
     ld, step = t.stride()
     if rows <= 1:
-        ld = cols if ld < cols else ld
+        ld = cols                                       # no second row: whatever its stride says
     if (cols > 1 and step != 1) or ld < cols:
         raise ValueError("%s must have contiguous rows that do not overlap (strides %s)" % (what, t.stride()))
     return ld
@@ -207,7 +207,9 @@ class AdapterPlan:
         if self._event is None:
             self._event = torch.cuda.Event()
             self._event.record(self._made_on or torch.cuda.ExternalStream(self._handle, device=self.device))
-        _stream_of(self.device, stream).wait_event(self._event)
+        stream = _stream_of(self.device, stream)
+        stream.wait_event(self._event)
+        self.workspace.record_stream(stream)            # not handed on before that stream is done with it
 
     def hidden(self, rank: int, stream=None) -> torch.Tensor:
         """A buffer that carries h from adapter_add to adapter_grads (opaque bytes)."""
@@ -436,7 +438,9 @@ class GradClip:
         """Scales every gradient by min(1, max_norm / (norm + 1e-6)) and returns the norm before (0-d float32)."""
         with _Launch(self.device, stream) as st:
             if st != self._handle and not torch.cuda.is_current_stream_capturing():
-                _stream_of(self.device, stream).wait_event(self._event)
+                other = _stream_of(self.device, stream)
+                other.wait_event(self._event)
+                self.workspace.record_stream(other)
             norm = _empty((), torch.float32, self.device, stream)
             _check(_lib().ecf8a_clip_run(ctypes.byref(self.c), float(max_norm), norm.data_ptr(), st),
                    "ecf8a_clip_run")

@@ -134,6 +134,14 @@ def test_more_than_two_to_the_31_elements():
     torch.cuda.empty_cache()
 
 
+def test_one_row_of_any_stride():
+    d = dev()
+    dy, w, s = make(1, 96, 64, torch.bfloat16, d, seed=8)
+    want = E.linear_fp8_input_grad(dy, w, s)
+    for stride in (1, 97, 1 << 24):
+        assert torch.equal(E.linear_fp8_input_grad(dy.as_strided((1, 96), (stride, 1)), w, s), want)
+
+
 def test_refusals():
     d = dev()
     dy, w, s = make(8, 48, 64, torch.bfloat16, d)
