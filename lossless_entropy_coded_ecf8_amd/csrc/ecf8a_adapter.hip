@@ -20,7 +20,8 @@
 //
 // Tokens are taken in the plan's order: sorted by adapter, each group padded
 // to 16 slots, cut into chunks of at most 64 slots that share one adapter.  Few
-// tokens take one kernel that does `low` and `wide` for 16 of them (few_kernel).
+// tokens need no plan (find_group); with small factors they take one kernel that
+// does `low` and `wide` for 16 of them (few_kernel).
 #include "ecf8a_common.h"
 
 #include <type_traits>
@@ -111,7 +112,7 @@ __device__ __forceinline__ void block_scan3(int v[3], int total[3], i32x4* lds)
 // its tokens 64 at a time, each behind those before it.  So slots depend on the
 // index alone, and every sum over a group has a fixed order.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restrict__ index, int index_bytes, int tokens,
-                                                            int adapters, int waves, int unit_slots, int max_chunks,
+                                                            int adapters, int waves, int unit_slots,
                                                             PlanView p)
 {
     __shared__ int lds[kPlanLds];
@@ -460,7 +461,7 @@ __device__ __forceinline__ void sum_waves(const f32x4* acc, f32x4* red, F done)
 
 // One workgroup: up to NT tiles of one chunk, 16 RT rank rows, one of gridDim.y
 // shares of the width.  Its waves take 64-column blocks in turn and meet in LDS.
-// tokens_of(n): this lane's token of tile n.
+// token_of(n): this lane's token of tile n.
 template <int TYPE, int VT, int RT, int NT, int WAVES, bool VEC, typename F>
 __device__ __forceinline__ void low_body(const LowArgs& A, int a, int slot0, int tokens, f32x4* red, F token_of)
 {
@@ -682,13 +683,13 @@ __device__ __forceinline__ void sum_planes(const float* z, int64_t plane, int sh
 }
 
 template <int TYPE, int RB, bool VEC, bool PLANES>
-__global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !PLANES) ? 4 : 3) : 2) void wide_kernel(WideArgs A)
+__device__ __forceinline__ void wide_rows(const WideArgs& A, int group)
 {
-    const int id = blockIdx.x / A.groups;                   // neighbouring workgroups: the same rows, next columns
+    const int id = group / A.groups;                        // neighbouring workgroups: the same rows, next columns
     const i32x4 chunk = A.plan.chunks[id];                  // there for every id, and sent for with the count
     if (id >= A.plan.head[0]) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int a = chunk[0], col = ((blockIdx.x - id * A.groups) * 4 + wave) * kStrip + 8 * c;
+    const int a = chunk[0], col = ((group - id * A.groups) * 4 + wave) * kStrip + 8 * c;
     if (col - 8 * c >= A.width) return;
     const bool bare = a >= A.adapters;
     if (bare && A.base == A.out) return;
@@ -765,6 +766,12 @@ __global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !
         for (int i = 0; i < 4; ++i)
             if (tok[i] >= 0) store_cols<VEC>(A.out + tok[i] * A.ld_out, col, A.width, add_row<TYPE>(base[i], acc, i));
     }
+}
+
+template <int TYPE, int RB, bool VEC, bool PLANES>
+__global__ __launch_bounds__(kThreads, TYPE == kBf16 ? (RB == 0 || (RB == 1 && !PLANES) ? 4 : 3) : 2) void wide_kernel(WideArgs A)
+{
+    wide_rows<TYPE, RB, VEC, PLANES>(A, blockIdx.x);
 }
 
 // ------------------------------------------------------------- few tokens: both at once
@@ -930,15 +937,15 @@ struct FactorArgs {
 // adapter of one unit is written at once, others leave float32 partial sums that
 // sum_kernel joins in order.
 template <int TYPE, int RT, int HALVES, bool VEC>
-__global__ __launch_bounds__(kThreads, (RT == 1 ? 4 : 3) - (TYPE == kFp16)) void factor_kernel(FactorArgs A)
+__device__ __forceinline__ void factor_unit(const FactorArgs& A, int group, int at_unit, int rank0)
 {
-    const i32x4 unit = A.plan.units[blockIdx.y];
-    if ((int)blockIdx.y >= A.plan.head[2]) return;
-    const bool second = (int)blockIdx.x >= A.groups;
+    const i32x4 unit = A.plan.units[at_unit];
+    if (at_unit >= A.plan.head[2]) return;
+    const bool second = group >= A.groups;
     const FactorSide& S = A.side[second];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int strip = (blockIdx.x - (second ? A.groups : 0)) * (4 / HALVES) + wave / HALVES;
-    const int col = strip * kStrip + 8 * c, r0 = blockIdx.z * 64 + wave % HALVES * 32;
+    const int strip = (group - (second ? A.groups : 0)) * (4 / HALVES) + wave / HALVES;
+    const int col = strip * kStrip + 8 * c, r0 = rank0 + wave % HALVES * 32;
     if (strip * kStrip >= S.width || r0 >= A.zr) return;
     f32x4 acc[RT][8] = {};
     i32x4 tok[2];
@@ -1035,11 +1042,34 @@ __global__ __launch_bounds__(kThreads, (RT == 1 ? 4 : 3) - (TYPE == kFp16)) void
                                 u32x4{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]), pack2<TYPE>(v[4], v[5]),
                                       pack2<TYPE>(v[6], v[7])});
             } else if (row < A.zr) {
-                float* p = S.part + ((int64_t)blockIdx.y * A.zr + row) * S.stride + col;
+                float* p = S.part + ((int64_t)at_unit * A.zr + row) * S.stride + col;
                 *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
         }
+}
+
+constexpr int factor_waves(int type, int rt) { return (rt == 1 ? 4 : 3) - (type == kFp16); }   // per SIMD
+
+template <int TYPE, int RT, int HALVES, bool VEC>
+__global__ __launch_bounds__(kThreads, factor_waves(TYPE, RT)) void factor_kernel(FactorArgs A)
+{
+    factor_unit<TYPE, RT, HALVES, VEC>(A, blockIdx.x, blockIdx.y, blockIdx.z * 64);
+}
+
+// dx and both factors' gradients need only z and h: one launch for both, the
+// workgroups of one spread evenly among those of the other, so that rows on their way
+// in and out and waits for rows to be multiplied overlap (whole calls: 4096 tokens of
+// 4096 and 4096 at rank 16 103 -> 96 us, 16384 of 5120 and 13824 at rank 64 650 -> 642).
+// Over rank 64 `wide` reads its factor again for each 64 rank rows and stays apart.
+template <int TYPE, int RB, int RT, int HALVES, bool VEC>
+__global__ __launch_bounds__(kThreads, factor_waves(TYPE, RT)) void wide_and_factor_kernel(WideArgs W, FactorArgs F, uint32_t factor_groups,
+                                                                                         uint32_t across)
+{
+    const uint32_t before = (uint32_t)((uint64_t)blockIdx.x * factor_groups / gridDim.x);
+    const uint32_t until = (uint32_t)((uint64_t)(blockIdx.x + 1) * factor_groups / gridDim.x);
+    if (until > before) factor_unit<TYPE, RT, HALVES, VEC>(F, before % across, before / across, 0);
+    else wide_rows<TYPE, RB, VEC, false>(W, blockIdx.x - before);
 }
 
 // The gradients of adapters with no unit (0) or several (their partial sums).
@@ -1284,13 +1314,18 @@ void launch_wide(const WideArgs& A, dim3 grid, hipStream_t st)
     else launch_wide_z<TYPE, VEC, false>(A, grid, st);
 }
 
+WideArgs wide_args(const PlanView& view, const ecf8a_bank& b, const Pass& s, const Forms& forms, const float* planes, uint32_t shares)
+{
+    return WideArgs{view, forms.slot, planes, forms.plane, (int)shares, static_cast<const uint16_t*>(s.f2), b.ranks,
+                    static_cast<const uint16_t*>(s.base), (int64_t)s.ld_base, static_cast<uint16_t*>(s.out),
+                    (int64_t)s.ld_out, (int)s.width, (int)b.rank, forms.zr, (int)b.adapters,
+                    (int)((s.width + 4 * kStrip - 1) / (4 * kStrip))};
+}
+
 void launch_wide_pass(const PlanView& view, const ecf8a_bank& b, const Pass& s, const Forms& forms, const float* planes,
                       uint32_t shares, uint32_t chunks, hipStream_t st)
 {
-    const WideArgs A{view, forms.slot, planes, forms.plane, (int)shares, static_cast<const uint16_t*>(s.f2), b.ranks,
-                     static_cast<const uint16_t*>(s.base), (int64_t)s.ld_base, static_cast<uint16_t*>(s.out),
-                     (int64_t)s.ld_out, (int)s.width, (int)b.rank, forms.zr, (int)b.adapters,
-                     (int)((s.width + 4 * kStrip - 1) / (4 * kStrip))};
+    const WideArgs A = wide_args(view, b, s, forms, planes, shares);
     const dim3 grid((uint32_t)A.groups * chunks);
     const bool vec = vec_wide(s);
     if (b.type == ECF8A_BF16) vec ? launch_wide<kBf16, true>(A, grid, st) : launch_wide<kBf16, false>(A, grid, st);
@@ -1324,12 +1359,31 @@ void launch_factor(const FactorArgs& A, dim3 grid, hipStream_t st)
 // Columns of a factor_kernel workgroup.
 uint32_t factor_columns(int zr) { return zr <= 32 ? 4 * kStrip : 2 * kStrip; }
 
-int run_factor(const ecf8a_plan& p, const ecf8a_bank& b, const FactorArgs& A, hipStream_t st)
+template <int TYPE, bool VEC>
+void launch_both(const WideArgs& W, const FactorArgs& F, uint32_t wide_groups, uint32_t factor_groups, uint32_t across, hipStream_t st)
+{
+    const uint32_t grid = wide_groups + factor_groups;
+    if (F.zr <= 16) wide_and_factor_kernel<TYPE, 0, 1, 1, VEC><<<grid, kThreads, 0, st>>>(W, F, factor_groups, across);
+    else if (F.zr <= 32) wide_and_factor_kernel<TYPE, 1, 2, 1, VEC><<<grid, kThreads, 0, st>>>(W, F, factor_groups, across);
+    else wide_and_factor_kernel<TYPE, 2, 2, 2, VEC><<<grid, kThreads, 0, st>>>(W, F, factor_groups, across);
+}
+
+// The factors' gradients; dx: its `wide` pass, if it is still to be done.
+int run_factor(const ecf8a_plan& p, const ecf8a_bank& b, const FactorArgs& A, const WideArgs* dx, bool dx_vec, hipStream_t st)
 {
     bool vec = true;
     for (const FactorSide& s : A.side) vec = vec && vec16(s.v, s.ldv) && vec16(s.grad, s.width);
     const uint32_t columns = factor_columns(A.zr), groups = A.groups + (A.side[1].stride + columns - 1) / columns;
-    if (p.tokens) {
+    if (dx) {
+        const bool both = vec && dx_vec;
+        const uint32_t wide_groups = (uint32_t)dx->groups * p.max_chunks, factor_groups = groups * p.max_units;
+        if (b.type == ECF8A_BF16)
+            both ? launch_both<kBf16, true>(*dx, A, wide_groups, factor_groups, groups, st)
+                 : launch_both<kBf16, false>(*dx, A, wide_groups, factor_groups, groups, st);
+        else
+            both ? launch_both<kFp16, true>(*dx, A, wide_groups, factor_groups, groups, st)
+                 : launch_both<kFp16, false>(*dx, A, wide_groups, factor_groups, groups, st);
+    } else if (p.tokens) {
         const dim3 grid(groups, p.max_units, (A.zr + 63) / 64);
         if (b.type == ECF8A_BF16) vec ? launch_factor<kBf16, true>(A, grid, st) : launch_factor<kBf16, false>(A, grid, st);
         else vec ? launch_factor<kFp16, true>(A, grid, st) : launch_factor<kFp16, false>(A, grid, st);
@@ -1396,7 +1450,7 @@ extern "C" int ecf8a_plan_prepare(const void* index, uint32_t index_bytes, uint6
     if (waves > kPlanThreads / 64) waves = kPlanThreads / 64;
     if (waves < 1) return ECF8_ERR_SIZE;
     plan_kernel<<<1, kPlanThreads, 0, static_cast<hipStream_t>(hip_stream)>>>(
-        index, (int)index_bytes, (int)tokens, (int)adapters, waves, (int)p.unit_slots, (int)p.max_chunks, view_of(p));
+        index, (int)index_bytes, (int)tokens, (int)adapters, waves, (int)p.unit_slots, view_of(p));
     const int rc = launch_status();
     if (rc == ECF8_OK) *plan = p;
     return rc;
@@ -1525,9 +1579,13 @@ extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const
     const uint64_t fb = form_bytes(*plan, bank->rank);
     void* const z_row = d_down ? w + fb : nullptr;
     float* const scratch = reinterpret_cast<float*>(w + 3 * fb);
+    const Pass s{dy, ld_dy, bank->type, nullptr, bank->up, N, bank->down, K, dx_base, ld_dx_base, dx, ld_dx};
+    const Forms zf = forms_of(*plan, bank->rank, w, z_row);
+    // dx waits for the factors' launch where both are wanted and `wide` keeps the factor in registers.
+    const bool later = plan->tokens && dx && d_down && bank->rank <= 64 && !one_kernel(plan->tokens, *bank);
     if (plan->tokens && (dx || d_down)) {
-        const Pass s{dy, ld_dy, bank->type, nullptr, bank->up, N, bank->down, K, dx_base, ld_dx_base, dx, ld_dx};
-        rc = run_pass(*plan, *bank, s, forms_of(*plan, bank->rank, w, z_row), scratch, st);
+        if (later) run_low(*plan, *bank, s, zf, scratch, st);
+        else rc = run_pass(*plan, *bank, s, zf, scratch, st);
         if (rc == ECF8_OK && d_down && !hidden) {
             const Pass h{x, ldx, bank->type, nullptr, bank->down, K, bank->up, N, nullptr, 0, nullptr, 0};
             rc = run_pass(*plan, *bank, h, forms_of(*plan, bank->rank, nullptr, w + 2 * fb), scratch, st);
@@ -1543,5 +1601,6 @@ extern "C" int ecf8a_grads(const ecf8a_plan* plan, const ecf8a_bank* bank, const
                        {{z.row, static_cast<const uint16_t*>(x), (int64_t)ldx, static_cast<uint16_t*>(d_down), scratch, (int)K, (int)sk},
                         {h, static_cast<const uint16_t*>(dy), (int64_t)ld_dy, static_cast<uint16_t*>(d_up), part_up, (int)N, (int)sn}},
                        bank->ranks, z.plane, (int)bank->rank, z.zr, (int)bank->adapters, (int)((sk + columns - 1) / columns)};
-    return run_factor(*plan, *bank, A, st);
+    const WideArgs W = wide_args(view_of(*plan), *bank, s, zf, nullptr, 1);
+    return run_factor(*plan, *bank, A, later ? &W : nullptr, vec_wide(s), st);
 }

@@ -117,6 +117,27 @@ def test_grads_against_formula(case, dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,K,N,R_", [(700, 264, 136, 16), (700, 65, 130, 9), (900, 512, 1032, 32), (900, 131, 70, 20),
+                                      (1100, 136, 520, 64), (1100, 77, 129, 50), (600, 72, 136, 100)])
+def test_gradients_together_and_apart(T, K, N, R_, dtype):
+    """dx and the factors' gradients asked for together are bit for bit what each is alone, and meet the formula."""
+    d = dev()
+    s = make(d, T, K, N, R_, 5, "tokens", dtype, ranks=True, seed=T + R_)
+    s["index"][s["index"] == 3] = -1                            # an adapter without a token
+    plan = E.AdapterPlan(s["index"], 5)
+    args = (s["dy"], s["x"], s["down"], s["up"], s["scaling"], plan)
+    kw = dict(ranks=s["ranks"], dx_base=s["dx_base"])
+    dx, d_down, d_up = E.adapter_grads(*args, **kw)
+    alone, none, _ = E.adapter_grads(*args, want=(True, False), **kw)
+    _, down, up = E.adapter_grads(*args, want=(False, True), ranks=s["ranks"])
+    assert none is None
+    want = reference(s, True)
+    for name, a, b in (("dx", dx, alone), ("d_down", d_down, down), ("d_up", d_up, up)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)), name
+        R.check(a, want[name], name)
+
+
 # --------------------------------------------------------------- both ways of adding
 
 @pytest.mark.parametrize("case", [(1, 256, 128, 4, 3), (37, 2048, 1024, 16, 5), (200, 8192, 520, 33, 40),
