@@ -1059,8 +1059,9 @@ __global__ __launch_bounds__(kThreads, factor_waves(TYPE, RT)) void factor_kerne
 
 // dx and both factors' gradients need only z and h: one launch for both, the
 // workgroups of one spread evenly among those of the other, so that rows on their way
-// in and out and waits for rows to be multiplied overlap (whole calls: 4096 tokens of
-// 4096 and 4096 at rank 16 103 -> 96 us, 16384 of 5120 and 13824 at rank 64 650 -> 642).
+// in and out and waits for rows to be multiplied overlap: 4096 tokens of 4096 and 4096
+// at rank 16 take 28 us instead of 17 + 14; 16384 of 5120 and 13824 at rank 64 take
+// 272 both ways, but for the launch between (whole calls: 103 -> 97, 650 -> 642).
 // Over rank 64 `wide` reads its factor again for each 64 rank rows and stays apart.
 template <int TYPE, int RB, int RT, int HALVES, bool VEC>
 __global__ __launch_bounds__(kThreads, factor_waves(TYPE, RT)) void wide_and_factor_kernel(WideArgs W, FactorArgs F, uint32_t factor_groups,
