@@ -648,18 +648,6 @@ __device__ __forceinline__ void wide_products(u32x4 zh, u32x4 zl, const u32x4* h
     }
 }
 
-// One wave: 128 columns of one chunk.  A lane's eight columns are consecutive
-// (column 8c + j goes to the j-th instruction), so that the factor's rows are
-// read, and the result's rows read and written, 16 bytes at a time, and no LDS
-// is used.  RB: blocks of 32 rank rows kept in registers for the whole chunk
-// (0: up to 16 rows; -1: any number, read again for each 16 tokens).
-//
-// Bound by the rows' way in and out.  What keeps that busy is many waves rather
-// than many loads of each: with the rows of all four tiles sent for at once a wave
-// holds 158 to 255 registers, and 8192 tokens x 14336 columns at rank 32 take 108
-// us, 16384 x 13824 at rank 64 take 338; tile by tile 93 and 222 (5.1 and 4.1
-// TB/s).  The result is stored past the caches, which are left to the base rows
-// (2048 x 8192 at rank 16: 17 -> 13 us).
 // Eight rank rows of one slot from the shares' sums, added in order.
 __device__ __forceinline__ void sum_planes(const float* z, int64_t plane, int shares, u32x4& zh, u32x4& zl)
 {
@@ -682,6 +670,21 @@ __device__ __forceinline__ void sum_planes(const float* z, int64_t plane, int sh
     split8(s0, s1, zh, zl);
 }
 
+// One wave: 128 columns of one chunk.  A lane's eight columns are consecutive
+// (column 8c + j goes to the j-th instruction), so that the factor's rows are
+// read, and the result's rows read and written, 16 bytes at a time, and no LDS
+// is used.  RB: blocks of 32 rank rows kept in registers for the whole chunk
+// (0: up to 16 rows; -1: any number, read again for each 16 tokens).
+//
+// Bound by the rows' way in and out.  What keeps that busy is many waves rather
+// than many loads of each: with the rows of all four tiles sent for at once a wave
+// holds 158 to 255 registers, and 8192 tokens x 14336 columns at rank 32 take 108
+// us, 16384 x 13824 at rank 64 take 338; tile by tile 88 and 188 (5.3 and 4.8
+// TB/s).  The result is stored past the caches, which are left to the base rows
+// (2048 x 8192 at rank 16: 17 -> 13 us).
+// Workgroups run along the rows, whatever die each falls on: columns kept to a die,
+// so that its cache holds their part of the factor, take 94 us at 8192 x 14336 and
+// 204 at 16384 x 13824; chunks of rows kept to a die 92 and 197.
 template <int TYPE, int RB, bool VEC, bool PLANES>
 __device__ __forceinline__ void wide_rows(const WideArgs& A, int group)
 {
