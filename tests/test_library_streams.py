@@ -1,0 +1,153 @@
+"""How the operators of include/ecf8a.h order streams, without a GPU: stand-ins for torch's streams and events, and for
+the library."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+from lossless_entropy_coded_ecf8_amd import adapters as A
+
+DEV = torch.device("cuda", 0)
+
+
+class Stream:
+    def __init__(self, handle, name, device=DEV):
+        self.cuda_stream, self.name, self.device, self.waits, self.capturing = handle, name, device, [], False
+
+    def wait_event(self, event):
+        self.waits.append(event)
+
+
+class Event:
+    made = 0
+
+    def __init__(self):
+        self.on = None
+        Event.made += 1
+
+    def record(self, stream):
+        self.on = stream
+
+
+class Memory:
+    """A device buffer: who else uses it."""
+
+    def __init__(self):
+        self.users = []
+
+    def record_stream(self, stream):
+        self.users.append(stream)
+
+    def data_ptr(self):
+        return 1 << 40
+
+    def numel(self):
+        return 1 << 30
+
+
+class Operand:
+    """A tensor on the GPU, as far as the argument checks look at one."""
+
+    def __init__(self, n, dtype):
+        self.n, self.dtype, self.device, self.is_cuda = n, dtype, DEV, True
+
+    def dim(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.n
+
+    def data_ptr(self):
+        return 1 << 41
+
+    def record_stream(self, stream):
+        pass
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """The default stream (handle 0) current on one device; a stream made from handle 0 is a new one, as torch's is."""
+    g = types.SimpleNamespace(default=Stream(0, "default"), calls=[])
+    g.current = g.default
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, g.current = g.current, s
+        yield
+        g.current = before
+
+    def call(name):
+        return lambda *a: g.calls.append(name) or 0
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: g.current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: g.current.capturing)
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle or 999, "from a handle"))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: g.current.cuda_stream, raising=False)
+    monkeypatch.setattr(A, "_empty", lambda *a: Memory())
+    lib = types.SimpleNamespace(ecf8a_plan_bytes=lambda *a: 256, ecf8a_plan_prepare=call("plan"),
+                                ecf8a_clip_bytes=lambda *a: 256, ecf8a_clip_prepare=call("clip_prepare"), ecf8a_clip_run=call("clip_run"))
+    monkeypatch.setattr(A, "_lib", lambda: lib)
+    return g
+
+
+def use(plan, gpu, stream=None):
+    """What a call does that uses the plan on `stream`."""
+    plan._order((stream or gpu.current).cuda_stream, stream)
+
+
+def test_a_plan_of_the_default_stream_is_waited_for(gpu):
+    """The event lies on the stream that groups, also where that is the default one, whose handle is 0."""
+    plan = A.AdapterPlan(Operand(10, torch.int32), 2)
+    use(plan, gpu)
+    side = Stream(5, "side")
+    use(plan, gpu, side)
+    assert gpu.default.waits == [] and [e.on for e in side.waits] == [gpu.default] and plan.workspace.users == [side]
+
+
+def test_a_plan_of_the_current_side_stream_is_waited_for(gpu):
+    maker, side = Stream(5, "maker"), Stream(6, "side")
+    with torch.cuda.stream(maker):
+        plan = A.AdapterPlan(Operand(10, torch.int32), 2)
+        use(plan, gpu)
+    use(plan, gpu)
+    use(plan, gpu, side)
+    assert maker.waits == [] and [e.on for e in gpu.default.waits + side.waits] == [maker, maker]
+
+
+def test_another_thread_sees_the_event_only_once_it_is_recorded(gpu, monkeypatch):
+    plan = A.AdapterPlan(Operand(10, torch.int32), 2)
+    other = Stream(6, "other thread's")
+
+    def record(event, stream):
+        monkeypatch.setattr(Event, "record", lambda e, s: setattr(e, "on", s))
+        use(plan, gpu, other)                                     # in the middle of this thread's record
+        event.on = stream
+
+    monkeypatch.setattr(Event, "record", record)
+    use(plan, gpu, Stream(5, "side"))
+    assert [e.on for e in other.waits] == [gpu.default]
+
+
+def test_captured_calls_and_captured_plans(gpu):
+    """What counts is whether the launch stream is captured, not whether the current one is."""
+    plan = A.AdapterPlan(Operand(10, torch.int32), 2)
+    side, eager = Stream(5, "side"), Stream(6, "eager")
+    side.capturing = True
+    use(plan, gpu, side)                                          # captured: no wait
+    with torch.cuda.stream(side):
+        captured = A.AdapterPlan(Operand(10, torch.int32), 2)
+        use(plan, gpu, eager)                                     # not captured, beside a capture
+    use(captured, gpu, eager)                                     # filled by the replay, which the caller orders
+    assert side.waits == [] and [e.on for e in eager.waits] == [gpu.default]
+    with torch.cuda.stream(Stream(7, "maker")) as _:
+        maker, plan = gpu.current, A.AdapterPlan(Operand(10, torch.int32), 2)
+    maker.capturing = True                                        # an event of it would be the capture's
+    with pytest.raises(RuntimeError):
+        use(plan, gpu, eager)
