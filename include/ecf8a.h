@@ -211,10 +211,11 @@ uint64_t ecf8a_clip_bytes(const ecf8a_grad* grads, uint32_t count);
  * for all) and puts their list into the workspace with one host-to-device copy
  * on hip_stream.  No grad or out may overlap another tensor's, and a grad that
  * is not its own out must not overlap it.  The plan stays valid while the
- * workspace and the tensors do.
- * Errors: ECF8_ERR_ARG (NULL with n > 0, misaligned, overlapping),
- * ECF8_ERR_UNSUPPORTED (type), ECF8_ERR_SIZE, ECF8_ERR_WORKSPACE,
- * ECF8_ERR_HIP. */
+ * workspace and the tensors do.  hip_stream must not be being captured: the
+ * copy reads a list that is gone when this returns.
+ * Errors: ECF8_ERR_ARG (NULL with n > 0, misaligned, overlapping, a stream
+ * that is being captured), ECF8_ERR_UNSUPPORTED (type), ECF8_ERR_SIZE,
+ * ECF8_ERR_WORKSPACE, ECF8_ERR_HIP. */
 int ecf8a_clip_prepare(const ecf8a_grad* grads, uint32_t count, uint32_t type, void* workspace,
                        uint64_t workspace_bytes, void* hip_stream, ecf8a_clip_plan* plan);
 

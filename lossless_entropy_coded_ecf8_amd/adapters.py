@@ -420,7 +420,8 @@ class GradClip:
 
     grads: contiguous tensors of one type (bfloat16, float16 or float32) on one GPU, none overlapping another; out:
     where the scaled values go (default: in place).  The list is put on the GPU once and run() reads the gradients'
-    values anew each time, so a plan serves as long as the tensors stay where they are.
+    values anew each time, so a plan serves as long as the tensors stay where they are.  It has to be made before a
+    capture (the list comes from the host); run() can be captured.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None, stream=None):
@@ -445,6 +446,8 @@ class GradClip:
         L = _lib()
         need = L.ecf8a_clip_bytes(arr, len(self.grads))
         with _Launch(self.device, stream) as st:
+            if _capturing(stream):
+                raise RuntimeError("a GradClip cannot be made while its stream is captured: make it before, and capture its run()")
             self.workspace = _empty(max(need, 256), torch.uint8, self.device, stream)
             self.c = ClipPlanA()
             _check(L.ecf8a_clip_prepare(arr, len(self.grads), _TYPES[first.dtype], self.workspace.data_ptr(),
@@ -468,7 +471,8 @@ class GradClip:
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                    stream=None) -> torch.Tensor:
-    """GradClip(grads, out).run(max_norm): for lists whose tensors change from step to step."""
+    """GradClip(grads, out).run(max_norm): for lists whose tensors change from step to step.  Not in a capture: a
+    captured step makes its GradClip beforehand."""
     return GradClip(grads, out, stream).run(max_norm, stream)
 
 
@@ -513,6 +517,7 @@ class AdapterBank(torch.nn.Module):
 
 
 def clip_adapter_grads(banks, max_norm: float, stream=None) -> torch.Tensor:
-    """clip_grad_norm over the gradients of these banks' parameters, in place; returns the norm before."""
+    """clip_grad_norm over the gradients of these banks' parameters, in place; returns the norm before.  Not in a
+    capture: there a GradClip of the same gradients, made before it, takes its place."""
     grads = [p.grad for b in banks for p in (b.down, b.up) if p.grad is not None]
     return clip_grad_norm(grads, max_norm, stream=stream)

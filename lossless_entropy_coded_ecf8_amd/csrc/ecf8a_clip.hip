@@ -267,6 +267,13 @@ extern "C" int ecf8a_clip_prepare(const ecf8a_grad* grads, uint32_t count, uint3
         for (uint64_t i = 1; i < m; ++i)
             if (ranges[i].at < ranges[i - 1].end) rc = ECF8_ERR_ARG;
     }
+    // A capture would record the copy with the address of this list, and every replay would read what lies there then.
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (rc == ECF8_OK && hipStreamIsCapturing(static_cast<hipStream_t>(hip_stream), &capture) != hipSuccess) {
+        (void)hipGetLastError();
+        rc = ECF8_ERR_HIP;
+    }
+    if (rc == ECF8_OK && capture != hipStreamCaptureStatusNone) rc = ECF8_ERR_ARG;
     if (rc == ECF8_OK && pieces &&
         hipMemcpyAsync(static_cast<char*>(workspace) + 8ull * kMaxGrid, list, sizeof(Piece) * pieces, hipMemcpyHostToDevice,
                        static_cast<hipStream_t>(hip_stream)) != hipSuccess)

@@ -1,10 +1,13 @@
 """The operators beside a compressed layer, made on one stream and used on another that was not told to wait."""
 import contextlib
+import ctypes
+import math
 
 import pytest
 import torch
 
 import lossless_entropy_coded_ecf8_amd as E
+from lossless_entropy_coded_ecf8_amd import adapters as A
 import adapter_reference as R
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +57,36 @@ def test_a_plan_behind_other_work_is_waited_for(on_default, given):
         torch.cuda.synchronize()
         for name, t in zip(("dx", "d_down", "d_up") if grads else ("out",), got):
             R.check(t, want[name], name)
+
+
+def test_a_clip_refused_in_a_capture_leaves_the_capture_whole():
+    """A GradClip made inside a capture is refused, by the library too; one made before runs in it."""
+    d = dev()
+    grads = [torch.randn(n, device=d) for n in (1000, 7, 70000)]
+    before = [g.clone() for g in grads]
+    plan = E.GradClip(grads, out=[torch.empty_like(g) for g in grads])
+    arr, c = (A.GradA * 1)(A.GradA(grads[0].data_ptr(), grads[0].data_ptr(), 1000)), A.ClipPlanA()
+    memory = torch.zeros(1 << 16, dtype=torch.uint8, device=d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError):
+            E.GradClip(grads)
+        with pytest.raises(RuntimeError):
+            E.clip_grad_norm(grads, 1.0)
+        rc = A._lib().ecf8a_clip_prepare(arr, 1, 3, memory.data_ptr(), memory.numel(), torch.cuda.current_stream().cuda_stream,
+                                         ctypes.byref(c))
+        norm = plan.run(0.5)
+    assert rc == -1 and c.pieces == 0
+    want = math.sqrt(math.fsum(float((g.double() ** 2).sum()) for g in before))
+    for _ in range(3):
+        for o in plan.out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        # one float32 rounding of the norm and one of its root; a scaled value: the factor's rounding, then its own
+        assert abs(float(norm) - want) <= 2.0 ** -23 * want
+        for g, b, o in zip(grads, before, plan.out):
+            ref = b.double() * (0.5 / (want + 1e-6))
+            assert torch.equal(g, b) and bool(((o.double() - ref).abs() <= ref.abs() * 2.0 ** -22 + 1e-44).all())
+    assert bool((memory == 0).all())

@@ -1,6 +1,9 @@
 """How the operators of include/ecf8a.h order streams, without a GPU: stand-ins for torch's streams and events, and for
 the library."""
 import contextlib
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -151,3 +154,47 @@ def test_captured_calls_and_captured_plans(gpu):
     maker.capturing = True                                        # an event of it would be the capture's
     with pytest.raises(RuntimeError):
         use(plan, gpu, eager)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_a_clip_is_not_made_in_a_capture(gpu, given):
+    """Its list comes from host memory that is gone when a replay would copy it."""
+    side = Stream(5, "side")
+    side.capturing = True
+    grads = [Operand(10, torch.float32)]
+    with contextlib.nullcontext() if given else torch.cuda.stream(side):
+        for make in (A.GradClip, lambda g, stream: A.clip_grad_norm(g, 1.0, stream=stream)):
+            with pytest.raises(RuntimeError):
+                make(grads, stream=side if given else None)
+    assert gpu.calls == []
+
+
+STAND_IN = r"""
+extern "C" int status, copies;
+int status = 0, copies = 0;
+extern "C" int hipStreamIsCapturing(void*, int* s) { *s = status; return 0; }
+extern "C" int hipMemcpyAsync(void*, const void*, unsigned long, int, void*) { ++copies; return 0; }
+"""
+
+PREPARE = r"""
+import ctypes, sys
+hip = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)           # before the library, so that it finds these functions
+from lossless_entropy_coded_ecf8_amd import adapters as A
+L, P = A._lib(), 1 << 40
+status, copies = (ctypes.c_int.in_dll(hip, n) for n in ("status", "copies"))
+got = []
+for status.value in (0, 1, 2):                                    # none, active, invalidated
+    arr, c = (A.GradA * 1)(A.GradA(P, P, 8)), A.ClipPlanA()
+    got += [L.ecf8a_clip_prepare(arr, 1, 3, P, 1 << 30, None, ctypes.byref(c)), copies.value, int(c.pieces)]
+print(got)
+"""
+
+
+def test_the_library_refuses_a_captured_stream(tmp_path):
+    """ecf8a_clip_prepare on a stream whose capture status the stand-in gives: no copy is asked for in a capture."""
+    src, so = tmp_path / "hip.cpp", tmp_path / "hip.so"
+    src.write_text(STAND_IN)
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", PREPARE, str(so)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.stdout.strip() == str([0, 1, 1, -1, 1, 0, -1, 1, 0]), (p.stdout, p.stderr[-2000:])
