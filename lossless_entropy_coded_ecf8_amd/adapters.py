@@ -14,6 +14,7 @@ adapter a adds to the weight is ``scaling[a] * up[a].T @ down[a]``.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -453,16 +454,24 @@ class GradClip:
             _check(L.ecf8a_clip_prepare(arr, len(self.grads), _TYPES[first.dtype], self.workspace.data_ptr(),
                                         self.workspace.numel(), st, ctypes.byref(self.c)),
                    "ecf8a_clip_prepare")
-            self._handle, self._event = st, torch.cuda.Event()
-            self._event.record(_stream_of(self.device, stream))
+            self._last, self._handle, self._lock = _stream_of(self.device, stream), st, threading.Lock()
 
     def run(self, max_norm: float, stream=None) -> torch.Tensor:
-        """Scales every gradient by min(1, max_norm / (norm + 1e-6)) and returns the norm before (0-d float32)."""
-        with _Launch(self.device, stream) as st:
-            if st != self._handle and not torch.cuda.is_current_stream_capturing():
-                other = _stream_of(self.device, stream)
-                other.wait_event(self._event)
-                self.workspace.record_stream(other)
+        """Scales every gradient by min(1, max_norm / (norm + 1e-6)) and returns the norm before (0-d float32).
+
+        All runs share the workspace's partial sums, so one on another stream than the last one's first waits for what
+        that stream has been given so far.  A captured run does not, and is not waited for: its replays have to be
+        ordered with the plan's other runs, and the plan kept as long as the graph."""
+        with _Launch(self.device, stream) as st, self._lock:
+            captured = st != self._handle and _capturing(stream)
+            if st != self._handle and not captured:
+                if _capturing(self._last):
+                    raise RuntimeError("the stream of the plan's last run is being captured: run it on another one before that")
+                event, other = torch.cuda.Event(), _stream_of(self.device, stream)
+                event.record(self._last)
+                other.wait_event(event)
+                self.workspace.record_stream(other)     # not handed on before that stream is done with it
+                self._last, self._handle = other, st
             norm = _empty((), torch.float32, self.device, stream)
             _check(_lib().ecf8a_clip_run(ctypes.byref(self.c), float(max_norm), norm.data_ptr(), st),
                    "ecf8a_clip_run")

@@ -90,3 +90,27 @@ def test_a_clip_refused_in_a_capture_leaves_the_capture_whole():
             ref = b.double() * (0.5 / (want + 1e-6))
             assert torch.equal(g, b) and bool(((o.double() - ref).abs() <= ref.abs() * 2.0 ** -22 + 1e-44).all())
     assert bool((memory == 0).all())
+
+
+def test_runs_of_one_clip_on_two_streams():
+    """Run after run on alternating streams, each with a larger norm allowed: all see one norm, and what stands at the end
+    is the last run's."""
+    d = dev()
+    grads = [torch.randn(1 << 20, device=d) for _ in range(8)]
+    out = [torch.empty_like(g) for g in grads]
+    plan = E.GradClip(grads, out=out)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    norms, first = [], [g.clone() for g in grads]
+    torch.cuda.synchronize()
+    for k in range(8):
+        norms.append(plan.run(1e-3 * (k + 1), stream=streams[k % 2]))
+    torch.cuda.synchronize()
+    want = math.sqrt(math.fsum(float((g.double() ** 2).sum()) for g in first))
+    for n in norms:
+        assert abs(float(n) - want) <= 2.0 ** -23 * want
+    for g, o in zip(first, out):
+        ref = g.double() * (8e-3 / (want + 1e-6))
+        # 8e-3 is rounded to float32, as are the factor and the product
+        assert bool(((o.double() - ref).abs() <= ref.abs() * (2.0 ** -22 + 2.0 ** -24) + 1e-44).all())

@@ -198,3 +198,34 @@ def test_the_library_refuses_a_captured_stream(tmp_path):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", PREPARE, str(so)], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.stdout.strip() == str([0, 1, 1, -1, 1, 0, -1, 1, 0]), (p.stdout, p.stderr[-2000:])
+
+
+def test_runs_of_one_clip_wait_for_each_other(gpu):
+    """They share the partial sums: a run waits for the last one's stream, whichever that was."""
+    plan = A.GradClip([Operand(10, torch.float32)])
+    one, two = Stream(5, "one"), Stream(6, "two")
+    plan.run(1.0)
+    assert gpu.default.waits == []
+    plan.run(1.0, stream=one)
+    plan.run(1.0, stream=one)
+    assert [e.on for e in one.waits] == [gpu.default]
+    plan.run(1.0, stream=two)
+    assert [e.on for e in two.waits] == [one]
+    plan.run(1.0)
+    assert [e.on for e in gpu.default.waits] == [two] and plan.workspace.users == [one, two, gpu.default]
+    assert gpu.calls == ["clip_prepare"] + ["clip_run"] * 5
+
+
+def test_captured_runs_of_a_clip(gpu):
+    """A captured run does not wait and is not waited for; the stream that counts is the launch stream."""
+    plan = A.GradClip([Operand(10, torch.float32)])
+    captured, eager = Stream(5, "captured"), Stream(6, "eager")
+    captured.capturing = True
+    plan.run(1.0, stream=captured)
+    with torch.cuda.stream(captured):
+        plan.run(1.0)
+        plan.run(1.0, stream=eager)                               # not captured, beside a capture
+    assert captured.waits == [] and [e.on for e in eager.waits] == [gpu.default]
+    eager.capturing = True                                        # an event of it would be the capture's
+    with pytest.raises(RuntimeError):
+        plan.run(1.0)
