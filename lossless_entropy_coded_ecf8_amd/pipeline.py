@@ -166,8 +166,10 @@ class ECF8Linear(torch.nn.Module):
 
         x: (T, in_features) in the adapters' type.  The frozen product takes x in E4M3 with x_scale (default: the
         largest magnitude of x over 448), which its gradient passes through as if it were exact; the adapters take x
-        itself.  The weight is decoded for the forward pass and again for the backward pass (weight_u8: a decoded weight
-        that is kept instead).  The weight and the bias get no gradient.  index as in forward.
+        itself.  The weight is decoded for the forward pass and again for the backward pass.  weight_u8: a decoded weight
+        that is kept instead, and holds this weight until the backward pass: one that torch has written, or a pipeline's
+        slot that has taken another layer, is refused there (a DecodePlan's own run into it is not seen).  The weight and
+        the bias get no gradient.  index as in forward.
         """
         plan = index if isinstance(index, AdapterPlan) else AdapterPlan(index, adapters.n_adapters)
         return _Adapted.apply(x, adapters.down, adapters.up, self, adapters, plan, x_scale, weight_u8)
@@ -193,15 +195,18 @@ class _Adapted(torch.autograd.Function):
         y = linear_fp8(xq, scale, w, layer.w_scale, layer.bias, out_dtype=down.dtype)
         hidden = plan.hidden(bank.rank) if ctx.needs_input_grad[1] or ctx.needs_input_grad[2] else None
         adapter_add(y, x, down, up, bank.scaling, plan, ranks=bank.ranks, out=y, hidden=hidden)
-        ctx.save_for_backward(x, down, up, bank.scaling, bank.ranks, hidden)
-        ctx.layer, ctx.plan, ctx.weight_u8 = layer, plan, weight_u8
+        # Saved as a tensor, a kept weight that is written before the backward pass is refused there.  One made in
+        # inference mode has no version to go by, and autograd does not take it.
+        plain = weight_u8 is not None and weight_u8.is_inference()
+        ctx.save_for_backward(x, down, up, bank.scaling, bank.ranks, hidden, None if plain else weight_u8)
+        ctx.layer, ctx.plan, ctx.plain_weight = layer, plan, weight_u8 if plain else None
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, down, up, scaling, ranks, hidden = ctx.saved_tensors
-        layer, w = ctx.layer, ctx.weight_u8
+        x, down, up, scaling, ranks, hidden, w = ctx.saved_tensors
+        layer, w = ctx.layer, ctx.plain_weight if w is None else w
         dy = dy.contiguous()                                  # a sum's gradient is one value, expanded
         if dy.data_ptr() % 16:
             dy = dy.clone()
@@ -243,6 +248,9 @@ class DecodePipeline:
         dev = self.layers[0].device
         self.slot_bytes = (max(l.numel for l in self.layers) + 255) // 256 * 256
         self.pool = torch.empty(slots * self.slot_bytes, dtype=torch.uint8, device=dev)
+        # .data: each slot has a version of its own, by which autograd sees that it has taken another layer.
+        self._slots = [self.pool[k * self.slot_bytes: (k + 1) * self.slot_bytes].data for k in range(slots)]
+        self._holds: List[Optional[ECF8Linear]] = [None] * slots
         self.side = torch.cuda.Stream(device=dev) if ahead > 0 else None
         self.plans: List[binding.DecodePlan] = []
         for i, layer in enumerate(self.layers):
@@ -253,8 +261,15 @@ class DecodePipeline:
         self.used = [torch.cuda.Event() for _ in self.layers]
 
     def slot(self, i: int) -> torch.Tensor:
+        return self._slots[i % self.slots][: self.layers[i].numel]
+
+    def _decode(self, i: int, stream):
+        """Decodes layer i into its slot."""
+        self.plans[i].run(stream)
         k = i % self.slots
-        return self.pool[k * self.slot_bytes: k * self.slot_bytes + self.layers[i].numel]
+        if self._holds[k] is not self.layers[i]:
+            self._holds[k] = self.layers[i]
+            torch.autograd.graph.increment_version(self._slots[k])
 
     def pool_bytes(self) -> int:
         return self.pool.numel()
@@ -279,21 +294,21 @@ class DecodePipeline:
                 index = AdapterPlan(index, first.n_adapters)
         if self.ahead == 0:
             for i in range(L):
-                self.plans[i].run(main)
+                self._decode(i, main)
                 outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
             self._check(main)
             return outs
         side = self.side
         side.wait_stream(main)          # inputs and the pool are ready on the caller's stream
         for j in range(min(self.ahead, L)):
-            self.plans[j].run(side)
+            self._decode(j, side)
             self.decoded[j].record(side)
         for i in range(L):
             j = i + self.ahead
             if j < L:
                 if j - self.slots >= 0:
                     side.wait_event(self.used[j - self.slots])
-                self.plans[j].run(side)
+                self._decode(j, side)
                 self.decoded[j].record(side)
             main.wait_event(self.decoded[i])
             outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
