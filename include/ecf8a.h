@@ -63,6 +63,7 @@ extern "C" {
 #define ECF8A_MAX_RANK 256
 #define ECF8A_MAX_TOKENS 16777216       /* 2^24 */
 #define ECF8A_FEW_TOKENS 512            /* of ecf8a_add_few */
+#define ECF8A_FEW_RANK 64               /* of ecf8a_add_few */
 #define ECF8A_MAX_FEATURES 1048576      /* 2^20 */
 
 /* ------------------------------ adapters ------------------------------- */
@@ -136,7 +137,8 @@ int ecf8a_add(const ecf8a_plan* plan, const ecf8a_bank* bank, const void* x, uin
               void* hidden, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
 /* Whether ecf8a_add_few takes this many tokens and this bank (1: at most
- * ECF8A_FEW_TOKENS tokens and rank 64) or a plan and ecf8a_add are needed (0). */
+ * ECF8A_FEW_TOKENS tokens and rank ECF8A_FEW_RANK) or a plan and ecf8a_add are
+ * needed (0). */
 int ecf8a_few(uint64_t tokens, const ecf8a_bank* bank);
 
 /* Workspace bytes of ecf8a_add_few (256-byte aligned; 0: none is used). */

@@ -485,7 +485,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     return GradClip(grads, out, stream).run(max_norm, stream)
 
 
-FEW_TOKENS = 512            # up to here a batch needs no AdapterPlan (ECF8A_FEW_TOKENS)
+FEW_TOKENS, FEW_RANK = 512, 64          # up to here a batch needs no AdapterPlan (ECF8A_FEW_TOKENS, ECF8A_FEW_RANK)
 
 
 class AdapterBank(torch.nn.Module):

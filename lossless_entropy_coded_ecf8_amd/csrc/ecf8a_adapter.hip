@@ -1195,7 +1195,7 @@ bool vec_wide(const Pass& s)
 }
 
 // Few tokens: from the index itself, without a plan.
-bool few(uint64_t tokens, const ecf8a_bank& b) { return tokens <= ECF8A_FEW_TOKENS && b.rank <= 64; }
+bool few(uint64_t tokens, const ecf8a_bank& b) { return tokens <= ECF8A_FEW_TOKENS && b.rank <= ECF8A_FEW_RANK; }
 
 // Whether few_kernel does both halves at once: factors of up to 256 KB, which one
 // compute unit reads in about as long as a second launch takes.  One token, 4096 x

@@ -28,7 +28,7 @@ from typing import List, Optional, Sequence
 import torch
 
 from . import binding
-from .adapters import FEW_TOKENS, AdapterBank, AdapterPlan, adapter_add, adapter_grads, linear_fp8_input_grad
+from .adapters import FEW_RANK, FEW_TOKENS, AdapterBank, AdapterPlan, adapter_add, adapter_grads, linear_fp8_input_grad
 
 E4M3_MAX = 448.0
 
@@ -278,24 +278,34 @@ class DecodePipeline:
             adapters: Optional[Sequence[Optional[AdapterBank]]] = None, index=None) -> List[torch.Tensor]:
         """Layer i computes on xs[i]; returns the outputs (caller's stream order).
 
-        adapters: a bank (or None) for each layer, all of the same number of adapters, added to the layer's output as
-        ECF8Linear.forward does; index: the adapter of each token, the same for all layers (it is grouped once)."""
+        adapters: a bank (or None) for each layer, added to the layer's output as ECF8Linear.forward does; index: the
+        adapter of each token, the same for all layers.  It is grouped once for all banks of one number of adapters
+        (few tokens and small ranks need no grouping)."""
         L = len(self.layers)
         main = torch.cuda.current_stream(self.layers[0].device)
         outs = []
         banks = list(adapters) if adapters is not None else [None] * L
         if len(banks) != L:
             raise ValueError("%d adapter banks for %d layers" % (len(banks), L))
-        first = next((b for b in banks if b is not None), None)
-        if first is not None:
+        indexes = [index] * L
+        if any(b is not None for b in banks):
             if index is None:
                 raise ValueError("adapters need the index of each token's adapter")
-            if not isinstance(index, AdapterPlan) and index.numel() > FEW_TOKENS:
-                index = AdapterPlan(index, first.n_adapters)
+            grouped = {}                # number of adapters: the plan
+            for i, b in enumerate(banks):
+                if b is None:
+                    continue
+                if isinstance(index, AdapterPlan):
+                    if index.adapters != b.n_adapters:
+                        raise ValueError("a plan of %d adapters with a bank of %d" % (index.adapters, b.n_adapters))
+                elif index.numel() > FEW_TOKENS or b.rank > FEW_RANK:
+                    if b.n_adapters not in grouped:
+                        grouped[b.n_adapters] = AdapterPlan(index, b.n_adapters)
+                    indexes[i] = grouped[b.n_adapters]
         if self.ahead == 0:
             for i in range(L):
                 self._decode(i, main)
-                outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
+                outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=indexes[i]))
             self._check(main)
             return outs
         side = self.side
@@ -311,7 +321,7 @@ class DecodePipeline:
                 self._decode(j, side)
                 self.decoded[j].record(side)
             main.wait_event(self.decoded[i])
-            outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=index))
+            outs.append(self.layers[i](xs[i], x_scales[i], weight_u8=self.slot(i), adapters=banks[i], index=indexes[i]))
             self.used[i].record(main)
         main.wait_stream(side)
         self._check(main)
