@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import threading
+import warnings
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -271,6 +272,19 @@ def _scratch(need, workspace, device, stream):
     return workspace
 
 
+_warned = False
+
+
+def _no_graph(base, x, down, up):
+    """Says once that a result carries no gradient where one may be expected."""
+    global _warned
+    if not _warned and (down.requires_grad or up.requires_grad or x.requires_grad or (base is not None and base.requires_grad)) \
+            and torch.is_grad_enabled():
+        _warned = True
+        warnings.warn("adapters were added to an output that keeps no gradients: ECF8Linear.adapted is the differentiable "
+                      "layer; when serving, torch.no_grad() or requires_grad_(False) says that none are wanted", stacklevel=3)
+
+
 def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
                 scaling: torch.Tensor, index, *, ranks: Optional[torch.Tensor] = None,
                 x_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -282,8 +296,10 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     float8_e4m3fn with a float32 x_scale; rows may lie apart (a column slice of a wider buffer).  index: the adapter
     of each token, or an AdapterPlan of it.  ranks: rows of each adapter that take part (default: all).  out: where
     the result goes (default: a new tensor); out=base adds in place and leaves tokens without an adapter untouched.
-    hidden: a plan.hidden(R) buffer that keeps h for adapter_grads.  Not differentiable by itself: see ECF8Linear.
+    hidden: a plan.hidden(R) buffer that keeps h for adapter_grads.  Not differentiable by itself (it warns once where
+    an operand requires gradients): see ECF8Linear.adapted.
     """
+    _no_graph(base, x, down, up)
     plan = index if isinstance(index, AdapterPlan) else None
     if plan is None:
         _index_ok(index)
@@ -520,7 +536,9 @@ class AdapterBank(torch.nn.Module):
         return self.down.shape[1]
 
     def add_(self, y: torch.Tensor, x: torch.Tensor, index, x_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """adapter_add into y, the shared projection's output; no gradients are kept."""
+        """adapter_add into y, the shared projection's output; no gradients are kept (it warns once where the bank's
+        parameters require them)."""
+        _no_graph(y, x, self.down, self.up)
         return adapter_add(y, x, self.down.detach(), self.up.detach(), self.scaling, index, ranks=self.ranks,
                            x_scale=x_scale, out=y)
 

@@ -151,7 +151,8 @@ class ECF8Linear(torch.nn.Module):
     def forward(self, x_fp8: torch.Tensor, x_scale: torch.Tensor, weight_u8: Optional[torch.Tensor] = None,
                 adapters: Optional[AdapterBank] = None, index=None) -> torch.Tensor:
         """adapters, index: low-rank adapters added to the output, and the adapter of each token (a vector on the GPU,
-        -1 for none, or an AdapterPlan of it).  The output then has the adapters' type."""
+        -1 for none, or an AdapterPlan of it).  The output then has the adapters' type, and no gradients: adapted trains
+        them."""
         w = self.decoded_weight() if weight_u8 is None else weight_u8.view(self.out_features, self.in_features)
         if adapters is None:
             return linear_fp8(x_fp8, x_scale, w, self.w_scale, self.bias)
