@@ -43,7 +43,7 @@ constexpr int kStrip = 128;               // columns of one wave: 16 lanes of 8
 struct PlanView {
     int* head;           // [0] chunks, [1] slots, [2] units
     i32x4* chunks;       // adapter (adapters: none), first slot, tokens, 0
-    i32x4* units;        // adapter, first slot, slots, 1 if the adapter's only unit
+    i32x4* units;        // adapter, first slot, slots, its partial sums' number (-1: the adapter's only unit, which has none)
     int* unit_start;     // per adapter, and the end
     int* slot_token;     // token of each slot, -1: padding
 };
@@ -75,25 +75,25 @@ __device__ __forceinline__ int read_index(const void* index, int bytes, int64_t 
     return a >= 0 && a < adapters ? (int)a : adapters;
 }
 
-// Exclusive prefix over the workgroup of three values at once.
-__device__ __forceinline__ void block_scan3(int v[3], int total[3], i32x4* lds)
+// Exclusive prefix over the workgroup of four values at once.
+__device__ __forceinline__ void block_scan4(int v[4], int total[4], i32x4* lds)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int inc[3] = {v[0], v[1], v[2]};
+    int inc[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int o = __shfl_up(inc[i], d);
             if (lane >= d) inc[i] += o;
         }
-    if (lane == 63) lds[wave] = i32x4{inc[0], inc[1], inc[2], 0};
+    if (lane == 63) lds[wave] = i32x4{inc[0], inc[1], inc[2], inc[3]};
     __syncthreads();
     i32x4 part[kPlanThreads / 64];
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 64; ++w) part[w] = lds[w];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
         int before = 0, all = 0;
 #pragma unroll
         for (int w = 0; w < kPlanThreads / 64; ++w) {
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
     // Per thread a run of groups, so that one scan over threads covers all.
     const int per = (groups + kPlanThreads - 1) / kPlanThreads;
     const int a0 = min(groups, tid * per), a1 = min(groups, a0 + per);
-    int v[3] = {0, 0, 0}, total[3];
+    int v[4] = {0, 0, 0, 0}, total[4];                      // slots, chunks, units, units with partial sums
     for (int a = a0; a < a1; ++a) {
         int h[kPlanThreads / 64], c = 0;
 #pragma unroll
@@ -164,9 +164,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
         const int s = (c + kTile - 1) / kTile * kTile;
         v[0] += s;
         v[1] += (c + kChunk - 1) / kChunk;
-        v[2] += a < adapters ? (s + unit_slots - 1) / unit_slots : 0;
+        const int units = a < adapters ? (s + unit_slots - 1) / unit_slots : 0;
+        v[2] += units;
+        v[3] += units > 1 ? units : 0;
     }
-    block_scan3(v, total, scan);
+    block_scan4(v, total, scan);
     for (int a = a0; a < a1; ++a) {
         const int c = count[a], s = (c + kTile - 1) / kTile * kTile;
         slot0[a] = v[0];
@@ -176,8 +178,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const void* __restri
             const int units = (s + unit_slots - 1) / unit_slots;
             p.unit_start[a] = v[2];
             for (int u = 0; u < units; ++u)
-                p.units[v[2] + u] = i32x4{a, v[0] + u * unit_slots, min(unit_slots, s - u * unit_slots), units == 1};
+                p.units[v[2] + u] = i32x4{a, v[0] + u * unit_slots, min(unit_slots, s - u * unit_slots), units > 1 ? v[3] + u : -1};
             v[2] += units;
+            v[3] += units > 1 ? units : 0;
         }
         v[0] += s;
         v[1] += (c + kChunk - 1) / kChunk;
@@ -917,7 +920,7 @@ struct FactorSide {
     const uint16_t* v;
     int64_t ldv;
     uint16_t* grad;          // (adapters, rank, width)
-    float* part;             // [unit][zr][stride]
+    float* part;             // [units with partial sums][zr][stride]
     int width, stride;
 };
 
@@ -1039,13 +1042,13 @@ __device__ __forceinline__ void factor_unit(const FactorArgs& A, int group, int 
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = row < rank ? acc[r][j][i] : 0.0f;
-            if (unit[3]) {
+            if (unit[3] < 0) {
                 if (row >= A.rank) continue;
                 store_cols<VEC>(S.grad + ((int64_t)a * A.rank + row) * S.width, col, S.width,
                                 u32x4{pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]), pack2<TYPE>(v[4], v[5]),
                                       pack2<TYPE>(v[6], v[7])});
             } else if (row < A.zr) {
-                float* p = S.part + ((int64_t)at_unit * A.zr + row) * S.stride + col;
+                float* p = S.part + ((int64_t)unit[3] * A.zr + row) * S.stride + col;
                 *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
                 *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
@@ -1088,14 +1091,15 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(FactorArgs A, int first)
     const int col = ((blockIdx.x - (second ? first : 0)) * kThreads + threadIdx.x) * 4;
     if (col >= S.width) return;
     f32x4 s{0, 0, 0, 0};
-    for (int u = u0; u < u1; u += 4) {                      // four loads in flight, added in order
+    const int first_part = u1 > u0 ? A.plan.units[u0][3] : 0, parts = u1 - u0;      // an adapter's parts lie together
+    for (int u = 0; u < parts; u += 4) {                    // four loads in flight, added in order
         f32x4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[j] = *reinterpret_cast<const f32x4*>(S.part + ((int64_t)min(u + j, u1 - 1) * A.zr + row) * S.stride + col);
+            v[j] = *reinterpret_cast<const f32x4*>(S.part + ((int64_t)(first_part + min(u + j, parts - 1)) * A.zr + row) * S.stride + col);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (u + j < u1) s += v[j];
+            if (u + j < parts) s += v[j];
     }
     uint16_t* p = S.grad + ((int64_t)a * A.rank + row) * S.width + col;
     if (VEC) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<TYPE>(s[0], s[1]), pack2<TYPE>(s[2], s[3]));
@@ -1140,14 +1144,24 @@ uint64_t low_bytes(const ecf8a_plan& p, uint32_t rank, uint64_t width)
     return s > 1 ? round_up(s * 4ull * p.max_slots * z_rows(rank), 256) : 0;
 }
 
+// Units that leave partial sums: those of adapters with several.  Such an adapter has c > unit_slots tokens and
+// ceil(c / unit_slots) <= 2 c / unit_slots units, so their number follows the tokens and not the bank (8192 tokens, 2048
+// adapters of rank 64, 8192 x 8192: 0.2 GB, where a place for every unit would take 8.7).
+uint64_t max_parts(const ecf8a_plan& p)
+{
+    if (p.tokens <= p.unit_slots) return 0;
+    const uint64_t most = 2 * p.tokens / p.unit_slots;
+    return most < p.max_units ? most : p.max_units;
+}
+
 uint64_t part_bytes(const ecf8a_plan& p, uint32_t rank, uint64_t width)
 {
-    return round_up(4ull * p.max_units * z_rows(rank) * round_up(width, kStrip), 256);
+    return round_up(4ull * max_parts(p) * z_rows(rank) * round_up(width, kStrip), 256);
 }
 
 bool plan_ok(const ecf8a_plan* p)
 {
-    return p && p->tokens <= ECF8A_MAX_TOKENS && p->adapters >= 1 && p->adapters <= ECF8A_MAX_ADAPTERS;
+    return p && p->tokens <= ECF8A_MAX_TOKENS && p->adapters >= 1 && p->adapters <= ECF8A_MAX_ADAPTERS && p->unit_slots >= 1;
 }
 
 int check_bank(const ecf8a_bank* b)
