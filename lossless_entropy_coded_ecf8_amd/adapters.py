@@ -210,8 +210,10 @@ class AdapterPlan:
             _check(L.ecf8a_plan_prepare(index.data_ptr(), _INDEX_BYTES[index.dtype], self.tokens, self.adapters,
                                         workspace.data_ptr(), workspace.numel(), st, ctypes.byref(self.c)),
                    "ecf8a_plan_prepare")
-            # The stream itself is kept: its handle does not give it back where it is the default stream's, 0.
-            self._made_on, self._handle, self._event = _stream_of(self.device, stream), st, None
+            # The stream is kept by its identity: its handle does not give it back where it is the default stream's, 0.
+            # (A Stream object of the current one would cost 2 us here; it is made when it is needed.)
+            self._made_on = torch._C._cuda_getCurrentStream(self.device.index) if stream is None else stream
+            self._handle, self._event = st, None
             self._captured = _capturing(stream)
 
     def _order(self, handle, stream):
@@ -223,10 +225,13 @@ class AdapterPlan:
             return
         event = self._event
         if event is None:
-            if _capturing(self._made_on):
+            made_on = self._made_on
+            if isinstance(made_on, tuple):
+                made_on = torch.cuda.Stream(stream_id=made_on[0], device_index=made_on[1], device_type=made_on[2])
+            if _capturing(made_on):
                 raise RuntimeError("the plan's stream is being captured: use the plan on another stream before that")
             event = torch.cuda.Event()
-            event.record(self._made_on)
+            event.record(made_on)
             self._event = event                         # seen by other threads only once it is recorded
         stream = _stream_of(self.device, stream)
         stream.wait_event(event)

@@ -87,6 +87,9 @@ def gpu(monkeypatch):
         return lambda *a: g.calls.append(name) or 0
 
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: g.current)
+    known = {}                                                    # torch's identity of a stream: id, device, type
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentStream", lambda i: known.setdefault(id(g.current), g.current) and (id(g.current), i, 1), raising=False)
+    monkeypatch.setattr(torch.cuda, "Stream", lambda stream_id, device_index, device_type: known[stream_id])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: g.current.capturing)
