@@ -30,8 +30,13 @@
  * Both factors are stored by rank row, down as (L, R, K) and up as (L, R, N),
  * so that the forward and the backward pass read either one the same way.
  * Products are exact and summed in float32 (the clip's squares in float64),
- * and each output is rounded once.  The order of every sum is fixed: the same
- * call gives the same bits.
+ * and each output is rounded once.  h and z, which are such sums, enter the
+ * products that they are part of (out, dx, d_down, d_up) as two bfloat16, with
+ * 16 significant bits: each term of those sums is off by up to 2^-16 of its
+ * magnitude (float16 factors and rows: 2^-15, since of four partial products
+ * the smallest is left out), far below the rounding of the result but for sums
+ * whose terms cancel.  The order of every sum is fixed: the same call gives
+ * the same bits.
  * ------------------------------------------------------------------------
  * Conventions as in ecf8.h: ECF8_OK or a negative ECF8_ERR_*; the caller owns
  * every buffer, device pointers unless said otherwise; a hipStream_t is passed

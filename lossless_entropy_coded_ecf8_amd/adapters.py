@@ -10,6 +10,9 @@ module checks arguments, supplies device memory and passes the current stream.
 Shapes: T tokens, K inputs, N outputs, L adapters of up to R rows.  ``down`` is
 (L, R, K) and ``up`` (L, R, N), both stored by rank row: the update that
 adapter a adds to the weight is ``scaling[a] * up[a].T @ down[a]``.
+
+Sums are held in float32 and results rounded once; between an adapter's two products its hidden values keep 16
+significant bits (include/ecf8a.h says what that comes to).
 """
 from __future__ import annotations
 

@@ -12,11 +12,14 @@
 //
 // Z is summed in float32 and handed on as two bfloat16 (split2), the form in which
 // the matrix instructions take it: 16 bits of it are kept for a second
-// instruction on a unit that waits for memory anyway.  It is written once in the
-// layout of each reader: by slot for `wide` (a lane takes eight rank rows of a
-// token), by rank row for `factor` (eight tokens of a rank row), so that both load
-// their operands 16 bytes at a time and compute nothing.  The float16 factors and
-// rows go in as two bfloat16 as well (exact), since a float16 cannot hold Z's range.
+// instruction on a unit that waits for memory anyway.  A term of the second sum is
+// then off by 2^-16 of itself (float16: 2^-15), where the result's own rounding is
+// 2^-8 or 2^-11; a third part would be a half more instructions and bytes of Z.  Z is
+// written once in the layout of each reader: by slot for `wide` (a lane takes eight
+// rank rows of a token), by rank row for `factor` (eight tokens of a rank row), so
+// that both load their operands 16 bytes at a time and compute nothing.  The float16
+// factors and rows go in as two bfloat16 as well (exact), since a float16 cannot hold
+// Z's range.
 //
 // Tokens are taken in the plan's order: sorted by adapter, each group padded
 // to 16 slots, cut into chunks of at most 64 slots that share one adapter.  Few

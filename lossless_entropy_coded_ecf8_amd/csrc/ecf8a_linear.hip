@@ -302,11 +302,11 @@ struct Shape {
 // of a workgroup alone on its compute unit, and of two side by side (the largest
 // two tiles leave no LDS for a second one).  Larger tiles take less from LDS and
 // memory for each product; smaller ones fill 256 compute units from fewer tokens.
-// 2048 x 4096 x 4096: 66 us in tiles of 128 x 256, 72 in 128 x 128, 96 in 256 x
-// 256, which win at 4096 tokens with 109 against 124.  Joining shares costs a
-// launch and their traffic: 1001 x 4096 x 4096 takes 45 us unsplit in 128 x 128,
-// 48 in 128 x 256 with two shares.  24 x 14336 x 4096: 18 us with 16 shares, 21
-// with 8, 22 with 28.
+// 2048 x 4096 x 4096: 67 us in tiles of 128 x 256, 73 in 128 x 128, 100 in 256 x
+// 256, which win at 4096 tokens with 109 against 122.  Joining shares costs a
+// launch and their traffic: 1001 x 4096 x 4096 takes 40 us unsplit in 128 x 128,
+// 44 in 128 x 256 with two shares.  24 x 14336 x 4096: 16.5 us with 16 shares, 17.7
+// with 8, 19.5 with 28.  (Whole calls, one after the other.)
 struct Cost {
     int bm, bn;
     double one, two;

@@ -167,7 +167,8 @@ class ECF8Linear(torch.nn.Module):
 
         x: (T, in_features) in the adapters' type.  The frozen product takes x in E4M3 with x_scale (default: the
         largest magnitude of x over 448), which its gradient passes through as if it were exact; the adapters take x
-        itself.  The weight is decoded for the forward pass and again for the backward pass.  weight_u8: a decoded weight
+        itself.  The gradient of x is the frozen part's, rounded to x's type, plus the adapters' part, rounded again.  The
+        weight is decoded for the forward pass and again for the backward pass.  weight_u8: a decoded weight
         that is kept instead, and holds this weight until the backward pass: one that torch has written, or a pipeline's
         slot that has taken another layer, is refused there (a DecodePlan's own run into it is not seen).  The weight and
         the bias get no gradient.  index as in forward.
@@ -215,6 +216,8 @@ class _Adapted(torch.autograd.Function):
         dx = None
         if want_x:
             w = layer.decoded_weight() if w is None else w.view(layer.out_features, layer.in_features)
+            # In x's 16 bits, to which the adapters' part is added and rounded again: half a step more, as where the two
+            # are layers of their own; a float32 sum between them would be four bytes a value more to write and read.
             dx = linear_fp8_input_grad(dy, w, layer.w_scale)
         dx, d_down, d_up = adapter_grads(dy, x, down, up, scaling, ctx.plan, hidden=hidden, ranks=ranks, dx_base=dx, dx=dx,
                                          want=(want_x, want_factors))
