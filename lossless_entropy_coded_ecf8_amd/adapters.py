@@ -209,6 +209,7 @@ class AdapterPlan:
                 workspace = _empty(need, torch.uint8, self.device, stream)
             else:
                 binding._check_buffer(workspace, self.device, "workspace")
+                _apart(workspace, [("index", index)], "workspace")
             self.workspace, self.c = workspace, PlanA()
             _check(L.ecf8a_plan_prepare(index.data_ptr(), _INDEX_BYTES[index.dtype], self.tokens, self.adapters,
                                         workspace.data_ptr(), workspace.numel(), st, ctypes.byref(self.c)),
@@ -273,10 +274,13 @@ def _hidden_ok(hidden, plan, rank):
         raise ValueError("hidden is smaller than plan.hidden(%d)" % rank)
 
 
-def _scratch(need, workspace, device, stream):
+def _scratch(need, workspace, device, stream, others):
+    """The workspace of a call: a new one, or the caller's, which must lie apart from the call's operands (the kernels
+    find row and adapter numbers in it)."""
     if workspace is None:
         return _empty(max(need, 256), torch.uint8, device, stream)
     binding._check_buffer(workspace, device, "workspace")
+    _apart(workspace, others, "workspace")
     return workspace
 
 
@@ -332,11 +336,13 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
         _apart(out, [("x", x), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks), ("x_scale", x_scale),
                      ("hidden", hidden), ("base", None if same else base)], "out")
     L = _lib()
+    operands = [("out", out), ("x", x), ("base", base), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks),
+                ("x_scale", x_scale), ("index", index if plan is None else None)]
     if plan is None:
         if L.ecf8a_few(T, ctypes.byref(bank)):
             with _Launch(dev, stream) as st:
                 need = L.ecf8a_add_few_bytes(T, ctypes.byref(bank))
-                ws = _scratch(need, workspace, dev, stream) if need else None
+                ws = _scratch(need, workspace, dev, stream, operands) if need else None
                 _check(L.ecf8a_add_few(index.data_ptr(), _INDEX_BYTES[index.dtype], T, ctypes.byref(bank), x.data_ptr(), ldx,
                                        _TYPES[x.dtype], _ptr(x_scale), _ptr(base), ld_base, out.data_ptr(), ld_out,
                                        _ptr(ws), 0 if ws is None else ws.numel(), st), "ecf8a_add_few")
@@ -349,7 +355,8 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     with _Launch(dev, stream) as st:
         plan._order(st, stream)
         need = L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank))
-        ws = _scratch(need, workspace, dev, stream) if need else None
+        operands += [("hidden", hidden), ("the plan's workspace", plan.workspace)]
+        ws = _scratch(need, workspace, dev, stream, operands) if need else None
         _check(L.ecf8a_add(ctypes.byref(plan.c), ctypes.byref(bank), x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(x_scale),
                            _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), _ptr(ws),
                            0 if ws is None else ws.numel(), st), "ecf8a_add")
@@ -400,7 +407,9 @@ def adapter_grads(dy: torch.Tensor, x: Optional[torch.Tensor], down: torch.Tenso
     L = _lib()
     with _Launch(dev, stream) as st:
         plan._order(st, stream)
-        ws = _scratch(L.ecf8a_grads_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream)
+        ws = _scratch(L.ecf8a_grads_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream,
+                      [("dx", dx), ("dy", dy), ("x", x), ("dx_base", dx_base), ("down", down), ("up", up), ("scaling", scaling),
+                       ("ranks", ranks), ("hidden", hidden), ("the plan's workspace", plan.workspace)])
         _check(L.ecf8a_grads(ctypes.byref(plan.c), ctypes.byref(bank), dy.data_ptr(), ld_dy,
                              _ptr(x) if want_factors else None, ldx, _ptr(hidden), _ptr(dx_base), ld_b, _ptr(dx), ld_dx,
                              _ptr(d_down), _ptr(d_up), ws.data_ptr(), ws.numel(), st), "ecf8a_grads")
@@ -433,7 +442,7 @@ def linear_fp8_input_grad(dy: torch.Tensor, w_u8: torch.Tensor, w_scale: torch.T
     L = _lib()
     with _Launch(dev, stream) as st:
         need = L.ecf8a_input_grad_bytes(T, N, K)
-        ws = _scratch(need, workspace, dev, stream) if need else None
+        ws = _scratch(need, workspace, dev, stream, [("out", out), ("dy", dy), ("w_u8", w_u8), ("w_scale", w_scale)]) if need else None
         _check(L.ecf8a_input_grad(dy.data_ptr(), ld_dy, T, N, w_u8.data_ptr(), K, w_scale.data_ptr(), _TYPES[dy.dtype],
                                   out.data_ptr(), ld_dx, _ptr(ws), 0 if ws is None else ws.numel(), st),
                "ecf8a_input_grad")
