@@ -336,8 +336,10 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
         _apart(out, [("x", x), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks), ("x_scale", x_scale),
                      ("hidden", hidden), ("base", None if same else base)], "out")
     L = _lib()
-    operands = [("out", out), ("x", x), ("base", base), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks),
-                ("x_scale", x_scale), ("index", index if plan is None else None)]
+    operands = None
+    if workspace is not None:
+        operands = [("out", out), ("x", x), ("base", base), ("down", down), ("up", up), ("scaling", scaling), ("ranks", ranks),
+                    ("x_scale", x_scale), ("hidden", hidden), ("index", index if plan is None else plan.workspace)]
     if plan is None:
         if L.ecf8a_few(T, ctypes.byref(bank)):
             with _Launch(dev, stream) as st:
@@ -355,7 +357,6 @@ def adapter_add(base: Optional[torch.Tensor], x: torch.Tensor, down: torch.Tenso
     with _Launch(dev, stream) as st:
         plan._order(st, stream)
         need = L.ecf8a_add_bytes(ctypes.byref(plan.c), ctypes.byref(bank))
-        operands += [("hidden", hidden), ("the plan's workspace", plan.workspace)]
         ws = _scratch(need, workspace, dev, stream, operands) if need else None
         _check(L.ecf8a_add(ctypes.byref(plan.c), ctypes.byref(bank), x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(x_scale),
                            _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(hidden), _ptr(ws),
@@ -408,8 +409,9 @@ def adapter_grads(dy: torch.Tensor, x: Optional[torch.Tensor], down: torch.Tenso
     with _Launch(dev, stream) as st:
         plan._order(st, stream)
         ws = _scratch(L.ecf8a_grads_bytes(ctypes.byref(plan.c), ctypes.byref(bank)), workspace, dev, stream,
-                      [("dx", dx), ("dy", dy), ("x", x), ("dx_base", dx_base), ("down", down), ("up", up), ("scaling", scaling),
-                       ("ranks", ranks), ("hidden", hidden), ("the plan's workspace", plan.workspace)])
+                      workspace is not None and [
+                          ("dx", dx), ("dy", dy), ("x", x), ("dx_base", dx_base), ("down", down), ("up", up), ("scaling", scaling),
+                          ("ranks", ranks), ("hidden", hidden), ("the plan's workspace", plan.workspace)])
         _check(L.ecf8a_grads(ctypes.byref(plan.c), ctypes.byref(bank), dy.data_ptr(), ld_dy,
                              _ptr(x) if want_factors else None, ldx, _ptr(hidden), _ptr(dx_base), ld_b, _ptr(dx), ld_dx,
                              _ptr(d_down), _ptr(d_up), ws.data_ptr(), ws.numel(), st), "ecf8a_grads")
