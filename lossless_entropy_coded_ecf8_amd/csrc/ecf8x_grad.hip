@@ -1,0 +1,343 @@
+// ecf8x_grad.hip -- the gradient that a frozen 4-bit weight passes to its input:
+// dx = dy w, dy (T x N) in a 16-bit type, w (N x K) in microscaled 4 bits.
+//
+// The reduction runs down the weight's columns, and a block's power of two
+// changes from row to row, so that an operand of eight rows has eight scales.
+// Each 16 bytes of codes (a block, under one scale) are therefore widened once
+// per workgroup, on their way to LDS, and the operands are turned there by the
+// transposing LDS read.  Widened values are exact bfloat16; float16 dy is split
+// into two bfloat16 (exact).  Sums in float32, rounded once.
+#include "ecf8x_common.h"
+
+namespace {
+
+using namespace ecf8x;
+
+constexpr int kThreads = 512, kStep = 64;
+
+struct Args {
+    const uint16_t* dy;
+    int64_t ld_dy;
+    const uint8_t *w, *w_scales;
+    uint16_t* dx;
+    int64_t ld_dx;
+    float* planes;              // [share][tokens][k]; nullptr: one share, written to dx
+    int64_t tokens;
+    int n, k, kp, share;        // share: reduction length of one of gridDim.y shares, a multiple of 64
+    int tiles_m, tiles_n;
+};
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef __attribute__((address_space(3))) void LdsMem;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 LdsQuad;
+
+// Every offset used with it is inside the operand, so the range is left open.
+__device__ __forceinline__ Rsrc buffer_of(const void* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
+}
+
+// One workgroup: BM tokens by BN columns of dx, eight waves in WM rows of WN, 64
+// rows of the weight at a time.  dy's tile goes straight to LDS, ahead by
+// STAGES - 1 steps; the weight's codes are loaded two steps ahead, widened and
+// stored one step ahead, into two buffers.
+//
+// Banks.  Unit u (16 bytes) of dy's row r sits at u ^ (r & 7).  Unit u of the
+// widened row r sits at u ^ turn(r): the transposing read takes two units of
+// four rows in each lane group, and the 16 units that half a wave touches lie in
+// different banks; so do those that 16 lanes store, since lanes of the second
+// half of a row store their units in another order.
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+struct Tile {
+    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+    static constexpr int BU = BN / 8;                          // 16-byte units of a widened row
+    static constexpr int kA = BM * 8, kB = kStep * BU;
+    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads;
+    static constexpr int kRaw = kStep * BN / 32;               // 16-byte units of codes
+    static constexpr int kLds = 16 * (STAGES * kA + 2 * kB);
+    static_assert(STAGES >= 2 && kLds <= 160 * 1024, "LDS");
+    static_assert(WM * WN == kThreads / 64 && MF >= 1 && NF >= 1 && kRaw <= kThreads && kRaw % 64 == 0, "eight waves");
+
+    static __device__ __forceinline__ int turn(int row) { return 2 * ((row & 3) | (row >> 1 & 4)) | (row >> 2 & 1); }
+
+    struct Places {
+        uint32_t a[kUnitsA];
+    };
+
+    static __device__ __forceinline__ Places places(const Args& A, int64_t t0)
+    {
+        Places at;
+#pragma unroll
+        for (int i = 0; i < kUnitsA; ++i) {
+            const int u = i * kThreads + threadIdx.x, row = u >> 3;
+            at.a[i] = 2 * ((uint32_t)min((int64_t)row, A.tokens - 1 - t0) * (uint32_t)A.ld_dy + 8 * ((u & 7) ^ (row & 7)));
+        }
+        return at;
+    }
+
+    static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n, u32x4* la)
+    {
+        const Rsrc ra = buffer_of(A.dy + t0 * A.ld_dy);
+#pragma unroll
+        for (int i = 0; i < kUnitsA; ++i) {
+            const int first = i * kThreads + (threadIdx.x & ~63);
+            if (kA % kThreads && first >= kA) break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + first), 16, at.a[i], 2 * n, 0, 0);
+        }
+    }
+
+    // The same where the reduction ends inside the step: zeros past n1.
+    static __device__ __forceinline__ void stage_tail(const Args& A, int64_t t0, int n, int n1, u32x4* la)
+    {
+        for (int u = threadIdx.x; u < kA; u += kThreads) {
+            const int row = u >> 3, first = n + 8 * ((u & 7) ^ (row & 7));
+            const uint16_t* p = A.dy + min(t0 + row, A.tokens - 1) * A.ld_dy + first;
+            u32x4 v{0, 0, 0, 0};
+            if (first + 8 <= n1) v = *reinterpret_cast<const u32x4*>(p);
+            else
+                for (int i = 0; first + i < n1; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+            la[u] = v;
+        }
+    }
+
+    // The block of codes that a thread widens: row threadIdx / (BN / 32) of the step.  Zero past n1 and past the stored row.
+    struct Raw {
+        u32x4 codes;
+        uint32_t scale;
+    };
+
+    static __device__ __forceinline__ Raw fetch(const Args& A, int k0, int n, int n1)
+    {
+        Raw r{u32x4{0, 0, 0, 0}, 0};
+        const int row = n + threadIdx.x / (BN / 32), col = k0 + 32 * (threadIdx.x % (BN / 32));
+        if ((kRaw < kThreads && threadIdx.x >= kRaw) || row >= n1 || col >= A.kp) return r;
+        r.codes = *reinterpret_cast<const u32x4*>(A.w + (int64_t)row * (A.kp / 2) + col / 2);
+        r.scale = A.w_scales[(int64_t)row * (A.kp / 32) + col / 32];
+        return r;
+    }
+
+    static __device__ __forceinline__ void widen(const Raw& r, u32x4* lb)
+    {
+        if (kRaw < kThreads && threadIdx.x >= kRaw) return;
+        const int row = threadIdx.x / (BN / 32), j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
+        const float s = scale_of(r.scale);
+        u32x4* p = lb + row * BU;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[(4 * j + (i ^ swap)) ^ turn(row)] = widen4(swap ? r.codes[i ^ 1] : r.codes[i], s);
+    }
+
+    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[NF])
+    {
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, row0 = wm * (BM / WM) + c;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 b[NF];
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 32 * kk + 8 * g + 4 * h + (c >> 2), u = (wn * (BN / WN) + 16 * n) / 8 + (c >> 1 & 1);
+                    const char* p = reinterpret_cast<const char*>(lb + row * BU + (u ^ turn(row))) + 8 * (c & 1);
+                    const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad*)p));
+                    b[n][2 * h] = v.x, b[n][2 * h + 1] = v.y;
+                }
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const u32x4 a = la[(row0 + 16 * m) * 8 + ((4 * kk + g) ^ (c & 7))];
+                if constexpr (TYPE == kBf16) {
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
+                } else {
+                    u32x4 hi, lo;
+                    split8_f16(a, hi, lo);
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], hi, acc[m][n]);
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], lo, acc[m][n]);
+                }
+            }
+        }
+    }
+
+    // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
+    static __device__ __forceinline__ Raw step(const Args& A, const Places& at, int64_t t0, int k0, int n, int ahead, int n1, const Raw& next,
+                                               u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
+                                               const u32x4* __restrict__ lb, int wm, int wn, f32x4 (*acc)[NF])
+    {
+        const Raw later = fetch(A, k0, n + 2 * kStep, n1);
+        stage(A, at, t0, ahead, to_a);
+        __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
+        widen(next, to_b);
+        multiply(la, lb, wm, wn, acc);
+        return later;
+    }
+};
+
+template <int LOADS>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
+{
+    typedef Tile<TYPE, BM, BN, WM, WN, STAGES> S;
+    extern __shared__ u32x4 lds[];
+    u32x4* const la = lds;
+    u32x4* const lb = lds + STAGES * S::kA;
+    const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+    // The order of tiles as in the forward product: a run of tiles for each die.
+    const int total = A.tiles_m * A.tiles_n;
+    int id = blockIdx.x;
+    if (total % 8 == 0) id = (id % 8) * (total / 8) + id / 8;
+    const int band = id / (8 * A.tiles_n), rows = min(8, A.tiles_m - band * 8), in_band = id - band * 8 * A.tiles_n;
+    const int tm = band * 8 + in_band % rows, tn = in_band / rows;
+    const int64_t t0 = (int64_t)tm * BM;
+    const int k0 = tn * BN;
+    const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
+    f32x4 acc[S::MF][S::NF] = {};
+    const typename S::Places at = S::places(A, t0);
+    typename S::Raw next = S::fetch(A, k0, n0, n1);
+    S::widen(next, lb);
+    next = S::fetch(A, k0, n0 + kStep, n1);
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0 + min(s, steps - 1) * kStep, la + s * S::kA);
+    }
+    wait_and_meet<0>();
+    // In step s the codes of step s + 1 are widened into the other buffer, those of
+    // step s + 2 sent for, and dy's tile of step s + STAGES - 1 (the last one again
+    // past the end).  dy's tile of step s + 1 is older than what may be under way at
+    // the end of the step: the loads of the steps behind it and two of codes.
+    constexpr int kAhead = (STAGES - 2) * (S::kA / kThreads);
+    int use = 0, fill = STAGES - 1;
+    for (int s = 0; s < steps; ++s) {
+        next = S::step(A, at, t0, k0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, next, la + fill * S::kA,
+                       lb + (s + 1 & 1) * S::kB, la + use * S::kA, lb + (s & 1) * S::kB, wm, wn, acc);
+        wait_and_meet<kAhead>();
+        use = use == STAGES - 1 ? 0 : use + 1;
+        fill = fill == STAGES - 1 ? 0 : fill + 1;
+    }
+    if (n0 + steps * kStep < n1) {                            // its codes are widened by now
+        wait_and_meet<0>();
+        S::stage_tail(A, t0, n0 + steps * kStep, n1, la);
+        wait_and_meet<0>();
+        S::multiply(la, lb + (steps & 1) * S::kB, wm, wn, acc);
+    }
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < S::MF; ++m) {
+        const int64_t t = t0 + wm * (BM / WM) + m * 16 + c;
+        if (t >= A.tokens) continue;
+#pragma unroll
+        for (int n = 0; n < S::NF; ++n) {
+            const int col = k0 + wn * (BN / WN) + n * 16 + 4 * g;   // K is a multiple of 32: an operand's columns are in or out
+            if (col >= A.k) continue;
+            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.k + col) = acc[m][n];
+            else store4<TYPE>(A.dx + t * A.ld_dx + col, acc[m][n], 4, true);
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // loads to LDS that no step used land before the workgroup ends
+}
+
+struct Shape {
+    int bm, bn;
+    uint32_t shares;
+};
+
+struct Cost {
+    int bm, bn;
+    double one, two;
+};
+constexpr Cost kCosts[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}, {64, 256, 0.7, 0.0}, {32, 256, 0.8, 0.0}};
+
+Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k)
+{
+    Shape best{32, 256, 1};
+    double least = -1.0;
+    for (const Cost& c : kCosts) {
+        if (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens) continue;      // over half of the rows would be padding
+        const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
+        for (uint32_t s = 1; s <= 16 && (s == 1 || n / s >= 256); ++s) {
+            const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
+            const double full = c.two > 0.0 ? c.two : c.one;
+            const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
+            const double us = turns * ((n + s - 1) / s + 63) / 64 + (s > 1 ? 4.0 + 8.0 * s * tokens * k / 5e6 : 0.0);
+            if (least < 0.0 || us < least) {
+                least = us;
+                best = Shape{c.bm, c.bn, s};
+            }
+        }
+    }
+    return best;
+}
+
+bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
+{
+    return tokens <= ECF8A_MAX_TOKENS && n >= 1 && n <= ECF8A_MAX_FEATURES && k >= ECF8X_BLOCK && k <= ECF8A_MAX_FEATURES &&
+           k % ECF8X_BLOCK == 0;
+}
+
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+int launch(Args A, uint32_t shares, hipStream_t st)
+{
+    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES>::kLds;
+    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES>;
+    if (bytes > 65536 &&
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return ECF8_ERR_HIP;
+    A.tiles_m = (int)((A.tokens + BM - 1) / BM);
+    A.tiles_n = (A.k + BN - 1) / BN;
+    kernel<<<dim3((uint32_t)A.tiles_m * A.tiles_n, shares), kThreads, bytes, st>>>(A);
+    return launch_status();
+}
+
+template <int TYPE>
+int run(const Args& A, const Shape& s, hipStream_t st)
+{
+    int rc;
+    if (s.bm == 256) rc = launch<TYPE, 256, 256, 2, 4, 3>(A, s.shares, st);
+    else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 3>(A, s.shares, st);
+    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 2>(A, s.shares, st);
+    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 3>(A, s.shares, st);
+    else rc = launch<TYPE, 32, 256, 2, 4, 3>(A, s.shares, st);
+    if (rc != ECF8_OK || s.shares < 2) return rc;
+    const uint64_t units = (uint64_t)A.tokens * A.k / 4;
+    join_kernel<TYPE><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.planes, A.tokens, A.k, A.k, (int)s.shares, nullptr, A.dx, A.ld_dx);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features)
+{
+    if (!sizes_ok(tokens, out_features, in_features)) return 0;
+    const uint64_t s = shape_of(tokens, out_features, in_features).shares;
+    return s > 1 ? round_up(4 * s * tokens * in_features, 256) : 0;
+}
+
+extern "C" int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, uint64_t tokens, uint64_t out_features, uint64_t in_features,
+                                const ecf8x_matrix* w, void* dx, uint64_t ld_dx, void* workspace, uint64_t workspace_bytes,
+                                void* hip_stream)
+{
+    if (type != ECF8A_BF16 && type != ECF8A_FP16) return ECF8_ERR_UNSUPPORTED;
+    if (!sizes_ok(tokens, out_features, in_features)) return ECF8_ERR_SIZE;
+    if (tokens == 0) return ECF8_OK;
+    if (tokens == 1) ld_dy = out_features, ld_dx = in_features;
+    if (!dy || !w || !w->codes || !w->scales || !dx || !aligned(dy, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 4) ||
+        !aligned(dx, 16) || (tokens > 1 && (ld_dy % 8 || ld_dx % 8)))
+        return ECF8_ERR_ARG;
+    if (ld_dy < out_features || ld_dx < in_features || ld_dy > (1u << 22) || ld_dx > (1ull << 40)) return ECF8_ERR_SIZE;
+    const uint64_t need = ecf8x_input_grad_bytes(tokens, out_features, in_features);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
+    const Shape s = shape_of(tokens, out_features, in_features);
+    const Args A{static_cast<const uint16_t*>(dy), (int64_t)ld_dy, w->codes, w->scales, static_cast<uint16_t*>(dx), (int64_t)ld_dx,
+                 s.shares > 1 ? static_cast<float*>(workspace) : nullptr, (int64_t)tokens, (int)out_features, (int)in_features,
+                 (int)padded(in_features), (int)round_up((out_features + s.shares - 1) / s.shares, 64), 0, 0};
+    hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    return type == ECF8A_BF16 ? run<kBf16>(A, s, st) : run<kFp16>(A, s, st);
+}

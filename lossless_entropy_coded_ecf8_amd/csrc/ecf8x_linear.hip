@@ -1,0 +1,577 @@
+// ecf8x_linear.hip -- y = x w^T + bias with w (N x K) in microscaled 4 bits and
+// x in a 16-bit type or in the same 4 bits.
+//
+// Sixteen-bit x: each code times its power of two is exact in bfloat16, so the
+// weight is widened in registers and the 16-bit matrix instruction gives exact
+// products, summed in float32.  float16 x is split into two bfloat16 (exact),
+// since a block's power of two need not fit float16.  Four-bit x: the scaled
+// matrix instruction takes codes and scale bytes as they are stored.
+#include "ecf8x_common.h"
+
+namespace {
+
+using namespace ecf8x;
+
+constexpr int kThreads = 512, kWaves = 8;
+
+struct Args {
+    const void* x;              // 16-bit rows, ld_x elements apart, or codes
+    const uint8_t* x_scales;
+    int64_t ld_x;
+    const uint8_t *w, *w_scales;
+    const uint16_t* bias;
+    uint16_t* y;
+    int64_t ld_y;
+    float* planes;              // [share][tokens][pitch]; nullptr: one share, written to y
+    int64_t tokens;
+    int n, k, kp;               // kp: k rounded up to 128
+    int pitch;                  // n rounded up to 4
+    int share;                  // reduction length of one of gridDim.y shares, a multiple of 256
+    int tiles_m, tiles_n;
+    bool vector;                // y's rows take 8-byte stores
+};
+
+template <int OUT>
+__device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
+{
+    if (A.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < A.n) v[i] += load1<OUT>(A.bias + n + i);
+    }
+    store4<OUT>(A.y + t * A.ld_y + n, v, A.n - n, A.vector);
+}
+
+// ------------------------------------------------------------ few tokens
+//
+// A workgroup takes 16 RF rows of the weight, its eight waves a share of the
+// reduction each, and joins the eight sums in LDS.  Weights go from memory to
+// registers, 64 contiguous bytes a lane; x comes through the caches.
+// Lane (c, g) holds chunks of row c of the weight and of token c.
+template <int XT, int OUT, int RF, int MF>
+__global__ __launch_bounds__(kThreads) void few_kernel(Args A)
+{
+    extern __shared__ f32x4 sums[];                           // [wave][RF][MF][lane]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16 * RF, row_bytes = A.kp / 2, row_scales = A.kp / 32;
+    const int units = A.kp / 128, u0 = units * wave / kWaves, u1 = units * (wave + 1) / kWaves;
+    const uint8_t *w[RF], *ws[RF];
+#pragma unroll
+    for (int r = 0; r < RF; ++r) {
+        const int64_t row = min(n0 + 16 * r + c, A.n - 1);    // rows past the last reach no result that is stored
+        w[r] = A.w + row * row_bytes;
+        ws[r] = A.w_scales + row * row_scales;
+    }
+    f32x4 acc[RF][MF] = {};
+    for (int u = u0; u < u1; u += 4) {
+        const int unit = u + g;                               // this lane group's 128 values
+        const bool in = unit < u1;
+        u32x4 b[RF][4];
+        uint32_t sb[RF];
+#pragma unroll
+        for (int r = 0; r < RF; ++r) {
+            sb[r] = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) b[r][s] = u32x4{0, 0, 0, 0};
+            if (in) {
+                sb[r] = *reinterpret_cast<const uint32_t*>(ws[r] + unit * 4);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) b[r][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[r] + unit * 64 + 16 * s));
+            }
+        }
+        if constexpr (XT == kMx4) {
+            u32x4 a[MF][4];
+            uint32_t sa[MF];
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const int64_t t = 16 * m + c;
+                sa[m] = 0;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) a[m][s] = u32x4{0, 0, 0, 0};
+                if (in && t < A.tokens) {
+                    sa[m] = *reinterpret_cast<const uint32_t*>(A.x_scales + t * row_scales + unit * 4);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        a[m][s] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(A.x) + t * row_bytes + unit * 64 + 16 * s);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RF; ++r)
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    acc[r][m] = mfma_mx4<0>(b[r][0], a[m][0], acc[r][m], sb[r], sa[m]);
+                    acc[r][m] = mfma_mx4<1>(b[r][1], a[m][1], acc[r][m], sb[r], sa[m]);
+                    acc[r][m] = mfma_mx4<2>(b[r][2], a[m][2], acc[r][m], sb[r], sa[m]);
+                    acc[r][m] = mfma_mx4<3>(b[r][3], a[m][3], acc[r][m], sb[r], sa[m]);
+                }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = unit * 128 + 32 * s;
+                u32x4 a[MF][4];
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const int64_t t = 16 * m + c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[m][j] = u32x4{0, 0, 0, 0};
+                    if (in && k < A.k && t < A.tokens) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            a[m][j] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(A.x) + t * A.ld_x + k + 8 * j);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u32x4 wide[RF];
+#pragma unroll
+                    for (int r = 0; r < RF; ++r) wide[r] = widen4(b[r][s][j], scale_of(sb[r] >> (8 * s) & 255));
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) {
+                        if constexpr (XT == kBf16) {
+#pragma unroll
+                            for (int r = 0; r < RF; ++r) acc[r][m] = mfma_bf16(wide[r], a[m][j], acc[r][m]);
+                        } else {
+                            u32x4 hi, lo;
+                            split8_f16(a[m][j], hi, lo);
+#pragma unroll
+                            for (int r = 0; r < RF; ++r) {
+                                acc[r][m] = mfma_bf16(wide[r], hi, acc[r][m]);
+                                acc[r][m] = mfma_bf16(wide[r], lo, acc[r][m]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RF; ++r)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) sums[((wave * RF + r) * MF + m) * 64 + lane] = acc[r][m];
+    __syncthreads();
+    if (threadIdx.x >= RF * MF * 64) return;
+    f32x4 v{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += sums[i * RF * MF * 64 + threadIdx.x];
+    const int m = (threadIdx.x >> 6) % MF, r = (threadIdx.x >> 6) / MF, n = n0 + 16 * r + 4 * g;
+    const int64_t t = 16 * m + c;
+    if (t < A.tokens && n < A.n) finish<OUT>(A, t, n, v);
+}
+
+// ------------------------------------------------------------ many tokens
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef __attribute__((address_space(3))) void LdsMem;
+
+// Every offset used with it is inside the operand, so the range is left open.
+__device__ __forceinline__ Rsrc buffer_of(const void* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
+}
+
+// One workgroup: BM tokens by BN outputs, eight waves in WM rows of WN, the
+// reduction in steps of 128 bytes of an x row: 64 values of 16 bits (32 bytes of
+// a weight row), 256 of 4 bits (128 bytes of a weight row).
+//
+// Tiles go from memory to LDS without passing registers into STAGES buffers:
+// while step s is multiplied, step s + STAGES - 1 is sent for.  A lane's operand
+// share lies in one or two 16-byte units of its row: lane group g takes units 2g
+// and 2g + 1 of an x row and the same values of a weight row, so that 16-bit x
+// meets 8 contiguous bytes of codes, under one scale.
+//
+// Banks: unit u of row r sits at u ^ (r & 7) (rows of 128 bytes); weight rows of
+// 32 bytes lie as they are.  The scales of a row's step: one dword (16-bit x: the
+// four blocks that two steps share) or two (4-bit).
+template <int XT, int BM, int BN, int WM, int WN, int STAGES>
+struct Tile {
+    static constexpr bool MX = XT == kMx4;
+    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = MX ? 256 : 64;
+    static constexpr int BU = MX ? 8 : 2;                      // 16-byte units of a weight row's step
+    static constexpr int kA = BM * 8, kB = BN * BU;            // 16-byte units of the two tiles
+    static constexpr int kS = MX ? 2 * (BM + BN) : BN;         // dwords of scales
+    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (kB + kThreads - 1) / kThreads,
+                         kUnitsS = (kS + kThreads - 1) / kThreads;
+    static constexpr int kStage = 16 * (kA + kB) + 4 * kS;     // bytes
+    static constexpr int kLds = STAGES * kStage;
+    // Loads that may be under way at the end of a step: those of all stages but the next one's.
+    static constexpr int kAhead = (STAGES - 2) * (kA / kThreads + kB / kThreads + kS / kThreads);
+    static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
+    static_assert(WM * WN == kWaves && MF >= 1 && NF >= 1, "eight waves");
+    static_assert(kA % 64 == 0 && kB % 64 == 0 && kS % 64 == 0, "whole waves stage");
+
+    // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
+    // no result that is stored.
+    struct Places {
+        uint32_t a[kUnitsA], b[kUnitsB], s[kUnitsS];
+    };
+
+    static __device__ __forceinline__ Places places(const Args& A, int64_t t0, int n0)
+    {
+        Places at;
+        const uint32_t pitch_x = MX ? A.kp / 2 : 2 * (uint32_t)A.ld_x, pitch_w = A.kp / 2, pitch_s = A.kp / 32;
+#pragma unroll
+        for (int i = 0; i < kUnitsA; ++i) {
+            const int u = i * kThreads + threadIdx.x, row = u >> 3;
+            at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * ((u & 7) ^ (row & 7));
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsB; ++i) {
+            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? (u & 7) ^ (row & 7) : u & 1;
+            at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * unit;
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsS; ++i) {
+            const int u = i * kThreads + threadIdx.x;
+            if constexpr (MX) {                                // [half][token], then [half][output]
+                if (u < 2 * BM) at.s[i] = (uint32_t)min((int64_t)(u % BM), A.tokens - 1 - t0) * pitch_s + 4 * (u / BM);
+                else at.s[i] = (uint32_t)min((u - 2 * BM) % BN, A.n - 1 - n0) * pitch_s + 4 * ((u - 2 * BM) / BN);
+            } else {
+                at.s[i] = (uint32_t)min(u, A.n - 1 - n0) * pitch_s;
+            }
+        }
+        return at;
+    }
+
+    // One step's tiles, straight to LDS: the newest loads are those that every wave has.
+    static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* buf)
+    {
+        u32x4 *la = buf, *lb = buf + kA;
+        uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
+        const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
+        const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2)), rs = buffer_of(A.w_scales + (int64_t)n0 * (A.kp / 32));
+        const int wave0 = threadIdx.x & ~63;
+#pragma unroll
+        for (int i = 0; i < kUnitsS; ++i) {
+            const int first = i * kThreads + wave0;
+            if (kS % kThreads && first >= kS) break;
+            if (MX && first < 2 * BM)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(A.x_scales + t0 * (A.kp / 32)), (LdsMem*)(ls + first), 4, at.s[i], k / 32, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsMem*)(ls + first), 4, at.s[i], MX ? k / 32 : (k / 128) * 4, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsB; ++i) {
+            const int first = i * kThreads + wave0;
+            if (kB % kThreads && first >= kB) break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + first), 16, at.b[i], k / 2, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitsA; ++i) {
+            const int first = i * kThreads + wave0;
+            if (kA % kThreads && first >= kA) break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + first), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
+        }
+    }
+
+    // The same where the reduction ends inside the step: zeros past k1 (a multiple of 32).
+    static __device__ __forceinline__ void stage_tail(const Args& A, int64_t t0, int n0, int k, int k1, u32x4* buf)
+    {
+        u32x4 *la = buf, *lb = buf + kA;
+        uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
+        for (int u = threadIdx.x; u < kA; u += kThreads) {
+            const int row = u >> 3, unit = (u & 7) ^ (row & 7);
+            const int64_t t = min(t0 + row, A.tokens - 1);
+            u32x4 v{0, 0, 0, 0};
+            if constexpr (MX) {
+                if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(A.x) + t * (A.kp / 2) + k / 2 + 16 * unit);
+            } else {
+                if (k + 8 * unit < k1) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(A.x) + t * A.ld_x + k + 8 * unit);
+            }
+            la[u] = v;
+        }
+        for (int u = threadIdx.x; u < kB; u += kThreads) {
+            const int row = u / BU, unit = MX ? (u & 7) ^ (row & 7) : u & 1;
+            u32x4 v{0, 0, 0, 0};
+            if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(A.w + (int64_t)min(n0 + row, A.n - 1) * (A.kp / 2) + k / 2 + 16 * unit);
+            lb[u] = v;
+        }
+        for (int u = threadIdx.x; u < kS; u += kThreads) {
+            const int v = u - 2 * BM, half = MX ? (u < 2 * BM ? u / BM : v / BN) : 0;
+            uint32_t s = 0;
+            if (!MX) s = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + u, A.n - 1) * (A.kp / 32) + (k / 128) * 4);
+            else if (k + 128 * half < k1) {
+                if (u < 2 * BM) s = *reinterpret_cast<const uint32_t*>(A.x_scales + min(t0 + u % BM, A.tokens - 1) * (A.kp / 32) + k / 32 + 4 * half);
+                else s = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + v % BN, A.n - 1) * (A.kp / 32) + k / 32 + 4 * half);
+            }
+            ls[u] = s;
+        }
+    }
+
+    // odd: whether the step is the second of the two that share a dword of scales (16-bit x).
+    static __device__ __forceinline__ void multiply(const u32x4* buf, int wm, int wn, int odd, f32x4 (*acc)[NF])
+    {
+        const u32x4 *la = buf, *lb = buf + kA;
+        const uint32_t* ls = reinterpret_cast<const uint32_t*>(lb + kB);
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+        const int row0 = wm * (BM / WM) + c, col0 = wn * (BN / WN) + c;
+        if constexpr (MX) {
+            u32x4 b[NF][2];
+            uint32_t sb[NF];
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                const int row = col0 + 16 * n;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) b[n][s] = lb[row * 8 + ((2 * g + s) ^ (row & 7))];
+                sb[n] = ls[2 * BM + (g >> 1) * BN + row] >> (16 * (g & 1));
+            }
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const int row = row0 + 16 * m;
+                const u32x4 a0 = la[row * 8 + ((2 * g) ^ (row & 7))], a1 = la[row * 8 + ((2 * g + 1) ^ (row & 7))];
+                const uint32_t sa = ls[(g >> 1) * BM + row] >> (16 * (g & 1));
+#pragma unroll
+                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<0>(b[n][0], a0, acc[m][n], sb[n], sa);
+#pragma unroll
+                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<1>(b[n][1], a1, acc[m][n], sb[n], sa);
+            }
+        } else {
+            uint2 raw[NF];
+            float scale[NF];
+            const int sh = 16 * odd + 8 * (g >> 1);
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                const int row = col0 + 16 * n;
+                raw[n] = reinterpret_cast<const uint2*>(lb)[row * 4 + g];
+                scale[n] = scale_of(ls[row] >> sh & 255);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                u32x4 b[NF];
+#pragma unroll
+                for (int n = 0; n < NF; ++n) b[n] = widen4(kk ? raw[n].y : raw[n].x, scale[n]);
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const int row = row0 + 16 * m;
+                    const u32x4 a = la[row * 8 + ((2 * g + kk) ^ (row & 7))];
+                    if constexpr (XT == kBf16) {
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
+                    } else {
+                        u32x4 hi, lo;
+                        split8_f16(a, hi, lo);
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], hi, acc[m][n]);
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], lo, acc[m][n]);
+                    }
+                }
+            }
+        }
+    }
+
+    // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
+    static __device__ __forceinline__ void stage_and_multiply(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* __restrict__ to,
+                                                              const u32x4* __restrict__ from, int wm, int wn, int odd, f32x4 (*acc)[NF])
+    {
+        stage(A, at, t0, n0, k, to);
+        __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
+        multiply(from, wm, wn, odd, acc);
+    }
+};
+
+// All but the newest LOADS loads have arrived, and every LDS access is done, in
+// every wave of the workgroup.
+template <int LOADS>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
+{
+    typedef Tile<XT, BM, BN, WM, WN, STAGES> S;
+    extern __shared__ u32x4 lds[];
+    const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+    // Workgroups go to the eight dies in turn; each die gets a run of tiles, in
+    // columns of eight tiles down the tokens, so that its cache sees the same rows
+    // of x and of the weight again.
+    const int total = A.tiles_m * A.tiles_n;
+    int id = blockIdx.x;
+    if (total % 8 == 0) id = (id % 8) * (total / 8) + id / 8;
+    const int band = id / (8 * A.tiles_n), rows = min(8, A.tiles_m - band * 8), in_band = id - band * 8 * A.tiles_n;
+    const int tm = band * 8 + in_band % rows, tn = in_band / rows;
+    const int64_t t0 = (int64_t)tm * BM;
+    const int n0 = tn * BN;
+    const int k0 = blockIdx.y * A.share, k1 = min(A.k, k0 + A.share), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
+    f32x4 acc[S::MF][S::NF] = {};
+    // At the end of step s the tiles of step s + 1 have to be there, and only those
+    // of the steps behind it may be under way.  Steps past the last are replaced by
+    // the last, so that this count holds in every step.
+    const typename S::Places at = S::places(A, t0, n0);
+    constexpr int kUnits = S::kStage / 16;
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0, k0 + min(s, steps - 1) * S::STEP, lds + s * kUnits);
+        wait_and_meet<S::kAhead>();
+    }
+    int use = 0, fill = STAGES - 1;                           // the buffers of steps s and s + STAGES - 1
+    for (int s = 0; s < steps; ++s) {
+        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, lds + fill * kUnits, lds + use * kUnits, wm, wn,
+                              s & 1, acc);
+        wait_and_meet<S::kAhead>();
+        use = use == STAGES - 1 ? 0 : use + 1;
+        fill = fill == STAGES - 1 ? 0 : fill + 1;
+    }
+    if (k0 + steps * S::STEP < k1) {
+        wait_and_meet<0>();
+        S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
+        wait_and_meet<0>();
+        S::multiply(lds, wm, wn, steps & 1, acc);
+    }
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < S::MF; ++m) {
+        const int64_t t = t0 + wm * (BM / WM) + m * 16 + c;
+        if (t >= A.tokens) continue;
+#pragma unroll
+        for (int n = 0; n < S::NF; ++n) {
+            const int col = n0 + wn * (BN / WN) + n * 16 + 4 * g;
+            if (col >= A.n) continue;
+            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.pitch + col) = acc[m][n];
+            else finish<OUT>(A, t, col, acc[m][n]);
+        }
+    }
+    // Loads to LDS that no step used are still under way: they land before the workgroup ends.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// ------------------------------------------------------------ choice
+
+constexpr uint64_t kFew = 64;             // tokens of few_kernel
+
+struct Shape {
+    int bm, bn;
+    uint32_t shares;
+};
+
+// Microseconds of a step of a workgroup, as in the table of the E4M3 weight's input gradient.
+struct Cost {
+    int bm, bn;
+    double one, two;
+};
+constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
+constexpr Cost kCostsMx[] = {{256, 256, 1.65, 0.0}, {128, 128, 0.7, 1.1}};
+
+Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
+{
+    Shape best{128, 128, 1};
+    double least = -1.0;
+    const Cost* costs = mx ? kCostsMx : kCosts16;
+    const int count = mx ? 2 : 3, step = mx ? 256 : 64;
+    for (int i = 0; i < count; ++i) {
+        const Cost& c = costs[i];
+        if (c.bm > 128 && (uint64_t)c.bm / 2 >= tokens) continue;     // over half of the rows would be padding
+        const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        for (uint32_t s = 1; s <= 16 && (s == 1 || k / s >= (uint64_t)4 * step); ++s) {
+            const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
+            const double full = c.two > 0.0 ? c.two : c.one;
+            const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
+            const double us = turns * ((k + s - 1) / s + step - 1) / step + (s > 1 ? 4.0 + 8.0 * s * tokens * n / 5e6 : 0.0);
+            if (least < 0.0 || us < least) {
+                least = us;
+                best = Shape{c.bm, c.bn, s};
+            }
+        }
+    }
+    return best;
+}
+
+bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
+{
+    return tokens <= ECF8A_MAX_TOKENS && n >= 1 && n <= ECF8A_MAX_FEATURES && k >= ECF8X_BLOCK && k <= ECF8A_MAX_FEATURES &&
+           k % ECF8X_BLOCK == 0;
+}
+
+template <int XT, int OUT, int RF, int MF>
+int launch_few(const Args& A, hipStream_t st)
+{
+    few_kernel<XT, OUT, RF, MF><<<(A.n + 16 * RF - 1) / (16 * RF), kThreads, kWaves * RF * MF * 1024, st>>>(A);
+    return launch_status();
+}
+
+template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
+int launch_tile(Args A, uint32_t shares, hipStream_t st)
+{
+    constexpr int bytes = Tile<XT, BM, BN, WM, WN, STAGES>::kLds;
+    auto* kernel = tile_kernel<XT, OUT, BM, BN, WM, WN, STAGES>;
+    if (bytes > 65536 &&
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return ECF8_ERR_HIP;
+    A.tiles_m = (int)((A.tokens + BM - 1) / BM);
+    A.tiles_n = (A.n + BN - 1) / BN;
+    kernel<<<dim3((uint32_t)A.tiles_m * A.tiles_n, shares), kThreads, bytes, st>>>(A);
+    return launch_status();
+}
+
+template <int XT, int OUT>
+int run(const Args& A, const Shape& s, hipStream_t st)
+{
+    if (A.tokens <= 16) return launch_few<XT, OUT, 1, 1>(A, st);
+    if (A.tokens <= 32) return launch_few<XT, OUT, 2, 2>(A, st);
+    if (A.tokens <= (int64_t)kFew) return launch_few<XT, OUT, 2, 4>(A, st);
+    int rc;
+    if constexpr (XT == kMx4) {
+        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 2>(A, s.shares, st);
+        else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 2>(A, s.shares, st);
+    } else {
+        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 3>(A, s.shares, st);
+        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 3>(A, s.shares, st);
+        else rc = launch_tile<XT, OUT, 128, 128, 4, 2, 3>(A, s.shares, st);
+    }
+    if (rc != ECF8_OK || s.shares < 2) return rc;
+    const uint64_t units = (uint64_t)A.tokens * A.pitch / 4;
+    join_kernel<OUT><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.planes, A.tokens, A.n, A.pitch, (int)s.shares, A.bias, A.y, A.ld_y);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" uint64_t ecf8x_linear_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t x_type)
+{
+    if (!sizes_ok(tokens, out_features, in_features) || tokens <= kFew) return 0;
+    const uint64_t s = shape_of(tokens, out_features, in_features, x_type == ECF8X_MX4).shares;
+    return s > 1 ? round_up(4 * s * tokens * round_up(out_features, 4), 256) : 0;
+}
+
+extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_x, uint32_t x_type, uint64_t tokens, uint64_t out_features,
+                            uint64_t in_features, const ecf8x_matrix* w, const void* bias, uint32_t y_type, void* y, uint64_t ld_y,
+                            void* workspace, uint64_t workspace_bytes, void* hip_stream)
+{
+    const bool mx = x_type == ECF8X_MX4;
+    if ((y_type != ECF8A_BF16 && y_type != ECF8A_FP16) || (!mx && x_type != y_type)) return ECF8_ERR_UNSUPPORTED;
+    if (!sizes_ok(tokens, out_features, in_features)) return ECF8_ERR_SIZE;
+    if (tokens == 0) return ECF8_OK;
+    if (tokens == 1) ld_x = in_features, ld_y = out_features;
+    if (!x || !w || !w->codes || !w->scales || !y || !aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(y, 2) ||
+        !aligned(bias, 2) || (mx ? !x_scales || !aligned(x_scales, 4) : x_scales != nullptr || (tokens > 1 && ld_x % 8)))
+        return ECF8_ERR_ARG;
+    if ((!mx && (ld_x < in_features || ld_x > (1u << 22))) || ld_y < out_features || ld_y > (1ull << 40)) return ECF8_ERR_SIZE;
+    const uint64_t need = ecf8x_linear_bytes(tokens, out_features, in_features, x_type);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
+    Shape s{128, 128, 1};
+    if (tokens > kFew) s = shape_of(tokens, out_features, in_features, mx);
+    Args A{};
+    A.x = x;
+    A.x_scales = x_scales;
+    A.ld_x = (int64_t)ld_x;
+    A.w = w->codes;
+    A.w_scales = w->scales;
+    A.bias = static_cast<const uint16_t*>(bias);
+    A.y = static_cast<uint16_t*>(y);
+    A.ld_y = (int64_t)ld_y;
+    A.planes = s.shares > 1 ? static_cast<float*>(workspace) : nullptr;
+    A.tokens = (int64_t)tokens;
+    A.n = (int)out_features;
+    A.k = (int)in_features;
+    A.kp = (int)padded(in_features);
+    A.pitch = (int)round_up(out_features, 4);
+    A.share = (int)round_up((in_features + s.shares - 1) / s.shares, 256);
+    A.vector = ld_y % 4 == 0 && aligned(y, 8);
+    hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const bool b = y_type == ECF8A_BF16;
+    if (mx) return b ? run<kMx4, kBf16>(A, s, st) : run<kMx4, kFp16>(A, s, st);
+    return b ? run<kBf16, kBf16>(A, s, st) : run<kFp16, kFp16>(A, s, st);
+}
