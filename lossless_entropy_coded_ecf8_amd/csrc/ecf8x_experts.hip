@@ -3,11 +3,10 @@
 //
 // What bounds the products is reading the chosen experts' weights, once.  Two
 // kernels: gate and up with the activation (h of every pair of a token and an
-// expert), then down and the weighted sum over a token's experts.  Weights go
-// from memory to registers, 64 contiguous bytes a lane, and are widened there
-// (exact); rows of the weight are operand A, the tokens of one expert operand B
-// of the matrix instruction.  No sum crosses a workgroup.
-#include "ecf8x_common.h"
+// expert), then down and the weighted sum over a token's experts.  Weights are
+// widened exactly; rows of the weight are operand A, the tokens of one expert
+// operand B of the matrix instruction.
+#include "ecf8x_stream.h"
 
 namespace {
 
@@ -130,8 +129,9 @@ struct MoeArgs {
     uint16_t* h;                // [pair][2][inner]: upper and lower bfloat16
     uint16_t* y;
     int64_t ld_y;
-    int tokens, top, pairs, features, inner, experts;
-    int slots;                  // sums that the second kernel has room for
+    float* part;                // [pair][features]
+    uint32_t* counters;         // of the second kernel's tiles: workgroups that have ended
+    int tokens, top, pairs, features, inner, experts, tiles;
     bool vector;                // y's rows take 8-byte stores
 };
 
@@ -185,232 +185,130 @@ __device__ __forceinline__ int group(const MoeArgs& A, Groups& G)
     return chosen;
 }
 
-// What 64 contiguous bytes of a weight row, a lane's share of a step, need: chunks
-// of 16 bytes, each VALUES values and OPS operands.
+// Bytes and scale bytes of a stored row.
 template <int W>
-struct Format {
-    static constexpr int VALUES = W == kMx4 ? 32 : 16, OPS = VALUES / 8;
-    static constexpr int UNIT = 4 * VALUES;                   // values of a lane's 64 bytes
+__device__ __forceinline__ uint32_t row_bytes(int cols) { return W == kMx4 ? (cols + 127) / 128 * 64 : cols; }
 
-    // Bytes and scale bytes of a stored row.
-    static __device__ __forceinline__ int64_t row_bytes(int cols) { return W == kMx4 ? (cols + 127) / 128 * 64 : cols; }
-    static __device__ __forceinline__ int64_t row_scales(int cols) { return (cols + 127) / 128 * 4; }
-};
+__device__ __forceinline__ uint32_t row_scales(int cols) { return (cols + 127) / 128 * 4; }
 
-// The 64 bytes of a row's unit, nothing past the last column; their scales.
-template <int W>
-struct Weights {
-    u32x4 chunk[4];
-    uint32_t scales;
-
-    __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* row_scales, int unit, bool in, int cols)
-    {
-        scales = 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) chunk[s] = u32x4{0, 0, 0, 0};
-        if (!in) return;
-        if constexpr (W == kMx4) {                            // stored rows are whole units
-            scales = *reinterpret_cast<const uint32_t*>(row_scales + 4 * unit);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) chunk[s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + 64 * unit + 16 * s));
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (64 * unit + 16 * s < cols) chunk[s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + 64 * unit + 16 * s));
-        }
-    }
-
-    // Operand j of chunk s, in TYPE (4-bit weights: bfloat16).
-    template <int TYPE>
-    __device__ __forceinline__ u32x4 operand(int s, int j) const
-    {
-        if constexpr (W == kMx4) return widen4(chunk[s][j], scale_of(scales >> (8 * s) & 255));
-        return widen8<TYPE>(chunk[s][2 * j], chunk[s][2 * j + 1]);
-    }
-};
-
-// h of every pair: a workgroup takes 16 rows of gate and of up of one expert, its
-// eight waves a share of the reduction each.
-template <int W, int TYPE, int MF>
+// h of every pair: a workgroup takes as many rows of gate as of up of one expert,
+// fragment 0 of a row group of the one, fragment 1 of the other.
+template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs A)
 {
-    typedef Format<W> F;
+    typedef Stream<W, TYPE, MF, RG> S;
     __shared__ Groups G;
-    __shared__ f32x4 sums[kWaves][2][MF][64];
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    if (blockIdx.x == 0 && blockIdx.y == 0)                   // nothing counts in the second kernel before this one ends
+        for (int i = threadIdx.x; i < A.tiles; i += kThreads) A.counters[i] = 0;
     const int chosen = group(A, G);
     if ((int)blockIdx.y >= chosen) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int e = G.expert[blockIdx.y], first = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - first;
-    const int i0 = blockIdx.x * 16;
-    const int64_t row = (int64_t)e * A.inner + min(i0 + c, A.inner - 1);       // rows past the last reach no result that is stored
-    const uint8_t *wg = A.gate.codes + row * F::row_bytes(A.features), *wu = A.up.codes + row * F::row_bytes(A.features);
-    const uint8_t *sg = A.gate.scales + row * F::row_scales(A.features), *su = A.up.scales + row * F::row_scales(A.features);
-    const int units = (A.features + F::UNIT - 1) / F::UNIT, u0 = units * wave / kWaves, u1 = units * (wave + 1) / kWaves;
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
+    const int i0 = blockIdx.x * (S::R / 2), frag = S::fragment(wave), first = min(i0 + 16 * (frag / 2), A.inner - 1);
+    const Matrix& w = frag & 1 ? A.up : A.gate;
+    const int64_t row = (int64_t)e * A.inner + first;         // rows past the last reach no result that is stored
+    const typename S::Rows rows{w.codes + row * row_bytes<W>(A.features), w.scales + row * row_scales(A.features), A.inner - 1 - first};
     for (int p0 = 0; p0 < count; p0 += 16 * MF) {
-        const uint16_t* x[MF];
-        bool there[MF];
+        const typename S::Places at = S::places(rows, row_bytes<W>(A.features), row_scales(A.features), A.x, nullptr, 0, [&](int i) {
+            return (uint32_t)(G.pair[begin + min(p0 + i, count - 1)] / A.top) * (uint32_t)A.ld_x * 2;
+        });
+        f32x4 acc[2][MF] = {};
+        if (p0) __syncthreads();                              // the sums of the pairs before are read
+        S::run(rows, at, A.x, nullptr, A.features, lds, acc);
+        if (wave >= RG) continue;
+        const float fa = A.gate.factors ? A.gate.factors[e] : 1.0f, fb = A.up.factors ? A.up.factors[e] : 1.0f;
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            there[m] = p0 + 16 * m + c < count;
-            x[m] = A.x + (int64_t)(G.pair[first + min(p0 + 16 * m + c, count - 1)] / A.top) * A.ld_x;
-        }
-        f32x4 acc[2][MF] = {};
-        for (int u = u0; u < u1; u += 4) {
-            const int unit = u + g;
-            const bool in = unit < u1;
-            Weights<W> a, b;
-            a.load(wg, sg, unit, in, A.features);
-            b.load(wu, su, unit, in, A.features);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = unit * F::UNIT + s * F::VALUES;
-                u32x4 v[MF][F::OPS];
-#pragma unroll
-                for (int m = 0; m < MF; ++m) {
-#pragma unroll
-                    for (int j = 0; j < F::OPS; ++j) v[m][j] = u32x4{0, 0, 0, 0};
-                    if (in && there[m] && k < A.features) {
-#pragma unroll
-                        for (int j = 0; j < F::OPS; ++j) v[m][j] = *reinterpret_cast<const u32x4*>(x[m] + k + 8 * j);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < F::OPS; ++j) {
-                    const u32x4 wa = a.template operand<TYPE>(s, j), wb = b.template operand<TYPE>(s, j);
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        if constexpr (W == kMx4 && TYPE == kFp16) {
-                            u32x4 hi, lo;
-                            split8_f16(v[m][j], hi, lo);
-                            acc[0][m] = mfma_bf16(wa, hi, acc[0][m]);
-                            acc[1][m] = mfma_bf16(wb, hi, acc[1][m]);
-                            acc[0][m] = mfma_bf16(wa, lo, acc[0][m]);
-                            acc[1][m] = mfma_bf16(wb, lo, acc[1][m]);
-                        } else {
-                            acc[0][m] = mfma<TYPE>(wa, v[m][j], acc[0][m]);
-                            acc[1][m] = mfma<TYPE>(wb, v[m][j], acc[1][m]);
-                        }
-                    }
-                }
-            }
-        }
-        if (p0) __syncthreads();                              // the sums of the pairs before are read
-#pragma unroll
-        for (int m = 0; m < MF; ++m) sums[wave][0][m][lane] = acc[0][m], sums[wave][1][m][lane] = acc[1][m];
-        __syncthreads();
-        const int m = wave, at = p0 + 16 * m + c, i = i0 + 4 * g;
-        if (m < MF && at < count && i < A.inner) {
-            f32x4 a{0, 0, 0, 0}, b{0, 0, 0, 0}, h;
-#pragma unroll
-            for (int q = 0; q < kWaves; ++q) a += sums[q][0][m][lane], b += sums[q][1][m][lane];
-            const float fa = A.gate.factors ? A.gate.factors[e] : 1.0f, fb = A.up.factors ? A.up.factors[e] : 1.0f;
+            const int p = p0 + 16 * m + c, i = i0 + 16 * wave + 4 * g;
+            if (p >= count || i >= A.inner) continue;
+            f32x4 h;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float v = a[q] * fa;
-                h[q] = v / (1.0f + expf(-v)) * (b[q] * fb);
+                const float v = acc[0][m][q] * fa;
+                h[q] = v / (1.0f + expf(-v)) * (acc[1][m][q] * fb);
             }
             uint32_t hi[2], lo[2];
             split2(h[0], h[1], hi[0], lo[0]);
             split2(h[2], h[3], hi[1], lo[1]);
-            uint16_t* out = A.h + (int64_t)G.pair[first + at] * 2 * A.inner + i;   // inner is a multiple of 16
+            uint16_t* out = A.h + (int64_t)G.pair[begin + p] * 2 * A.inner + i;      // inner is a multiple of 16
             *reinterpret_cast<uint2*>(out) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(out + A.inner) = make_uint2(lo[0], lo[1]);
         }
     }
 }
 
-// y: a workgroup takes 16 RF features of every chosen expert, a wave an expert (or
-// a share of its reduction, where few are chosen) at a time.  Each pair's sums go to
-// a place of their own in LDS, and a token's are added in the order of its choices.
-template <int W, int TYPE, int RF, int MF>
+// Sums that workgroups on other dies read: written through the die's own cache, and
+// read past it.  (Plain stores and a release fence, which writes that whole cache
+// back, took 114 us where this takes 30: one token, 8 experts, 117 MB of weights.)
+constexpr int kPastDie = 16;
+
+__device__ __forceinline__ void put(Rsrc r, uint32_t at, f32x4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at, 0, kPastDie);
+}
+
+__device__ __forceinline__ f32x4 get(Rsrc r, uint32_t at)
+{
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kPastDie));
+}
+
+// y: a workgroup takes R features of one expert and leaves its pairs' sums in the
+// workspace; the last one of these features to end adds them up, a token's in the
+// order of its choices, whichever workgroup that is.
+template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
 {
-    typedef Format<W> F;
+    typedef Stream<W, kPair, MF, RG> S;
     __shared__ Groups G;
-    extern __shared__ f32x4 sums[];                           // [share][pair][4 RF]
+    __shared__ uint32_t ended;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
     const int chosen = group(A, G);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int k0 = blockIdx.x * 16 * RF;
-    int shares = 1;
-    while (shares < kWaves && chosen * shares < kWaves && 2 * shares * A.pairs <= A.slots) shares *= 2;
-    const int units = (A.inner + F::UNIT - 1) / F::UNIT;
-    for (int job = wave; job < chosen * shares; job += kWaves) {
-        const int r = job / shares, share = job % shares, u0 = units * share / shares, u1 = units * (share + 1) / shares;
-        const int e = G.expert[r], first = G.first[r], count = G.first[r + 1] - first;
-        const uint8_t *w[RF], *ws[RF];
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            const int64_t row = (int64_t)e * A.features + min(k0 + 16 * f + c, A.features - 1);
-            w[f] = A.down.codes + row * F::row_bytes(A.inner);
-            ws[f] = A.down.scales + row * F::row_scales(A.inner);
-        }
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int k0 = blockIdx.x * S::R;
+    const Rsrc part = buffer_of(A.part);
+    if ((int)blockIdx.y >= (chosen ? chosen : 1)) return;
+    if (chosen) {
+        const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
+        const int first = min(k0 + 16 * S::fragment(wave), A.features - 1);
+        const int64_t row = (int64_t)e * A.features + first;
+        const typename S::Rows rows{A.down.codes + row * row_bytes<W>(A.inner), A.down.scales + row * row_scales(A.inner), A.features - 1 - first};
         const float factor = A.down.factors ? A.down.factors[e] : 1.0f;
         for (int p0 = 0; p0 < count; p0 += 16 * MF) {
-            const uint16_t* h[MF];
-            bool there[MF];
-            int pair[MF];
+            const typename S::Places at = S::places(rows, row_bytes<W>(A.inner), row_scales(A.inner), A.h, nullptr, 2 * A.inner, [&](int i) {
+                return (uint32_t)G.pair[begin + min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
+            });
+            f32x4 acc[S::RF][MF] = {};
+            if (p0) __syncthreads();
+            S::run(rows, at, A.h, nullptr, A.inner, lds, acc);
+            if (wave >= RG) continue;
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                there[m] = p0 + 16 * m + c < count;
-                pair[m] = G.pair[first + min(p0 + 16 * m + c, count - 1)];
-                h[m] = A.h + (int64_t)pair[m] * 2 * A.inner;
-            }
-            f32x4 acc[RF][MF] = {};
-            for (int u = u0; u < u1; u += 4) {
-                const int unit = u + g;
-                const bool in = unit < u1;
-                Weights<W> a[RF];
+            for (int f = 0; f < S::RF; ++f)
 #pragma unroll
-                for (int f = 0; f < RF; ++f) a[f].load(w[f], ws[f], unit, in, A.inner);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k = unit * F::UNIT + s * F::VALUES;
-                    u32x4 v[2][MF][F::OPS];
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-#pragma unroll
-                        for (int j = 0; j < F::OPS; ++j) v[0][m][j] = v[1][m][j] = u32x4{0, 0, 0, 0};
-                        if (in && there[m] && k < A.inner) {
-#pragma unroll
-                            for (int j = 0; j < F::OPS; ++j) {
-                                v[0][m][j] = *reinterpret_cast<const u32x4*>(h[m] + k + 8 * j);
-                                v[1][m][j] = *reinterpret_cast<const u32x4*>(h[m] + A.inner + k + 8 * j);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < F::OPS; ++j)
-#pragma unroll
-                        for (int f = 0; f < RF; ++f) {
-                            const u32x4 wide = a[f].template operand<kBf16>(s, j);
-#pragma unroll
-                            for (int m = 0; m < MF; ++m) {
-                                acc[f][m] = mfma_bf16(wide, v[0][m][j], acc[f][m]);
-                                acc[f][m] = mfma_bf16(wide, v[1][m][j], acc[f][m]);
-                            }
-                        }
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MF; ++m)
-                if (there[m]) {
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) sums[(share * A.pairs + pair[m]) * 4 * RF + 4 * f + g] = acc[f][m] * factor;
+                for (int m = 0; m < MF; ++m) {
+                    const int p = p0 + 16 * m + c, k = k0 + 16 * (wave * S::RF + f) + 4 * g;
+                    if (p < count && k < A.features)          // features are a multiple of 16
+                        put(part, 4 * (G.pair[begin + p] * (uint32_t)A.features + k), acc[f][m] * factor);
                 }
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // every wave's sums are where other dies see them
+        __syncthreads();
+        if (threadIdx.x == 0) ended = __hip_atomic_fetch_add(A.counters + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if ((int)ended != chosen - 1) return;
+        asm volatile("" ::: "memory");
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < A.tokens * 4 * RF; i += kThreads) {
-        const int t = i / (4 * RF), q = i % (4 * RF), k = k0 + 4 * q;
+    constexpr int kQuads = S::R / 4;
+    for (int i = threadIdx.x; i < A.tokens * kQuads; i += kThreads) {
+        const int t = i / kQuads, k = k0 + 4 * (i % kQuads);
+        if (k >= A.features) continue;
         f32x4 y{0, 0, 0, 0};
         for (int j = 0; j < A.top; ++j) {
             const int pair = t * A.top + j, id = A.ids[pair];
             if (id < 0 || id >= A.experts) continue;
-            f32x4 v = sums[pair * 4 * RF + q];
-            for (int s = 1; s < shares; ++s) v += sums[(s * A.pairs + pair) * 4 * RF + q];
-            y += v * A.weights[pair];
+            y += get(part, 4 * (pair * (uint32_t)A.features + k)) * A.weights[pair];
         }
-        if (k < A.features) store4<TYPE>(A.y + t * A.ld_y + k, y, 4, A.vector);     // features: a multiple of 16
+        store4<TYPE>(A.y + t * A.ld_y + k, y, 4, A.vector);
     }
 }
 
@@ -423,17 +321,30 @@ void route(const RouteArgs& A, hipStream_t st)
     else route_kernel<TYPE, 16><<<grid, 256, 0, st>>>(A);
 }
 
-// A second kernel's rows of 16 features, and the room for its sums.
-constexpr int kRows = 1;
-
-template <int W, int TYPE, int MF>
-int moe(const MoeArgs& A, hipStream_t st)
+template <class Kernel>
+int allow(Kernel* kernel, int bytes)
 {
-    const int most = A.pairs < A.experts ? A.pairs : A.experts;
-    gate_up_kernel<W, TYPE, MF><<<dim3((A.inner + 15) / 16, most), kThreads, 0, st>>>(A);
+    return bytes <= 65536 || hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess
+               ? ECF8_OK
+               : ECF8_ERR_HIP;
+}
+
+// Features of a workgroup of the second kernel: the fewest that any choice below has.
+constexpr uint64_t kLeastRows = 64;
+
+template <int W, int TYPE, int MF, int RG>
+int moe(MoeArgs A, hipStream_t st)
+{
+    typedef Stream<W, TYPE, MF, RG> First;
+    typedef Stream<W, kPair, MF, RG> Second;
+    const int most = A.pairs < A.experts ? A.pairs : A.experts, rows = First::R / 2;
+    A.tiles = (A.features + Second::R - 1) / Second::R;
+    if (allow(gate_up_kernel<W, TYPE, MF, RG>, First::kLds) != ECF8_OK || allow(down_kernel<W, TYPE, MF, RG>, Second::kLds) != ECF8_OK)
+        return ECF8_ERR_HIP;
+    gate_up_kernel<W, TYPE, MF, RG><<<dim3((A.inner + rows - 1) / rows, most), kThreads, First::kLds, st>>>(A);
     const int rc = launch_status();
     if (rc != ECF8_OK) return rc;
-    down_kernel<W, TYPE, kRows, MF><<<(A.features + 16 * kRows - 1) / (16 * kRows), kThreads, A.slots * kRows * 64, st>>>(A);
+    down_kernel<W, TYPE, MF, RG><<<dim3(A.tiles, most), kThreads, Second::kLds, st>>>(A);
     return launch_status();
 }
 
@@ -441,8 +352,8 @@ template <int W, int TYPE>
 int moe(const MoeArgs& A, hipStream_t st)
 {
     // Columns of the matrix instructions: 16 where an expert meets few tokens.
-    if (A.tokens <= 16 || A.pairs <= 8 * A.experts) return moe<W, TYPE, 1>(A, st);
-    return moe<W, TYPE, 2>(A, st);
+    if (A.tokens <= 16 || A.pairs <= 8 * A.experts) return moe<W, TYPE, 1, 4>(A, st);
+    return moe<W, TYPE, 2, 4>(A, st);
 }
 
 bool layer_ok(const ecf8x_experts& L)
@@ -480,7 +391,9 @@ extern "C" int ecf8x_route(const void* logits, uint64_t ld, uint32_t type, uint6
 extern "C" uint64_t ecf8x_moe_bytes(uint64_t tokens, uint32_t top, const ecf8x_experts* layer)
 {
     if (!layer || !layer_ok(*layer) || top > ECF8X_MAX_TOP || tokens > ECF8X_MAX_PAIRS || tokens * top > ECF8X_MAX_PAIRS) return 0;
-    return round_up(tokens * top * 4 * layer->inner, 256);
+    // h, the pairs' sums, the counters
+    return round_up(tokens * top * 4 * layer->inner, 256) + round_up(tokens * top * 4 * layer->features, 256) +
+           round_up(4 * ((layer->features + kLeastRows - 1) / kLeastRows), 256);
 }
 
 extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t tokens, uint32_t top, const int32_t* ids, const float* weights,
@@ -495,7 +408,7 @@ extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t t
     if (!x || !y || !ids || !weights || !aligned(x, 16) || !aligned(y, 2) || !aligned(ids, 4) || !aligned(weights, 4) || (tokens > 1 && ld_x % 8) ||
         !matrix_ok(layer->gate, mx) || !matrix_ok(layer->up, mx) || !matrix_ok(layer->down, mx))
         return ECF8_ERR_ARG;
-    if (ld_x < layer->features || ld_y < layer->features || ld_x > (1ull << 40) || ld_y > (1ull << 40)) return ECF8_ERR_SIZE;
+    if (ld_x < layer->features || ld_y < layer->features || ld_x > (1u << 21) || ld_y > (1ull << 40)) return ECF8_ERR_SIZE;   // 512 rows: 32-bit offsets
     const uint64_t need = ecf8x_moe_bytes(tokens, top, layer);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ECF8_ERR_WORKSPACE;
     MoeArgs A{};
@@ -508,6 +421,8 @@ extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t t
     A.ids = ids;
     A.weights = weights;
     A.h = static_cast<uint16_t*>(workspace);
+    A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * top * 4 * layer->inner, 256));
+    A.counters = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(A.part) + round_up(tokens * top * 4 * layer->features, 256));
     A.y = static_cast<uint16_t*>(y);
     A.ld_y = (int64_t)ld_y;
     A.tokens = (int)tokens;
@@ -516,7 +431,6 @@ extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t t
     A.features = (int)layer->features;
     A.inner = (int)layer->inner;
     A.experts = (int)layer->experts;
-    A.slots = A.pairs * kWaves < kPairs ? A.pairs * kWaves : kPairs;
     A.vector = ld_y % 4 == 0 && aligned(y, 8);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     if (mx) return type == ECF8A_BF16 ? moe<kMx4, kBf16>(A, st) : moe<kMx4, kFp16>(A, st);

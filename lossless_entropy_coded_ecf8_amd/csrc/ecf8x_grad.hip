@@ -7,7 +7,7 @@
 // per workgroup, on their way to LDS, and the operands are turned there by the
 // transposing LDS read.  Widened values are exact bfloat16; float16 dy is split
 // into two bfloat16 (exact).  Sums in float32, rounded once.
-#include "ecf8x_common.h"
+#include "ecf8x_stream.h"
 
 namespace {
 
@@ -27,16 +27,8 @@ struct Args {
     int tiles_m, tiles_n;
 };
 
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-typedef __attribute__((address_space(3))) void LdsMem;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 LdsQuad;
-
-// Every offset used with it is inside the operand, so the range is left open.
-__device__ __forceinline__ Rsrc buffer_of(const void* p)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
-}
 
 // One workgroup: BM tokens by BN columns of dx, eight waves in WM rows of WN, 64
 // rows of the weight at a time.  dy's tile goes straight to LDS, ahead by
@@ -173,14 +165,6 @@ struct Tile {
         return later;
     }
 };
-
-template <int LOADS>
-__device__ __forceinline__ void wait_and_meet()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)

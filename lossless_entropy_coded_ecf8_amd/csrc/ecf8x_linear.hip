@@ -6,7 +6,7 @@
 // products, summed in float32.  float16 x is split into two bfloat16 (exact),
 // since a block's power of two need not fit float16.  Four-bit x: the scaled
 // matrix instruction takes codes and scale bytes as they are stored.
-#include "ecf8x_common.h"
+#include "ecf8x_stream.h"
 
 namespace {
 
@@ -43,131 +43,33 @@ __device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
 }
 
 // ------------------------------------------------------------ few tokens
-//
-// A workgroup takes 16 RF rows of the weight, its eight waves a share of the
-// reduction each, and joins the eight sums in LDS.  Weights go from memory to
-// registers, 64 contiguous bytes a lane; x comes through the caches.
-// Lane (c, g) holds chunks of row c of the weight and of token c.
-template <int XT, int OUT, int RF, int MF>
+
+template <int XT, int OUT, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 {
-    extern __shared__ f32x4 sums[];                           // [wave][RF][MF][lane]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16 * RF, row_bytes = A.kp / 2, row_scales = A.kp / 32;
-    const int units = A.kp / 128, u0 = units * wave / kWaves, u1 = units * (wave + 1) / kWaves;
-    const uint8_t *w[RF], *ws[RF];
+    typedef Stream<kMx4, XT, MF, RG> S;
+    extern __shared__ __attribute__((aligned(16))) char few_lds[];
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * S::R, row_bytes = A.kp / 2, row_scales = A.kp / 32;
+    const int first = min(n0 + 16 * S::fragment(wave), A.n - 1);       // rows past the last reach no result that is stored
+    const typename S::Rows rows{A.w + (int64_t)first * row_bytes, A.w_scales + (int64_t)first * row_scales, A.n - 1 - first};
+    const typename S::Places at = S::places(rows, row_bytes, row_scales, A.x, A.x_scales, 0, [&](int i) {
+        const uint32_t t = (uint32_t)min((int64_t)i, A.tokens - 1);
+        return XT == kMx4 ? t : 2 * t * (uint32_t)A.ld_x;
+    });
+    f32x4 acc[S::RF][MF] = {};
+    S::run(rows, at, A.x, A.x_scales, XT == kMx4 ? A.kp : A.k, few_lds, acc);
+    if (wave >= RG) return;
 #pragma unroll
-    for (int r = 0; r < RF; ++r) {
-        const int64_t row = min(n0 + 16 * r + c, A.n - 1);    // rows past the last reach no result that is stored
-        w[r] = A.w + row * row_bytes;
-        ws[r] = A.w_scales + row * row_scales;
-    }
-    f32x4 acc[RF][MF] = {};
-    for (int u = u0; u < u1; u += 4) {
-        const int unit = u + g;                               // this lane group's 128 values
-        const bool in = unit < u1;
-        u32x4 b[RF][4];
-        uint32_t sb[RF];
+    for (int f = 0; f < S::RF; ++f)
 #pragma unroll
-        for (int r = 0; r < RF; ++r) {
-            sb[r] = 0;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) b[r][s] = u32x4{0, 0, 0, 0};
-            if (in) {
-                sb[r] = *reinterpret_cast<const uint32_t*>(ws[r] + unit * 4);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) b[r][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[r] + unit * 64 + 16 * s));
-            }
+        for (int m = 0; m < MF; ++m) {
+            const int n = n0 + 16 * (wave * S::RF + f) + 4 * g, t = 16 * m + c;
+            if (t < A.tokens && n < A.n) finish<OUT>(A, t, n, acc[f][m]);
         }
-        if constexpr (XT == kMx4) {
-            u32x4 a[MF][4];
-            uint32_t sa[MF];
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const int64_t t = 16 * m + c;
-                sa[m] = 0;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[m][s] = u32x4{0, 0, 0, 0};
-                if (in && t < A.tokens) {
-                    sa[m] = *reinterpret_cast<const uint32_t*>(A.x_scales + t * row_scales + unit * 4);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        a[m][s] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(A.x) + t * row_bytes + unit * 64 + 16 * s);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < RF; ++r)
-#pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    acc[r][m] = mfma_mx4<0>(b[r][0], a[m][0], acc[r][m], sb[r], sa[m]);
-                    acc[r][m] = mfma_mx4<1>(b[r][1], a[m][1], acc[r][m], sb[r], sa[m]);
-                    acc[r][m] = mfma_mx4<2>(b[r][2], a[m][2], acc[r][m], sb[r], sa[m]);
-                    acc[r][m] = mfma_mx4<3>(b[r][3], a[m][3], acc[r][m], sb[r], sa[m]);
-                }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = unit * 128 + 32 * s;
-                u32x4 a[MF][4];
-#pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    const int64_t t = 16 * m + c;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a[m][j] = u32x4{0, 0, 0, 0};
-                    if (in && k < A.k && t < A.tokens) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            a[m][j] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(A.x) + t * A.ld_x + k + 8 * j);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u32x4 wide[RF];
-#pragma unroll
-                    for (int r = 0; r < RF; ++r) wide[r] = widen4(b[r][s][j], scale_of(sb[r] >> (8 * s) & 255));
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        if constexpr (XT == kBf16) {
-#pragma unroll
-                            for (int r = 0; r < RF; ++r) acc[r][m] = mfma_bf16(wide[r], a[m][j], acc[r][m]);
-                        } else {
-                            u32x4 hi, lo;
-                            split8_f16(a[m][j], hi, lo);
-#pragma unroll
-                            for (int r = 0; r < RF; ++r) {
-                                acc[r][m] = mfma_bf16(wide[r], hi, acc[r][m]);
-                                acc[r][m] = mfma_bf16(wide[r], lo, acc[r][m]);
-                            }
-                        }
-                    }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RF; ++r)
-#pragma unroll
-        for (int m = 0; m < MF; ++m) sums[((wave * RF + r) * MF + m) * 64 + lane] = acc[r][m];
-    __syncthreads();
-    if (threadIdx.x >= RF * MF * 64) return;
-    f32x4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) v += sums[i * RF * MF * 64 + threadIdx.x];
-    const int m = (threadIdx.x >> 6) % MF, r = (threadIdx.x >> 6) / MF, n = n0 + 16 * r + 4 * g;
-    const int64_t t = 16 * m + c;
-    if (t < A.tokens && n < A.n) finish<OUT>(A, t, n, v);
 }
 
 // ------------------------------------------------------------ many tokens
-
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-typedef __attribute__((address_space(3))) void LdsMem;
-
-// Every offset used with it is inside the operand, so the range is left open.
-__device__ __forceinline__ Rsrc buffer_of(const void* p)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
-}
 
 // One workgroup: BM tokens by BN outputs, eight waves in WM rows of WN, the
 // reduction in steps of 128 bytes of an x row: 64 values of 16 bits (32 bytes of
@@ -369,16 +271,6 @@ struct Tile {
     }
 };
 
-// All but the newest LOADS loads have arrived, and every LDS access is done, in
-// every wave of the workgroup.
-template <int LOADS>
-__device__ __forceinline__ void wait_and_meet()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 {
@@ -485,10 +377,15 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
            k % ECF8X_BLOCK == 0;
 }
 
-template <int XT, int OUT, int RF, int MF>
+template <int XT, int OUT, int MF, int RG>
 int launch_few(const Args& A, hipStream_t st)
 {
-    few_kernel<XT, OUT, RF, MF><<<(A.n + 16 * RF - 1) / (16 * RF), kThreads, kWaves * RF * MF * 1024, st>>>(A);
+    typedef Stream<kMx4, XT, MF, RG> S;
+    auto* kernel = few_kernel<XT, OUT, MF, RG>;
+    if (S::kLds > 65536 &&
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds) != hipSuccess)
+        return ECF8_ERR_HIP;
+    kernel<<<(A.n + S::R - 1) / S::R, kThreads, S::kLds, st>>>(A);
     return launch_status();
 }
 
@@ -509,9 +406,12 @@ int launch_tile(Args A, uint32_t shares, hipStream_t st)
 template <int XT, int OUT>
 int run(const Args& A, const Shape& s, hipStream_t st)
 {
-    if (A.tokens <= 16) return launch_few<XT, OUT, 1, 1>(A, st);
-    if (A.tokens <= 32) return launch_few<XT, OUT, 2, 2>(A, st);
-    if (A.tokens <= (int64_t)kFew) return launch_few<XT, OUT, 2, 4>(A, st);
+    if (A.tokens <= (int64_t)kFew) {
+        // Row groups: 64 rows a workgroup until those of 128 give every compute unit one.
+        if (A.tokens <= 16) return A.n < 32768 ? launch_few<XT, OUT, 1, 2>(A, st) : launch_few<XT, OUT, 1, 4>(A, st);
+        if (A.tokens <= 32) return A.n < 16384 ? launch_few<XT, OUT, 2, 2>(A, st) : launch_few<XT, OUT, 2, 4>(A, st);
+        return launch_few<XT, OUT, 4, 4>(A, st);
+    }
     int rc;
     if constexpr (XT == kMx4) {
         if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 2>(A, s.shares, st);

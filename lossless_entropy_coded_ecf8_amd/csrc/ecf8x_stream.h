@@ -1,0 +1,316 @@
+// ecf8x_stream.h -- the product of a few tokens with a weight that is read once.
+//
+// What bounds it is the stream of weights from memory.  A workgroup of eight
+// waves takes R rows of the weight; both operands go from memory to LDS without
+// passing registers, 64 KG bytes of each row a step, into STAGES buffers, so that
+// all but one of them are on their way while one is multiplied.  (Loads to
+// registers in the matrix instruction's own layout, 16 rows in a run of lanes, came
+// at 2.2 to 2.9 TB/s; a run of lanes here reads whole rows.)  The waves stand in RG
+// row groups of 16 RF rows and KG shares of the step: a wave reads one 16-byte unit
+// of each of its rows a step, 16 values of E4M3 or a block of 32 in 4 bits, and
+// widens it for two or four operands, which meet the tokens of all its row fragments.
+//
+// Weight rows are operand A and tokens operand B: lane (c, g) of a result holds
+// token 16 m + c, rows 4 g .. 4 g + 3 of fragment f.
+#ifndef ECF8X_STREAM_H
+#define ECF8X_STREAM_H
+
+#include "ecf8x_common.h"
+
+namespace ecf8x {
+
+constexpr int kPair = 6;                  // x as two bfloat16 rows, the upper and the lower halves of its values
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef __attribute__((address_space(3))) void LdsMem;
+
+// Every offset used with it is inside the operand, so the range is left open.
+__device__ __forceinline__ Rsrc buffer_of(const void* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
+}
+
+// The wave's number, known to be the same in all of its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// All but the newest LOADS loads have arrived, and every LDS access is done, in
+// every wave of the workgroup.
+template <int LOADS>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int W, int X, int MF, int RG>
+struct Stream {
+    static constexpr int RF = 2, KG = 8 / RG, kThreads = 512;
+    static constexpr int R = 16 * RF * RG;                     // rows
+    static constexpr int VALUES = W == kMx4 ? 32 : 16;         // of a 16-byte unit of weights
+    static constexpr int STEP = 4 * KG * VALUES;               // values of a step
+    static constexpr int WU = 4 * KG;                          // units of a weight row's step
+    static constexpr int XU = X == kMx4 ? 4 * KG : X == kPair ? STEP / 4 : STEP / 8;   // of a token's
+    static constexpr int kW = R * WU, kX = 16 * MF * XU;       // units of a stage
+    static constexpr int kS = W == kMx4 ? R * KG : 0, kXS = X == kMx4 ? 16 * MF * KG : 0;   // dwords of scales
+    static constexpr int kStage = 16 * (kW + kX) + 4 * (kS + kXS);
+    // Two workgroups a compute unit where three stages fit for both, else one; 8 KB are left to the callers.
+    static constexpr int kFit = 72 * 1024 / kStage, STAGES = kFit >= 3 ? (kFit < 6 ? kFit : 6) : 152 * 1024 / kStage;
+    static constexpr int kLds = STAGES * kStage > 16 * 64 * 8 * RF * MF ? STAGES * kStage : 16 * 64 * 8 * RF * MF;
+    // Loads of a wave and a stage: the same in every wave, some with part of its lanes.
+    static constexpr int kEachX = kX / 8 < 64 ? 1 : kX / 512;
+    static constexpr int kLoads = kW / 512 + (kS > 0) + kEachX + (kXS > 0);
+    static constexpr int kAhead = (STAGES - 2) * kLoads;
+    static_assert(RG * KG == 8 && kW == 1024 && STAGES >= 2 && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
+    static_assert(kX % 8 == 0 && (kX / 8 < 64 || kX % 512 == 0) && kXS / 8 <= 64 && kS / 8 <= 64 && kStage % 16 == 0, "waves stage alike");
+
+    // Where unit u of a row of `units` lies, so that 16 rows' units of one number fall in different banks.
+    template <int UNITS>
+    static __device__ __forceinline__ int turn(int row) { return UNITS == 8 ? row >> 1 & 7 : row & 15; }
+
+    // The rows that this wave sends for, 16 RF RG / 8 of them: its fragment's first row, and the last that exists
+    // from there on.
+    struct Rows {
+        const uint8_t *codes, *scales;
+        int last;
+    };
+
+    // Fragment of the rows that wave w stages, in the order [row group][fragment].
+    static __device__ __forceinline__ int fragment(int w) { return w * (R / 8) / 16; }
+
+    struct Places {
+        Rsrc w, s, x, xs;
+        uint32_t at_w[2], at_s, at_x[kEachX], at_xs;
+    };
+
+    // token(i): byte offset of token row i (0 .. 16 MF - 1) from x, for kMx4 its number.
+    template <class Token>
+    static __device__ __forceinline__ Places places(const Rows& rows, uint32_t row_bytes, uint32_t row_scales, const void* x, const void* x_scales,
+                                                    uint32_t low, Token token)
+    {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        Places p;
+        p.w = buffer_of(rows.codes);
+        p.s = buffer_of(rows.scales);
+        p.x = buffer_of(x);
+        p.xs = buffer_of(x_scales);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int u = wave * 128 + i * 64 + lane, row = u / WU, local = row % 16;
+            p.at_w[i] = (uint32_t)min(local, rows.last) * row_bytes + 16 * ((u % WU) ^ turn<WU>(row));
+        }
+        p.at_s = p.at_xs = 0;
+        if constexpr (W == kMx4) {
+            const int d = wave * 32 + (lane & 31), row = d / KG;
+            p.at_s = (uint32_t)min(row % 16, rows.last) * row_scales + 4 * (d % KG);
+        }
+#pragma unroll
+        for (int i = 0; i < kEachX; ++i) {
+            const int u = kX / 8 < 64 ? wave * (kX / 8) + lane % (kX / 8) : wave * (kX / 8) + i * 64 + lane, row = u / XU;
+            const int unit = (u % XU) ^ turn<XU>(row);
+            if constexpr (X == kMx4) p.at_x[i] = (uint32_t)token(row) * row_bytes + 16 * unit;
+            else if constexpr (X == kPair) p.at_x[i] = (uint32_t)token(row) + (unit < XU / 2 ? 16 * unit : low + 16 * (unit - XU / 2));
+            else p.at_x[i] = (uint32_t)token(row) + 16 * unit;
+        }
+        if constexpr (X == kMx4) {
+            const int d = wave * (kXS / 8) + lane % (kXS / 8);
+            p.at_xs = (uint32_t)token(d / KG) * row_scales + 4 * (d % KG);
+        }
+        return p;
+    }
+
+    static __device__ __forceinline__ void stage(const Places& p, int step, char* buf)
+    {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        u32x4 *lw = reinterpret_cast<u32x4*>(buf), *lx = lw + kW;
+        uint32_t *ls = reinterpret_cast<uint32_t*>(lx + kX), *lxs = ls + kS;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(p.w, (LdsMem*)(lw + wave * 128 + i * 64), 16, p.at_w[i], step * 16 * WU, 0, 2);
+        if constexpr (W == kMx4) {
+            if (lane < 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.s, (LdsMem*)(ls + wave * 32), 4, p.at_s, step * 4 * KG, 0, 0);
+        }
+        const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;      // of a token's plane
+        if constexpr (kX / 8 < 64) {
+            if (lane < kX / 8) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / 8)), 16, p.at_x[0], step * bytes, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEachX; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / 8) + i * 64), 16, p.at_x[i], step * bytes, 0, 0);
+        }
+        if constexpr (X == kMx4) {
+            if (lane < kXS / 8) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.xs, (LdsMem*)(lxs + wave * (kXS / 8)), 4, p.at_xs, step * 4 * KG, 0, 0);
+        }
+    }
+
+    // The step where the reduction of `cols` values ends: zeros past it.  The places are byte offsets already; the value
+    // that a unit begins with tells whether it is in.
+    static __device__ __forceinline__ void stage_tail(const Places& p, const Rows& rows, const void* x, const void* x_scales, int step, int cols,
+                                                      char* buf)
+    {
+        const int lane = threadIdx.x & 63, wave = wave_id(), left = cols - step * STEP;
+        u32x4 *lw = reinterpret_cast<u32x4*>(buf), *lx = lw + kW;
+        uint32_t *ls = reinterpret_cast<uint32_t*>(lx + kX), *lxs = ls + kS;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int u = wave * 128 + i * 64 + lane, unit = (u % WU) ^ turn<WU>(u / WU);
+            u32x4 v{0, 0, 0, 0};
+            if (unit * VALUES < left) v = *reinterpret_cast<const u32x4*>(rows.codes + p.at_w[i] + step * 16 * WU);
+            lw[u] = v;
+        }
+        if constexpr (W == kMx4) {
+            const int d = wave * 32 + lane;
+            if (lane < 32) ls[d] = 128 * (d % KG) < left ? *reinterpret_cast<const uint32_t*>(rows.scales + p.at_s + step * 4 * KG) : 0;
+        }
+        const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;
+#pragma unroll
+        for (int i = 0; i < kEachX; ++i) {
+            const int u = wave * (kX / 8) + i * 64 + lane, unit = ((u % XU) ^ turn<XU>(u / XU)) % (X == kPair ? XU / 2 : XU);
+            if (kX / 8 < 64 && lane >= kX / 8) break;
+            u32x4 v{0, 0, 0, 0};
+            if (unit * (X == kMx4 ? 32 : 8) < left) v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(x) + p.at_x[i] + step * bytes);
+            lx[u] = v;
+        }
+        if constexpr (X == kMx4) {
+            const int d = wave * (kXS / 8) + lane;
+            if (lane < kXS / 8)
+                lxs[d] = 128 * (d % KG) < left ? *reinterpret_cast<const uint32_t*>(static_cast<const char*>(x_scales) + p.at_xs + step * 4 * KG) : 0;
+        }
+    }
+
+    // What a wave reads of a stage: all of it before the first product, so that one LDS latency stands in a step.  (Read
+    // as they were needed, the operands of a step took 1.1 us with two waves a SIMD, where its loads take 0.7.)
+    struct Operands {
+        static constexpr int OPS = X == kMx4 ? 1 : VALUES / 8;
+        u32x4 w[RF], x[MF][OPS], low[X == kPair ? MF : 1][X == kPair ? OPS : 1];
+        uint32_t sw[RF], sx[MF];
+
+        __device__ __forceinline__ void read(const char* buf)
+        {
+            const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4, rg = wave % RG, q = wave / RG;
+            const u32x4 *lw = reinterpret_cast<const u32x4*>(buf), *lx = lw + kW;
+            const uint32_t *ls = reinterpret_cast<const uint32_t*>(lx + kX), *lxs = ls + kS;
+#pragma unroll
+            for (int f = 0; f < RF; ++f) {
+                const int row = (rg * RF + f) * 16 + c;
+                w[f] = lw[row * WU + ((4 * q + g) ^ turn<WU>(row))];
+                if constexpr (W == kMx4) sw[f] = ls[row * KG + q];
+            }
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const int row = 16 * m + c;
+#pragma unroll
+                for (int j = 0; j < OPS; ++j) {
+                    const int unit = (4 * q + g) * OPS + j;
+                    x[m][j] = lx[row * XU + (unit ^ turn<XU>(row))];
+                    if constexpr (X == kPair) low[m][j] = lx[row * XU + ((XU / 2 + unit) ^ turn<XU>(row))];
+                }
+                if constexpr (X == kMx4) sx[m] = lxs[row * KG + q];
+            }
+        }
+
+        // 16-bit operands are of x's type, or bfloat16 where x is split or the weights are in 4 bits.
+        __device__ __forceinline__ void multiply(f32x4 (*acc)[MF])
+        {
+            const int g = threadIdx.x >> 4 & 3;
+            if constexpr (X == kMx4) {
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0], acc[f][m], sw[f] >> (8 * g) & 255, sx[m] >> (8 * g) & 255);
+            } else {
+                constexpr int TYPE = X == kFp16 && W != kMx4 ? kFp16 : kBf16;
+                float scale[RF];
+#pragma unroll
+                for (int f = 0; f < RF; ++f) scale[f] = W == kMx4 ? scale_of(sw[f] >> (8 * g) & 255) : 1.0f;
+#pragma unroll
+                for (int j = 0; j < OPS; ++j) {
+                    u32x4 wide[RF];
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) {
+                        if constexpr (W == kMx4) wide[f] = widen4(w[f][j], scale[f]);
+                        else wide[f] = widen8<TYPE>(w[f][2 * j], w[f][2 * j + 1]);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) {
+                        u32x4 hi = x[m][j], lo;
+                        if constexpr (X == kPair) lo = low[m][j];
+                        if constexpr (X == kFp16 && TYPE == kBf16) split8_f16(x[m][j], hi, lo);
+#pragma unroll
+                        for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], hi, acc[f][m]);
+                        if constexpr (X == kPair || (X == kFp16 && TYPE == kBf16)) {
+#pragma unroll
+                            for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], lo, acc[f][m]);
+                        }
+                    }
+                }
+            }
+        }
+    };
+
+    static __device__ __forceinline__ void multiply(const char* buf, f32x4 (*acc)[MF])
+    {
+        Operands o;
+        o.read(buf);
+        __builtin_amdgcn_sched_barrier(0);
+        o.multiply(acc);
+    }
+
+    // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
+    static __device__ __forceinline__ void stage_and_multiply(const Places& p, int step, char* __restrict__ to, const char* __restrict__ from,
+                                                              f32x4 (*acc)[MF])
+    {
+        stage(p, step, to);
+        __builtin_amdgcn_sched_barrier(0);                     // loads leave before the products that hide them
+        multiply(from, acc);
+    }
+
+    // The whole reduction of `cols` values; every wave of the workgroup.  Afterwards the waves with q = wave / RG = 0 hold
+    // the sums of row group wave % RG, and LDS may be used again after a barrier.
+    static __device__ __forceinline__ void run(const Rows& rows, const Places& p, const void* x, const void* x_scales, int cols, char* lds,
+                                               f32x4 (*acc)[MF])
+    {
+        const int steps = cols / STEP, wave = wave_id(), lane = threadIdx.x & 63;
+        // At the end of step s the tiles of step s + 1 have to be there, and only those of the steps behind it may be
+        // under way.  Steps past the last are replaced by the last, so that this count holds in every step.
+        if (steps > 0) {
+#pragma unroll
+            for (int s = 0; s < STAGES - 1; ++s) stage(p, min(s, steps - 1), lds + s * kStage);
+            wait_and_meet<kAhead>();
+        }
+        int use = 0, fill = STAGES - 1;
+        for (int s = 0; s < steps; ++s) {
+            stage_and_multiply(p, min(s + STAGES - 1, steps - 1), lds + fill * kStage, lds + use * kStage, acc);
+            wait_and_meet<kAhead>();
+            use = use == STAGES - 1 ? 0 : use + 1;
+            fill = fill == STAGES - 1 ? 0 : fill + 1;
+        }
+        wait_and_meet<0>();                                    // no load to LDS is under way from here on
+        if (steps * STEP < cols) {
+            stage_tail(p, rows, x, x_scales, steps, cols, lds);
+            wait_and_meet<0>();
+            multiply(lds, acc);
+            wait_and_meet<0>();
+        }
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);           // [wave][RF][MF][lane]
+        if (wave >= RG) {
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int m = 0; m < MF; ++m) sums[((wave * RF + f) * MF + m) * 64 + lane] = acc[f][m];
+        }
+        __syncthreads();
+        if (wave < RG) {
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+#pragma unroll
+                    for (int q = 1; q < KG; ++q) acc[f][m] += sums[(((q * RG + wave) * RF + f) * MF + m) * 64 + lane];
+        }
+    }
+};
+
+}  // namespace ecf8x
+
+#endif
