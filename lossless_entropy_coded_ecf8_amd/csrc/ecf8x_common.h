@@ -35,6 +35,31 @@ __device__ __forceinline__ u32x4 widen4(uint32_t codes, float scale)
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3))};
 }
 
+// Eight codes of a dword as they are, without their scale, as one float16 operand.
+__device__ __forceinline__ u32x4 widen4_f16(uint32_t codes)
+{
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3))};
+}
+
+// The value of a scale byte, 2^-127 and NaN included: the code of 1 under it.
+__device__ __forceinline__ float value_of_scale(uint32_t byte) { return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(2u, scale_of(byte), 0)[0]; }
+
+__device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Four rows' sums of one block, times the block's scales.
+__device__ __forceinline__ f32x4 add_scaled(f32x4 acc, f32x4 block, const float* scale)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(block[i], scale[i], acc[i]);
+    return acc;
+}
+
 // Eight E4M3 bytes as one operand of a 16-bit type.  Exact.
 template <int TYPE>
 __device__ __forceinline__ u32x4 widen8(uint32_t a, uint32_t b)

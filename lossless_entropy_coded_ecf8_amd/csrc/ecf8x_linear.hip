@@ -3,9 +3,10 @@
 //
 // Sixteen-bit x: each code times its power of two is exact in bfloat16, so the
 // weight is widened in registers and the 16-bit matrix instruction gives exact
-// products, summed in float32.  float16 x is split into two bfloat16 (exact),
-// since a block's power of two need not fit float16.  Four-bit x: the scaled
-// matrix instruction takes codes and scale bytes as they are stored.
+// products, summed in float32.  A block's power of two need not fit float16, so
+// with float16 x an instruction takes one block of 32 unscaled, and its float32
+// result is scaled as it is added.  Four-bit x: the scaled matrix instruction takes
+// codes and scale bytes as they are stored.
 #include "ecf8x_stream.h"
 
 namespace {
@@ -227,34 +228,48 @@ struct Tile {
                 for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<1>(b[n][1], a1, acc[m][n], sb[n], sa);
             }
         } else {
-            uint2 raw[NF];
+            // Lane group g: bfloat16, values 16 g .. 16 g + 15 of the step, 8 in each of two operands; float16, values
+            // 8 g .. 8 g + 7 of each of its two blocks, whose sums are scaled as they are added.
+            constexpr bool BLOCKS = XT == kFp16;
+            uint32_t raw[NF][2];
             float scale[NF];
+            u32x4 rows[BLOCKS ? NF : 1];
             const int sh = 16 * odd + 8 * (g >> 1);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 const int row = col0 + 16 * n;
-                raw[n] = reinterpret_cast<const uint2*>(lb)[row * 4 + g];
-                scale[n] = scale_of(ls[row] >> sh & 255);
+                if constexpr (BLOCKS) {
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) raw[n][kk] = reinterpret_cast<const uint32_t*>(lb)[row * 8 + 4 * kk + g];
+                    rows[n] = *reinterpret_cast<const u32x4*>(ls + wn * (BN / WN) + 16 * n + 4 * g);
+                } else {
+                    const uint2 v = reinterpret_cast<const uint2*>(lb)[row * 4 + g];
+                    raw[n][0] = v.x, raw[n][1] = v.y;
+                    scale[n] = scale_of(ls[row] >> sh & 255);
+                }
             }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 u32x4 b[NF];
+                float by[BLOCKS ? NF : 1][4];
 #pragma unroll
-                for (int n = 0; n < NF; ++n) b[n] = widen4(kk ? raw[n].y : raw[n].x, scale[n]);
+                for (int n = 0; n < NF; ++n) {
+                    if constexpr (BLOCKS) {
+                        b[n] = widen4_f16(raw[n][kk]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) by[n][i] = value_of_scale(rows[n][i] >> (16 * odd + 8 * kk) & 255);
+                    } else {
+                        b[n] = widen4(raw[n][kk], scale[n]);
+                    }
+                }
 #pragma unroll
                 for (int m = 0; m < MF; ++m) {
                     const int row = row0 + 16 * m;
-                    const u32x4 a = la[row * 8 + ((2 * g + kk) ^ (row & 7))];
-                    if constexpr (XT == kBf16) {
+                    const u32x4 a = la[row * 8 + ((BLOCKS ? 4 * kk + g : 2 * g + kk) ^ (row & 7))];
 #pragma unroll
-                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
-                    } else {
-                        u32x4 hi, lo;
-                        split8_f16(a, hi, lo);
-#pragma unroll
-                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], hi, acc[m][n]);
-#pragma unroll
-                        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], lo, acc[m][n]);
+                    for (int n = 0; n < NF; ++n) {
+                        if constexpr (BLOCKS) acc[m][n] = add_scaled(acc[m][n], mfma_f16(b[n], a, f32x4{0, 0, 0, 0}), by[n]);
+                        else acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
                     }
                 }
             }

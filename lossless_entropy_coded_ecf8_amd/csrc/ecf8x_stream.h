@@ -182,8 +182,11 @@ struct Stream {
     // as they were needed, the operands of a step took 1.1 us with two waves a SIMD, where its loads take 0.7.)
     struct Operands {
         static constexpr int OPS = X == kMx4 ? 1 : VALUES / 8;
+        // float16 tokens and 4-bit weights: a block's power of two need not fit float16, so each instruction takes one
+        // block of 32 (lane group g its values 8 g ..), unscaled, and its result is scaled, exactly, as it is added.
+        static constexpr bool BLOCKS = X == kFp16 && W == kMx4;
         u32x4 w[RF], x[MF][OPS], low[X == kPair ? MF : 1][X == kPair ? OPS : 1];
-        uint32_t sw[RF], sx[MF];
+        uint32_t sw[RF], sx[MF], rows[BLOCKS ? RF : 1][4];
 
         __device__ __forceinline__ void read(const char* buf)
         {
@@ -193,15 +196,23 @@ struct Stream {
 #pragma unroll
             for (int f = 0; f < RF; ++f) {
                 const int row = (rg * RF + f) * 16 + c;
-                w[f] = lw[row * WU + ((4 * q + g) ^ turn<WU>(row))];
-                if constexpr (W == kMx4) sw[f] = ls[row * KG + q];
+                if constexpr (BLOCKS) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        w[f][j] = reinterpret_cast<const uint32_t*>(lw + row * WU + ((4 * q + j) ^ turn<WU>(row)))[g];
+                        rows[f][j] = ls[((rg * RF + f) * 16 + 4 * g + j) * KG + q];
+                    }
+                } else {
+                    w[f] = lw[row * WU + ((4 * q + g) ^ turn<WU>(row))];
+                    if constexpr (W == kMx4) sw[f] = ls[row * KG + q];
+                }
             }
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
                 const int row = 16 * m + c;
 #pragma unroll
                 for (int j = 0; j < OPS; ++j) {
-                    const int unit = (4 * q + g) * OPS + j;
+                    const int unit = BLOCKS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
                     x[m][j] = lx[row * XU + (unit ^ turn<XU>(row))];
                     if constexpr (X == kPair) low[m][j] = lx[row * XU + ((XU / 2 + unit) ^ turn<XU>(row))];
                 }
@@ -209,7 +220,7 @@ struct Stream {
             }
         }
 
-        // 16-bit operands are of x's type, or bfloat16 where x is split or the weights are in 4 bits.
+        // 16-bit operands are of x's type, or bfloat16 where x is split.
         __device__ __forceinline__ void multiply(f32x4 (*acc)[MF])
         {
             const int g = threadIdx.x >> 4 & 3;
@@ -218,8 +229,20 @@ struct Stream {
                 for (int m = 0; m < MF; ++m)
 #pragma unroll
                     for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0], acc[f][m], sw[f] >> (8 * g) & 255, sx[m] >> (8 * g) & 255);
+            } else if constexpr (BLOCKS) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) {
+                        const u32x4 wide = widen4_f16(w[f][j]);
+                        float scale[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) scale[i] = value_of_scale(rows[f][i] >> (8 * j) & 255);
+#pragma unroll
+                        for (int m = 0; m < MF; ++m) acc[f][m] = add_scaled(acc[f][m], mfma_f16(wide, x[m][j], f32x4{0, 0, 0, 0}), scale);
+                    }
             } else {
-                constexpr int TYPE = X == kFp16 && W != kMx4 ? kFp16 : kBf16;
+                constexpr int TYPE = X == kFp16 ? kFp16 : kBf16;
                 float scale[RF];
 #pragma unroll
                 for (int f = 0; f < RF; ++f) scale[f] = W == kMx4 ? scale_of(sw[f] >> (8 * g) & 255) : 1.0f;
@@ -233,14 +256,12 @@ struct Stream {
                     }
 #pragma unroll
                     for (int m = 0; m < MF; ++m) {
-                        u32x4 hi = x[m][j], lo;
-                        if constexpr (X == kPair) lo = low[m][j];
-                        if constexpr (X == kFp16 && TYPE == kBf16) split8_f16(x[m][j], hi, lo);
+                        const u32x4 hi = x[m][j];
 #pragma unroll
                         for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], hi, acc[f][m]);
-                        if constexpr (X == kPair || (X == kFp16 && TYPE == kBf16)) {
+                        if constexpr (X == kPair) {
 #pragma unroll
-                            for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], lo, acc[f][m]);
+                            for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], low[m][j], acc[f][m]);
                         }
                     }
                 }
