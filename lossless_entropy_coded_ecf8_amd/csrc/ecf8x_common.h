@@ -22,9 +22,15 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 inline uint64_t padded(uint64_t cols) { return round_up(cols, ECF8X_PITCH); }
 
-// The float that a scale byte stands for, as the conversions take it (they read
-// the exponent field alone: 0 is 2^-127, 255 NaN).
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+// The float that a scale byte stands for, as the conversions take it: they read
+// the exponent field alone (0 is 2^-127, 255 NaN), so that neighbouring bytes may
+// come along.  Byte `at` of a dword, and the low byte.
+__device__ __forceinline__ float scale_at(uint32_t dword, int at)
+{
+    return __builtin_bit_cast(float, at == 3 ? dword >> 1 : dword << (23 - 8 * at));
+}
+
+__device__ __forceinline__ float scale_of(uint32_t low) { return scale_at(low, 0); }
 
 // Eight codes of a dword, times the scale, as one bfloat16 operand.  Exact.
 __device__ __forceinline__ u32x4 widen4(uint32_t codes, float scale)
@@ -44,8 +50,8 @@ __device__ __forceinline__ u32x4 widen4_f16(uint32_t codes)
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3))};
 }
 
-// The value of a scale byte, 2^-127 and NaN included: the code of 1 under it.
-__device__ __forceinline__ float value_of_scale(uint32_t byte) { return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(2u, scale_of(byte), 0)[0]; }
+// The value of a scale, 2^-127 and NaN included: the code of 1 under it.
+__device__ __forceinline__ float value_of(float scale) { return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(2u, scale, 0)[0]; }
 
 __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c)
 {

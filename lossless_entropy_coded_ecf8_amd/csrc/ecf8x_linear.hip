@@ -27,7 +27,7 @@ struct Args {
     int64_t tokens;
     int n, k, kp;               // kp: k rounded up to 128
     int pitch;                  // n rounded up to 4
-    int share;                  // reduction length of one of gridDim.y shares, a multiple of 256
+    int share;                  // reduction length of one of gridDim.y shares, a multiple of 256 (few tokens: 1024)
     int tiles_m, tiles_n;
     bool vector;                // y's rows take 8-byte stores
 };
@@ -45,28 +45,34 @@ __device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
 
 // ------------------------------------------------------------ few tokens
 
-template <int XT, int OUT, int MF, int RG>
+// A share of the reduction is a multiple of 1024 values, so that it begins with a step.
+template <int XT, int OUT, int MF, int RG, int TR>
 __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 {
-    typedef Stream<kMx4, XT, MF, RG> S;
+    typedef Stream<kMx4, XT, MF, RG, TR> S;
     extern __shared__ __attribute__((aligned(16))) char few_lds[];
     const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * S::R, row_bytes = A.kp / 2, row_scales = A.kp / 32;
     const int first = min(n0 + 16 * S::fragment(wave), A.n - 1);       // rows past the last reach no result that is stored
-    const typename S::Rows rows{A.w + (int64_t)first * row_bytes, A.w_scales + (int64_t)first * row_scales, A.n - 1 - first};
-    const typename S::Places at = S::places(rows, row_bytes, row_scales, A.x, A.x_scales, 0, [&](int i) {
+    const int cols = XT == kMx4 ? A.kp : A.k, k0 = blockIdx.y * A.share, count = max(0, min(cols - k0, A.share));
+    const typename S::Rows rows{A.w + (int64_t)first * row_bytes + k0 / 2, A.w_scales + (int64_t)first * row_scales + k0 / 32, A.n - 1 - first};
+    const char* x = static_cast<const char*>(A.x) + (XT == kMx4 ? k0 / 2 : 2 * k0);
+    const uint8_t* x_scales = A.x_scales + (XT == kMx4 ? k0 / 32 : 0);
+    const typename S::Places at = S::places(rows, row_bytes, row_scales, x, x_scales, 0, [&](int i) {
         const uint32_t t = (uint32_t)min((int64_t)i, A.tokens - 1);
         return XT == kMx4 ? t : 2 * t * (uint32_t)A.ld_x;
     });
     f32x4 acc[S::RF][MF] = {};
-    S::run(rows, at, A.x, A.x_scales, XT == kMx4 ? A.kp : A.k, few_lds, acc);
+    S::run(rows, at, x, x_scales, count, few_lds, acc);
     if (wave >= RG) return;
 #pragma unroll
     for (int f = 0; f < S::RF; ++f)
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
             const int n = n0 + 16 * (wave * S::RF + f) + 4 * g, t = 16 * m + c;
-            if (t < A.tokens && n < A.n) finish<OUT>(A, t, n, acc[f][m]);
+            if (t >= A.tokens || n >= A.n) continue;
+            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.pitch + n) = acc[f][m];
+            else finish<OUT>(A, t, n, acc[f][m]);
         }
 }
 
@@ -82,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // and 2g + 1 of an x row and the same values of a weight row, so that 16-bit x
 // meets 8 contiguous bytes of codes, under one scale.
 //
-// Banks: unit u of row r sits at u ^ (r & 7) (rows of 128 bytes); weight rows of
+// Banks: place p of row r (rows of 128 bytes) sits at p ^ (r & 7); weight rows of
 // 32 bytes lie as they are.  The scales of a row's step: one dword (16-bit x: the
 // four blocks that two steps share) or two (4-bit).
 template <int XT, int BM, int BN, int WM, int WN, int STAGES>
@@ -102,6 +108,10 @@ struct Tile {
     static_assert(WM * WN == kWaves && MF >= 1 && NF >= 1, "eight waves");
     static_assert(kA % 64 == 0 && kB % 64 == 0 && kS % 64 == 0, "whole waves stage");
 
+    // The unit of a row that lies at place p of its eight (before the turn by the row): places are numbered so that
+    // lane group g reads g and 4 + g, which the lanes of one cycle spread over all banks.
+    static __device__ __forceinline__ int unit_at(int p) { return XT == kFp16 ? p : (p & 3) << 1 | p >> 2; }
+
     // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
     // no result that is stored.
     struct Places {
@@ -115,11 +125,11 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
             const int u = i * kThreads + threadIdx.x, row = u >> 3;
-            at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * ((u & 7) ^ (row & 7));
+            at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * unit_at((u & 7) ^ (row & 7));
         }
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? (u & 7) ^ (row & 7) : u & 1;
+            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? unit_at((u & 7) ^ (row & 7)) : u & 1;
             at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * unit;
         }
 #pragma unroll
@@ -172,7 +182,7 @@ struct Tile {
         u32x4 *la = buf, *lb = buf + kA;
         uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
         for (int u = threadIdx.x; u < kA; u += kThreads) {
-            const int row = u >> 3, unit = (u & 7) ^ (row & 7);
+            const int row = u >> 3, unit = unit_at((u & 7) ^ (row & 7));
             const int64_t t = min(t0 + row, A.tokens - 1);
             u32x4 v{0, 0, 0, 0};
             if constexpr (MX) {
@@ -183,7 +193,7 @@ struct Tile {
             la[u] = v;
         }
         for (int u = threadIdx.x; u < kB; u += kThreads) {
-            const int row = u / BU, unit = MX ? (u & 7) ^ (row & 7) : u & 1;
+            const int row = u / BU, unit = MX ? unit_at((u & 7) ^ (row & 7)) : u & 1;
             u32x4 v{0, 0, 0, 0};
             if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(A.w + (int64_t)min(n0 + row, A.n - 1) * (A.kp / 2) + k / 2 + 16 * unit);
             lb[u] = v;
@@ -214,13 +224,13 @@ struct Tile {
             for (int n = 0; n < NF; ++n) {
                 const int row = col0 + 16 * n;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) b[n][s] = lb[row * 8 + ((2 * g + s) ^ (row & 7))];
+                for (int s = 0; s < 2; ++s) b[n][s] = lb[row * 8 + ((4 * s + g) ^ (row & 7))];
                 sb[n] = ls[2 * BM + (g >> 1) * BN + row] >> (16 * (g & 1));
             }
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
                 const int row = row0 + 16 * m;
-                const u32x4 a0 = la[row * 8 + ((2 * g) ^ (row & 7))], a1 = la[row * 8 + ((2 * g + 1) ^ (row & 7))];
+                const u32x4 a0 = la[row * 8 + (g ^ (row & 7))], a1 = la[row * 8 + ((4 + g) ^ (row & 7))];
                 const uint32_t sa = ls[(g >> 1) * BM + row] >> (16 * (g & 1));
 #pragma unroll
                 for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<0>(b[n][0], a0, acc[m][n], sb[n], sa);
@@ -245,7 +255,7 @@ struct Tile {
                 } else {
                     const uint2 v = reinterpret_cast<const uint2*>(lb)[row * 4 + g];
                     raw[n][0] = v.x, raw[n][1] = v.y;
-                    scale[n] = scale_of(ls[row] >> sh & 255);
+                    scale[n] = scale_of(ls[row] >> sh);
                 }
             }
 #pragma unroll
@@ -257,19 +267,30 @@ struct Tile {
                     if constexpr (BLOCKS) {
                         b[n] = widen4_f16(raw[n][kk]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) by[n][i] = value_of_scale(rows[n][i] >> (16 * odd + 8 * kk) & 255);
+                        for (int i = 0; i < 4; ++i) by[n][i] = value_of(scale_of(rows[n][i] >> (16 * odd + 8 * kk)));
                     } else {
                         b[n] = widen4(raw[n][kk], scale[n]);
                     }
                 }
+                // float16: the sums of one group of tokens are added while the next group's are made.
+                f32x4 sums[BLOCKS ? 2 : 1][NF];
 #pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    const int row = row0 + 16 * m;
-                    const u32x4 a = la[row * 8 + ((BLOCKS ? 4 * kk + g : 2 * g + kk) ^ (row & 7))];
+                for (int m = 0; m < MF + BLOCKS; ++m) {
+                    if (m < MF) {
+                        const int row = row0 + 16 * m;
+                        const u32x4 a = la[row * 8 + ((4 * kk + g) ^ (row & 7))];
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) {
-                        if constexpr (BLOCKS) acc[m][n] = add_scaled(acc[m][n], mfma_f16(b[n], a, f32x4{0, 0, 0, 0}), by[n]);
-                        else acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
+                        for (int n = 0; n < NF; ++n) {
+                            if constexpr (BLOCKS) sums[m & 1][n] = mfma_f16(b[n], a, f32x4{0, 0, 0, 0});
+                            else acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
+                        }
+                    }
+                    if constexpr (BLOCKS) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (m > 0) {
+#pragma unroll
+                            for (int n = 0; n < NF; ++n) acc[m - 1][n] = add_scaled(acc[m - 1][n], sums[~m & 1][n], by[n]);
+                        }
                     }
                 }
             }
@@ -386,22 +407,52 @@ Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
     return best;
 }
 
+// Few tokens: rows of a workgroup, as many as leave every compute unit one (two, where two fit: up to four tokens), and
+// shares of the reduction where even the fewest do not.
+Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k)
+{
+    const int least = tokens <= 4 ? 32 : tokens <= 32 ? 64 : 128;
+    int rows = 128;
+    while (rows > least && (n + rows - 1) / rows < (tokens <= 4 && rows > 64 ? 256 : 192)) rows /= 2;
+    const uint64_t groups = (n + rows - 1) / rows, steps = (k + 32768 / rows - 1) / (32768 / rows);
+    uint32_t shares = 1;
+    while (shares < 8 && groups * shares <= 128 && steps / (2 * shares) * (32768 / rows) >= 1024 && steps - steps / (2 * shares) >= 8) shares *= 2;
+    return Shape{0, rows, shares};
+}
+
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
 {
     return tokens <= ECF8A_MAX_TOKENS && n >= 1 && n <= ECF8A_MAX_FEATURES && k >= ECF8X_BLOCK && k <= ECF8A_MAX_FEATURES &&
            k % ECF8X_BLOCK == 0;
 }
 
-template <int XT, int OUT, int MF, int RG>
-int launch_few(const Args& A, hipStream_t st)
+Shape any_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
-    typedef Stream<kMx4, XT, MF, RG> S;
-    auto* kernel = few_kernel<XT, OUT, MF, RG>;
+    return tokens <= kFew ? few_shape_of(tokens, n, k) : shape_of(tokens, n, k, mx);
+}
+
+template <int XT, int OUT, int MF, int RG, int TR = 16 * MF>
+int launch_few(const Args& A, uint32_t shares, hipStream_t st)
+{
+    typedef Stream<kMx4, XT, MF, RG, TR> S;
+    auto* kernel = few_kernel<XT, OUT, MF, RG, TR>;
     if (S::kLds > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds) != hipSuccess)
         return ECF8_ERR_HIP;
-    kernel<<<(A.n + S::R - 1) / S::R, kThreads, S::kLds, st>>>(A);
+    kernel<<<dim3((A.n + S::R - 1) / S::R, shares), S::kThreads, S::kLds, st>>>(A);
     return launch_status();
+}
+
+template <int XT, int OUT>
+int run_few(const Args& A, const Shape& s, hipStream_t st)
+{
+    if (A.tokens <= 4) {
+        if (s.bn == 128) return launch_few<XT, OUT, 1, 4, 4>(A, s.shares, st);
+        return s.bn == 64 ? launch_few<XT, OUT, 1, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 1, 4>(A, s.shares, st);
+    }
+    if (A.tokens <= 16) return s.bn == 128 ? launch_few<XT, OUT, 1, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 2>(A, s.shares, st);
+    if (A.tokens <= 32) return s.bn == 128 ? launch_few<XT, OUT, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 2, 2>(A, s.shares, st);
+    return A.tokens <= 48 ? launch_few<XT, OUT, 3, 4>(A, s.shares, st) : launch_few<XT, OUT, 4, 4>(A, s.shares, st);
 }
 
 template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
@@ -421,14 +472,10 @@ int launch_tile(Args A, uint32_t shares, hipStream_t st)
 template <int XT, int OUT>
 int run(const Args& A, const Shape& s, hipStream_t st)
 {
-    if (A.tokens <= (int64_t)kFew) {
-        // Row groups: 64 rows a workgroup until those of 128 give every compute unit one.
-        if (A.tokens <= 16) return A.n < 32768 ? launch_few<XT, OUT, 1, 2>(A, st) : launch_few<XT, OUT, 1, 4>(A, st);
-        if (A.tokens <= 32) return A.n < 16384 ? launch_few<XT, OUT, 2, 2>(A, st) : launch_few<XT, OUT, 2, 4>(A, st);
-        return launch_few<XT, OUT, 4, 4>(A, st);
-    }
     int rc;
-    if constexpr (XT == kMx4) {
+    if (A.tokens <= (int64_t)kFew) {
+        rc = run_few<XT, OUT>(A, s, st);
+    } else if constexpr (XT == kMx4) {
         if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 2>(A, s.shares, st);
         else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 2>(A, s.shares, st);
     } else {
@@ -446,8 +493,8 @@ int run(const Args& A, const Shape& s, hipStream_t st)
 
 extern "C" uint64_t ecf8x_linear_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t x_type)
 {
-    if (!sizes_ok(tokens, out_features, in_features) || tokens <= kFew) return 0;
-    const uint64_t s = shape_of(tokens, out_features, in_features, x_type == ECF8X_MX4).shares;
+    if (!sizes_ok(tokens, out_features, in_features)) return 0;
+    const uint64_t s = any_shape_of(tokens, out_features, in_features, x_type == ECF8X_MX4).shares;
     return s > 1 ? round_up(4 * s * tokens * round_up(out_features, 4), 256) : 0;
 }
 
@@ -466,8 +513,7 @@ extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_
     if ((!mx && (ld_x < in_features || ld_x > (1u << 22))) || ld_y < out_features || ld_y > (1ull << 40)) return ECF8_ERR_SIZE;
     const uint64_t need = ecf8x_linear_bytes(tokens, out_features, in_features, x_type);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
-    Shape s{128, 128, 1};
-    if (tokens > kFew) s = shape_of(tokens, out_features, in_features, mx);
+    const Shape s = any_shape_of(tokens, out_features, in_features, mx);
     Args A{};
     A.x = x;
     A.x_scales = x_scales;
@@ -483,7 +529,7 @@ extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_
     A.k = (int)in_features;
     A.kp = (int)padded(in_features);
     A.pitch = (int)round_up(out_features, 4);
-    A.share = (int)round_up((in_features + s.shares - 1) / s.shares, 256);
+    A.share = (int)round_up((in_features + s.shares - 1) / s.shares, tokens <= kFew ? 1024 : 256);
     A.vector = ld_y % 4 == 0 && aligned(y, 8);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const bool b = y_type == ECF8A_BF16;

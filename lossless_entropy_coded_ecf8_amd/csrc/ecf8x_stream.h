@@ -1,7 +1,7 @@
 // ecf8x_stream.h -- the product of a few tokens with a weight that is read once.
 //
-// What bounds it is the stream of weights from memory.  A workgroup of eight
-// waves takes R rows of the weight; both operands go from memory to LDS without
+// What bounds it is the stream of weights from memory.  A workgroup takes
+// R rows of the weight; both operands go from memory to LDS without
 // passing registers, 64 KG bytes of each row a step, into STAGES buffers, so that
 // all but one of them are on their way while one is multiplied.  (Loads to
 // registers in the matrix instruction's own layout, 16 rows in a run of lanes, came
@@ -9,6 +9,8 @@
 // row groups of 16 RF rows and KG shares of the step: a wave reads one 16-byte unit
 // of each of its rows a step, 16 values of E4M3 or a block of 32 in 4 bits, and
 // widens it for two or four operands, which meet the tokens of all its row fragments.
+// A step is 128 bytes of a row at least, a whole line: steps of 64 bytes with four waves
+// and twice the stages took 52 us where these take 32 (32 tokens x 28672 x 8192).
 //
 // Weight rows are operand A and tokens operand B: lane (c, g) of a result holds
 // token 16 m + c, rows 4 g .. 4 g + 3 of fragment f.
@@ -43,32 +45,43 @@ __device__ __forceinline__ void wait_and_meet()
     asm volatile("" ::: "memory");
 }
 
-template <int W, int X, int MF, int RG>
+// TR: rows of tokens that a stage holds, 16 MF, or 4 where there are no more (lanes then share them).
+template <int W, int X, int MF, int RG, int TR = 16 * MF>
 struct Stream {
-    static constexpr int RF = 2, KG = 8 / RG, kThreads = 512;
+    static constexpr int RF = 2, NW = 8, KG = NW / RG, kThreads = 64 * NW;
     static constexpr int R = 16 * RF * RG;                     // rows
     static constexpr int VALUES = W == kMx4 ? 32 : 16;         // of a 16-byte unit of weights
     static constexpr int STEP = 4 * KG * VALUES;               // values of a step
     static constexpr int WU = 4 * KG;                          // units of a weight row's step
     static constexpr int XU = X == kMx4 ? 4 * KG : X == kPair ? STEP / 4 : STEP / 8;   // of a token's
-    static constexpr int kW = R * WU, kX = 16 * MF * XU;       // units of a stage
-    static constexpr int kS = W == kMx4 ? R * KG : 0, kXS = X == kMx4 ? 16 * MF * KG : 0;   // dwords of scales
+    static constexpr int kW = R * WU, kX = TR * XU;       // units of a stage
+    static constexpr int kS = W == kMx4 ? R * KG : 0, kXS = X == kMx4 ? TR * KG : 0;   // dwords of scales
     static constexpr int kStage = 16 * (kW + kX) + 4 * (kS + kXS);
     // Two workgroups a compute unit where three stages fit for both, else one; 8 KB are left to the callers.
-    static constexpr int kFit = 72 * 1024 / kStage, STAGES = kFit >= 3 ? (kFit < 6 ? kFit : 6) : 152 * 1024 / kStage;
-    static constexpr int kLds = STAGES * kStage > 16 * 64 * 8 * RF * MF ? STAGES * kStage : 16 * 64 * 8 * RF * MF;
+    static constexpr int kFit = 72 * 1024 / kStage, kMost = 152 * 1024 / kStage,
+                         STAGES = kFit >= 3 ? (kFit < 6 ? kFit : 6) : kMost < 8 ? kMost : 8;
+    static constexpr int kSums = 16 * 64 * NW * RF * MF, kLds = STAGES * kStage > kSums ? STAGES * kStage : kSums;
     // Loads of a wave and a stage: the same in every wave, some with part of its lanes.
-    static constexpr int kEachX = kX / 8 < 64 ? 1 : kX / 512;
-    static constexpr int kLoads = kW / 512 + (kS > 0) + kEachX + (kXS > 0);
+    static constexpr int kEachX = kX / NW < 64 ? 1 : kX / kThreads;
+    static constexpr int kLoads = kW / kThreads + (kS > 0) + kEachX + (kXS > 0);
     static constexpr int kAhead = (STAGES - 2) * kLoads;
-    static_assert(RG * KG == 8 && kW == 1024 && STAGES >= 2 && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
-    static_assert(kX % 8 == 0 && (kX / 8 < 64 || kX % 512 == 0) && kXS / 8 <= 64 && kS / 8 <= 64 && kStage % 16 == 0, "waves stage alike");
+    static_assert(RG * KG == NW && kW == 128 * NW && STAGES >= 2 && (TR == 16 * MF || (TR == 4 && MF == 1)) && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
+    static_assert(kX % NW == 0 && (kX / NW < 64 || kX % kThreads == 0) && kXS / NW <= 64 && kS / NW <= 64 && kStage % 16 == 0, "waves stage alike");
 
     // Where unit u of a row of `units` lies, so that 16 rows' units of one number fall in different banks.
     template <int UNITS>
-    static __device__ __forceinline__ int turn(int row) { return UNITS == 8 ? row >> 1 & 7 : row & 15; }
+    static __device__ __forceinline__ int turn(int row)
+    {
+        static_assert(UNITS == 8 || UNITS % 16 == 0, "whole turns");
+        return UNITS == 8 ? row >> 1 & 7 : row & 15;
+    }
 
-    // The rows that this wave sends for, 16 RF RG / 8 of them: its fragment's first row, and the last that exists
+    // The unit of a token row that lies at place p: where a lane group has four neighbouring units, places are numbered
+    // so that the groups' places of one read are neighbours, which the lanes of one cycle spread over all banks.
+    static constexpr bool FOURS = W == kMx4 && (X == kBf16 || X == kPair);
+    static __device__ __forceinline__ int token_unit(int p) { return FOURS ? (p & ~15) | (p & 3) << 2 | (p >> 2 & 3) : p; }
+
+    // The rows that this wave sends for, 16 RF / KG of them: its fragment's first row, and the last that exists
     // from there on.
     struct Rows {
         const uint8_t *codes, *scales;
@@ -76,14 +89,14 @@ struct Stream {
     };
 
     // Fragment of the rows that wave w stages, in the order [row group][fragment].
-    static __device__ __forceinline__ int fragment(int w) { return w * (R / 8) / 16; }
+    static __device__ __forceinline__ int fragment(int w) { return w * (R / NW) / 16; }
 
     struct Places {
         Rsrc w, s, x, xs;
         uint32_t at_w[2], at_s, at_x[kEachX], at_xs;
     };
 
-    // token(i): byte offset of token row i (0 .. 16 MF - 1) from x, for kMx4 its number.
+    // token(i): byte offset of token row i (0 .. TR - 1) from x, for kMx4 its number.
     template <class Token>
     static __device__ __forceinline__ Places places(const Rows& rows, uint32_t row_bytes, uint32_t row_scales, const void* x, const void* x_scales,
                                                     uint32_t low, Token token)
@@ -106,14 +119,14 @@ struct Stream {
         }
 #pragma unroll
         for (int i = 0; i < kEachX; ++i) {
-            const int u = kX / 8 < 64 ? wave * (kX / 8) + lane % (kX / 8) : wave * (kX / 8) + i * 64 + lane, row = u / XU;
-            const int unit = (u % XU) ^ turn<XU>(row);
+            const int u = kX / NW < 64 ? wave * (kX / NW) + lane % (kX / NW) : wave * (kX / NW) + i * 64 + lane, row = u / XU;
+            const int unit = token_unit((u % XU) ^ turn<XU>(row));
             if constexpr (X == kMx4) p.at_x[i] = (uint32_t)token(row) * row_bytes + 16 * unit;
             else if constexpr (X == kPair) p.at_x[i] = (uint32_t)token(row) + (unit < XU / 2 ? 16 * unit : low + 16 * (unit - XU / 2));
             else p.at_x[i] = (uint32_t)token(row) + 16 * unit;
         }
         if constexpr (X == kMx4) {
-            const int d = wave * (kXS / 8) + lane % (kXS / 8);
+            const int d = wave * (kXS / NW) + lane % (kXS / NW);
             p.at_xs = (uint32_t)token(d / KG) * row_scales + 4 * (d % KG);
         }
         return p;
@@ -131,15 +144,15 @@ struct Stream {
             if (lane < 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.s, (LdsMem*)(ls + wave * 32), 4, p.at_s, step * 4 * KG, 0, 0);
         }
         const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;      // of a token's plane
-        if constexpr (kX / 8 < 64) {
-            if (lane < kX / 8) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / 8)), 16, p.at_x[0], step * bytes, 0, 0);
+        if constexpr (kX / NW < 64) {
+            if (lane < kX / NW) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / NW)), 16, p.at_x[0], step * bytes, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < kEachX; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / 8) + i * 64), 16, p.at_x[i], step * bytes, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / NW) + i * 64), 16, p.at_x[i], step * bytes, 0, 0);
         }
         if constexpr (X == kMx4) {
-            if (lane < kXS / 8) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.xs, (LdsMem*)(lxs + wave * (kXS / 8)), 4, p.at_xs, step * 4 * KG, 0, 0);
+            if (lane < kXS / NW) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.xs, (LdsMem*)(lxs + wave * (kXS / NW)), 4, p.at_xs, step * 4 * KG, 0, 0);
         }
     }
 
@@ -165,21 +178,20 @@ struct Stream {
         const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;
 #pragma unroll
         for (int i = 0; i < kEachX; ++i) {
-            const int u = wave * (kX / 8) + i * 64 + lane, unit = ((u % XU) ^ turn<XU>(u / XU)) % (X == kPair ? XU / 2 : XU);
-            if (kX / 8 < 64 && lane >= kX / 8) break;
+            const int u = wave * (kX / NW) + i * 64 + lane, unit = token_unit((u % XU) ^ turn<XU>(u / XU)) % (X == kPair ? XU / 2 : XU);
+            if (kX / NW < 64 && lane >= kX / NW) break;
             u32x4 v{0, 0, 0, 0};
             if (unit * (X == kMx4 ? 32 : 8) < left) v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(x) + p.at_x[i] + step * bytes);
             lx[u] = v;
         }
         if constexpr (X == kMx4) {
-            const int d = wave * (kXS / 8) + lane;
-            if (lane < kXS / 8)
+            const int d = wave * (kXS / NW) + lane;
+            if (lane < kXS / NW)
                 lxs[d] = 128 * (d % KG) < left ? *reinterpret_cast<const uint32_t*>(static_cast<const char*>(x_scales) + p.at_xs + step * 4 * KG) : 0;
         }
     }
 
-    // What a wave reads of a stage: all of it before the first product, so that one LDS latency stands in a step.  (Read
-    // as they were needed, the operands of a step took 1.1 us with two waves a SIMD, where its loads take 0.7.)
+    // What a wave reads of a stage.
     struct Operands {
         static constexpr int OPS = X == kMx4 ? 1 : VALUES / 8;
         // float16 tokens and 4-bit weights: a block's power of two need not fit float16, so each instruction takes one
@@ -209,10 +221,10 @@ struct Stream {
             }
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const int row = 16 * m + c;
+                const int row = (16 * m + c) % TR;
 #pragma unroll
                 for (int j = 0; j < OPS; ++j) {
-                    const int unit = BLOCKS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
+                    const int unit = BLOCKS || FOURS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
                     x[m][j] = lx[row * XU + (unit ^ turn<XU>(row))];
                     if constexpr (X == kPair) low[m][j] = lx[row * XU + ((XU / 2 + unit) ^ turn<XU>(row))];
                 }
@@ -228,24 +240,36 @@ struct Stream {
 #pragma unroll
                 for (int m = 0; m < MF; ++m)
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0], acc[f][m], sw[f] >> (8 * g) & 255, sx[m] >> (8 * g) & 255);
+                    for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0], acc[f][m], sw[f] >> (8 * g), sx[m] >> (8 * g));
             } else if constexpr (BLOCKS) {
+                // A block's sums are added while the next block's are made.
+                f32x4 sums[2][RF][MF];
+                float scale[2][RF][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 5; ++j) {
+                    if (j < 4) {
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) {
-                        const u32x4 wide = widen4_f16(w[f][j]);
-                        float scale[4];
+                        for (int f = 0; f < RF; ++f) {
+                            const u32x4 wide = widen4_f16(w[f][j]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) scale[i] = value_of_scale(rows[f][i] >> (8 * j) & 255);
+                            for (int m = 0; m < MF; ++m) sums[j & 1][f][m] = mfma_f16(wide, x[m][j], f32x4{0, 0, 0, 0});
 #pragma unroll
-                        for (int m = 0; m < MF; ++m) acc[f][m] = add_scaled(acc[f][m], mfma_f16(wide, x[m][j], f32x4{0, 0, 0, 0}), scale);
+                            for (int i = 0; i < 4; ++i) scale[j & 1][f][i] = value_of(scale_at(rows[f][i], j));
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
+                    if (j > 0) {
+#pragma unroll
+                        for (int f = 0; f < RF; ++f)
+#pragma unroll
+                            for (int m = 0; m < MF; ++m) acc[f][m] = add_scaled(acc[f][m], sums[~j & 1][f][m], scale[~j & 1][f]);
+                    }
+                }
             } else {
                 constexpr int TYPE = X == kFp16 ? kFp16 : kBf16;
                 float scale[RF];
 #pragma unroll
-                for (int f = 0; f < RF; ++f) scale[f] = W == kMx4 ? scale_of(sw[f] >> (8 * g) & 255) : 1.0f;
+                for (int f = 0; f < RF; ++f) scale[f] = W == kMx4 ? scale_of(sw[f] >> (8 * g)) : 1.0f;
 #pragma unroll
                 for (int j = 0; j < OPS; ++j) {
                     u32x4 wide[RF];
@@ -269,31 +293,25 @@ struct Stream {
         }
     };
 
-    static __device__ __forceinline__ void multiply(const char* buf, f32x4 (*acc)[MF])
-    {
-        Operands o;
-        o.read(buf);
-        __builtin_amdgcn_sched_barrier(0);
-        o.multiply(acc);
-    }
-
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
-    static __device__ __forceinline__ void stage_and_multiply(const Places& p, int step, char* __restrict__ to, const char* __restrict__ from,
+    static __device__ __forceinline__ void stage_and_multiply(const Places& p, int later, char* __restrict__ to, const char* __restrict__ from,
                                                               f32x4 (*acc)[MF])
     {
-        stage(p, step, to);
+        stage(p, later, to);
         __builtin_amdgcn_sched_barrier(0);                     // loads leave before the products that hide them
-        multiply(from, acc);
+        Operands now;
+        now.read(from);
+        now.multiply(acc);
     }
 
-    // The whole reduction of `cols` values; every wave of the workgroup.  Afterwards the waves with q = wave / RG = 0 hold
+    // The reduction of `cols` values from step 0 of the places; every wave of the workgroup.  Afterwards the waves with q = wave / RG = 0 hold
     // the sums of row group wave % RG, and LDS may be used again after a barrier.
     static __device__ __forceinline__ void run(const Rows& rows, const Places& p, const void* x, const void* x_scales, int cols, char* lds,
                                                f32x4 (*acc)[MF])
     {
         const int steps = cols / STEP, wave = wave_id(), lane = threadIdx.x & 63;
-        // At the end of step s the tiles of step s + 1 have to be there, and only those of the steps behind it may be
-        // under way.  Steps past the last are replaced by the last, so that this count holds in every step.
+        // At the end of step s the stage of step s + 1 has to be there, and only those behind it may be under way.  Steps
+        // past the last are replaced by the last, so that this count holds in every step.
         if (steps > 0) {
 #pragma unroll
             for (int s = 0; s < STAGES - 1; ++s) stage(p, min(s, steps - 1), lds + s * kStage);
@@ -310,7 +328,9 @@ struct Stream {
         if (steps * STEP < cols) {
             stage_tail(p, rows, x, x_scales, steps, cols, lds);
             wait_and_meet<0>();
-            multiply(lds, acc);
+            Operands now;
+            now.read(lds);
+            now.multiply(acc);
             wait_and_meet<0>();
         }
         f32x4* sums = reinterpret_cast<f32x4*>(lds);           // [wave][RF][MF][lane]

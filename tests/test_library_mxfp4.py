@@ -64,7 +64,7 @@ def test_product_refusals():
     assert need >= 2 * 4 * 100 * 64 and need % 256 == 0
     for k in (dict(ws=None), dict(ws=P + 16, n=1 << 40), dict(ws=P, n=need - 1)):
         assert call(**big, **k) == WORKSPACE
-    for sizes in ((1, 64, 65536), (64, 64, 65536), (100, 64, 48), (100, 0, 64)):
+    for sizes in ((1, 28672, 8192), (64, 28672, 8192), (100, 64, 48), (100, 0, 64)):
         assert L.ecf8x_linear_bytes(*sizes, 1) == 0
 
     def grad(dy=P, ld=64, t=1, T=3, N=64, K=64, w=matrix(), dx=P, ldx=64, ws=None, n=0):
