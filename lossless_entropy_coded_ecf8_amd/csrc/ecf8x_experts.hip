@@ -13,6 +13,7 @@ namespace {
 using namespace ecf8x;
 
 constexpr int kFp32 = ECF8A_FP32, kThreads = 512, kWaves = 8;
+constexpr int kHalf = 72;                 // KB of LDS with which two workgroups fit a compute unit
 constexpr int kPairs = ECF8X_MAX_PAIRS, kExperts = ECF8X_MAX_EXPERTS;
 
 // ---------------------------------------------------------------- choice
@@ -191,50 +192,59 @@ __device__ __forceinline__ uint32_t row_bytes(int cols) { return W == kMx4 ? (co
 
 __device__ __forceinline__ uint32_t row_scales(int cols) { return (cols + 127) / 128 * 4; }
 
-// h of every pair: a workgroup takes as many rows of gate as of up of one expert,
+// h of an expert's pairs p0 .. p0 + TR - 1, for as many rows of gate as of up:
 // fragment 0 of a row group of the one, fragment 1 of the other.
+template <class S, int W, int MF, int RG, int TR>
+__device__ __forceinline__ void gate_up(const MoeArgs& A, const Groups& G, int e, int begin, int count, int p0, char* lds)
+{
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int i0 = blockIdx.x * (S::R / 2), frag = S::fragment(wave), first = min(i0 + 16 * (frag / 2), A.inner - 1);
+    const Matrix& w = frag & 1 ? A.up : A.gate;
+    const int64_t row = (int64_t)e * A.inner + first;         // rows past the last reach no result that is stored
+    const typename S::Rows rows{w.codes + row * row_bytes<W>(A.features), w.scales + row * row_scales(A.features), A.inner - 1 - first};
+    const typename S::Places at = S::places(rows, row_bytes<W>(A.features), row_scales(A.features), A.x, nullptr, 0, [&](int i) {
+        return (uint32_t)(G.pair[begin + min(p0 + i, count - 1)] / A.top) * (uint32_t)A.ld_x * 2;
+    });
+    f32x4 acc[2][MF] = {};
+    if (p0) __syncthreads();                                  // the sums of the pairs before are read
+    S::run(rows, at, A.x, nullptr, A.features, lds, acc);
+    if (wave >= RG) return;
+    const float fa = A.gate.factors ? A.gate.factors[e] : 1.0f, fb = A.up.factors ? A.up.factors[e] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const int p = p0 + 16 * m + c, i = i0 + 16 * wave + 4 * g;
+        if (p >= count || 16 * m + c >= TR || i >= A.inner) continue;
+        f32x4 h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float v = acc[0][m][q] * fa;
+            h[q] = v / (1.0f + expf(-v)) * (acc[1][m][q] * fb);
+        }
+        uint32_t hi[2], lo[2];
+        split2(h[0], h[1], hi[0], lo[0]);
+        split2(h[2], h[3], hi[1], lo[1]);
+        uint16_t* out = A.h + (int64_t)G.pair[begin + p] * 2 * A.inner + i;          // inner is a multiple of 16
+        *reinterpret_cast<uint2*>(out) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(out + A.inner) = make_uint2(lo[0], lo[1]);
+    }
+}
+
 template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs A)
 {
-    typedef Stream<W, TYPE, MF, RG> S;
     __shared__ Groups G;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     if (blockIdx.x == 0 && blockIdx.y == 0)                   // nothing counts in the second kernel before this one ends
         for (int i = threadIdx.x; i < A.tiles; i += kThreads) A.counters[i] = 0;
     const int chosen = group(A, G);
     if ((int)blockIdx.y >= chosen) return;
-    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
     const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
-    const int i0 = blockIdx.x * (S::R / 2), frag = S::fragment(wave), first = min(i0 + 16 * (frag / 2), A.inner - 1);
-    const Matrix& w = frag & 1 ? A.up : A.gate;
-    const int64_t row = (int64_t)e * A.inner + first;         // rows past the last reach no result that is stored
-    const typename S::Rows rows{w.codes + row * row_bytes<W>(A.features), w.scales + row * row_scales(A.features), A.inner - 1 - first};
-    for (int p0 = 0; p0 < count; p0 += 16 * MF) {
-        const typename S::Places at = S::places(rows, row_bytes<W>(A.features), row_scales(A.features), A.x, nullptr, 0, [&](int i) {
-            return (uint32_t)(G.pair[begin + min(p0 + i, count - 1)] / A.top) * (uint32_t)A.ld_x * 2;
-        });
-        f32x4 acc[2][MF] = {};
-        if (p0) __syncthreads();                              // the sums of the pairs before are read
-        S::run(rows, at, A.x, nullptr, A.features, lds, acc);
-        if (wave >= RG) continue;
-        const float fa = A.gate.factors ? A.gate.factors[e] : 1.0f, fb = A.up.factors ? A.up.factors[e] : 1.0f;
-#pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int p = p0 + 16 * m + c, i = i0 + 16 * wave + 4 * g;
-            if (p >= count || i >= A.inner) continue;
-            f32x4 h;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float v = acc[0][m][q] * fa;
-                h[q] = v / (1.0f + expf(-v)) * (acc[1][m][q] * fb);
-            }
-            uint32_t hi[2], lo[2];
-            split2(h[0], h[1], hi[0], lo[0]);
-            split2(h[2], h[3], hi[1], lo[1]);
-            uint16_t* out = A.h + (int64_t)G.pair[begin + p] * 2 * A.inner + i;      // inner is a multiple of 16
-            *reinterpret_cast<uint2*>(out) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(out + A.inner) = make_uint2(lo[0], lo[1]);
-        }
+    if constexpr (MF == 0) {
+        if (count <= 4) gate_up<Stream<W, TYPE, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, e, begin, count, 0, lds);
+        else
+            for (int p0 = 0; p0 < count; p0 += 8) gate_up<Stream<W, TYPE, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, e, begin, count, p0, lds);
+    } else {
+        for (int p0 = 0; p0 < count; p0 += 16 * MF) gate_up<Stream<W, TYPE, MF, RG>, W, MF, RG, 16 * MF>(A, G, e, begin, count, p0, lds);
     }
 }
 
@@ -253,43 +263,53 @@ __device__ __forceinline__ f32x4 get(Rsrc r, uint32_t at)
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kPastDie));
 }
 
+// The sums of an expert's pairs p0 .. p0 + TR - 1 for R features.
+template <class S, int W, int MF, int RG, int TR>
+__device__ __forceinline__ void down(const MoeArgs& A, const Groups& G, Rsrc part, int e, int begin, int count, int p0, char* lds)
+{
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int k0 = blockIdx.x * S::R, first = min(k0 + 16 * S::fragment(wave), A.features - 1);
+    const int64_t row = (int64_t)e * A.features + first;
+    const typename S::Rows rows{A.down.codes + row * row_bytes<W>(A.inner), A.down.scales + row * row_scales(A.inner), A.features - 1 - first};
+    const float factor = A.down.factors ? A.down.factors[e] : 1.0f;
+    const typename S::Places at = S::places(rows, row_bytes<W>(A.inner), row_scales(A.inner), A.h, nullptr, 2 * A.inner, [&](int i) {
+        return (uint32_t)G.pair[begin + min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
+    });
+    f32x4 acc[S::RF][MF] = {};
+    if (p0) __syncthreads();
+    S::run(rows, at, A.h, nullptr, A.inner, lds, acc);
+    if (wave >= RG) return;
+#pragma unroll
+    for (int f = 0; f < S::RF; ++f)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int p = p0 + 16 * m + c, k = k0 + 16 * (wave * S::RF + f) + 4 * g;
+            if (p < count && 16 * m + c < TR && k < A.features)       // features are a multiple of 16
+                put(part, 4 * (G.pair[begin + p] * (uint32_t)A.features + k), acc[f][m] * factor);
+        }
+}
+
 // y: a workgroup takes R features of one expert and leaves its pairs' sums in the
 // workspace; the last one of these features to end adds them up, a token's in the
 // order of its choices, whichever workgroup that is.
 template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
 {
-    typedef Stream<W, kPair, MF, RG> S;
+    typedef Stream<W, kPair, MF ? MF : 1, RG> S;
     __shared__ Groups G;
     __shared__ uint32_t ended;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int chosen = group(A, G);
-    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
-    const int k0 = blockIdx.x * S::R;
+    const int chosen = group(A, G), k0 = blockIdx.x * S::R;
     const Rsrc part = buffer_of(A.part);
     if ((int)blockIdx.y >= (chosen ? chosen : 1)) return;
     if (chosen) {
         const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
-        const int first = min(k0 + 16 * S::fragment(wave), A.features - 1);
-        const int64_t row = (int64_t)e * A.features + first;
-        const typename S::Rows rows{A.down.codes + row * row_bytes<W>(A.inner), A.down.scales + row * row_scales(A.inner), A.features - 1 - first};
-        const float factor = A.down.factors ? A.down.factors[e] : 1.0f;
-        for (int p0 = 0; p0 < count; p0 += 16 * MF) {
-            const typename S::Places at = S::places(rows, row_bytes<W>(A.inner), row_scales(A.inner), A.h, nullptr, 2 * A.inner, [&](int i) {
-                return (uint32_t)G.pair[begin + min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
-            });
-            f32x4 acc[S::RF][MF] = {};
-            if (p0) __syncthreads();
-            S::run(rows, at, A.h, nullptr, A.inner, lds, acc);
-            if (wave >= RG) continue;
-#pragma unroll
-            for (int f = 0; f < S::RF; ++f)
-#pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    const int p = p0 + 16 * m + c, k = k0 + 16 * (wave * S::RF + f) + 4 * g;
-                    if (p < count && k < A.features)          // features are a multiple of 16
-                        put(part, 4 * (G.pair[begin + p] * (uint32_t)A.features + k), acc[f][m] * factor);
-                }
+        if constexpr (MF == 0) {
+            if (count <= 4) down<Stream<W, kPair, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, part, e, begin, count, 0, lds);
+            else
+                for (int p0 = 0; p0 < count; p0 += 8) down<Stream<W, kPair, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, part, e, begin, count, p0, lds);
+        } else {
+            for (int p0 = 0; p0 < count; p0 += 16 * MF) down<S, W, MF, RG, 16 * MF>(A, G, part, e, begin, count, p0, lds);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // every wave's sums are where other dies see them
         __syncthreads();
@@ -335,23 +355,25 @@ constexpr uint64_t kLeastRows = 64;
 template <int W, int TYPE, int MF, int RG>
 int moe(MoeArgs A, hipStream_t st)
 {
-    typedef Stream<W, TYPE, MF, RG> First;
-    typedef Stream<W, kPair, MF, RG> Second;
-    const int most = A.pairs < A.experts ? A.pairs : A.experts, rows = First::R / 2;
-    A.tiles = (A.features + Second::R - 1) / Second::R;
-    if (allow(gate_up_kernel<W, TYPE, MF, RG>, First::kLds) != ECF8_OK || allow(down_kernel<W, TYPE, MF, RG>, Second::kLds) != ECF8_OK)
-        return ECF8_ERR_HIP;
-    gate_up_kernel<W, TYPE, MF, RG><<<dim3((A.inner + rows - 1) / rows, most), kThreads, First::kLds, st>>>(A);
+    constexpr int R = 32 * RG, rows = R / 2;
+    int first, second;                                        // LDS
+    if constexpr (MF == 0) first = second = kHalf * 1024;
+    else first = Stream<W, TYPE, MF, RG>::kLds, second = Stream<W, kPair, MF, RG>::kLds;
+    const int most = A.pairs < A.experts ? A.pairs : A.experts;
+    A.tiles = (A.features + R - 1) / R;
+    if (allow(gate_up_kernel<W, TYPE, MF, RG>, first) != ECF8_OK || allow(down_kernel<W, TYPE, MF, RG>, second) != ECF8_OK) return ECF8_ERR_HIP;
+    gate_up_kernel<W, TYPE, MF, RG><<<dim3((A.inner + rows - 1) / rows, most), kThreads, first, st>>>(A);
     const int rc = launch_status();
     if (rc != ECF8_OK) return rc;
-    down_kernel<W, TYPE, MF, RG><<<dim3(A.tiles, most), kThreads, Second::kLds, st>>>(A);
+    down_kernel<W, TYPE, MF, RG><<<dim3(A.tiles, most), kThreads, second, st>>>(A);
     return launch_status();
 }
 
 template <int W, int TYPE>
 int moe(const MoeArgs& A, hipStream_t st)
 {
-    // Columns of the matrix instructions: 16 where an expert meets few tokens.
+    // Tokens that an expert meets together: 4 or 8, with room for two workgroups a compute unit, where they are few.
+    if (A.pairs <= 4 * A.experts) return moe<W, TYPE, 0, 4>(A, st);
     if (A.tokens <= 16 || A.pairs <= 8 * A.experts) return moe<W, TYPE, 1, 4>(A, st);
     return moe<W, TYPE, 2, 4>(A, st);
 }

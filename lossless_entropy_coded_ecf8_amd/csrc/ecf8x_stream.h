@@ -45,8 +45,9 @@ __device__ __forceinline__ void wait_and_meet()
     asm volatile("" ::: "memory");
 }
 
-// TR: rows of tokens that a stage holds, 16 MF, or 4 where there are no more (lanes then share them).
-template <int W, int X, int MF, int RG, int TR = 16 * MF>
+// TR: rows of tokens that a stage holds, 16 MF, or 4 or 8 where there are no more (lanes then share them).
+// ROOM: KB of LDS for the stages; 0: half of a compute unit's, for two workgroups, where three stages fit in it, else all.
+template <int W, int X, int MF, int RG, int TR = 16 * MF, int ROOM = 0>
 struct Stream {
     static constexpr int RF = 2, NW = 8, KG = NW / RG, kThreads = 64 * NW;
     static constexpr int R = 16 * RF * RG;                     // rows
@@ -57,15 +58,16 @@ struct Stream {
     static constexpr int kW = R * WU, kX = TR * XU;       // units of a stage
     static constexpr int kS = W == kMx4 ? R * KG : 0, kXS = X == kMx4 ? TR * KG : 0;   // dwords of scales
     static constexpr int kStage = 16 * (kW + kX) + 4 * (kS + kXS);
-    // Two workgroups a compute unit where three stages fit for both, else one; 8 KB are left to the callers.
+    // 8 KB of a workgroup's share are left to the callers.
     static constexpr int kFit = 72 * 1024 / kStage, kMost = 152 * 1024 / kStage,
-                         STAGES = kFit >= 3 ? (kFit < 6 ? kFit : 6) : kMost < 8 ? kMost : 8;
+                         kRoom = ROOM ? ROOM * 1024 / kStage : kFit >= 3 ? kFit : kMost,
+                         STAGES = kRoom < 8 ? kRoom : 8;
     static constexpr int kSums = 16 * 64 * NW * RF * MF, kLds = STAGES * kStage > kSums ? STAGES * kStage : kSums;
     // Loads of a wave and a stage: the same in every wave, some with part of its lanes.
     static constexpr int kEachX = kX / NW < 64 ? 1 : kX / kThreads;
     static constexpr int kLoads = kW / kThreads + (kS > 0) + kEachX + (kXS > 0);
     static constexpr int kAhead = (STAGES - 2) * kLoads;
-    static_assert(RG * KG == NW && kW == 128 * NW && STAGES >= 2 && (TR == 16 * MF || (TR == 4 && MF == 1)) && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
+    static_assert(RG * KG == NW && kW == 128 * NW && STAGES >= 2 && (TR == 16 * MF || (TR < 16 && MF == 1)) && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
     static_assert(kX % NW == 0 && (kX / NW < 64 || kX % kThreads == 0) && kXS / NW <= 64 && kS / NW <= 64 && kStage % 16 == 0, "waves stage alike");
 
     // Where unit u of a row of `units` lies, so that 16 rows' units of one number fall in different banks.
