@@ -12,7 +12,7 @@ namespace {
 
 using namespace ecf8x;
 
-constexpr int kFp32 = ECF8A_FP32, kThreads = 512, kWaves = 8;
+constexpr int kFp32 = ECF8A_FP32, kThreads = 512;
 constexpr int kHalf = 72;                 // KB of LDS with which two workgroups fit a compute unit
 constexpr int kPairs = ECF8X_MAX_PAIRS, kExperts = ECF8X_MAX_EXPERTS;
 
@@ -136,52 +136,43 @@ struct MoeArgs {
     bool vector;                // y's rows take 8-byte stores
 };
 
-// The pairs sorted by expert, in LDS.  Order within an expert is free: a pair's
-// results do not depend on its column.
-struct Groups {
-    uint32_t count[kExperts];                                 // of each expert, then where its pairs begin
-    uint32_t total[kWaves];
-    uint16_t expert[kPairs], first[kPairs + 1];               // of the chosen experts, in order
+// The pairs of one expert, in LDS.  Their order is free: a pair's results do not
+// depend on its column.
+struct Group {
+    uint32_t chosen[kExperts / 32], count;                    // a bit for each expert that some pair names
     uint16_t pair[kPairs];
 };
 
-// Returns the number of chosen experts.
-__device__ __forceinline__ int group(const MoeArgs& A, Groups& G)
+// The chosen expert of rank r, in the order of their numbers, and its pairs: the
+// number of chosen experts, expert -1 where there are no more than r.
+__device__ __forceinline__ int find(const MoeArgs& A, Group& G, int r, int& expert)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < A.experts; e += kThreads) G.count[e] = 0;
+    const int tid = threadIdx.x, lane = tid & 63;
+    if (tid <= kExperts / 32) G.chosen[tid] = 0;              // and the count
     int id = -1;
     if (tid < A.pairs) id = A.ids[tid];
     const bool is = id >= 0 && id < A.experts;
     __syncthreads();
-    uint32_t rank = 0;
-    if (is) rank = atomicAdd(&G.count[id], 1u);
+    if (is) atomicOr(&G.chosen[id >> 5], 1u << (id & 31));
     __syncthreads();
-    // Two experts a thread: pairs in the low half, chosen experts in the high half of one running sum.
-    const int e0 = 2 * tid, e1 = e0 + 1;
-    const uint32_t c0 = e0 < A.experts ? G.count[e0] : 0, c1 = e1 < A.experts ? G.count[e1] : 0;
-    const uint32_t own = (c0 + c1) | ((uint32_t)((c0 != 0) + (c1 != 0)) << 16);
-    uint32_t sum = own;
+    // Every wave finds the r-th bit for itself.
+    uint32_t word = lane < kExperts / 32 ? G.chosen[lane] : 0;
+    const int own = __popc(word);
+    int upto = own;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(sum, d);
-        if (lane >= d) sum += o;
+    for (int d = 1; d < kExperts / 32; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
     }
-    if (lane == 63) G.total[wave] = sum;
-    __syncthreads();
-    uint32_t before = sum - own;
-    for (int i = 0; i < wave; ++i) before += G.total[i];
-    const uint32_t pos = before & 0xFFFF, at = before >> 16;
-    if (c0) G.expert[at] = (uint16_t)e0, G.first[at] = (uint16_t)pos;
-    if (c1) G.expert[at + (c0 != 0)] = (uint16_t)e1, G.first[at + (c0 != 0)] = (uint16_t)(pos + c0);
-    if (e0 < A.experts) G.count[e0] = pos;
-    if (e1 < A.experts) G.count[e1] = pos + c0;
-    uint32_t all = 0;
-    for (int i = 0; i < kWaves; ++i) all += G.total[i];
-    const int chosen = (int)(all >> 16);
-    if (tid == 0) G.first[chosen] = (uint16_t)(all & 0xFFFF);
-    __syncthreads();
-    if (is) G.pair[G.count[id] + rank] = (uint16_t)tid;
+    const int chosen = __shfl(upto, kExperts / 32 - 1);
+    expert = -1;
+    if (r < chosen) {
+        const int at = __ffsll((unsigned long long)__ballot(lane < kExperts / 32 && upto > r)) - 1;
+        word = __shfl(word, at);
+        for (int skip = r - __shfl(upto - own, at); skip > 0; --skip) word &= word - 1;
+        expert = 32 * at + __ffs(word) - 1;
+    }
+    if (is && id == expert) G.pair[atomicAdd(&G.count, 1u)] = (uint16_t)tid;
     __syncthreads();
     return chosen;
 }
@@ -195,15 +186,15 @@ __device__ __forceinline__ uint32_t row_scales(int cols) { return (cols + 127) /
 // h of an expert's pairs p0 .. p0 + TR - 1, for as many rows of gate as of up:
 // fragment 0 of a row group of the one, fragment 1 of the other.
 template <class S, int W, int MF, int RG, int TR>
-__device__ __forceinline__ void gate_up(const MoeArgs& A, const Groups& G, int e, int begin, int count, int p0, char* lds)
+__device__ __forceinline__ void gate_up(const MoeArgs& A, const Group& G, int e, int p0, char* lds)
 {
-    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4, count = G.count;
     const int i0 = blockIdx.x * (S::R / 2), frag = S::fragment(wave), first = min(i0 + 16 * (frag / 2), A.inner - 1);
     const Matrix& w = frag & 1 ? A.up : A.gate;
     const int64_t row = (int64_t)e * A.inner + first;         // rows past the last reach no result that is stored
     const typename S::Rows rows{w.codes + row * row_bytes<W>(A.features), w.scales + row * row_scales(A.features), A.inner - 1 - first};
     const typename S::Places at = S::places(rows, row_bytes<W>(A.features), row_scales(A.features), A.x, nullptr, 0, [&](int i) {
-        return (uint32_t)(G.pair[begin + min(p0 + i, count - 1)] / A.top) * (uint32_t)A.ld_x * 2;
+        return (uint32_t)(G.pair[min(p0 + i, count - 1)] / A.top) * (uint32_t)A.ld_x * 2;
     });
     f32x4 acc[2][MF] = {};
     if (p0) __syncthreads();                                  // the sums of the pairs before are read
@@ -223,7 +214,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs& A, const Groups& G, int e
         uint32_t hi[2], lo[2];
         split2(h[0], h[1], hi[0], lo[0]);
         split2(h[2], h[3], hi[1], lo[1]);
-        uint16_t* out = A.h + (int64_t)G.pair[begin + p] * 2 * A.inner + i;          // inner is a multiple of 16
+        uint16_t* out = A.h + (int64_t)G.pair[p] * 2 * A.inner + i;          // inner is a multiple of 16
         *reinterpret_cast<uint2*>(out) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(out + A.inner) = make_uint2(lo[0], lo[1]);
     }
@@ -232,19 +223,20 @@ __device__ __forceinline__ void gate_up(const MoeArgs& A, const Groups& G, int e
 template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs A)
 {
-    __shared__ Groups G;
+    __shared__ Group G;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     if (blockIdx.x == 0 && blockIdx.y == 0)                   // nothing counts in the second kernel before this one ends
         for (int i = threadIdx.x; i < A.tiles; i += kThreads) A.counters[i] = 0;
-    const int chosen = group(A, G);
-    if ((int)blockIdx.y >= chosen) return;
-    const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
+    int e;
+    find(A, G, blockIdx.y, e);
+    if (e < 0) return;
+    const int count = G.count;
     if constexpr (MF == 0) {
-        if (count <= 4) gate_up<Stream<W, TYPE, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, e, begin, count, 0, lds);
+        if (count <= 4) gate_up<Stream<W, TYPE, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, e, 0, lds);
         else
-            for (int p0 = 0; p0 < count; p0 += 8) gate_up<Stream<W, TYPE, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, e, begin, count, p0, lds);
+            for (int p0 = 0; p0 < count; p0 += 8) gate_up<Stream<W, TYPE, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, e, p0, lds);
     } else {
-        for (int p0 = 0; p0 < count; p0 += 16 * MF) gate_up<Stream<W, TYPE, MF, RG>, W, MF, RG, 16 * MF>(A, G, e, begin, count, p0, lds);
+        for (int p0 = 0; p0 < count; p0 += 16 * MF) gate_up<Stream<W, TYPE, MF, RG>, W, MF, RG, 16 * MF>(A, G, e, p0, lds);
     }
 }
 
@@ -265,15 +257,15 @@ __device__ __forceinline__ f32x4 get(Rsrc r, uint32_t at)
 
 // The sums of an expert's pairs p0 .. p0 + TR - 1 for R features.
 template <class S, int W, int MF, int RG, int TR>
-__device__ __forceinline__ void down(const MoeArgs& A, const Groups& G, Rsrc part, int e, int begin, int count, int p0, char* lds)
+__device__ __forceinline__ void down(const MoeArgs& A, const Group& G, Rsrc part, int e, int p0, char* lds)
 {
-    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_id(), c = lane & 15, g = lane >> 4, count = G.count;
     const int k0 = blockIdx.x * S::R, first = min(k0 + 16 * S::fragment(wave), A.features - 1);
     const int64_t row = (int64_t)e * A.features + first;
     const typename S::Rows rows{A.down.codes + row * row_bytes<W>(A.inner), A.down.scales + row * row_scales(A.inner), A.features - 1 - first};
     const float factor = A.down.factors ? A.down.factors[e] : 1.0f;
     const typename S::Places at = S::places(rows, row_bytes<W>(A.inner), row_scales(A.inner), A.h, nullptr, 2 * A.inner, [&](int i) {
-        return (uint32_t)G.pair[begin + min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
+        return (uint32_t)G.pair[min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
     });
     f32x4 acc[S::RF][MF] = {};
     if (p0) __syncthreads();
@@ -285,7 +277,7 @@ __device__ __forceinline__ void down(const MoeArgs& A, const Groups& G, Rsrc par
         for (int m = 0; m < MF; ++m) {
             const int p = p0 + 16 * m + c, k = k0 + 16 * (wave * S::RF + f) + 4 * g;
             if (p < count && 16 * m + c < TR && k < A.features)       // features are a multiple of 16
-                put(part, 4 * (G.pair[begin + p] * (uint32_t)A.features + k), acc[f][m] * factor);
+                put(part, 4 * (G.pair[p] * (uint32_t)A.features + k), acc[f][m] * factor);
         }
 }
 
@@ -296,20 +288,20 @@ template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
 {
     typedef Stream<W, kPair, MF ? MF : 1, RG> S;
-    __shared__ Groups G;
+    __shared__ Group G;
     __shared__ uint32_t ended;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int chosen = group(A, G), k0 = blockIdx.x * S::R;
+    int e;
+    const int chosen = find(A, G, blockIdx.y, e), k0 = blockIdx.x * S::R, count = G.count;
     const Rsrc part = buffer_of(A.part);
-    if ((int)blockIdx.y >= (chosen ? chosen : 1)) return;
+    if (e < 0 && (chosen || blockIdx.y)) return;              // where no token has an expert one workgroup clears y
     if (chosen) {
-        const int e = G.expert[blockIdx.y], begin = G.first[blockIdx.y], count = G.first[blockIdx.y + 1] - begin;
         if constexpr (MF == 0) {
-            if (count <= 4) down<Stream<W, kPair, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, part, e, begin, count, 0, lds);
+            if (count <= 4) down<Stream<W, kPair, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, part, e, 0, lds);
             else
-                for (int p0 = 0; p0 < count; p0 += 8) down<Stream<W, kPair, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, part, e, begin, count, p0, lds);
+                for (int p0 = 0; p0 < count; p0 += 8) down<Stream<W, kPair, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, part, e, p0, lds);
         } else {
-            for (int p0 = 0; p0 < count; p0 += 16 * MF) down<S, W, MF, RG, 16 * MF>(A, G, part, e, begin, count, p0, lds);
+            for (int p0 = 0; p0 < count; p0 += 16 * MF) down<S, W, MF, RG, 16 * MF>(A, G, part, e, p0, lds);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // every wave's sums are where other dies see them
         __syncthreads();
@@ -355,7 +347,7 @@ constexpr uint64_t kLeastRows = 64;
 template <int W, int TYPE, int MF, int RG>
 int moe(MoeArgs A, hipStream_t st)
 {
-    constexpr int R = 32 * RG, rows = R / 2;
+    constexpr int R = 32 * RG, rows = R / 2;                  // features of a workgroup of the second kernel, rows of gate of the first
     int first, second;                                        // LDS
     if constexpr (MF == 0) first = second = kHalf * 1024;
     else first = Stream<W, TYPE, MF, RG>::kLds, second = Stream<W, kPair, MF, RG>::kLds;
@@ -373,7 +365,10 @@ template <int W, int TYPE>
 int moe(const MoeArgs& A, hipStream_t st)
 {
     // Tokens that an expert meets together: 4 or 8, with room for two workgroups a compute unit, where they are few.
-    if (A.pairs <= 4 * A.experts) return moe<W, TYPE, 0, 4>(A, st);
+    if (A.pairs <= 4 * A.experts) {
+        const int most = A.pairs < A.experts ? A.pairs : A.experts;
+        return (A.features + 127) / 128 * most <= 256 ? moe<W, TYPE, 0, 2>(A, st) : moe<W, TYPE, 0, 4>(A, st);
+    }
     if (A.tokens <= 16 || A.pairs <= 8 * A.experts) return moe<W, TYPE, 1, 4>(A, st);
     return moe<W, TYPE, 2, 4>(A, st);
 }
