@@ -122,7 +122,7 @@ int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_x, uint32_t
                  uint64_t in_features, const ecf8x_matrix* w, const void* bias, uint32_t y_type, void* y, uint64_t ld_y,
                  void* workspace, uint64_t workspace_bytes, void* hip_stream);
 
-uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features);
+uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t type);
 
 /* dx = dy w, dy (tokens x out_features) and dx (tokens x in_features) of one
  * type (ECF8A_BF16 or ECF8A_FP16), rows on 16-byte borders.  Errors as

@@ -31,55 +31,126 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 
 // One workgroup: BM tokens by BN columns of dx, eight waves in WM rows of WN, 64
-// rows of the weight at a time.  dy's tile goes straight to LDS, ahead by
-// STAGES - 1 steps; the weight's codes are loaded two steps ahead, widened and
-// stored one step ahead, into two buffers.
+// rows of the weight at a time.  The weight's codes are loaded to registers AHEAD
+// steps early, widened and stored one step early, into two buffers.  bfloat16 dy
+// goes straight to LDS, STAGES - 1 steps early; float16 dy is loaded like the codes,
+// split into two bfloat16 and stored one step early, so that each value is split
+// once per workgroup.
 //
 // Banks.  Unit u (16 bytes) of dy's row r sits at u ^ (r & 7).  Unit u of the
 // widened row r sits at u ^ turn(r): the transposing read takes two units of
 // four rows in each lane group, and the 16 units that half a wave touches lie in
 // different banks; so do those that 16 lanes store, since lanes of the second
 // half of a row store their units in another order.
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 struct Tile {
+    static constexpr bool SPLIT = TYPE == kFp16;
     static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
     static constexpr int BU = BN / 8;                          // 16-byte units of a widened row
-    static constexpr int kA = BM * 8, kB = kStep * BU;
-    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads;
+    static constexpr int kA = BM * 8, kB = kStep * BU;         // of a plane of dy's tile, of the widened tile
+    static constexpr int kWaveA = kA / 8, kUnitsA = kWaveA < 64 ? 1 : kWaveA / 64;    // a wave sends for the same number as any other
     static constexpr int kRaw = kStep * BN / 32;               // 16-byte units of codes
-    static constexpr int kLds = 16 * (STAGES * kA + 2 * kB);
-    static_assert(STAGES >= 2 && kLds <= 160 * 1024, "LDS");
+    static constexpr int kBuffers = SPLIT ? 4 : STAGES;        // split: two planes, two steps
+    static constexpr int kLds = 16 * (kBuffers * kA + 2 * kB);
+    // Loads that may be under way at the end of a step: those of all steps behind the next one's dy, codes included.
+    static constexpr int kAhead = (STAGES - 2) * (kUnitsA + 2);
+    static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64, "LDS and the load counter");
     static_assert(WM * WN == kThreads / 64 && MF >= 1 && NF >= 1 && kRaw <= kThreads && kRaw % 64 == 0, "eight waves");
+    static_assert(kWaveA < 64 || kWaveA % 64 == 0, "waves stage alike");
 
     static __device__ __forceinline__ int turn(int row) { return 2 * ((row & 3) | (row >> 1 & 4)) | (row >> 2 & 1); }
 
+    // Unit i that this lane sends for; lanes past a wave's share repeat others'.
+    static __device__ __forceinline__ int unit_a(int i)
+    {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        return kWaveA < 64 ? wave * kWaveA + lane % kWaveA : wave * kWaveA + i * 64 + lane;
+    }
+
     struct Places {
         uint32_t a[kUnitsA];
+        uint32_t codes, scale;                                 // of this thread's block in the first row of the tile's first step
+        int row;                                               // of a step, that this thread widens
     };
 
-    static __device__ __forceinline__ Places places(const Args& A, int64_t t0)
+    static __device__ __forceinline__ Places places(const Args& A, int64_t t0, int k0)
     {
         Places at;
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u >> 3;
+            const int u = unit_a(i), row = u >> 3;
             at.a[i] = 2 * ((uint32_t)min((int64_t)row, A.tokens - 1 - t0) * (uint32_t)A.ld_dy + 8 * ((u & 7) ^ (row & 7)));
         }
+        const int u = threadIdx.x % kRaw, col = k0 + 32 * (u % (BN / 32));
+        at.row = u / (BN / 32);
+        at.codes = (col < A.kp ? col : 0) / 2;                 // past the last column: results that are not stored
+        at.scale = at.codes / 16;
         return at;
     }
 
     static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n, u32x4* la)
     {
         const Rsrc ra = buffer_of(A.dy + t0 * A.ld_dy);
+        const int wave = wave_id();
+        if constexpr (kWaveA < 64) {
+            if ((int)(threadIdx.x & 63) < kWaveA) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + wave * kWaveA), 16, at.a[0], 2 * n, 0, 0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kUnitsA; ++i) {
-            const int first = i * kThreads + (threadIdx.x & ~63);
-            if (kA % kThreads && first >= kA) break;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + first), 16, at.a[i], 2 * n, 0, 0);
+            for (int i = 0; i < kUnitsA; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + wave * kWaveA + i * 64), 16, at.a[i], 2 * n, 0, 0);
         }
     }
 
-    // The same where the reduction ends inside the step: zeros past n1.
+    // What a thread loads early: a block of codes with its scale, and float16 dy.
+    struct Early {
+        u32x4 codes;
+        uint32_t scale;
+        u32x4 dy[SPLIT ? kUnitsA : 1];
+    };
+
+    // Every lane loads, so that every wave has as many loads under way: rows past n1 read the last one, dy's steps past
+    // its last whole one that one (`whole`; none: no dy).
+    static __device__ __forceinline__ void fetch(const Args& A, const Places& at, int64_t t0, int n, int n1, int whole, Early& e)
+    {
+        const int64_t row = max(0, min(n + at.row, n1 - 1));
+        e.codes = *reinterpret_cast<const u32x4*>(A.w + row * (A.kp / 2) + at.codes);
+        e.scale = A.w_scales[row * (A.kp / 32) + at.scale];
+        if constexpr (SPLIT) {
+            if (whole >= 0) {
+                const char* p = reinterpret_cast<const char*>(A.dy + t0 * A.ld_dy + min(n, whole));
+#pragma unroll
+                for (int i = 0; i < kUnitsA; ++i) e.dy[i] = *reinterpret_cast<const u32x4*>(p + at.a[i]);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void put_split(u32x4 v, int u, u32x4* la)
+    {
+        u32x4 hi, lo;
+        split8_f16(v, hi, lo);
+        la[u] = hi;
+        la[kA + u] = lo;
+    }
+
+    // Stores what was loaded for the step whose first row is n; rows past n1 are zero.
+    static __device__ __forceinline__ void store(const Places& at, int n, int n1, const Early& e, u32x4* la, u32x4* lb)
+    {
+        if (kRaw == kThreads || threadIdx.x < kRaw) {
+            const int j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
+            const bool in = n + at.row < n1;
+            const float s = scale_of(in ? e.scale : 0);
+            u32x4* p = lb + at.row * BU;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[(4 * j + (i ^ swap)) ^ turn(at.row)] = widen4(in ? (swap ? e.codes[i ^ 1] : e.codes[i]) : 0, s);
+        }
+        if constexpr (SPLIT) {
+#pragma unroll
+            for (int i = 0; i < kUnitsA; ++i)
+                if (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA) put_split(e.dy[i], unit_a(i), la);
+        }
+    }
+
+    // dy's tile where the reduction ends inside the step: zeros past n1.
     static __device__ __forceinline__ void stage_tail(const Args& A, int64_t t0, int n, int n1, u32x4* la)
     {
         for (int u = threadIdx.x; u < kA; u += kThreads) {
@@ -89,34 +160,9 @@ struct Tile {
             if (first + 8 <= n1) v = *reinterpret_cast<const u32x4*>(p);
             else
                 for (int i = 0; first + i < n1; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-            la[u] = v;
+            if constexpr (SPLIT) put_split(v, u, la);
+            else la[u] = v;
         }
-    }
-
-    // The block of codes that a thread widens: row threadIdx / (BN / 32) of the step.  Zero past n1 and past the stored row.
-    struct Raw {
-        u32x4 codes;
-        uint32_t scale;
-    };
-
-    static __device__ __forceinline__ Raw fetch(const Args& A, int k0, int n, int n1)
-    {
-        Raw r{u32x4{0, 0, 0, 0}, 0};
-        const int row = n + threadIdx.x / (BN / 32), col = k0 + 32 * (threadIdx.x % (BN / 32));
-        if ((kRaw < kThreads && threadIdx.x >= kRaw) || row >= n1 || col >= A.kp) return r;
-        r.codes = *reinterpret_cast<const u32x4*>(A.w + (int64_t)row * (A.kp / 2) + col / 2);
-        r.scale = A.w_scales[(int64_t)row * (A.kp / 32) + col / 32];
-        return r;
-    }
-
-    static __device__ __forceinline__ void widen(const Raw& r, u32x4* lb)
-    {
-        if (kRaw < kThreads && threadIdx.x >= kRaw) return;
-        const int row = threadIdx.x / (BN / 32), j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
-        const float s = scale_of(r.scale);
-        u32x4* p = lb + row * BU;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[(4 * j + (i ^ swap)) ^ turn(row)] = widen4(swap ? r.codes[i ^ 1] : r.codes[i], s);
     }
 
     static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[NF])
@@ -136,15 +182,12 @@ struct Tile {
                 }
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const u32x4 a = la[(row0 + 16 * m) * 8 + ((4 * kk + g) ^ (c & 7))];
-                if constexpr (TYPE == kBf16) {
+                const int u = (row0 + 16 * m) * 8 + ((4 * kk + g) ^ (c & 7));
+                const u32x4 a = la[u];
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
-                } else {
-                    u32x4 hi, lo;
-                    split8_f16(a, hi, lo);
-#pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], hi, acc[m][n]);
+                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
+                if constexpr (SPLIT) {
+                    const u32x4 lo = la[kA + u];
 #pragma unroll
                     for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], lo, acc[m][n]);
                 }
@@ -153,27 +196,26 @@ struct Tile {
     }
 
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
-    static __device__ __forceinline__ Raw step(const Args& A, const Places& at, int64_t t0, int k0, int n, int ahead, int n1, const Raw& next,
-                                               u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
-                                               const u32x4* __restrict__ lb, int wm, int wn, f32x4 (*acc)[NF])
+    static __device__ __forceinline__ void step(const Args& A, const Places& at, int64_t t0, int n, int later, int n1, int whole, const Early& next,
+                                                Early& early, u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
+                                                const u32x4* __restrict__ lb, int wm, int wn, f32x4 (*acc)[NF])
     {
-        const Raw later = fetch(A, k0, n + 2 * kStep, n1);
-        stage(A, at, t0, ahead, to_a);
+        fetch(A, at, t0, n + AHEAD * kStep, n1, whole, early);
+        if constexpr (!SPLIT) stage(A, at, t0, later, to_a);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        widen(next, to_b);
+        store(at, n + kStep, n1, next, to_a, to_b);
         multiply(la, lb, wm, wn, acc);
-        return later;
     }
 };
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 {
-    typedef Tile<TYPE, BM, BN, WM, WN, STAGES> S;
+    typedef Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD> S;
     extern __shared__ u32x4 lds[];
     u32x4* const la = lds;
-    u32x4* const lb = lds + STAGES * S::kA;
-    const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+    u32x4* const lb = lds + S::kBuffers * S::kA;
+    const int wave = wave_id(), wm = wave / WN, wn = wave % WN;
     // The order of tiles as in the forward product: a run of tiles for each die.
     const int total = A.tiles_m * A.tiles_n;
     int id = blockIdx.x;
@@ -183,30 +225,44 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
     const int64_t t0 = (int64_t)tm * BM;
     const int k0 = tn * BN;
     const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
+    const int whole = steps > 0 ? n0 + (steps - 1) * kStep : -1;     // dy's last whole step
     f32x4 acc[S::MF][S::NF] = {};
-    const typename S::Places at = S::places(A, t0);
-    typename S::Raw next = S::fetch(A, k0, n0, n1);
-    S::widen(next, lb);
-    next = S::fetch(A, k0, n0 + kStep, n1);
-    if (steps > 0) {
+    const typename S::Places at = S::places(A, t0, k0);
+    typename S::Early early[AHEAD];                           // of step s at s % AHEAD
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0 + min(s, steps - 1) * kStep, la + s * S::kA);
+    for (int s = 0; s < AHEAD; ++s) S::fetch(A, at, t0, n0 + s * kStep, n1, whole, early[s]);
+    if constexpr (!S::SPLIT) {
+        if (steps > 0) {
+#pragma unroll
+            for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0 + min(s, steps - 1) * kStep, la + s * S::kA);
+        }
     }
+    if (!S::SPLIT || steps > 0) S::store(at, n0, n1, early[0], la, lb);
+    else S::store(at, n0, n1, early[0], la + 2 * S::kA, lb);  // no dy was loaded: into the other buffer, which nothing reads
     wait_and_meet<0>();
-    // In step s the codes of step s + 1 are widened into the other buffer, those of
-    // step s + 2 sent for, and dy's tile of step s + STAGES - 1 (the last one again
-    // past the end).  dy's tile of step s + 1 is older than what may be under way at
-    // the end of the step: the loads of the steps behind it and two of codes.
-    constexpr int kAhead = (STAGES - 2) * (S::kA / kThreads);
-    int use = 0, fill = STAGES - 1;
-    for (int s = 0; s < steps; ++s) {
-        next = S::step(A, at, t0, k0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, next, la + fill * S::kA,
-                       lb + (s + 1 & 1) * S::kB, la + use * S::kA, lb + (s & 1) * S::kB, wm, wn, acc);
-        wait_and_meet<kAhead>();
-        use = use == STAGES - 1 ? 0 : use + 1;
-        fill = fill == STAGES - 1 ? 0 : fill + 1;
+    // In step s the codes (and float16 dy) of step s + 1 are stored, those of step s + AHEAD sent for, and bfloat16 dy's
+    // tile of step s + STAGES - 1 (the last one again past the end).
+    int use = 0, fill = S::SPLIT ? 1 : STAGES - 1;
+    constexpr int kPlanes = S::SPLIT ? 2 : 1, kTurn = S::SPLIT ? 2 : STAGES;
+    for (int s0 = 0; s0 < steps; s0 += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int s = s0 + i;
+            if (s >= steps) break;
+            S::step(A, at, t0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, whole, early[(i + 1) % AHEAD], early[i],
+                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, acc);
+            if constexpr (S::SPLIT) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            } else {
+                wait_and_meet<S::kAhead>();
+            }
+            use = use == kTurn - 1 ? 0 : use + 1;
+            fill = fill == kTurn - 1 ? 0 : fill + 1;
+        }
     }
-    if (n0 + steps * kStep < n1) {                            // its codes are widened by now
+    if (n0 + steps * kStep < n1) {                            // its codes are stored by now
         wait_and_meet<0>();
         S::stage_tail(A, t0, n0 + steps * kStep, n1, la);
         wait_and_meet<0>();
@@ -237,14 +293,15 @@ struct Cost {
     int bm, bn;
     double one, two;
 };
+// (float16: no tiles of 256 tokens, whose two planes leave no room for a second buffer.)
 constexpr Cost kCosts[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}, {64, 256, 0.7, 0.0}, {32, 256, 0.8, 0.0}};
 
-Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k)
+Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
     Shape best{32, 256, 1};
     double least = -1.0;
     for (const Cost& c : kCosts) {
-        if (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens) continue;      // over half of the rows would be padding
+        if ((split && c.bm == 256) || (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens)) continue;      // over half of the rows would be padding
         const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
         for (uint32_t s = 1; s <= 16 && (s == 1 || n / s >= 256); ++s) {
             const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
@@ -266,11 +323,11 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
            k % ECF8X_BLOCK == 0;
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 int launch(Args A, uint32_t shares, hipStream_t st)
 {
-    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES>::kLds;
-    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES>;
+    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD>::kLds;
+    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
@@ -284,11 +341,13 @@ template <int TYPE>
 int run(const Args& A, const Shape& s, hipStream_t st)
 {
     int rc;
-    if (s.bm == 256) rc = launch<TYPE, 256, 256, 2, 4, 3>(A, s.shares, st);
-    else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 3>(A, s.shares, st);
-    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 2>(A, s.shares, st);
-    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 3>(A, s.shares, st);
-    else rc = launch<TYPE, 32, 256, 2, 4, 3>(A, s.shares, st);
+    if (s.bm == 256) {
+        if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, s.shares, st);
+        else rc = ECF8_ERR_UNSUPPORTED;                       // shape_of gives float16 none of these
+    } else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
+    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, s.shares, st);
+    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, s.shares, st);
+    else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, s.shares, st);
     if (rc != ECF8_OK || s.shares < 2) return rc;
     const uint64_t units = (uint64_t)A.tokens * A.k / 4;
     join_kernel<TYPE><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.planes, A.tokens, A.k, A.k, (int)s.shares, nullptr, A.dx, A.ld_dx);
@@ -297,10 +356,10 @@ int run(const Args& A, const Shape& s, hipStream_t st)
 
 }  // namespace
 
-extern "C" uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features)
+extern "C" uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t type)
 {
     if (!sizes_ok(tokens, out_features, in_features)) return 0;
-    const uint64_t s = shape_of(tokens, out_features, in_features).shares;
+    const uint64_t s = shape_of(tokens, out_features, in_features, type == ECF8A_FP16).shares;
     return s > 1 ? round_up(4 * s * tokens * in_features, 256) : 0;
 }
 
@@ -316,9 +375,9 @@ extern "C" int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, u
         !aligned(dx, 16) || (tokens > 1 && (ld_dy % 8 || ld_dx % 8)))
         return ECF8_ERR_ARG;
     if (ld_dy < out_features || ld_dx < in_features || ld_dy > (1u << 22) || ld_dx > (1ull << 40)) return ECF8_ERR_SIZE;
-    const uint64_t need = ecf8x_input_grad_bytes(tokens, out_features, in_features);
+    const uint64_t need = ecf8x_input_grad_bytes(tokens, out_features, in_features, type);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
-    const Shape s = shape_of(tokens, out_features, in_features);
+    const Shape s = shape_of(tokens, out_features, in_features, type == ECF8A_FP16);
     const Args A{static_cast<const uint16_t*>(dy), (int64_t)ld_dy, w->codes, w->scales, static_cast<uint16_t*>(dx), (int64_t)ld_dx,
                  s.shares > 1 ? static_cast<float*>(workspace) : nullptr, (int64_t)tokens, (int)out_features, (int)in_features,
                  (int)padded(in_features), (int)round_up((out_features + s.shares - 1) / s.shares, 64), 0, 0};

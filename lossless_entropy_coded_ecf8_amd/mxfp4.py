@@ -47,7 +47,7 @@ def _lib() -> ctypes.CDLL:
         "ecf8x_dequantize": (i, [vp, vp, u64, u64, u32, vp, u64, vp]),
         "ecf8x_linear_bytes": (u64, [u64, u64, u64, u32]),
         "ecf8x_linear": (i, [vp, vp, u64, u32, u64, u64, u64, matrix, vp, u32, vp, u64, vp, u64, vp]),
-        "ecf8x_input_grad_bytes": (u64, [u64, u64, u64]),
+        "ecf8x_input_grad_bytes": (u64, [u64, u64, u64, u32]),
         "ecf8x_input_grad": (i, [vp, u64, u32, u64, u64, u64, matrix, vp, u64, vp, u64, vp]),
         "ecf8x_route": (i, [vp, u64, u32, u64, u32, u32, u32, u32, f, vp, vp, vp]),
         "ecf8x_moe_bytes": (u64, [u64, u32, experts]),
@@ -228,7 +228,7 @@ def linear_mxfp4_input_grad(dy: torch.Tensor, w: MXFP4, *, out: Optional[torch.T
         if not fresh:
             _apart(out, reads, "out")
         L = _lib()
-        need = L.ecf8x_input_grad_bytes(T, N, K)
+        need = L.ecf8x_input_grad_bytes(T, N, K, _TYPES[dy.dtype])
         ws = _scratch(need, workspace, dev, stream, reads + [("out", out)]) if need else None
         _check(L.ecf8x_input_grad(dy.data_ptr(), ld_dy, _TYPES[dy.dtype], T, N, K, ctypes.byref(w._c()), out.data_ptr(), ld_dx,
                                   _ptr(ws), 0 if ws is None else ws.numel(), st), "ecf8x_input_grad")
