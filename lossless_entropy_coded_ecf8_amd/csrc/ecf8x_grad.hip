@@ -56,6 +56,7 @@ struct Tile {
     static constexpr int kAhead = (STAGES - 2) * (kUnitsA + 2);
     static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64, "LDS and the load counter");
     static_assert(WM * WN == kThreads / 64 && MF >= 1 && NF >= 1 && kRaw <= kThreads && kRaw % 64 == 0, "eight waves");
+    static_assert(kUnitsA <= 4 && (MF < 2 || MF % 2 == 0), "quarters and groups");
     static_assert(kWaveA < 64 || kWaveA % 64 == 0, "waves stage alike");
 
     static __device__ __forceinline__ int turn(int row) { return 2 * ((row & 3) | (row >> 1 & 4)) | (row >> 2 & 1); }
@@ -132,21 +133,19 @@ struct Tile {
         la[kA + u] = lo;
     }
 
-    // Stores what was loaded for the step whose first row is n; rows past n1 are zero.
-    static __device__ __forceinline__ void store(const Places& at, int n, int n1, const Early& e, u32x4* la, u32x4* lb)
+    // Stores a quarter of what was loaded for the step whose first row is n; rows past n1 are zero.
+    static __device__ __forceinline__ void store(int i, const Places& at, int n, int n1, const Early& e, u32x4* la, u32x4* lb)
     {
         if (kRaw == kThreads || threadIdx.x < kRaw) {
             const int j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
             const bool in = n + at.row < n1;
             const float s = scale_of(in ? e.scale : 0);
-            u32x4* p = lb + at.row * BU;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[(4 * j + (i ^ swap)) ^ turn(at.row)] = widen4(in ? (swap ? e.codes[i ^ 1] : e.codes[i]) : 0, s);
+            lb[at.row * BU + ((4 * j + (i ^ swap)) ^ turn(at.row))] = widen4(in ? (swap ? e.codes[i ^ 1] : e.codes[i]) : 0, s);
         }
         if constexpr (SPLIT) {
 #pragma unroll
-            for (int i = 0; i < kUnitsA; ++i)
-                if (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA) put_split(e.dy[i], unit_a(i), la);
+            for (int d = 0; d < kUnitsA; ++d)
+                if (d % 4 == i && (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA)) put_split(e.dy[d], unit_a(d), la);
         }
     }
 
@@ -165,12 +164,17 @@ struct Tile {
         }
     }
 
-    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[NF])
+    // The products of a step, token fragments PER at a time: the operands of a group are read while the group before is
+    // multiplied.  between(i): what else there is to do, a quarter before each of the first four groups that have
+    // products; its VALU and LDS work then goes beside the other wave's products.  (All of it ahead of the products:
+    // 2.0 us a step of 256 x 256, 1.6 of them the products and their operands.)  live: fragments that hold tokens.
+    template <class Between>
+    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, int live, f32x4 (*acc)[NF], Between between)
     {
+        constexpr int PER = MF < 2 ? 1 : 2, GROUPS = 2 * MF / PER;
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, row0 = wm * (BM / WM) + c;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 b[NF];
+        u32x4 a[2][PER], low[2][SPLIT ? PER : 1], b[2][NF];
+        const auto read_b = [&](int kk) {
 #pragma unroll
             for (int n = 0; n < NF; ++n)
 #pragma unroll
@@ -178,33 +182,55 @@ struct Tile {
                     const int row = 32 * kk + 8 * g + 4 * h + (c >> 2), u = (wn * (BN / WN) + 16 * n) / 8 + (c >> 1 & 1);
                     const char* p = reinterpret_cast<const char*>(lb + row * BU + (u ^ turn(row))) + 8 * (c & 1);
                     const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad*)p));
-                    b[n][2 * h] = v.x, b[n][2 * h + 1] = v.y;
+                    b[kk][n][2 * h] = v.x, b[kk][n][2 * h + 1] = v.y;
                 }
+        };
+        const auto read_a = [&](int i) {
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const int u = (row0 + 16 * m) * 8 + ((4 * kk + g) ^ (c & 7));
-                const u32x4 a = la[u];
+            for (int p = 0; p < PER; ++p) {
+                const int kk = i * PER / MF, m = i * PER % MF + p, u = (row0 + 16 * m) * 8 + ((4 * kk + g) ^ (c & 7));
+                a[i & 1][p] = la[u];
+                if constexpr (SPLIT) low[i & 1][p] = la[kA + u];
+            }
+        };
+        read_b(0);
+        read_a(0);
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], a, acc[m][n]);
-                if constexpr (SPLIT) {
-                    const u32x4 lo = la[kA + u];
+        for (int i = 0; i < GROUPS; ++i) {
+            const int kk = i * PER / MF, m = i * PER % MF;
+            if (i + 1 < GROUPS) {
+                if ((i + 1) * PER % MF == 0) read_b(kk + 1);
+                read_a(i + 1);
+            }
+            if (GROUPS >= 4 ? i < 4 : true) {
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[m][n] = mfma_bf16(b[n], lo, acc[m][n]);
+                for (int q = 0; q < (GROUPS >= 4 ? 1 : 4 / GROUPS); ++q) between(i * (GROUPS >= 4 ? 1 : 4 / GROUPS) + q);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (m < live) {
+#pragma unroll
+                for (int p = 0; p < PER; ++p) {
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], a[i & 1][p], acc[m + p][n]);
+                    if constexpr (SPLIT) {
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], low[i & 1][p], acc[m + p][n]);
+                    }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
     static __device__ __forceinline__ void step(const Args& A, const Places& at, int64_t t0, int n, int later, int n1, int whole, const Early& next,
                                                 Early& early, u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
-                                                const u32x4* __restrict__ lb, int wm, int wn, f32x4 (*acc)[NF])
+                                                const u32x4* __restrict__ lb, int wm, int wn, int live, f32x4 (*acc)[NF])
     {
         fetch(A, at, t0, n + AHEAD * kStep, n1, whole, early);
         if constexpr (!SPLIT) stage(A, at, t0, later, to_a);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        store(at, n + kStep, n1, next, to_a, to_b);
-        multiply(la, lb, wm, wn, acc);
+        multiply(la, lb, wm, wn, live, acc, [&](int i) { store(i, at, n + kStep, n1, next, to_a, to_b); });
     }
 };
 
@@ -227,6 +253,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
     const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
     const int whole = steps > 0 ? n0 + (steps - 1) * kStep : -1;     // dy's last whole step
     f32x4 acc[S::MF][S::NF] = {};
+    const int live = (int)min((int64_t)S::MF, (A.tokens - t0 - wm * (BM / WM) + 15) / 16);      // this wave's fragments that hold tokens
     const typename S::Places at = S::places(A, t0, k0);
     typename S::Early early[AHEAD];                           // of step s at s % AHEAD
 #pragma unroll
@@ -237,8 +264,9 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
             for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0 + min(s, steps - 1) * kStep, la + s * S::kA);
         }
     }
-    if (!S::SPLIT || steps > 0) S::store(at, n0, n1, early[0], la, lb);
-    else S::store(at, n0, n1, early[0], la + 2 * S::kA, lb);  // no dy was loaded: into the other buffer, which nothing reads
+    // Where no float16 dy was loaded: into the other buffer, which nothing reads.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S::store(i, at, n0, n1, early[0], S::SPLIT && steps == 0 ? la + 2 * S::kA : la, lb);
     wait_and_meet<0>();
     // In step s the codes (and float16 dy) of step s + 1 are stored, those of step s + AHEAD sent for, and bfloat16 dy's
     // tile of step s + STAGES - 1 (the last one again past the end).
@@ -250,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
             const int s = s0 + i;
             if (s >= steps) break;
             S::step(A, at, t0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, whole, early[(i + 1) % AHEAD], early[i],
-                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, acc);
+                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, live, acc);
             if constexpr (S::SPLIT) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
@@ -266,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
         wait_and_meet<0>();
         S::stage_tail(A, t0, n0 + steps * kStep, n1, la);
         wait_and_meet<0>();
-        S::multiply(la, lb + (steps & 1) * S::kB, wm, wn, acc);
+        S::multiply(la, lb + (steps & 1) * S::kB, wm, wn, live, acc, [](int) {});
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -289,19 +317,26 @@ struct Shape {
     uint32_t shares;
 };
 
+// Measured on MI355X: microseconds of a step (64 rows of the weight) of a workgroup alone on its compute unit, and of two
+// side by side (0: no LDS for a second one).  Shares cost their sums' traffic and the launch that joins them: 77 x 14336 x
+// 4096 in bfloat16 takes 25 + 5 us with 16 shares, 38 + 4 with 8.  float16 has twice the products, and no tiles of 256
+// tokens, whose two planes leave no room for a second buffer.
 struct Cost {
     int bm, bn;
     double one, two;
 };
-// (float16: no tiles of 256 tokens, whose two planes leave no room for a second buffer.)
-constexpr Cost kCosts[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}, {64, 256, 0.7, 0.0}, {32, 256, 0.8, 0.0}};
+constexpr Cost kCosts[] = {{256, 256, 2.0, 0.0}, {128, 256, 1.25, 0.0}, {128, 128, 0.75, 1.5}, {64, 256, 0.9, 0.0}, {32, 256, 0.7, 0.0}};
+constexpr Cost kCostsSplit[] = {{128, 256, 1.9, 0.0}, {128, 128, 1.4, 2.6}, {64, 256, 1.3, 0.0}, {32, 256, 0.9, 0.0}};
 
 Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
     Shape best{32, 256, 1};
     double least = -1.0;
-    for (const Cost& c : kCosts) {
-        if ((split && c.bm == 256) || (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens)) continue;      // over half of the rows would be padding
+    const Cost* costs = split ? kCostsSplit : kCosts;
+    const int count = split ? 4 : 5;
+    for (int i = 0; i < count; ++i) {
+        const Cost& c = costs[i];
+        if (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens) continue;      // over half of the rows would be padding
         const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
         for (uint32_t s = 1; s <= 16 && (s == 1 || n / s >= 256); ++s) {
             const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;

@@ -227,15 +227,25 @@ struct Tile {
                 for (int s = 0; s < 2; ++s) b[n][s] = lb[row * 8 + ((4 * s + g) ^ (row & 7))];
                 sb[n] = ls[2 * BM + (g >> 1) * BN + row] >> (16 * (g & 1));
             }
+            // Token operands are read one fragment ahead of their use.
+            u32x4 a[2][2];
+            uint32_t sa[2];
+            const auto read_a = [&](int m) {
+                const int row = row0 + 16 * m;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) a[m & 1][s] = la[row * 8 + ((4 * s + g) ^ (row & 7))];
+                sa[m & 1] = ls[(g >> 1) * BM + row] >> (16 * (g & 1));
+            };
+            read_a(0);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const int row = row0 + 16 * m;
-                const u32x4 a0 = la[row * 8 + (g ^ (row & 7))], a1 = la[row * 8 + ((4 + g) ^ (row & 7))];
-                const uint32_t sa = ls[(g >> 1) * BM + row] >> (16 * (g & 1));
+                if (m + 1 < MF) read_a(m + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<0>(b[n][0], a0, acc[m][n], sb[n], sa);
+                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<0>(b[n][0], a[m & 1][0], acc[m][n], sb[n], sa[m & 1]);
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<1>(b[n][1], a1, acc[m][n], sb[n], sa);
+                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<1>(b[n][1], a[m & 1][1], acc[m][n], sb[n], sa[m & 1]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
             // Lane group g: bfloat16, values 16 g .. 16 g + 15 of the step, 8 in each of two operands; float16, values
@@ -381,14 +391,14 @@ struct Cost {
     double one, two;
 };
 constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
-constexpr Cost kCostsMx[] = {{256, 256, 1.65, 0.0}, {128, 128, 0.7, 1.1}};
+constexpr Cost kCostsMx[] = {{256, 256, 2.75, 0.0}, {128, 256, 1.9, 0.0}, {128, 128, 1.45, 2.45}};
 
 Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
     Shape best{128, 128, 1};
     double least = -1.0;
     const Cost* costs = mx ? kCostsMx : kCosts16;
-    const int count = mx ? 2 : 3, step = mx ? 256 : 64;
+    const int count = 3, step = mx ? 256 : 64;
     for (int i = 0; i < count; ++i) {
         const Cost& c = costs[i];
         if (c.bm > 128 && (uint64_t)c.bm / 2 >= tokens) continue;     // over half of the rows would be padding
@@ -477,6 +487,7 @@ int run(const Args& A, const Shape& s, hipStream_t st)
         rc = run_few<XT, OUT>(A, s, st);
     } else if constexpr (XT == kMx4) {
         if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 2>(A, s.shares, st);
+        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 3>(A, s.shares, st);
         else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 2>(A, s.shares, st);
     } else {
         if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 3>(A, s.shares, st);
