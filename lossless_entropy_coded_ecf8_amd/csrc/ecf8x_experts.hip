@@ -133,7 +133,6 @@ struct MoeArgs {
     float* part;                // [pair][features]
     uint32_t* counters;         // of the second kernel's tiles: workgroups that have ended
     int tokens, top, pairs, features, inner, experts, tiles;
-    bool vector;                // y's rows take 8-byte stores
 };
 
 // The pairs of one expert, in LDS.  Their order is free: a pair's results do not
@@ -320,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
             if (id < 0 || id >= A.experts) continue;
             y += get(part, 4 * (pair * (uint32_t)A.features + k)) * A.weights[pair];
         }
-        store4<TYPE>(A.y + t * A.ld_y + k, y, 4, A.vector);
+        store4<TYPE>(A.y + t * A.ld_y + k, y, 4);
     }
 }
 
@@ -448,7 +447,6 @@ extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t t
     A.features = (int)layer->features;
     A.inner = (int)layer->inner;
     A.experts = (int)layer->experts;
-    A.vector = ld_y % 4 == 0 && aligned(y, 8);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     if (mx) return type == ECF8A_BF16 ? moe<kMx4, kBf16>(A, st) : moe<kMx4, kFp16>(A, st);
     return type == ECF8A_BF16 ? moe<kE4m3, kBf16>(A, st) : moe<kE4m3, kFp16>(A, st);

@@ -306,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
             const int col = k0 + wn * (BN / WN) + n * 16 + 4 * g;   // K is a multiple of 32: an operand's columns are in or out
             if (col >= A.k) continue;
             if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.k + col) = acc[m][n];
-            else store4<TYPE>(A.dx + t * A.ld_dx + col, acc[m][n], 4, true);
+            else store4<TYPE>(A.dx + t * A.ld_dx + col, acc[m][n], 4);
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // loads to LDS that no step used land before the workgroup ends

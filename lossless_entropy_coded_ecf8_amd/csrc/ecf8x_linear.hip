@@ -29,7 +29,6 @@ struct Args {
     int pitch;                  // n rounded up to 4
     int share;                  // reduction length of one of gridDim.y shares, a multiple of 256 (few tokens: 1024)
     int tiles_m, tiles_n;
-    bool vector;                // y's rows take 8-byte stores
 };
 
 template <int OUT>
@@ -40,7 +39,7 @@ __device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
         for (int i = 0; i < 4; ++i)
             if (n + i < A.n) v[i] += load1<OUT>(A.bias + n + i);
     }
-    store4<OUT>(A.y + t * A.ld_y + n, v, A.n - n, A.vector);
+    store4<OUT>(A.y + t * A.ld_y + n, v, A.n - n);
 }
 
 // ------------------------------------------------------------ few tokens
@@ -79,25 +78,24 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // ------------------------------------------------------------ many tokens
 
 // One workgroup: BM tokens by BN outputs, eight waves in WM rows of WN, the
-// reduction in steps of 128 bytes of an x row: 64 values of 16 bits (32 bytes of
-// a weight row), 256 of 4 bits (128 bytes of a weight row).
+// reduction in steps: 64 values of 16 bits (128 bytes of an x row, 32 of a weight
+// row), or 128 of 4 bits (64 bytes of each).
 //
 // Tiles go from memory to LDS without passing registers into STAGES buffers:
-// while step s is multiplied, step s + STAGES - 1 is sent for.  A lane's operand
-// share lies in one or two 16-byte units of its row: lane group g takes units 2g
-// and 2g + 1 of an x row and the same values of a weight row, so that 16-bit x
-// meets 8 contiguous bytes of codes, under one scale.
+// while step s is multiplied, step s + STAGES - 1 is sent for.  With 16-bit x lane group g takes units 2g and
+// 2g + 1 of an x row and the same values of a weight row, so that it meets 8
+// contiguous bytes of codes, under one scale; with 4-bit x unit g of either.
 //
-// Banks: place p of row r (rows of 128 bytes) sits at p ^ (r & 7); weight rows of
-// 32 bytes lie as they are.  The scales of a row's step: one dword (16-bit x: the
-// four blocks that two steps share) or two (4-bit).
+// Banks: place p of row r sits at p ^ turn(r); weight rows of 32 bytes lie as they
+// are.  The scales of a row's step: one dword (16-bit x: the four blocks that two
+// steps share).
 template <int XT, int BM, int BN, int WM, int WN, int STAGES>
 struct Tile {
     static constexpr bool MX = XT == kMx4;
-    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = MX ? 256 : 64;
-    static constexpr int BU = MX ? 8 : 2;                      // 16-byte units of a weight row's step
-    static constexpr int kA = BM * 8, kB = BN * BU;            // 16-byte units of the two tiles
-    static constexpr int kS = MX ? 2 * (BM + BN) : BN;         // dwords of scales
+    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = MX ? 128 : 64;
+    static constexpr int AU = MX ? 4 : 8, BU = MX ? 4 : 2;     // 16-byte units of a row's step: x, weight
+    static constexpr int kA = BM * AU, kB = BN * BU;            // 16-byte units of the two tiles
+    static constexpr int kS = MX ? BM + BN : BN;         // dwords of scales
     static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (kB + kThreads - 1) / kThreads,
                          kUnitsS = (kS + kThreads - 1) / kThreads;
     static constexpr int kStage = 16 * (kA + kB) + 4 * kS;     // bytes
@@ -105,12 +103,14 @@ struct Tile {
     // Loads that may be under way at the end of a step: those of all stages but the next one's.
     static constexpr int kAhead = (STAGES - 2) * (kA / kThreads + kB / kThreads + kS / kThreads);
     static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
-    static_assert(WM * WN == kWaves && MF >= 1 && NF >= 1, "eight waves");
+    static_assert(WM * WN == kWaves && (MX ? MF % 2 == 0 : MF >= 1) && NF >= 1, "eight waves");
     static_assert(kA % 64 == 0 && kB % 64 == 0 && kS % 64 == 0, "whole waves stage");
 
     // The unit of a row that lies at place p of its eight (before the turn by the row): places are numbered so that
     // lane group g reads g and 4 + g, which the lanes of one cycle spread over all banks.
-    static __device__ __forceinline__ int unit_at(int p) { return XT == kFp16 ? p : (p & 3) << 1 | p >> 2; }
+    static __device__ __forceinline__ int unit_at(int p) { return XT != kBf16 ? p : (p & 3) << 1 | p >> 2; }
+
+    static __device__ __forceinline__ int turn(int row) { return MX ? 0x78 >> (row >> 1 & 6) & 3 : row & 7; }
 
     // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
     // no result that is stored.
@@ -124,23 +124,19 @@ struct Tile {
         const uint32_t pitch_x = MX ? A.kp / 2 : 2 * (uint32_t)A.ld_x, pitch_w = A.kp / 2, pitch_s = A.kp / 32;
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u >> 3;
-            at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * unit_at((u & 7) ^ (row & 7));
+            const int u = i * kThreads + threadIdx.x, row = u / AU;
+            at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * unit_at((u % AU) ^ turn(row));
         }
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? unit_at((u & 7) ^ (row & 7)) : u & 1;
+            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? (u & 3) ^ turn(row) : u & 1;
             at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * unit;
         }
 #pragma unroll
         for (int i = 0; i < kUnitsS; ++i) {
             const int u = i * kThreads + threadIdx.x;
-            if constexpr (MX) {                                // [half][token], then [half][output]
-                if (u < 2 * BM) at.s[i] = (uint32_t)min((int64_t)(u % BM), A.tokens - 1 - t0) * pitch_s + 4 * (u / BM);
-                else at.s[i] = (uint32_t)min((u - 2 * BM) % BN, A.n - 1 - n0) * pitch_s + 4 * ((u - 2 * BM) / BN);
-            } else {
-                at.s[i] = (uint32_t)min(u, A.n - 1 - n0) * pitch_s;
-            }
+            if (MX && u < BM) at.s[i] = (uint32_t)min((int64_t)u, A.tokens - 1 - t0) * pitch_s;      // tokens first
+            else at.s[i] = (uint32_t)min(MX ? u - BM : u, A.n - 1 - n0) * pitch_s;
         }
         return at;
     }
@@ -157,10 +153,10 @@ struct Tile {
         for (int i = 0; i < kUnitsS; ++i) {
             const int first = i * kThreads + wave0;
             if (kS % kThreads && first >= kS) break;
-            if (MX && first < 2 * BM)
+            if (MX && first < BM)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(A.x_scales + t0 * (A.kp / 32)), (LdsMem*)(ls + first), 4, at.s[i], k / 32, 0, 0);
             else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsMem*)(ls + first), 4, at.s[i], MX ? k / 32 : (k / 128) * 4, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsMem*)(ls + first), 4, at.s[i], (k / 128) * 4, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
@@ -176,38 +172,26 @@ struct Tile {
         }
     }
 
-    // The same where the reduction ends inside the step: zeros past k1 (a multiple of 32).
+    // The same where a reduction of 16-bit x ends inside the step: zeros past k1, a multiple of 32.  (Rows of 4 bits are
+    // stored in whole steps.)
     static __device__ __forceinline__ void stage_tail(const Args& A, int64_t t0, int n0, int k, int k1, u32x4* buf)
     {
         u32x4 *la = buf, *lb = buf + kA;
         uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
         for (int u = threadIdx.x; u < kA; u += kThreads) {
-            const int row = u >> 3, unit = unit_at((u & 7) ^ (row & 7));
-            const int64_t t = min(t0 + row, A.tokens - 1);
+            const int row = u / AU, unit = unit_at((u % AU) ^ turn(row));
             u32x4 v{0, 0, 0, 0};
-            if constexpr (MX) {
-                if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(A.x) + t * (A.kp / 2) + k / 2 + 16 * unit);
-            } else {
-                if (k + 8 * unit < k1) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(A.x) + t * A.ld_x + k + 8 * unit);
-            }
+            if (k + 8 * unit < k1) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(A.x) + min(t0 + row, A.tokens - 1) * A.ld_x + k + 8 * unit);
             la[u] = v;
         }
         for (int u = threadIdx.x; u < kB; u += kThreads) {
-            const int row = u / BU, unit = MX ? unit_at((u & 7) ^ (row & 7)) : u & 1;
+            const int row = u / BU, unit = u % BU;
             u32x4 v{0, 0, 0, 0};
             if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(A.w + (int64_t)min(n0 + row, A.n - 1) * (A.kp / 2) + k / 2 + 16 * unit);
             lb[u] = v;
         }
-        for (int u = threadIdx.x; u < kS; u += kThreads) {
-            const int v = u - 2 * BM, half = MX ? (u < 2 * BM ? u / BM : v / BN) : 0;
-            uint32_t s = 0;
-            if (!MX) s = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + u, A.n - 1) * (A.kp / 32) + (k / 128) * 4);
-            else if (k + 128 * half < k1) {
-                if (u < 2 * BM) s = *reinterpret_cast<const uint32_t*>(A.x_scales + min(t0 + u % BM, A.tokens - 1) * (A.kp / 32) + k / 32 + 4 * half);
-                else s = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + v % BN, A.n - 1) * (A.kp / 32) + k / 32 + 4 * half);
-            }
-            ls[u] = s;
-        }
+        for (int u = threadIdx.x; u < kS; u += kThreads)
+            ls[u] = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + u, A.n - 1) * (A.kp / 32) + (k / 128) * 4);
     }
 
     // odd: whether the step is the second of the two that share a dword of scales (16-bit x).
@@ -218,33 +202,33 @@ struct Tile {
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
         const int row0 = wm * (BM / WM) + c, col0 = wn * (BN / WN) + c;
         if constexpr (MX) {
-            u32x4 b[NF][2];
-            uint32_t sb[NF];
+            // Token operands are read two fragments ahead of their use.
+            u32x4 a[2][2], b[NF];
+            uint32_t sa[2][2], sb[NF];
+            const auto read_a = [&](int m, u32x4* to, uint32_t* scale) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int row = row0 + 16 * (m + p);
+                    to[p] = la[row * AU + (g ^ turn(row))];
+                    scale[p] = ls[row] >> (8 * g);
+                }
+            };
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 const int row = col0 + 16 * n;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) b[n][s] = lb[row * 8 + ((4 * s + g) ^ (row & 7))];
-                sb[n] = ls[2 * BM + (g >> 1) * BN + row] >> (16 * (g & 1));
+                b[n] = lb[row * BU + (g ^ turn(row))];
+                sb[n] = ls[BM + row] >> (8 * g);
             }
-            // Token operands are read one fragment ahead of their use.
-            u32x4 a[2][2];
-            uint32_t sa[2];
-            const auto read_a = [&](int m) {
-                const int row = row0 + 16 * m;
+            read_a(0, a[0], sa[0]);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) a[m & 1][s] = la[row * 8 + ((4 * s + g) ^ (row & 7))];
-                sa[m & 1] = ls[(g >> 1) * BM + row] >> (16 * (g & 1));
-            };
-            read_a(0);
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                if (m + 1 < MF) read_a(m + 1);
+            for (int m = 0; m < MF; m += 2) {
+                const int now = m / 2 & 1;
+                if (m + 2 < MF) read_a(m + 2, a[!now], sa[!now]);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<0>(b[n][0], a[m & 1][0], acc[m][n], sb[n], sa[m & 1]);
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[m][n] = mfma_mx4<1>(b[n][1], a[m & 1][1], acc[m][n], sb[n], sa[m & 1]);
+                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_mx4<0>(b[n], a[now][p], acc[m + p][n], sb[n], sa[now][p]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
@@ -288,7 +272,7 @@ struct Tile {
                 for (int m = 0; m < MF + BLOCKS; ++m) {
                     if (m < MF) {
                         const int row = row0 + 16 * m;
-                        const u32x4 a = la[row * 8 + ((4 * kk + g) ^ (row & 7))];
+                        const u32x4 a = la[row * AU + ((4 * kk + g) ^ turn(row))];
 #pragma unroll
                         for (int n = 0; n < NF; ++n) {
                             if constexpr (BLOCKS) sums[m & 1][n] = mfma_f16(b[n], a, f32x4{0, 0, 0, 0});
@@ -333,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     const int tm = band * 8 + in_band % rows, tn = in_band / rows;
     const int64_t t0 = (int64_t)tm * BM;
     const int n0 = tn * BN;
-    const int k0 = blockIdx.y * A.share, k1 = min(A.k, k0 + A.share), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
+    const int k0 = blockIdx.y * A.share, k1 = min(XT == kMx4 ? A.kp : A.k, k0 + A.share), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
     f32x4 acc[S::MF][S::NF] = {};
     // At the end of step s the tiles of step s + 1 have to be there, and only those
     // of the steps behind it may be under way.  Steps past the last are replaced by
@@ -353,11 +337,13 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
         use = use == STAGES - 1 ? 0 : use + 1;
         fill = fill == STAGES - 1 ? 0 : fill + 1;
     }
-    if (k0 + steps * S::STEP < k1) {
-        wait_and_meet<0>();
-        S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
-        wait_and_meet<0>();
-        S::multiply(lds, wm, wn, steps & 1, acc);
+    if constexpr (XT != kMx4) {
+        if (k0 + steps * S::STEP < k1) {
+            wait_and_meet<0>();
+            S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
+            wait_and_meet<0>();
+            S::multiply(lds, wm, wn, steps & 1, acc);
+        }
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -391,19 +377,19 @@ struct Cost {
     double one, two;
 };
 constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
-constexpr Cost kCostsMx[] = {{256, 256, 2.75, 0.0}, {128, 256, 1.9, 0.0}, {128, 128, 1.45, 2.45}};
+constexpr Cost kCostsMx[] = {{256, 256, 1.4, 0.0}, {128, 256, 1.1, 0.0}, {128, 128, 0.6, 1.2}};
 
 Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
     Shape best{128, 128, 1};
     double least = -1.0;
     const Cost* costs = mx ? kCostsMx : kCosts16;
-    const int count = 3, step = mx ? 256 : 64;
+    const int count = 3, step = mx ? 128 : 64;
     for (int i = 0; i < count; ++i) {
         const Cost& c = costs[i];
         if (c.bm > 128 && (uint64_t)c.bm / 2 >= tokens) continue;     // over half of the rows would be padding
         const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-        for (uint32_t s = 1; s <= 16 && (s == 1 || k / s >= (uint64_t)4 * step); ++s) {
+        for (uint32_t s = 1; s <= 16 && (s == 1 || k / s >= 4 * 256); ++s) {
             const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
             const double full = c.two > 0.0 ? c.two : c.one;
             const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
@@ -486,9 +472,9 @@ int run(const Args& A, const Shape& s, hipStream_t st)
     if (A.tokens <= (int64_t)kFew) {
         rc = run_few<XT, OUT>(A, s, st);
     } else if constexpr (XT == kMx4) {
-        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 2>(A, s.shares, st);
-        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 3>(A, s.shares, st);
-        else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 2>(A, s.shares, st);
+        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 4>(A, s.shares, st);
+        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 5>(A, s.shares, st);
+        else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 4>(A, s.shares, st);
     } else {
         if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 3>(A, s.shares, st);
         else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 3>(A, s.shares, st);
@@ -541,7 +527,6 @@ extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_
     A.kp = (int)padded(in_features);
     A.pitch = (int)round_up(out_features, 4);
     A.share = (int)round_up((in_features + s.shares - 1) / s.shares, tokens <= kFew ? 1024 : 256);
-    A.vector = ld_y % 4 == 0 && aligned(y, 8);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const bool b = y_type == ECF8A_BF16;
     if (mx) return b ? run<kMx4, kBf16>(A, s, st) : run<kMx4, kFp16>(A, s, st);

@@ -104,8 +104,9 @@ def moe_few(x: torch.Tensor, gate, up, down, ids: torch.Tensor, weights: torch.T
     fresh = out is None
     with _Launch(dev, stream) as st:
         if fresh:
-            out = _empty((T, K), x.dtype, dev, stream)
-        ld_out = _rows(out, "out", T, K, (x.dtype,), dev)
+            out, ld_out = _empty((T, K), x.dtype, dev, stream), K
+        else:
+            ld_out = _rows(out, "out", T, K, (x.dtype,), dev)
         layer = ExpertsX(cg, cu, cd, K, inner, E, _MX4 if four else _TYPES[torch.float8_e4m3fn])
         need = _lib().ecf8x_moe_bytes(T, top, ctypes.byref(layer))
         reads = None

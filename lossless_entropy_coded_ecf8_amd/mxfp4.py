@@ -80,6 +80,13 @@ class MXFP4:
             raise ValueError("data must start on a 16-byte border, scales on a 4-byte one")
         self.data, self.scales, self.features = data, scales, features
 
+    @classmethod
+    def _of(cls, data, scales, features) -> "MXFP4":
+        """Of tensors made for it, which need no checks."""
+        q = cls.__new__(cls)
+        q.data, q.scales, q.features = data, scales, features
+        return q
+
     @property
     def shape(self) -> Tuple[int, ...]:
         return tuple(self.data.shape[:-1]) + (self.features,)
@@ -140,7 +147,7 @@ def quantize_mxfp4(x: torch.Tensor, x_scale: Optional[torch.Tensor] = None, *, o
     with _Launch(dev, stream) as st:
         if out is None:
             wide, lead = -(-K // PITCH) * PITCH, tuple(x.shape[:-1])
-            out = MXFP4(_empty(lead + (wide // 2,), torch.uint8, dev, stream), _empty(lead + (wide // BLOCK,), torch.uint8, dev, stream), K)
+            out = MXFP4._of(_empty(lead + (wide // 2,), torch.uint8, dev, stream), _empty(lead + (wide // BLOCK,), torch.uint8, dev, stream), K)
         else:
             if out.shape != tuple(x.shape) or out.device != dev:
                 raise ValueError("out is %s on %s, x %s on %s" % (out.shape, out.device, tuple(x.shape), dev))
@@ -190,15 +197,17 @@ def linear_mxfp4(x, w: MXFP4, bias: Optional[torch.Tensor] = None, *, out_dtype:
         raise ValueError("bias must be %d contiguous %s values on %s" % (N, dtype, dev))
     fresh = out is None
     with _Launch(dev, stream) as st:
+        reads = None
+        if not fresh or workspace is not None:
+            reads = [("x", x.data if four else x), ("x.scales", x.scales if four else None), ("w", w.data), ("w.scales", w.scales), ("bias", bias)]
         if fresh:
-            out = _empty((T, N), dtype, dev, stream)
-        ld_out = _rows(out, "out", T, N, (dtype,), dev)
-        reads = [("x", x.data if four else x), ("x.scales", x.scales if four else None), ("w", w.data), ("w.scales", w.scales), ("bias", bias)]
-        if not fresh:
+            out, ld_out = _empty((T, N), dtype, dev, stream), N
+        else:
+            ld_out = _rows(out, "out", T, N, (dtype,), dev)
             _apart(out, reads, "out")
         L, kind = _lib(), _MX4 if four else _TYPES[dtype]
         need = L.ecf8x_linear_bytes(T, N, K, kind)
-        ws = _scratch(need, workspace, dev, stream, reads + [("out", out)]) if need else None
+        ws = _scratch(need, workspace, dev, stream, reads and reads + [("out", out)]) if need else None
         _check(L.ecf8x_linear(xp, xs, ldx, kind, T, N, K, ctypes.byref(w._c()), _ptr(bias), _TYPES[dtype], out.data_ptr(), ld_out,
                               _ptr(ws), 0 if ws is None else ws.numel(), st), "ecf8x_linear")
     return out
