@@ -87,24 +87,34 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // contiguous bytes of codes, under one scale; with 4-bit x unit g of either.
 //
 // Banks: place p of row r sits at p ^ turn(r); weight rows of 32 bytes lie as they
-// are.  The scales of a row's step: one dword (16-bit x: the four blocks that two
-// steps share).
+// are.
+//
+// Scales: a dword of every row comes with the step (16-bit x: the four blocks that two
+// steps share).  It asks the cache for as many lines as the codes do, so for the large
+// tiles of 4-bit x they come in groups of 512 values instead, 16 bytes of a row, two
+// groups ahead: each step sends for some rows' next but one group (4096 x 28672 x 8192:
+// 631 -> 585 us; 512 x 4096 x 4096, in tiles of 128 x 128: 18 -> 21, so not there; 16-bit
+// x gained nothing).
 template <int XT, int BM, int BN, int WM, int WN, int STAGES>
 struct Tile {
     static constexpr bool MX = XT == kMx4;
     static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = MX ? 128 : 64;
     static constexpr int AU = MX ? 4 : 8, BU = MX ? 4 : 2;     // 16-byte units of a row's step: x, weight
     static constexpr int kA = BM * AU, kB = BN * BU;            // 16-byte units of the two tiles
-    static constexpr int kS = MX ? BM + BN : BN;         // dwords of scales
-    static constexpr int kUnitsA = (kA + kThreads - 1) / kThreads, kUnitsB = (kB + kThreads - 1) / kThreads,
-                         kUnitsS = (kS + kThreads - 1) / kThreads;
-    static constexpr int kStage = 16 * (kA + kB) + 4 * kS;     // bytes
-    static constexpr int kLds = STAGES * kStage;
-    // Loads that may be under way at the end of a step: those of all stages but the next one's.
-    static constexpr int kAhead = (STAGES - 2) * (kA / kThreads + kB / kThreads + kS / kThreads);
-    static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
+    static constexpr bool GROUPED = MX && BN == 256;
+    static constexpr int GROUP = 512 / STEP;                   // steps of a group of scales
+    static constexpr int kRowsX = MX ? BM : 0, kRows = kRowsX + BN;    // rows of scales: tokens', then outputs'
+    static constexpr int kWaveB = kB / 8, kUnitsA = kA / kThreads, kUnitsB = kWaveB < 64 ? 1 : kB / kThreads;
+    static constexpr int kStage = 16 * (kA + kB) + (GROUPED ? 0 : 4 * kRows);                    // bytes
+    static constexpr int kLds = STAGES * kStage + (GROUPED ? 3 * 16 * kRows : 0);
+    // Loads that may be under way at the end of a step, the same in every wave, some with part of its lanes: those of all
+    // steps behind the next one; of groups of scales those sent for since its tiles, at least one step's.
+    static constexpr int kTiles = kUnitsA + kUnitsB, kScales = 1 + MX;
+    static constexpr int kAhead = GROUPED ? (STAGES - 2) * kTiles + kScales : (STAGES - 2) * (kTiles + kScales);
+    static_assert(STAGES >= 2 && (!GROUPED || STAGES <= GROUP + 2) && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
+    static_assert(kA % kThreads == 0 && (kWaveB < 64 || kWaveB % 64 == 0), "waves stage alike");
+    static_assert(GROUPED ? BN % (8 * GROUP) == 0 && kRowsX % (8 * GROUP) == 0 : BN <= 512 && kRowsX <= 512, "so for the scales");
     static_assert(WM * WN == kWaves && (MX ? MF % 2 == 0 : MF >= 1) && NF >= 1, "eight waves");
-    static_assert(kA % 64 == 0 && kB % 64 == 0 && kS % 64 == 0, "whole waves stage");
 
     // The unit of a row that lies at place p of its eight (before the turn by the row): places are numbered so that
     // lane group g reads g and 4 + g, which the lanes of one cycle spread over all banks.
@@ -114,62 +124,87 @@ struct Tile {
 
     // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
     // no result that is stored.
+    // Of scales: the byte offset of a lane's row, in groups that of the first of GROUP parts.  Rows past the last are past
+    // the end of the buffer, whose loads give 0.
     struct Places {
-        uint32_t a[kUnitsA], b[kUnitsB], s[kUnitsS];
+        uint32_t a[kUnitsA], b[kUnitsB], sx, sw;
+        Rsrc x_scales, w_scales;
     };
+    static constexpr int kPartX = kRowsX / (GROUPED ? 8 * GROUP : 8), kPartW = BN / (GROUPED ? 8 * GROUP : 8);    // rows of a wave
 
     static __device__ __forceinline__ Places places(const Args& A, int64_t t0, int n0)
     {
         Places at;
-        const uint32_t pitch_x = MX ? A.kp / 2 : 2 * (uint32_t)A.ld_x, pitch_w = A.kp / 2, pitch_s = A.kp / 32;
+        const uint32_t pitch_x = MX ? A.kp / 2 : 2 * (uint32_t)A.ld_x, pitch_w = A.kp / 2;
+        const int lane = threadIdx.x & 63, wave = wave_id();
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u / AU;
+            const int u = (wave * kUnitsA + i) * 64 + lane, row = u / AU;
             at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * unit_at((u % AU) ^ turn(row));
         }
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
-            const int u = i * kThreads + threadIdx.x, row = u / BU, unit = MX ? (u & 3) ^ turn(row) : u & 1;
-            at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * unit;
+            const int u = kWaveB < 64 ? wave * kWaveB + lane % kWaveB : wave * kWaveB + i * 64 + lane, row = u / BU;
+            at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * (MX ? (u & 3) ^ turn(row) : u & 1);
         }
-#pragma unroll
-        for (int i = 0; i < kUnitsS; ++i) {
-            const int u = i * kThreads + threadIdx.x;
-            if (MX && u < BM) at.s[i] = (uint32_t)min((int64_t)u, A.tokens - 1 - t0) * pitch_s;      // tokens first
-            else at.s[i] = (uint32_t)min(MX ? u - BM : u, A.n - 1 - n0) * pitch_s;
-        }
+        const bool small = GROUPED && A.kp < 512;
+        const uint32_t pitch = small ? 0 : A.kp / 32;
+        at.sx = (wave * kPartX + lane) * pitch;
+        at.sw = (wave * kPartW + lane) * pitch;
+        at.w_scales = buffer_of(small ? A.w : A.w_scales + (int64_t)n0 * (A.kp / 32), small ? 16 : (uint32_t)min(BN, A.n - n0) * pitch);
+        if constexpr (MX) at.x_scales = buffer_of(small ? A.w : A.x_scales + t0 * (A.kp / 32), small ? 16 : (uint32_t)min((int64_t)BM, A.tokens - t0) * pitch);
         return at;
     }
 
-    // One step's tiles, straight to LDS: the newest loads are those that every wave has.
+    // The first dword of a row's scales in group `group` of a share that begins at k0: 16 bytes of the row, the last ones
+    // where it ends before.  (Rows of fewer than 16 bytes: see small_scales.)
+    static __device__ __forceinline__ int first_of(const Args& A, int k0, int group) { return min(k0 / 128 + 4 * group, A.kp / 128 - 4); }
+
+    // Part `part` of GROUP of the rows' scales, `dword` of each on.  Where rows are shorter than a group there is nothing to
+    // send for; the same loads then read codes, which nobody looks at.
+    static __device__ __forceinline__ void stage_group(const Args& A, const Places& at, int dword, int part, u32x4* to)
+    {
+        const int lane = threadIdx.x & 63, wave = wave_id(), pitch = A.kp < 512 ? 0 : A.kp / 32, from = A.kp < 512 ? 0 : 4 * dword;
+        if (lane < kPartX)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(to + (part * 8 + wave) * kPartX), 16, at.sx, from + part * 8 * kPartX * pitch, 0, 0);
+        if (lane < kPartW)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(to + kRowsX + (part * 8 + wave) * kPartW), 16, at.sw,
+                                                     from + part * 8 * kPartW * pitch, 0, 0);
+    }
+
+    // Rows of fewer than 16 bytes of scales: all of them, as group 0.
+    static __device__ __forceinline__ void small_scales(const Args& A, int64_t t0, int n0, u32x4* scales)
+    {
+        uint32_t* to = reinterpret_cast<uint32_t*>(scales);
+        const int dwords = A.kp / 128;
+        for (int r = threadIdx.x; r < kRows; r += kThreads) {
+            const uint8_t* row = r < kRowsX ? A.x_scales + min(t0 + r, A.tokens - 1) * (A.kp / 32) : A.w_scales + (int64_t)min(n0 + r - kRowsX, A.n - 1) * (A.kp / 32);
+            for (int i = 0; i < dwords; ++i) to[4 * r + i] = reinterpret_cast<const uint32_t*>(row)[i];
+        }
+    }
+
+    // One step's tiles, straight to LDS.
     static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* buf)
     {
         u32x4 *la = buf, *lb = buf + kA;
         uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
         const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
-        const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2)), rs = buffer_of(A.w_scales + (int64_t)n0 * (A.kp / 32));
-        const int wave0 = threadIdx.x & ~63;
+        const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2));
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        if constexpr (!GROUPED) {
+            if (MX && lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(ls + wave * kPartX), 4, at.sx, (k / 128) * 4, 0, 0);
+            if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(ls + kRowsX + wave * kPartW), 4, at.sw, (k / 128) * 4, 0, 0);
+        }
+        if constexpr (kWaveB < 64) {
+            if (lane < kWaveB) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB), 16, at.b[0], k / 2, 0, 0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kUnitsS; ++i) {
-            const int first = i * kThreads + wave0;
-            if (kS % kThreads && first >= kS) break;
-            if (MX && first < BM)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(A.x_scales + t0 * (A.kp / 32)), (LdsMem*)(ls + first), 4, at.s[i], k / 32, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsMem*)(ls + first), 4, at.s[i], (k / 128) * 4, 0, 0);
+            for (int i = 0; i < kUnitsB; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB + i * 64), 16, at.b[i], k / 2, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < kUnitsB; ++i) {
-            const int first = i * kThreads + wave0;
-            if (kB % kThreads && first >= kB) break;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + first), 16, at.b[i], k / 2, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kUnitsA; ++i) {
-            const int first = i * kThreads + wave0;
-            if (kA % kThreads && first >= kA) break;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + first), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
-        }
+        for (int i = 0; i < kUnitsA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + (wave * kUnitsA + i) * 64), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
     }
 
     // The same where a reduction of 16-bit x ends inside the step: zeros past k1, a multiple of 32.  (Rows of 4 bits are
@@ -177,7 +212,6 @@ struct Tile {
     static __device__ __forceinline__ void stage_tail(const Args& A, int64_t t0, int n0, int k, int k1, u32x4* buf)
     {
         u32x4 *la = buf, *lb = buf + kA;
-        uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
         for (int u = threadIdx.x; u < kA; u += kThreads) {
             const int row = u / AU, unit = unit_at((u % AU) ^ turn(row));
             u32x4 v{0, 0, 0, 0};
@@ -190,15 +224,18 @@ struct Tile {
             if (k + 32 * unit < k1) v = *reinterpret_cast<const u32x4*>(A.w + (int64_t)min(n0 + row, A.n - 1) * (A.kp / 2) + k / 2 + 16 * unit);
             lb[u] = v;
         }
-        for (int u = threadIdx.x; u < kS; u += kThreads)
+        uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
+        for (int u = threadIdx.x; u < BN; u += kThreads)
             ls[u] = *reinterpret_cast<const uint32_t*>(A.w_scales + (int64_t)min(n0 + u, A.n - 1) * (A.kp / 32) + (k / 128) * 4);
     }
 
-    // odd: whether the step is the second of the two that share a dword of scales (16-bit x).
-    static __device__ __forceinline__ void multiply(const u32x4* buf, int wm, int wn, int odd, f32x4 (*acc)[NF])
+    // ls: the step's dword of the first row's scales, where they come in groups; odd: whether the step is the second of the
+    // two that share one (16-bit x).
+    static __device__ __forceinline__ void multiply(const u32x4* buf, const uint32_t* ls, int wm, int wn, int odd, f32x4 (*acc)[NF])
     {
         const u32x4 *la = buf, *lb = buf + kA;
-        const uint32_t* ls = reinterpret_cast<const uint32_t*>(lb + kB);
+        constexpr int EACH = GROUPED ? 4 : 1;                  // dwords from row to row
+        if constexpr (!GROUPED) ls = reinterpret_cast<const uint32_t*>(lb + kB);
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
         const int row0 = wm * (BM / WM) + c, col0 = wn * (BN / WN) + c;
         if constexpr (MX) {
@@ -210,14 +247,14 @@ struct Tile {
                 for (int p = 0; p < 2; ++p) {
                     const int row = row0 + 16 * (m + p);
                     to[p] = la[row * AU + (g ^ turn(row))];
-                    scale[p] = ls[row] >> (8 * g);
+                    scale[p] = ls[EACH * row] >> (8 * g);
                 }
             };
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 const int row = col0 + 16 * n;
                 b[n] = lb[row * BU + (g ^ turn(row))];
-                sb[n] = ls[BM + row] >> (8 * g);
+                sb[n] = ls[EACH * (BM + row)] >> (8 * g);
             }
             read_a(0, a[0], sa[0]);
 #pragma unroll
@@ -291,13 +328,22 @@ struct Tile {
         }
     }
 
-    // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
-    static __device__ __forceinline__ void stage_and_multiply(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* __restrict__ to,
-                                                              const u32x4* __restrict__ from, int wm, int wn, int odd, f32x4 (*acc)[NF])
+    // One step.  The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
+    static __device__ __forceinline__ void stage_and_multiply(const Args& A, const Places& at, int64_t t0, int n0, int later, int dword, int part,
+                                                              u32x4* __restrict__ to, u32x4* __restrict__ to_scales, const u32x4* __restrict__ from,
+                                                              const uint32_t* __restrict__ ls, int wm, int wn, int odd, f32x4 (*acc)[NF])
     {
-        stage(A, at, t0, n0, k, to);
+        if constexpr (GROUPED) stage_group(A, at, dword, part, to_scales);
+        stage(A, at, t0, n0, later, to);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        multiply(from, wm, wn, odd, acc);
+        multiply(from, ls, wm, wn, odd, acc);
+    }
+
+    // Where the dword of a group's first step lies.
+    static __device__ __forceinline__ const uint32_t* scales_of(const Args& A, int k0, int group, const u32x4* scales)
+    {
+        const int skip = A.kp < 512 ? 0 : k0 / 128 + 4 * group - first_of(A, k0, group);
+        return reinterpret_cast<const uint32_t*>(scales + group % 3 * kRows) + skip;
     }
 };
 
@@ -306,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 {
     typedef Tile<XT, BM, BN, WM, WN, STAGES> S;
     extern __shared__ u32x4 lds[];
-    const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+    const int wave = wave_id(), wm = wave / WN, wn = wave % WN;
     // Workgroups go to the eight dies in turn; each die gets a run of tiles, in
     // columns of eight tiles down the tokens, so that its cache sees the same rows
     // of x and of the weight again.
@@ -319,30 +365,54 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     const int n0 = tn * BN;
     const int k0 = blockIdx.y * A.share, k1 = min(XT == kMx4 ? A.kp : A.k, k0 + A.share), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
     f32x4 acc[S::MF][S::NF] = {};
-    // At the end of step s the tiles of step s + 1 have to be there, and only those
-    // of the steps behind it may be under way.  Steps past the last are replaced by
-    // the last, so that this count holds in every step.
     const typename S::Places at = S::places(A, t0, n0);
     constexpr int kUnits = S::kStage / 16;
+    u32x4* const scales = lds + STAGES * kUnits;              // of GROUPED tiles
+    if (S::GROUPED && k1 > k0) {
+        if (A.kp < 512) S::small_scales(A, t0, n0, scales);
+        else
+#pragma unroll
+            for (int i = 0; i < S::GROUP; ++i) S::stage_group(A, at, S::first_of(A, k0, 0), i, scales);
+    }
     if (steps > 0) {
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) S::stage(A, at, t0, n0, k0 + min(s, steps - 1) * S::STEP, lds + s * kUnits);
+        for (int s = 0; s < STAGES - 1; ++s) {
+            S::stage(A, at, t0, n0, k0 + min(s, steps - 1) * S::STEP, lds + s * kUnits);
+            if (S::GROUPED && s == 0) {
+#pragma unroll
+                for (int i = 0; i < S::GROUP; ++i) S::stage_group(A, at, S::first_of(A, k0, 1), i, scales + S::kRows);
+            }
+        }
         wait_and_meet<S::kAhead>();
     }
+    // At the end of step s the tiles of step s + 1 have to be there, and only what the
+    // steps behind the one that sent for them did send for may be under way.  Steps past
+    // the last are replaced by the last, so that this count holds in every step.
     int use = 0, fill = STAGES - 1;                           // the buffers of steps s and s + STAGES - 1
+    int group = 0, part = 0, dword = S::first_of(A, k0, 2);   // the step's group, its place in it; where the next but one begins
+    u32x4* to_scales = scales + 2 * S::kRows;
+    const uint32_t* ls = S::scales_of(A, k0, 0, scales);
     for (int s = 0; s < steps; ++s) {
-        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, lds + fill * kUnits, lds + use * kUnits, wm, wn,
-                              s & 1, acc);
+        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, dword, part, lds + fill * kUnits, to_scales,
+                              lds + use * kUnits, ls, wm, wn, s & 1, acc);
         wait_and_meet<S::kAhead>();
         use = use == STAGES - 1 ? 0 : use + 1;
         fill = fill == STAGES - 1 ? 0 : fill + 1;
+        ++ls;
+        if (S::GROUPED && ++part == S::GROUP) {
+            part = 0;
+            ++group;
+            dword = S::first_of(A, k0, group + 2);
+            to_scales = scales + (group + 2) % 3 * S::kRows;
+            ls = S::scales_of(A, k0, group, scales);
+        }
     }
     if constexpr (XT != kMx4) {
         if (k0 + steps * S::STEP < k1) {
             wait_and_meet<0>();
             S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
             wait_and_meet<0>();
-            S::multiply(lds, wm, wn, steps & 1, acc);
+            S::multiply(lds, ls, wm, wn, steps & 1, acc);
         }
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;

@@ -26,10 +26,10 @@ constexpr int kPair = 6;                  // x as two bfloat16 rows, the upper a
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void LdsMem;
 
-// Every offset used with it is inside the operand, so the range is left open.
-__device__ __forceinline__ Rsrc buffer_of(const void* p)
+// bytes: the range, past which loads give 0; left open where every offset is inside the operand.
+__device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes = ~0u)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
 // The wave's number, known to be the same in all of its lanes.
