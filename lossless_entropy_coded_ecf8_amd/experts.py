@@ -12,9 +12,9 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import binding
-from .adapters import _TYPES, _apart, _empty, _Launch, _ptr, _rows, _scratch
+from .adapters import _TYPES, _apart, _capturing, _empty, _Launch, _ptr, _rows, _scratch
 from .binding import _check
-from .mxfp4 import _HALF, _MX4, MXFP4, ExpertsX, MatrixX, _lib, _on_gpu
+from .mxfp4 import _HALF, _MX4, MXFP4, ExpertsX, MatrixX, _lib, _no_graph, _on_gpu, quantize_mxfp4
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_PAIRS = 512                          # tokens * top of one moe_few (ECF8X_MAX_PAIRS)
@@ -28,8 +28,9 @@ def moe_route(logits: torch.Tensor, top: int, *, score: str = "softmax", normali
     logits: (T, E) float32, bfloat16 or float16.  A weight is exp(v - max) (softmax) or 1 / (1 + exp(-v)) (sigmoid) of
     the chosen logit v, over the sum of the chosen ones (normalise), else softmax's over the sum over all experts;
     times scale.  An expert with logit -inf is never chosen: where fewer than `top` are left the ids are -1 and the
-    weights 0, which moe_few leaves out.
+    weights 0, which moe_few leaves out.  Serving only: no gradients (it warns once where the logits require them).
     """
+    _no_graph("moe_route", logits)
     _on_gpu(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be (T, E), got %s" % (tuple(logits.shape),))
@@ -77,8 +78,10 @@ def moe_few(x: torch.Tensor, gate, up, down, ids: torch.Tensor, weights: torch.T
     x: (T, K) bfloat16 or float16, rows on 16-byte borders.  gate, up: (E, I, K), down: (E, K, I), all three MXFP4, or
     all three uint8 E4M3 bytes (K and I multiples of 16) with a float32 scale for each expert (default 1).  ids: (T, top)
     int32, a value outside [0, E) adds nothing; weights: (T, top) float32; both contiguous.  T * top is at most 512: each
-    chosen expert's weights are read once, which is what bounds few tokens.  Returns (T, K) in x's type.
+    chosen expert's weights are read once, which is what bounds few tokens.  Returns (T, K) in x's type.  Serving only: no
+    gradients (it warns once where an operand requires them).
     """
+    _no_graph("moe_few", x, weights)
     _on_gpu(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be (T, K), got %s" % (tuple(x.shape),))
@@ -151,24 +154,36 @@ class ECF8Experts(torch.nn.Module):
             raise ValueError("scales must be (3, %d), got %s" % (self.experts, tuple(scales.shape)))
         self.register_buffer("scales", scales.contiguous())
         self._pool: Optional[torch.Tensor] = None
-        self._plans: dict = {}
+        self._whole: Optional[binding.DecodePlan] = None        # of the whole layer
+        self._named: tuple = ((), None)                         # the experts last named, and their plan
 
     def compressed_bytes(self) -> int:
         return sum(e.compressed_bytes() for e in self.encs)
 
     def _plan(self, experts: Optional[Tuple[int, ...]], stream):
+        if experts is None and self._whole is not None:
+            return self._whole
+        if experts is not None and self._named[0] == experts:
+            return self._named[1]
+        if _capturing(stream):
+            raise RuntimeError("a plan cannot be made while its stream is captured: decode the same experts once before")
         if self._pool is None:
             self._pool = _empty(3 * self.experts * self.inner * self.features, torch.uint8, self.device, stream)
-        if experts not in self._plans:
-            named = range(self.experts) if experts is None else experts
-            at = [m * self.experts + e for m in range(3) for e in named]
-            size = self.inner * self.features
-            self._plans[experts] = binding.DecodePlan([self.encs[i] for i in at], out=self._pool, offsets=[i * size for i in at], stream=stream)
-        return self._plans[experts]
+        named = range(self.experts) if experts is None else experts
+        at = [m * self.experts + e for m in range(3) for e in named]
+        size = self.inner * self.features
+        plan = binding.DecodePlan([self.encs[i] for i in at], out=self._pool, offsets=[i * size for i in at], stream=stream)
+        if experts is None:
+            self._whole = plan
+        else:
+            self._named = (experts, plan)
+        return plan
 
     def decode(self, experts: Optional[Sequence[int]] = None, stream=None):
-        """Decodes the layer, or the experts named (a plan is kept for each set of them), into the layer's pool; returns
-        gate, up and down as moe_few takes them.  Other experts' places are left as they are."""
+        """Decodes the layer, or the experts named, into the layer's pool; returns gate, up and down as moe_few takes them.
+        Other experts' places are left as they are.  The plan of the whole layer is kept, and that of the experts last named:
+        naming others costs their plan, which is made on the host.  All calls write the one pool: on several streams the
+        caller orders them, and what reads it."""
         if experts is not None:
             experts = tuple(sorted({int(e) for e in experts}))
             if not experts or experts[0] < 0 or experts[-1] >= self.experts:
@@ -186,7 +201,6 @@ class ECF8Experts(torch.nn.Module):
 
     def in_four_bits(self) -> Tuple[MXFP4, MXFP4, MXFP4]:
         """The layer's weights in MXFP4, for moe_few: decoded, scaled and quantised expert by expert."""
-        from .mxfp4 import quantize_mxfp4
         stacks = []
         for m, w in enumerate(self.decode()):
             each = [quantize_mxfp4(w[e].view(torch.float8_e4m3fn), self.scales[m, e]) for e in range(self.experts)]

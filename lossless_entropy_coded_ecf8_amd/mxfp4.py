@@ -9,6 +9,7 @@ this module checks arguments, supplies device memory and passes the current stre
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -114,6 +115,17 @@ class MXFP4:
         return MatrixX(self.data.data_ptr(), self.scales.data_ptr(), None)
 
 
+_warned = set()
+
+
+def _no_graph(name: str, *operands):
+    """Says once that a result carries no gradient where one may be expected."""
+    if name not in _warned and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in operands):
+        _warned.add(name)
+        warnings.warn("%s keeps no gradients%s; when serving, torch.no_grad() or requires_grad_(False) says that none are wanted"
+                      % (name, ": MXFP4Linear.adapted is the differentiable layer" if "linear" in name else ""), stacklevel=3)
+
+
 def _on_gpu(t, what: str):
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU, got %s" % (what, t.device))
@@ -173,10 +185,14 @@ def linear_mxfp4(x, w: MXFP4, bias: Optional[torch.Tensor] = None, *, out_dtype:
     """y = x w^T + bias with a weight (N, K) in 4 bits (ecf8x_linear); (T, N), summed in float32 and rounded once.
 
     x: (T, K) bfloat16 or float16, rows on 16-byte borders (y has its type), or an MXFP4 (y is out_dtype, bfloat16
-    unless given).  bias: (N,) in y's type.  out: where y goes.  Not differentiable by itself: MXFP4Linear.adapted is.
+    unless given).  bias: (N,) in y's type.  out: where y goes.  Not differentiable by itself (it warns once where an operand
+    requires gradients): MXFP4Linear.adapted is.
     """
+    four = isinstance(x, MXFP4)
+    if not four:
+        _no_graph("linear_mxfp4", x, bias)
     N, K = _weight_ok(w)
-    dev, four = w.device, isinstance(x, MXFP4)
+    dev = w.device
     if len(x.shape) != 2 or x.shape[1] != K:
         raise ValueError("x must be (T, %d), got %s" % (K, tuple(x.shape)))
     T = x.shape[0]
@@ -245,7 +261,8 @@ def linear_mxfp4_input_grad(dy: torch.Tensor, w: MXFP4, *, out: Optional[torch.T
 
 
 class MXFP4Linear(torch.nn.Module):
-    """A linear layer whose frozen weight is kept in 4 bits: ``data`` and ``scales`` are buffers, 0.53 bytes a weight.
+    """A linear layer whose frozen weight is kept in 4 bits: ``data``, ``scales`` and ``bias`` are buffers,
+    0.53 bytes a weight.
 
     ``forward`` takes 16-bit activations, or quantises them to 4 bits first where ``four_bit_input`` is set (the product
     then runs on the scaled matrix instruction); adapters and index add low-rank adapters as ECF8Linear.forward does.
@@ -258,7 +275,7 @@ class MXFP4Linear(torch.nn.Module):
         self.four_bit_input = four_bit_input
         self.register_buffer("data", weight.data)
         self.register_buffer("scales", weight.scales)
-        self.bias = None if bias is None else bias.detach().to(weight.device)
+        self.register_buffer("bias", None if bias is None else bias.detach().to(weight.device))
 
     @classmethod
     def from_linear(cls, linear: torch.nn.Linear, device="cuda", four_bit_input: bool = False) -> "MXFP4Linear":
@@ -276,7 +293,7 @@ class MXFP4Linear(torch.nn.Module):
 
     @property
     def weight(self) -> MXFP4:
-        return MXFP4(self.data, self.scales, self.in_features)
+        return MXFP4._of(self.data, self.scales, self.in_features)
 
     def _bias(self, dtype):
         return None if self.bias is None else self.bias.to(dtype)
@@ -328,7 +345,7 @@ class _Frozen(torch.autograd.Function):
     def backward(ctx, dy):
         if not ctx.needs_input_grad[0]:
             return None, None
-        return linear_mxfp4_input_grad(_whole(dy), MXFP4(*ctx.saved_tensors, ctx.features)), None
+        return linear_mxfp4_input_grad(_whole(dy), MXFP4._of(*ctx.saved_tensors, ctx.features)), None
 
 
 class _AdaptedMX(torch.autograd.Function):
@@ -350,7 +367,7 @@ class _AdaptedMX(torch.autograd.Function):
         dy = _whole(dy)
         want_x, want_factors = ctx.needs_input_grad[0], ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         # In x's 16 bits, to which the adapters' part is added and rounded again, as where the two are layers of their own.
-        dx = linear_mxfp4_input_grad(dy, MXFP4(data, scales, ctx.features)) if want_x else None
+        dx = linear_mxfp4_input_grad(dy, MXFP4._of(data, scales, ctx.features)) if want_x else None
         dx, d_down, d_up = adapter_grads(dy, x, down, up, scaling, ctx.plan, hidden=hidden, ranks=ranks, dx_base=dx, dx=dx,
                                          want=(want_x, want_factors))
         return dx, d_down, d_up, None, None, None

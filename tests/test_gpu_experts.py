@@ -221,7 +221,8 @@ def test_compressed_experts_decode_route_and_run():
     x = torch.randn(4, K, generator=gen(9)).bfloat16()
     ids, w = E.moe_route(torch.randn(4, n, generator=gen(10)).to(D), 2)
     ref, tol = R.layer(x.double(), *values, ids.cpu(), w.cpu().double(), BF)
-    y = layer(x.to(D), ids, w)
+    on = x.to(D)
+    y = layer(on, ids, w)
     R.check(y, ref, tol)
     layer._pool.zero_()
     named = layer.decode(experts=ids.unique().tolist())           # only what was chosen
@@ -235,3 +236,22 @@ def test_compressed_experts_decode_route_and_run():
     R.check(E.moe_few(x.to(D), *four, ids, w), ref, tol)
     with pytest.raises(ValueError):
         layer.decode(experts=[5])
+    layer.decode(experts=[0, 3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                                 # both plans are there
+        again = layer(on, ids, w)
+        layer.decode(experts=[3, 0])
+    for _ in range(3):
+        layer._pool.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, y)
+
+
+def test_a_plan_is_not_made_in_a_capture(monkeypatch):
+    from lossless_entropy_coded_ecf8_amd import experts as X
+    given, scales, _ = stacks(2, 32, 32, False, 9)
+    layer = E.ECF8Experts(*[[w[e].cpu() for e in range(2)] for w in given], torch.ones(3, 2), device=D)
+    monkeypatch.setattr(X, "_capturing", lambda stream: True)
+    with pytest.raises(RuntimeError):
+        layer.decode()

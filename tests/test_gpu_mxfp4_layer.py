@@ -51,7 +51,10 @@ def test_four_bit_form_of_a_compressed_layer():
     x = torch.randn(3, 64, generator=gen(4)).to(FP)
     R.check(small(x.to(D)), *R.product(x.double(), R.values(*want, 64), FP, lin.bias.detach().to(FP).double()))
     state = small.state_dict()
-    assert set(state) == {"data", "scales"}
+    assert set(state) == {"data", "scales", "bias"}
+    again = E.MXFP4Linear.from_linear(torch.nn.Linear(64, 24), device=D)
+    again.load_state_dict(state)
+    assert torch.equal(again(x.to(D)), small(x.to(D)))
 
 
 @pytest.mark.parametrize("T", [1, 50, 600])

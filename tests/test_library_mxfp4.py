@@ -141,3 +141,18 @@ def test_calls_off_the_gpu_or_of_other_shapes_are_refused():
             call()
     with pytest.raises(TypeError):
         E.linear_mxfp4(x, torch.zeros(5, 64))
+
+
+def test_calls_that_keep_no_gradients_say_so_once(monkeypatch):
+    import warnings
+    monkeypatch.setattr(M, "_warned", set())
+    w = four(5)
+    calls = {"linear_mxfp4": lambda x: E.linear_mxfp4(x, w), "moe_route": lambda x: E.moe_route(x, 2),
+             "moe_few": lambda x: E.moe_few(x, w, w, w, torch.zeros(3, 1, dtype=torch.int32), torch.zeros(3, 1))}
+    for name, call in calls.items():
+        for grad, heard in ((False, 0), (True, 1), (True, 0)):
+            with warnings.catch_warnings(record=True) as got:
+                warnings.simplefilter("always")
+                with pytest.raises(ValueError):                   # not on a GPU
+                    call(torch.zeros(3, 64, dtype=torch.bfloat16).requires_grad_(grad))
+            assert len(got) == heard and all(name in str(m.message) for m in got), name
