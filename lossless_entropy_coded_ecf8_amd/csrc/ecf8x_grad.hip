@@ -42,7 +42,9 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // four rows in each lane group, and the 16 units that half a wave touches lie in
 // different banks; so do those that 16 lanes store, since lanes of the second
 // half of a row store their units in another order.
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
+// PART: fragments without tokens are left out.  (A choice that keeps the compiler from reading operands ahead; for tiles that
+// are not full, so few tokens that there is one tile of them.)
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
 struct Tile {
     static constexpr bool SPLIT = TYPE == kFp16;
     static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
@@ -138,9 +140,9 @@ struct Tile {
     {
         if (kRaw == kThreads || threadIdx.x < kRaw) {
             const int j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
-            const bool in = n + at.row < n1;
-            const float s = scale_of(in ? e.scale : 0);
-            lb[at.row * BU + ((4 * j + (i ^ swap)) ^ turn(at.row))] = widen4(in ? (swap ? e.codes[i ^ 1] : e.codes[i]) : 0, s);
+            // Masks: no branch between the products, no register chosen by a number that only the lane knows.
+            const uint32_t in = n + at.row < n1 ? ~0u : 0, other = -(uint32_t)swap;
+            lb[at.row * BU + ((4 * j + (i ^ swap)) ^ turn(at.row))] = widen4(((e.codes[i ^ 1] & other) | (e.codes[i] & ~other)) & in, scale_of(e.scale & in));
         }
         if constexpr (SPLIT) {
 #pragma unroll
@@ -165,9 +167,9 @@ struct Tile {
     }
 
     // The products of a step, token fragments PER at a time: the operands of a group are read while the group before is
-    // multiplied.  between(i): what else there is to do, a quarter before each of the first four groups that have
-    // products; its VALU and LDS work then goes beside the other wave's products.  (All of it ahead of the products:
-    // 2.0 us a step of 256 x 256, 1.6 of them the products and their operands.)  live: fragments that hold tokens.
+    // multiplied.  between(i): what else there is to do, a quarter before each of the first groups; its VALU and LDS work
+    // then goes beside the other wave's products.  (All of it ahead of them: 2.0 us a step of 256 x 256; so: 1.6.)
+    // live: fragments that hold tokens.
     template <class Between>
     static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, int live, f32x4 (*acc)[NF], Between between)
     {
@@ -207,7 +209,7 @@ struct Tile {
                 for (int q = 0; q < (GROUPS >= 4 ? 1 : 4 / GROUPS); ++q) between(i * (GROUPS >= 4 ? 1 : 4 / GROUPS) + q);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (m < live) {
+            if (!PART || m < live) {
 #pragma unroll
                 for (int p = 0; p < PER; ++p) {
 #pragma unroll
@@ -225,19 +227,19 @@ struct Tile {
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
     static __device__ __forceinline__ void step(const Args& A, const Places& at, int64_t t0, int n, int later, int n1, int whole, const Early& next,
                                                 Early& early, u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
-                                                const u32x4* __restrict__ lb, int wm, int wn, int live, f32x4 (*acc)[NF])
+                                                const u32x4* __restrict__ lb, int wm, int wn, int live, bool real, f32x4 (*acc)[NF])
     {
         fetch(A, at, t0, n + AHEAD * kStep, n1, whole, early);
         if constexpr (!SPLIT) stage(A, at, t0, later, to_a);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        multiply(la, lb, wm, wn, live, acc, [&](int i) { store(i, at, n + kStep, n1, next, to_a, to_b); });
+        if (real) multiply(la, lb, wm, wn, live, acc, [&](int i) { store(i, at, n + kStep, n1, next, to_a, to_b); });
     }
 };
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
 __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 {
-    typedef Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD> S;
+    typedef Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART> S;
     extern __shared__ u32x4 lds[];
     u32x4* const la = lds;
     u32x4* const lb = lds + S::kBuffers * S::kA;
@@ -272,13 +274,13 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
     // tile of step s + STAGES - 1 (the last one again past the end).
     int use = 0, fill = S::SPLIT ? 1 : STAGES - 1;
     constexpr int kPlanes = S::SPLIT ? 2 : 1, kTurn = S::SPLIT ? 2 : STAGES;
+    // Whole turns of AHEAD steps: a turn that is left inside makes the compiler copy what is being loaded, and wait for it.
     for (int s0 = 0; s0 < steps; s0 += AHEAD) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int s = s0 + i;
-            if (s >= steps) break;
             S::step(A, at, t0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, whole, early[(i + 1) % AHEAD], early[i],
-                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, live, acc);
+                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, live, s < steps, acc);
             if constexpr (S::SPLIT) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
@@ -290,11 +292,14 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
             fill = fill == kTurn - 1 ? 0 : fill + 1;
         }
     }
-    if (n0 + steps * kStep < n1) {                            // its codes are stored by now
+    if (n0 + steps * kStep < n1) {
         wait_and_meet<0>();
-        S::stage_tail(A, t0, n0 + steps * kStep, n1, la);
+        S::fetch(A, at, t0, n0 + steps * kStep, n1, -1, early[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S::store(i, at, n0 + steps * kStep, n1, early[0], la + (S::SPLIT ? 2 * S::kA : 0), lb);
+        S::stage_tail(A, t0, n0 + steps * kStep, n1, la);     // (float16 dy: stale values went to the other buffer)
         wait_and_meet<0>();
-        S::multiply(la, lb + (steps & 1) * S::kB, wm, wn, live, acc, [](int) {});
+        S::multiply(la, lb, wm, wn, live, acc, [](int) {});
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -319,14 +324,14 @@ struct Shape {
 
 // Measured on MI355X: microseconds of a step (64 rows of the weight) of a workgroup alone on its compute unit, and of two
 // side by side (0: no LDS for a second one).  Shares cost their sums' traffic and the launch that joins them: 77 x 14336 x
-// 4096 in bfloat16 takes 25 + 5 us with 16 shares, 38 + 4 with 8.  float16 has twice the products, and no tiles of 256
+// 4096 in bfloat16 takes 24 + 5 us with 16 shares.  float16 has twice the products, and no tiles of 256
 // tokens, whose two planes leave no room for a second buffer.
 struct Cost {
     int bm, bn;
     double one, two;
 };
-constexpr Cost kCosts[] = {{256, 256, 2.0, 0.0}, {128, 256, 1.25, 0.0}, {128, 128, 0.75, 1.5}, {64, 256, 0.9, 0.0}, {32, 256, 0.7, 0.0}};
-constexpr Cost kCostsSplit[] = {{128, 256, 1.9, 0.0}, {128, 128, 1.4, 2.6}, {64, 256, 1.3, 0.0}, {32, 256, 0.9, 0.0}};
+constexpr Cost kCosts[] = {{256, 256, 1.62, 0.0}, {128, 256, 1.2, 0.0}, {128, 128, 0.7, 1.4}, {64, 256, 0.85, 0.0}, {32, 256, 0.65, 0.0}};
+constexpr Cost kCostsSplit[] = {{128, 256, 1.65, 0.0}, {128, 128, 1.3, 2.4}, {64, 256, 1.15, 0.0}, {32, 256, 0.85, 0.0}};
 
 Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
@@ -358,11 +363,11 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
            k % ECF8X_BLOCK == 0;
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART = false>
 int launch(Args A, uint32_t shares, hipStream_t st)
 {
-    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD>::kLds;
-    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD>;
+    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>::kLds;
+    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
@@ -379,7 +384,8 @@ int run(const Args& A, const Shape& s, hipStream_t st)
     if (s.bm == 256) {
         if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, s.shares, st);
         else rc = ECF8_ERR_UNSUPPORTED;                       // shape_of gives float16 none of these
-    } else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
+    } else if (s.bm == 128 && s.bn == 256 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, true>(A, s.shares, st);
+    else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
     else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, s.shares, st);
     else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, s.shares, st);
     else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, s.shares, st);
