@@ -473,13 +473,15 @@ Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
     return best;
 }
 
-// Few tokens: rows of a workgroup, as many as leave every compute unit one (two, where two fit: up to four tokens), and
+// Few tokens: rows of a workgroup, as many as leave every compute unit one (two, where two fit: up to four tokens of 16
+// bits, 16 of 4: 28672 x 8192 for one bfloat16 token 32 us with 128 rows, 28 with 64, for 16 of 4 bits 30 and 27), and
 // shares of the reduction where even the fewest do not.
-Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k)
+Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
     const int least = tokens <= 4 ? 32 : tokens <= 32 ? 64 : 128;
+    const bool two = tokens <= 4 || (mx && tokens <= 16);
     int rows = 128;
-    while (rows > least && (n + rows - 1) / rows < (tokens <= 4 && rows > 64 ? 256 : 192)) rows /= 2;
+    while (rows > least && (n + rows - 1) / rows < (two && rows > 64 ? 256 : 192)) rows /= 2;
     const uint64_t groups = (n + rows - 1) / rows, steps = (k + 32768 / rows - 1) / (32768 / rows);
     uint32_t shares = 1;
     while (shares < 8 && groups * shares <= 128 && steps / (2 * shares) * (32768 / rows) >= 1024 && steps - steps / (2 * shares) >= 8) shares *= 2;
@@ -494,7 +496,7 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
 
 Shape any_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
-    return tokens <= kFew ? few_shape_of(tokens, n, k) : shape_of(tokens, n, k, mx);
+    return tokens <= kFew ? few_shape_of(tokens, n, k, mx) : shape_of(tokens, n, k, mx);
 }
 
 template <int XT, int OUT, int MF, int RG, int TR = 16 * MF>

@@ -212,25 +212,29 @@ struct Stream {
                 const int row = (rg * RF + f) * 16 + c;
                 if constexpr (BLOCKS) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[f][j] = reinterpret_cast<const uint32_t*>(lw + row * WU + ((4 * q + j) ^ turn<WU>(row)))[g];
-                        rows[f][j] = ls[((rg * RF + f) * 16 + 4 * g + j) * KG + q];
-                    }
+                    for (int i = 0; i < 4; ++i) rows[f][i] = ls[((rg * RF + f) * 16 + 4 * g + i) * KG + q];
                 } else {
                     w[f] = lw[row * WU + ((4 * q + g) ^ turn<WU>(row))];
                     if constexpr (W == kMx4) sw[f] = ls[row * KG + q];
                 }
             }
+            // In the order in which the products take them, which begin with the first.
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const int row = (16 * m + c) % TR;
+            for (int j = 0; j < OPS; ++j) {
+                if constexpr (BLOCKS) {
 #pragma unroll
-                for (int j = 0; j < OPS; ++j) {
-                    const int unit = BLOCKS || FOURS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
+                    for (int f = 0; f < RF; ++f) {
+                        const int row = (rg * RF + f) * 16 + c;
+                        w[f][j] = reinterpret_cast<const uint32_t*>(lw + row * WU + ((4 * q + j) ^ turn<WU>(row)))[g];
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const int row = (16 * m + c) % TR, unit = BLOCKS || FOURS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
                     x[m][j] = lx[row * XU + (unit ^ turn<XU>(row))];
                     if constexpr (X == kPair) low[m][j] = lx[row * XU + ((XU / 2 + unit) ^ turn<XU>(row))];
+                    if constexpr (X == kMx4) sx[m] = lxs[row * KG + q];
                 }
-                if constexpr (X == kMx4) sx[m] = lxs[row * KG + q];
             }
         }
 
