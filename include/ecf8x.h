@@ -32,7 +32,9 @@
  *   linear:      y[t][n]  = sum_k x[t][k] * w[n][k] + bias[n]
  *   input_grad:  dx[t][k] = sum_n dy[t][n] * w[n][k]
  * Products are exact, sums are held in float32, and each result is rounded
- * once.  float16 activations enter the products as two bfloat16, exactly.
+ * once.  Widened weights are exact in bfloat16.  A block's power of two need not fit
+ * float16: with float16 x the sums of one block at a time are scaled, in float32,
+ * as they are added, and float16 dy enters as two bfloat16, exactly.
  *
  *   route: the `top` largest of a token's E logits, largest first, of equal
  *          ones the lowest expert (NaN counts as the largest); an expert with
@@ -115,7 +117,8 @@ uint64_t ecf8x_linear_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_
  * with their x_scales (ld_x unused).  w: (out_features x in_features) in 4
  * bits.  bias: out_features values of y's type (y_type: ECF8A_BF16 or
  * ECF8A_FP16) or NULL.  y: rows ld_y elements apart, aligned to its elements.
- * in_features: a multiple of 32; any number of tokens and out_features.
+ * in_features: a multiple of 32; any number of tokens and out_features within
+ * ecf8a.h's limits; ld_x up to 2^22 (offsets inside a tile have 32 bits).
  * Errors: ECF8_ERR_UNSUPPORTED (types), ECF8_ERR_SIZE, ECF8_ERR_ARG,
  * ECF8_ERR_WORKSPACE, ECF8_ERR_HIP. */
 int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_x, uint32_t x_type, uint64_t tokens, uint64_t out_features,
@@ -125,8 +128,8 @@ int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_x, uint32_t
 uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t type);
 
 /* dx = dy w, dy (tokens x out_features) and dx (tokens x in_features) of one
- * type (ECF8A_BF16 or ECF8A_FP16), rows on 16-byte borders.  Errors as
- * ecf8x_linear. */
+ * type (ECF8A_BF16 or ECF8A_FP16), rows on 16-byte borders, ld_dy up to 2^22.
+ * Errors as ecf8x_linear. */
 int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, uint64_t tokens, uint64_t out_features, uint64_t in_features,
                      const ecf8x_matrix* w, void* dx, uint64_t ld_dx, void* workspace, uint64_t workspace_bytes,
                      void* hip_stream);
@@ -138,7 +141,9 @@ int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, uint64_t tok
 
 /* logits (tokens x experts) of type ECF8A_FP32, ECF8A_BF16 or ECF8A_FP16, rows
  * ld elements apart; ids and weights: tokens x top.  1 <= top <= experts,
- * top <= ECF8X_MAX_TOP, experts <= ECF8X_MAX_EXPERTS. */
+ * top <= ECF8X_MAX_TOP, experts <= ECF8X_MAX_EXPERTS.  Errors:
+ * ECF8_ERR_UNSUPPORTED (type, score), ECF8_ERR_SIZE, ECF8_ERR_ARG,
+ * ECF8_ERR_HIP. */
 int ecf8x_route(const void* logits, uint64_t ld, uint32_t type, uint64_t tokens, uint32_t experts, uint32_t top, uint32_t score,
                 uint32_t normalise, float scale, int32_t* ids, float* weights, void* hip_stream);
 
@@ -156,7 +161,8 @@ uint64_t ecf8x_moe_bytes(uint64_t tokens, uint32_t top, const ecf8x_experts* lay
 
 /* x (tokens x features) and y of one type (ECF8A_BF16 or ECF8A_FP16), rows of x
  * on 16-byte borders, y's aligned to its elements; ids and weights tokens x top,
- * contiguous; tokens * top <= ECF8X_MAX_PAIRS.  Two launches. */
+ * contiguous; tokens * top <= ECF8X_MAX_PAIRS; features and inner up to 65536,
+ * ld_x up to 2^21.  Two launches.  Errors as ecf8x_linear. */
 int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t tokens, uint32_t top, const int32_t* ids, const float* weights,
               const ecf8x_experts* layer, void* y, uint64_t ld_y, void* workspace, uint64_t workspace_bytes, void* hip_stream);
 

@@ -90,8 +90,8 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
 }
 
 // Stores the first `count` of four values in a 16-bit type, eight bytes at any
-// address where all are wanted.  (Value by value, rows of an odd length took a fifth
-// of the time of 331 x 13821 x 5120.)
+// address where all are wanted.  (Value by value where rows have an odd length:
+// 1024 x 13821 x 5120 from 4 bits took 78 us where this takes 67.)
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
 template <int TYPE>

@@ -4,7 +4,12 @@
 // the block's largest magnitude is found by two exchanges between them, every
 // load is a whole run of a wave's lanes, and a lane stores its codes as one
 // dword.  The largest magnitude is compared as an integer, so that infinities
-// and NaN are larger than every number.
+// and NaN are larger than every number.  Rows without a gap and aligned ones need
+// no kernel of their own: one with 16-byte loads known to be aligned, over one long
+// row, took as long (28672 x 8192 bfloat16: 107 us and 106).
+//
+// Measured: 28672 x 8192 bfloat16 quantised in 106 us, 595 MB read and written at
+// 5.6 TB/s; E4M3 of the same size in 69, and back to bfloat16 in 84.
 #include "ecf8x_common.h"
 
 namespace {
@@ -24,26 +29,25 @@ struct ConvertArgs {
 };
 
 // The eight values of unit u of a row.
-template <int TYPE, bool ALIGNED>
+template <int TYPE>
 __device__ __forceinline__ void load8(const void* x, int64_t at, float factor, float v[8])
 {
     if constexpr (TYPE == kFp32) {
         const char* p = static_cast<const char*>(x) + 4 * at;
-        const f32x4 a = __builtin_bit_cast(f32x4, load16<ALIGNED>(p)), b = __builtin_bit_cast(f32x4, load16<ALIGNED>(p + 16));
+        const f32x4 a = __builtin_bit_cast(f32x4, load16<false>(p)), b = __builtin_bit_cast(f32x4, load16<false>(p + 16));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     } else if constexpr (TYPE == kE4m3) {
         const char* p = static_cast<const char*>(x) + at;
         uint32_t d[2];
-        if constexpr (ALIGNED) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(p);
-        else __builtin_memcpy(d, p, 8);
+        __builtin_memcpy(d, p, 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[i], true);
             v[4 * i] = lo[0] * factor, v[4 * i + 1] = lo[1] * factor, v[4 * i + 2] = hi[0] * factor, v[4 * i + 3] = hi[1] * factor;
         }
     } else {
-        const u32x4 d = load16<ALIGNED>(static_cast<const char*>(x) + 2 * at);
+        const u32x4 d = load16<false>(static_cast<const char*>(x) + 2 * at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x2 p = unpack2<TYPE>(d[i]);
@@ -58,8 +62,7 @@ __device__ __forceinline__ uint32_t of_block(uint32_t m)
     return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));    // lane ^ 2
 }
 
-// FLAT: rows without a gap and without padding, so that they are one long row.
-template <int TYPE, bool ALIGNED, bool FLAT>
+template <int TYPE>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(ConvertArgs A)
 {
     const float factor = TYPE == kE4m3 && A.x_scale ? *A.x_scale : 1.0f;
@@ -68,16 +71,10 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(ConvertArgs A)
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t u = unit[i] = (blockIdx.x * kUnits + i) * (uint32_t)kThreads + threadIdx.x;
-        int64_t at = (int64_t)u * 8;
-        bool in = u < A.total;
-        if constexpr (!FLAT) {
-            const uint32_t row = u / A.units_row, col = u - row * A.units_row;
-            at = (int64_t)row * A.ld + col * 8;
-            in = in && col < A.units_in;
-        }
+        const uint32_t row = u / A.units_row, col = u - row * A.units_row;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        if (in) load8<TYPE, ALIGNED>(A.x, at, factor, v[i]);
+        if (u < A.total && col < A.units_in) load8<TYPE>(A.x, (int64_t)row * A.ld + col * 8, factor, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -148,15 +145,6 @@ uint64_t rows_of_launch(uint64_t units_row) { return (1ull << 31) / units_row; }
 
 uint32_t grid_of(uint64_t units) { return (uint32_t)((units + kThreads * kUnits - 1) / (kThreads * kUnits)); }
 
-template <int TYPE>
-void quantize(const ConvertArgs& A, bool aligned16, bool flat, hipStream_t st)
-{
-    const uint32_t grid = grid_of(A.total);
-    if (flat && aligned16) quantize_kernel<TYPE, true, true><<<grid, kThreads, 0, st>>>(A);
-    else if (aligned16) quantize_kernel<TYPE, true, false><<<grid, kThreads, 0, st>>>(A);
-    else quantize_kernel<TYPE, false, false><<<grid, kThreads, 0, st>>>(A);
-}
-
 }  // namespace
 
 extern "C" int ecf8x_quantize(const void* x, uint64_t ld_x, uint32_t type, const float* x_scale, uint64_t rows, uint64_t cols,
@@ -171,9 +159,6 @@ extern "C" int ecf8x_quantize(const void* x, uint64_t ld_x, uint32_t type, const
         return ECF8_ERR_ARG;
     if (rows > 1 && (ld_x < cols || ld_x > (1ull << 40))) return ECF8_ERR_SIZE;
     if (rows == 1) ld_x = cols;
-    // Eight values are 32, 16 or 8 bytes: one aligned load, or several.
-    const bool al = aligned(x, size == 1 ? 8 : 16) && ld_x * size % (size == 1 ? 8 : 16) == 0;
-    const bool flat = ld_x == cols && cols % ECF8X_PITCH == 0;
     for (uint64_t r = 0; r < rows; r += rows_of_launch(units_row)) {
         const uint64_t part = rows - r < rows_of_launch(units_row) ? rows - r : rows_of_launch(units_row);
         ConvertArgs A{};
@@ -185,11 +170,12 @@ extern "C" int ecf8x_quantize(const void* x, uint64_t ld_x, uint32_t type, const
         A.units_row = (uint32_t)units_row;
         A.units_in = (uint32_t)(cols / 8);
         A.total = (uint32_t)(part * units_row);
+        const uint32_t grid = grid_of(A.total);
         hipStream_t st = static_cast<hipStream_t>(hip_stream);
-        if (type == ECF8A_BF16) quantize<kBf16>(A, al, flat, st);
-        else if (type == ECF8A_FP16) quantize<kFp16>(A, al, flat, st);
-        else if (type == ECF8A_FP32) quantize<kFp32>(A, al, flat, st);
-        else quantize<kE4m3>(A, al, flat, st);
+        if (type == ECF8A_BF16) quantize_kernel<kBf16><<<grid, kThreads, 0, st>>>(A);
+        else if (type == ECF8A_FP16) quantize_kernel<kFp16><<<grid, kThreads, 0, st>>>(A);
+        else if (type == ECF8A_FP32) quantize_kernel<kFp32><<<grid, kThreads, 0, st>>>(A);
+        else quantize_kernel<kE4m3><<<grid, kThreads, 0, st>>>(A);
         const int rc = launch_status();
         if (rc != ECF8_OK) return rc;
     }

@@ -62,7 +62,9 @@ __device__ __forceinline__ float wave_sum(float v)
 
 // One wave a token; lane l holds experts l, 64 + l, ...: PER of them.  A round finds the largest logit that is left, and
 // the lowest expert that has it.  (Keys of 64 bits that hold both, exchanged through LDS: 14 us where this takes 9, 8192
-// tokens, 8 of 256.)
+// tokens, 8 of 256.)  What bounds it is the rounds, one after another: 8 of 256 for one token take 4.2 us, for 8192 8.7
+// (8.4 MB read, at 1 TB/s), 8 of 1024 20.
+// PER: 1, 4 or 16, the fewest that hold the experts: 64 of them for 8192 tokens 5.6, 8.0 and 18 us, 256 8.7 and 19.
 template <int TYPE, int PER>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs A)
 {
@@ -145,7 +147,8 @@ struct MoeArgs {
 // The pairs of one expert, in LDS.  Their order is free: a pair's results do not
 // depend on its column.
 struct Group {
-    uint32_t chosen[kExperts / 32], count;                    // a bit for each expert that some pair names
+    uint32_t chosen[kExperts / 32];                           // a bit for each expert that some pair names
+    uint32_t count;
     uint16_t pair[kPairs];
 };
 
@@ -154,7 +157,8 @@ struct Group {
 __device__ __forceinline__ int find(const MoeArgs& A, Group& G, int r, int& expert)
 {
     const int tid = threadIdx.x, lane = tid & 63;
-    if (tid <= kExperts / 32) G.chosen[tid] = 0;              // and the count
+    if (tid < kExperts / 32) G.chosen[tid] = 0;
+    if (tid == 0) G.count = 0;
     int id = -1;
     if (tid < A.pairs) id = A.ids[tid];
     const bool is = id >= 0 && id < A.experts;
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs A)
 
 // Sums that workgroups on other dies read: written through the die's own cache, and
 // read past it.  (Plain stores and a release fence, which writes that whole cache
-// back, took 114 us where this takes 30: one token, 8 experts, 117 MB of weights.)
+// back, took 114 us where the whole kernel takes 25 so: one token, 8 experts, 117 MB of weights.)
 constexpr int kPastDie = 16;
 
 __device__ __forceinline__ void put(Rsrc r, uint32_t at, f32x4 v)
@@ -370,11 +374,16 @@ int moe(MoeArgs A, hipStream_t st)
 template <int W, int TYPE>
 int moe(const MoeArgs& A, hipStream_t st)
 {
-    // Tokens that an expert meets together: 4 or 8, with room for two workgroups a compute unit, where they are few.
-    if (A.pairs <= 4 * A.experts) {
-        const int most = A.pairs < A.experts ? A.pairs : A.experts;
-        return (A.features + 127) / 128 * most <= 256 ? moe<W, TYPE, 0, 2>(A, st) : moe<W, TYPE, 0, 4>(A, st);
-    }
+    // Token rows of a stage, by how many an expert meets on average, up to the most that any can.  Microseconds of both
+    // launches, experts x features x inner:
+    //   4 or 8 rows (two workgroups a compute unit) or 16: 128 x 4096 x 1024, 4 pairs an expert: 4-bit weights 218 and 284,
+    //     E4M3 301 and 288; 2 an expert: 188 and 257, 234 and 233; 8 an expert (64 x 2048 x 1408): 143 and 141, 164 and 125;
+    //   16 or 32: 64 x 2048 x 1408, 8 an expert: E4M3 125 and 138; 8 x 4096 x 2048, 16 an expert of 64 tokens: 79 and 56.
+    // With so few chosen experts that 128 features a workgroup would not give every compute unit one, 64: 8 experts of
+    // 4096 x 1024 for one token 26 and 31 us (4 bits: 22 and 28); 32 of 2048 x 1408: 56 and 52.
+    const int most = A.pairs < A.experts ? A.pairs : A.experts;
+    const bool small = (A.features + 127) / 128 * most <= 256;
+    if (A.pairs <= (W == kMx4 || small ? 4 : 2) * A.experts) return small ? moe<W, TYPE, 0, 2>(A, st) : moe<W, TYPE, 0, 4>(A, st);
     if (A.tokens <= 16 || A.pairs <= 8 * A.experts) return moe<W, TYPE, 1, 4>(A, st);
     return moe<W, TYPE, 2, 4>(A, st);
 }

@@ -42,8 +42,9 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // four rows in each lane group, and the 16 units that half a wave touches lie in
 // different banks; so do those that 16 lanes store, since lanes of the second
 // half of a row store their units in another order.
-// PART: fragments without tokens are left out.  (A choice that keeps the compiler from reading operands ahead; for tiles that
-// are not full, so few tokens that there is one tile of them.)
+// PART: fragments without tokens are left out.  For float16, whose products are twice as many, where at most three quarters of
+// one tile of 128 hold tokens: 77 x 14336 x 4096 takes 35 us and 37 without; 112 tokens 41 either way, and bfloat16
+// gains nothing at any number (28 us).
 template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
 struct Tile {
     static constexpr bool SPLIT = TYPE == kFp16;
@@ -384,9 +385,10 @@ int run(const Args& A, const Shape& s, hipStream_t st)
     if (s.bm == 256) {
         if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, s.shares, st);
         else rc = ECF8_ERR_UNSUPPORTED;                       // shape_of gives float16 none of these
-    } else if (s.bm == 128 && s.bn == 256 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, true>(A, s.shares, st);
-    else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
-    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, s.shares, st);
+    } else if (s.bm == 128 && s.bn == 256) {
+        if (TYPE == kFp16 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, TYPE == kFp16>(A, s.shares, st);
+        else rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
+    } else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, s.shares, st);
     else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, s.shares, st);
     else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, s.shares, st);
     if (rc != ECF8_OK || s.shares < 2) return rc;

@@ -13,7 +13,7 @@ namespace {
 
 using namespace ecf8x;
 
-constexpr int kThreads = 512, kWaves = 8;
+constexpr int kThreads = 512, kWaves = 8;      // of tile_kernel
 
 struct Args {
     const void* x;              // 16-bit rows, ld_x elements apart, or codes
@@ -434,14 +434,19 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 
 // ------------------------------------------------------------ choice
 
-constexpr uint64_t kFew = 64;             // tokens of few_kernel
+// Tokens of few_kernel, which widens each code for up to 64 tokens, and tiles of 128 for 128.  64 x 28672 x 8192 in
+// bfloat16, float16 and 4 bits: 48, 58 and 38 us, in tiles 72, 113 and 45; 64 x 4096 x 4096: 15, 16 and 14, in tiles 17, 28
+// and 12.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
+constexpr uint64_t kFew = 64;
 
 struct Shape {
     int bm, bn;
     uint32_t shares;
 };
 
-// Microseconds of a step of a workgroup, as in the table of the E4M3 weight's input gradient.
+// Microseconds of a step of a workgroup, measured: of one alone on its compute unit and of two side by side (0: no LDS
+// for a second one).  Shares cost their sums' traffic and the launch that joins them.  bfloat16's; float16 takes longer in
+// every tile and chooses as bfloat16 does.
 struct Cost {
     int bm, bn;
     double one, two;
@@ -473,9 +478,12 @@ Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
     return best;
 }
 
-// Few tokens: rows of a workgroup, as many as leave every compute unit one (two, where two fit: up to four tokens of 16
-// bits, 16 of 4: 28672 x 8192 for one bfloat16 token 32 us with 128 rows, 28 with 64, for 16 of 4 bits 30 and 27), and
-// shares of the reduction where even the fewest do not.
+// Few tokens.  Rows of a workgroup: as many as leave every compute unit one (two, where two fit: up to four tokens of 16
+// bits, 16 of 4), 128, 64 or 32.  28672 x 8192: one bfloat16 token 30, 26 and 35 us, 16 of 4 bits 31 and 27, 24 of bfloat16
+// 35 and 40; 4096 x 4096, one token: 8.7, 7.8 and 6.6.
+// Shares of the reduction, where even the fewest rows leave compute units without one: if they save as many steps as the
+// joining launch costs, 2 to 2.5 us.  A step takes 0.5 to 1.1 us with 16-bit tokens, 0.4 with 4 bits: 8 x 4096 x 4096 in
+// float16 11.0 us whole and 8.5 in four shares, 32 in 4 bits 8.6 and 9.1; one token (four steps) 6.6 and 7.8.
 Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
     const int least = tokens <= 4 ? 32 : tokens <= 32 ? 64 : 128;
@@ -484,8 +492,8 @@ Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
     while (rows > least && (n + rows - 1) / rows < (two && rows > 64 ? 256 : 192)) rows /= 2;
     const uint64_t groups = (n + rows - 1) / rows, steps = (k + 32768 / rows - 1) / (32768 / rows);
     uint32_t shares = 1;
-    while (shares < 8 && groups * shares <= 128 && steps / (2 * shares) * (32768 / rows) >= 1024 && steps - steps / (2 * shares) >= 8) shares *= 2;
-    return Shape{0, rows, shares};
+    while (shares < 8 && groups * shares <= 128 && steps / (2 * shares) * (32768 / rows) >= 1024) shares *= 2;
+    return Shape{0, rows, steps - steps / shares >= (mx ? 8 : 5) ? shares : 1};
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
@@ -514,9 +522,12 @@ int launch_few(const Args& A, uint32_t shares, hipStream_t st)
 template <int XT, int OUT>
 int run_few(const Args& A, const Shape& s, hipStream_t st)
 {
+    // Token rows of a stage: 16 for each fragment, but four where there are no more and they are not the small part of it
+    // (28672 x 8192, four tokens of bfloat16 26 us and with 16 rows 30, float16 30 and 36; 4 bits 25 either way).
     if (A.tokens <= 4) {
-        if (s.bn == 128) return launch_few<XT, OUT, 1, 4, 4>(A, s.shares, st);
-        return s.bn == 64 ? launch_few<XT, OUT, 1, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 1, 4>(A, s.shares, st);
+        constexpr int TR = XT == kMx4 ? 16 : 4;
+        if (s.bn == 128) return launch_few<XT, OUT, 1, 4, TR>(A, s.shares, st);
+        return s.bn == 64 ? launch_few<XT, OUT, 1, 2, TR>(A, s.shares, st) : launch_few<XT, OUT, 1, 1, TR>(A, s.shares, st);
     }
     if (A.tokens <= 16) return s.bn == 128 ? launch_few<XT, OUT, 1, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 2>(A, s.shares, st);
     if (A.tokens <= 32) return s.bn == 128 ? launch_few<XT, OUT, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 2, 2>(A, s.shares, st);

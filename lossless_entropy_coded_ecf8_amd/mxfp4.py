@@ -189,8 +189,7 @@ def linear_mxfp4(x, w: MXFP4, bias: Optional[torch.Tensor] = None, *, out_dtype:
     requires gradients): MXFP4Linear.adapted is.
     """
     four = isinstance(x, MXFP4)
-    if not four:
-        _no_graph("linear_mxfp4", x, bias)
+    _no_graph("linear_mxfp4", None if four else x, bias)
     N, K = _weight_ok(w)
     dev = w.device
     if len(x.shape) != 2 or x.shape[1] != K:
@@ -302,6 +301,7 @@ class MXFP4Linear(torch.nn.Module):
         if adapters is not None and index is None:
             raise ValueError("adapters need the index of each token's adapter")
         if self.four_bit_input:
+            _no_graph("linear_mxfp4", x)
             y = linear_mxfp4(quantize_mxfp4(x), self.weight, self._bias(x.dtype), out_dtype=x.dtype)
         else:
             y = linear_mxfp4(x, self.weight, self._bias(x.dtype))
