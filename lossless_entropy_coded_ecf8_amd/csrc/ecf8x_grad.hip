@@ -8,6 +8,7 @@
 // transposing LDS read.  Widened values are exact bfloat16; float16 dy is split
 // into two bfloat16 (exact).  Sums in float32, rounded once.
 #include "ecf8x_stream.h"
+#include "ecf8x_tiles.h"
 
 namespace {
 
@@ -21,10 +22,10 @@ struct Args {
     const uint8_t *w, *w_scales;
     uint16_t* dx;
     int64_t ld_dx;
-    float* planes;              // [share][tokens][k]; nullptr: one share, written to dx
+    float* sums;                // [share][tile that was left][BM][BN]
     int64_t tokens;
-    int n, k, kp, share;        // share: reduction length of one of gridDim.y shares, a multiple of 64
-    int tiles_m, tiles_n;
+    int n, k, kp;
+    Tiling tiling;              // shares of a multiple of 64
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -44,7 +45,8 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // half of a row store their units in another order.
 // PART: fragments without tokens are left out.  For float16, whose products are twice as many, where at most three quarters of
 // one tile of 128 hold tokens: 77 x 14336 x 4096 takes 35 us and 37 without; 112 tokens 41 either way, and bfloat16
-// gains nothing at any number (28 us).
+// gains nothing at any number (28 us).  (Fragments given to the wave rows in turn, each left out by itself: 96 tokens 36 us
+// so, 39 then.)
 template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
 struct Tile {
     static constexpr bool SPLIT = TYPE == kFp16;
@@ -245,15 +247,10 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
     u32x4* const la = lds;
     u32x4* const lb = lds + S::kBuffers * S::kA;
     const int wave = wave_id(), wm = wave / WN, wn = wave % WN;
-    // The order of tiles as in the forward product: a run of tiles for each die.
-    const int total = A.tiles_m * A.tiles_n;
-    int id = blockIdx.x;
-    if (total % 8 == 0) id = (id % 8) * (total / 8) + id / 8;
-    const int band = id / (8 * A.tiles_n), rows = min(8, A.tiles_m - band * 8), in_band = id - band * 8 * A.tiles_n;
-    const int tm = band * 8 + in_band % rows, tn = in_band / rows;
-    const int64_t t0 = (int64_t)tm * BM;
-    const int k0 = tn * BN;
-    const int n0 = blockIdx.y * A.share, n1 = min(A.n, n0 + A.share), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
+    const Part part = part_of(A.tiling, blockIdx.x);
+    const int64_t t0 = (int64_t)part.tm * BM;
+    const int k0 = part.tn * BN;
+    const int n0 = part.share * A.tiling.length, n1 = part.at < 0 ? A.n : min(A.n, n0 + A.tiling.length), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
     const int whole = steps > 0 ? n0 + (steps - 1) * kStep : -1;     // dy's last whole step
     f32x4 acc[S::MF][S::NF] = {};
     const int live = (int)min((int64_t)S::MF, (A.tokens - t0 - wm * (BM / WM) + 15) / 16);      // this wave's fragments that hold tokens
@@ -311,51 +308,24 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
         for (int n = 0; n < S::NF; ++n) {
             const int col = k0 + wn * (BN / WN) + n * 16 + 4 * g;   // K is a multiple of 32: an operand's columns are in or out
             if (col >= A.k) continue;
-            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.k + col) = acc[m][n];
+            if (part.at >= 0) *reinterpret_cast<f32x4*>(A.sums + ((int64_t)part.at * BM + (t - t0)) * BN + (col - k0)) = acc[m][n];
             else store4<TYPE>(A.dx + t * A.ld_dx + col, acc[m][n], 4);
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // loads to LDS that no step used land before the workgroup ends
 }
 
-struct Shape {
-    int bm, bn;
-    uint32_t shares;
-};
-
 // Measured on MI355X: microseconds of a step (64 rows of the weight) of a workgroup alone on its compute unit, and of two
 // side by side (0: no LDS for a second one).  Shares cost their sums' traffic and the launch that joins them: 77 x 14336 x
-// 4096 in bfloat16 takes 24 + 5 us with 16 shares.  float16 has twice the products, and no tiles of 256
+// 4096 in bfloat16 takes 24 + 5 us with 16 shares; 4096 x 13824 x 5120 530 us with all tiles in three shares, 455 with the 64
+// that are left of 320 in four.  float16 has twice the products, and no tiles of 256
 // tokens, whose two planes leave no room for a second buffer.
-struct Cost {
-    int bm, bn;
-    double one, two;
-};
 constexpr Cost kCosts[] = {{256, 256, 1.62, 0.0}, {128, 256, 1.2, 0.0}, {128, 128, 0.7, 1.4}, {64, 256, 0.85, 0.0}, {32, 256, 0.65, 0.0}};
 constexpr Cost kCostsSplit[] = {{128, 256, 1.65, 0.0}, {128, 128, 1.3, 2.4}, {64, 256, 1.15, 0.0}, {32, 256, 0.85, 0.0}};
 
-Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
+Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
-    Shape best{32, 256, 1};
-    double least = -1.0;
-    const Cost* costs = split ? kCostsSplit : kCosts;
-    const int count = split ? 4 : 5;
-    for (int i = 0; i < count; ++i) {
-        const Cost& c = costs[i];
-        if (c.bm > 32 && (uint64_t)c.bm / 2 >= tokens) continue;      // over half of the rows would be padding
-        const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
-        for (uint32_t s = 1; s <= 16 && (s == 1 || n / s >= 256); ++s) {
-            const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
-            const double full = c.two > 0.0 ? c.two : c.one;
-            const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
-            const double us = turns * ((n + s - 1) / s + 63) / 64 + (s > 1 ? 4.0 + 8.0 * s * tokens * k / 5e6 : 0.0);
-            if (least < 0.0 || us < least) {
-                least = us;
-                best = Shape{c.bm, c.bn, s};
-            }
-        }
-    }
-    return best;
+    return split ? tiling_of(kCostsSplit, tokens, k, n, kStep, kStep, 256, 32) : tiling_of(kCosts, tokens, k, n, kStep, kStep, 256, 32);
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
@@ -365,36 +335,33 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART = false>
-int launch(Args A, uint32_t shares, hipStream_t st)
+int launch(const Args& A, hipStream_t st)
 {
     constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>::kLds;
     auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
-    A.tiles_m = (int)((A.tokens + BM - 1) / BM);
-    A.tiles_n = (A.k + BN - 1) / BN;
-    kernel<<<dim3((uint32_t)A.tiles_m * A.tiles_n, shares), kThreads, bytes, st>>>(A);
+    kernel<<<groups_of(A.tiling), kThreads, bytes, st>>>(A);
     return launch_status();
 }
 
 template <int TYPE>
-int run(const Args& A, const Shape& s, hipStream_t st)
+int run(const Args& A, hipStream_t st)
 {
+    const Tiling& s = A.tiling;
     int rc;
     if (s.bm == 256) {
-        if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, s.shares, st);
+        if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, st);
         else rc = ECF8_ERR_UNSUPPORTED;                       // shape_of gives float16 none of these
     } else if (s.bm == 128 && s.bn == 256) {
-        if (TYPE == kFp16 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, TYPE == kFp16>(A, s.shares, st);
-        else rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, s.shares, st);
-    } else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, s.shares, st);
-    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, s.shares, st);
-    else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, s.shares, st);
-    if (rc != ECF8_OK || s.shares < 2) return rc;
-    const uint64_t units = (uint64_t)A.tokens * A.k / 4;
-    join_kernel<TYPE><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.planes, A.tokens, A.k, A.k, (int)s.shares, nullptr, A.dx, A.ld_dx);
-    return launch_status();
+        if (TYPE == kFp16 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, TYPE == kFp16>(A, st);
+        else rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, st);
+    } else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, st);
+    else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, st);
+    else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, st);
+    if (rc != ECF8_OK || s.rest == 0) return rc;
+    return join_tiles<TYPE>(A.sums, s, A.tokens, A.k, nullptr, A.dx, A.ld_dx, st);
 }
 
 }  // namespace
@@ -402,8 +369,8 @@ int run(const Args& A, const Shape& s, hipStream_t st)
 extern "C" uint64_t ecf8x_input_grad_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t type)
 {
     if (!sizes_ok(tokens, out_features, in_features)) return 0;
-    const uint64_t s = shape_of(tokens, out_features, in_features, type == ECF8A_FP16).shares;
-    return s > 1 ? round_up(4 * s * tokens * in_features, 256) : 0;
+    if (tokens == 0) return 0;
+    return sums_of(tiles_of(tokens, out_features, in_features, type == ECF8A_FP16));
 }
 
 extern "C" int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, uint64_t tokens, uint64_t out_features, uint64_t in_features,
@@ -420,10 +387,9 @@ extern "C" int ecf8x_input_grad(const void* dy, uint64_t ld_dy, uint32_t type, u
     if (ld_dy < out_features || ld_dx < in_features || ld_dy > (1u << 22) || ld_dx > (1ull << 40)) return ECF8_ERR_SIZE;
     const uint64_t need = ecf8x_input_grad_bytes(tokens, out_features, in_features, type);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
-    const Shape s = shape_of(tokens, out_features, in_features, type == ECF8A_FP16);
     const Args A{static_cast<const uint16_t*>(dy), (int64_t)ld_dy, w->codes, w->scales, static_cast<uint16_t*>(dx), (int64_t)ld_dx,
-                 s.shares > 1 ? static_cast<float*>(workspace) : nullptr, (int64_t)tokens, (int)out_features, (int)in_features,
-                 (int)padded(in_features), (int)round_up((out_features + s.shares - 1) / s.shares, 64), 0, 0};
+                 static_cast<float*>(workspace), (int64_t)tokens, (int)out_features, (int)in_features, (int)padded(in_features),
+                 tiles_of(tokens, out_features, in_features, type == ECF8A_FP16)};
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    return type == ECF8A_BF16 ? run<kBf16>(A, s, st) : run<kFp16>(A, s, st);
+    return type == ECF8A_BF16 ? run<kBf16>(A, st) : run<kFp16>(A, st);
 }

@@ -8,6 +8,7 @@
 // result is scaled as it is added.  Four-bit x: the scaled matrix instruction takes
 // codes and scale bytes as they are stored.
 #include "ecf8x_stream.h"
+#include "ecf8x_tiles.h"
 
 namespace {
 
@@ -23,12 +24,11 @@ struct Args {
     const uint16_t* bias;
     uint16_t* y;
     int64_t ld_y;
-    float* planes;              // [share][tokens][pitch]; nullptr: one share, written to y
+    float* sums;                // few tokens: [share][token][pitch], nullptr where there is one share; else [share][tile that was left][BM][BN]
     int64_t tokens;
     int n, k, kp;               // kp: k rounded up to 128
-    int pitch;                  // n rounded up to 4
-    int share;                  // reduction length of one of gridDim.y shares, a multiple of 256 (few tokens: 1024)
-    int tiles_m, tiles_n;
+    int pitch, share;           // few tokens: n rounded up to 4; length of one of gridDim.y shares, a multiple of 1024
+    Tiling tiling;              // more: shares of a multiple of 256
 };
 
 template <int OUT>
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
         for (int m = 0; m < MF; ++m) {
             const int n = n0 + 16 * (wave * S::RF + f) + 4 * g, t = 16 * m + c;
             if (t >= A.tokens || n >= A.n) continue;
-            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.pitch + n) = acc[f][m];
+            if (A.sums) *reinterpret_cast<f32x4*>(A.sums + ((int64_t)blockIdx.y * A.tokens + t) * A.pitch + n) = acc[f][m];
             else finish<OUT>(A, t, n, acc[f][m]);
         }
 }
@@ -353,17 +353,10 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     typedef Tile<XT, BM, BN, WM, WN, STAGES> S;
     extern __shared__ u32x4 lds[];
     const int wave = wave_id(), wm = wave / WN, wn = wave % WN;
-    // Workgroups go to the eight dies in turn; each die gets a run of tiles, in
-    // columns of eight tiles down the tokens, so that its cache sees the same rows
-    // of x and of the weight again.
-    const int total = A.tiles_m * A.tiles_n;
-    int id = blockIdx.x;
-    if (total % 8 == 0) id = (id % 8) * (total / 8) + id / 8;
-    const int band = id / (8 * A.tiles_n), rows = min(8, A.tiles_m - band * 8), in_band = id - band * 8 * A.tiles_n;
-    const int tm = band * 8 + in_band % rows, tn = in_band / rows;
-    const int64_t t0 = (int64_t)tm * BM;
-    const int n0 = tn * BN;
-    const int k0 = blockIdx.y * A.share, k1 = min(XT == kMx4 ? A.kp : A.k, k0 + A.share), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
+    const Part part = part_of(A.tiling, blockIdx.x);
+    const int64_t t0 = (int64_t)part.tm * BM;
+    const int n0 = part.tn * BN;
+    const int end = XT == kMx4 ? A.kp : A.k, k0 = part.share * A.tiling.length, k1 = part.at < 0 ? end : min(end, k0 + A.tiling.length), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
     f32x4 acc[S::MF][S::NF] = {};
     const typename S::Places at = S::places(A, t0, n0);
     constexpr int kUnits = S::kStage / 16;
@@ -389,18 +382,18 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     // steps behind the one that sent for them did send for may be under way.  Steps past
     // the last are replaced by the last, so that this count holds in every step.
     int use = 0, fill = STAGES - 1;                           // the buffers of steps s and s + STAGES - 1
-    int group = 0, part = 0, dword = S::first_of(A, k0, 2);   // the step's group, its place in it; where the next but one begins
+    int group = 0, turn = 0, dword = S::first_of(A, k0, 2);   // the step's group, its place in it; where the next but one begins
     u32x4* to_scales = scales + 2 * S::kRows;
     const uint32_t* ls = S::scales_of(A, k0, 0, scales);
     for (int s = 0; s < steps; ++s) {
-        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, dword, part, lds + fill * kUnits, to_scales,
+        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, dword, turn, lds + fill * kUnits, to_scales,
                               lds + use * kUnits, ls, wm, wn, s & 1, acc);
         wait_and_meet<S::kAhead>();
         use = use == STAGES - 1 ? 0 : use + 1;
         fill = fill == STAGES - 1 ? 0 : fill + 1;
         ++ls;
-        if (S::GROUPED && ++part == S::GROUP) {
-            part = 0;
+        if (S::GROUPED && ++turn == S::GROUP) {
+            turn = 0;
             ++group;
             dword = S::first_of(A, k0, group + 2);
             to_scales = scales + (group + 2) % 3 * S::kRows;
@@ -424,7 +417,7 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
         for (int n = 0; n < S::NF; ++n) {
             const int col = n0 + wn * (BN / WN) + n * 16 + 4 * g;
             if (col >= A.n) continue;
-            if (A.planes) *reinterpret_cast<f32x4*>(A.planes + ((int64_t)blockIdx.y * A.tokens + t) * A.pitch + col) = acc[m][n];
+            if (part.at >= 0) *reinterpret_cast<f32x4*>(A.sums + ((int64_t)part.at * BM + (t - t0)) * BN + (col - n0)) = acc[m][n];
             else finish<OUT>(A, t, col, acc[m][n]);
         }
     }
@@ -439,44 +432,21 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 // and 12.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
 constexpr uint64_t kFew = 64;
 
-struct Shape {
-    int bm, bn;
-    uint32_t shares;
-};
-
 // Microseconds of a step of a workgroup, measured: of one alone on its compute unit and of two side by side (0: no LDS
 // for a second one).  Shares cost their sums' traffic and the launch that joins them.  bfloat16's; float16 takes longer in
 // every tile and chooses as bfloat16 does.
-struct Cost {
-    int bm, bn;
-    double one, two;
-};
 constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
 constexpr Cost kCostsMx[] = {{256, 256, 1.4, 0.0}, {128, 256, 1.1, 0.0}, {128, 128, 0.6, 1.2}};
 
-Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
+Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
-    Shape best{128, 128, 1};
-    double least = -1.0;
-    const Cost* costs = mx ? kCostsMx : kCosts16;
-    const int count = 3, step = mx ? 128 : 64;
-    for (int i = 0; i < count; ++i) {
-        const Cost& c = costs[i];
-        if (c.bm > 128 && (uint64_t)c.bm / 2 >= tokens) continue;     // over half of the rows would be padding
-        const uint64_t tiles = ((tokens + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-        for (uint32_t s = 1; s <= 16 && (s == 1 || k / s >= 4 * 256); ++s) {
-            const uint64_t groups = tiles * s, slots = c.two > 0.0 ? 512 : 256, whole = groups / slots, rest = groups % slots;
-            const double full = c.two > 0.0 ? c.two : c.one;
-            const double turns = whole * full + (rest == 0 ? 0.0 : rest <= 256 ? c.one : full);
-            const double us = turns * ((k + s - 1) / s + step - 1) / step + (s > 1 ? 4.0 + 8.0 * s * tokens * n / 5e6 : 0.0);
-            if (least < 0.0 || us < least) {
-                least = us;
-                best = Shape{c.bm, c.bn, s};
-            }
-        }
-    }
-    return best;
+    return mx ? tiling_of(kCostsMx, tokens, n, k, 128, 256, 1024, 128) : tiling_of(kCosts16, tokens, n, k, 64, 256, 1024, 128);
 }
+
+struct Few {
+    int rows;
+    uint32_t shares;
+};
 
 // Few tokens.  Rows of a workgroup: as many as leave every compute unit one (two, where two fit: up to four tokens of 16
 // bits, 16 of 4), 128, 64 or 32.  28672 x 8192: one bfloat16 token 30, 26 and 35 us, 16 of 4 bits 31 and 27, 24 of bfloat16
@@ -484,7 +454,7 @@ Shape shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 // Shares of the reduction, where even the fewest rows leave compute units without one: if they save as many steps as the
 // joining launch costs, 2 to 2.5 us.  A step takes 0.5 to 1.1 us with 16-bit tokens, 0.4 with 4 bits: 8 x 4096 x 4096 in
 // float16 11.0 us whole and 8.5 in four shares, 32 in 4 bits 8.6 and 9.1; one token (four steps) 6.6 and 7.8.
-Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
+Few few_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
     const int least = tokens <= 4 ? 32 : tokens <= 32 ? 64 : 128;
     const bool two = tokens <= 4 || (mx && tokens <= 16);
@@ -493,18 +463,13 @@ Shape few_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
     const uint64_t groups = (n + rows - 1) / rows, steps = (k + 32768 / rows - 1) / (32768 / rows);
     uint32_t shares = 1;
     while (shares < 8 && groups * shares <= 128 && steps / (2 * shares) * (32768 / rows) >= 1024) shares *= 2;
-    return Shape{0, rows, steps - steps / shares >= (mx ? 8 : 5) ? shares : 1};
+    return Few{rows, steps - steps / shares >= (mx ? 8 : 5) ? shares : 1};
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
 {
     return tokens <= ECF8A_MAX_TOKENS && n >= 1 && n <= ECF8A_MAX_FEATURES && k >= ECF8X_BLOCK && k <= ECF8A_MAX_FEATURES &&
            k % ECF8X_BLOCK == 0;
-}
-
-Shape any_shape_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
-{
-    return tokens <= kFew ? few_shape_of(tokens, n, k, mx) : shape_of(tokens, n, k, mx);
 }
 
 template <int XT, int OUT, int MF, int RG, int TR = 16 * MF>
@@ -520,53 +485,56 @@ int launch_few(const Args& A, uint32_t shares, hipStream_t st)
 }
 
 template <int XT, int OUT>
-int run_few(const Args& A, const Shape& s, hipStream_t st)
+int run_few(const Args& A, const Few& s, hipStream_t st)
 {
     // Token rows of a stage: 16 for each fragment, but four where there are no more and they are not the small part of it
     // (28672 x 8192, four tokens of bfloat16 26 us and with 16 rows 30, float16 30 and 36; 4 bits 25 either way).
     if (A.tokens <= 4) {
         constexpr int TR = XT == kMx4 ? 16 : 4;
-        if (s.bn == 128) return launch_few<XT, OUT, 1, 4, TR>(A, s.shares, st);
-        return s.bn == 64 ? launch_few<XT, OUT, 1, 2, TR>(A, s.shares, st) : launch_few<XT, OUT, 1, 1, TR>(A, s.shares, st);
+        if (s.rows == 128) return launch_few<XT, OUT, 1, 4, TR>(A, s.shares, st);
+        return s.rows == 64 ? launch_few<XT, OUT, 1, 2, TR>(A, s.shares, st) : launch_few<XT, OUT, 1, 1, TR>(A, s.shares, st);
     }
-    if (A.tokens <= 16) return s.bn == 128 ? launch_few<XT, OUT, 1, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 2>(A, s.shares, st);
-    if (A.tokens <= 32) return s.bn == 128 ? launch_few<XT, OUT, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 2, 2>(A, s.shares, st);
+    if (A.tokens <= 16) return s.rows == 128 ? launch_few<XT, OUT, 1, 4>(A, s.shares, st) : launch_few<XT, OUT, 1, 2>(A, s.shares, st);
+    if (A.tokens <= 32) return s.rows == 128 ? launch_few<XT, OUT, 2, 4>(A, s.shares, st) : launch_few<XT, OUT, 2, 2>(A, s.shares, st);
     return A.tokens <= 48 ? launch_few<XT, OUT, 3, 4>(A, s.shares, st) : launch_few<XT, OUT, 4, 4>(A, s.shares, st);
 }
 
 template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
-int launch_tile(Args A, uint32_t shares, hipStream_t st)
+int launch_tile(const Args& A, hipStream_t st)
 {
     constexpr int bytes = Tile<XT, BM, BN, WM, WN, STAGES>::kLds;
     auto* kernel = tile_kernel<XT, OUT, BM, BN, WM, WN, STAGES>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
-    A.tiles_m = (int)((A.tokens + BM - 1) / BM);
-    A.tiles_n = (A.n + BN - 1) / BN;
-    kernel<<<dim3((uint32_t)A.tiles_m * A.tiles_n, shares), kThreads, bytes, st>>>(A);
+    kernel<<<groups_of(A.tiling), kThreads, bytes, st>>>(A);
     return launch_status();
 }
 
 template <int XT, int OUT>
-int run(const Args& A, const Shape& s, hipStream_t st)
+int run(Args A, float* workspace, hipStream_t st)
 {
-    int rc;
+    constexpr bool MX = XT == kMx4;
     if (A.tokens <= (int64_t)kFew) {
-        rc = run_few<XT, OUT>(A, s, st);
-    } else if constexpr (XT == kMx4) {
-        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 4>(A, s.shares, st);
-        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 5>(A, s.shares, st);
-        else rc = launch_tile<XT, OUT, 128, 128, 2, 4, 4>(A, s.shares, st);
-    } else {
-        if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, 3>(A, s.shares, st);
-        else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, 3>(A, s.shares, st);
-        else rc = launch_tile<XT, OUT, 128, 128, 4, 2, 3>(A, s.shares, st);
+        const Few s = few_of(A.tokens, A.n, A.k, MX);
+        A.pitch = (A.n + 3) / 4 * 4;
+        A.share = (int)round_up((A.k + s.shares - 1) / s.shares, 1024);
+        A.sums = s.shares > 1 ? workspace : nullptr;
+        const int rc = run_few<XT, OUT>(A, s, st);
+        if (rc != ECF8_OK || s.shares < 2) return rc;
+        const uint64_t units = (uint64_t)A.tokens * A.pitch / 4;
+        join_kernel<OUT><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.sums, A.tokens, A.n, A.pitch, (int)s.shares, A.bias, A.y, A.ld_y);
+        return launch_status();
     }
-    if (rc != ECF8_OK || s.shares < 2) return rc;
-    const uint64_t units = (uint64_t)A.tokens * A.pitch / 4;
-    join_kernel<OUT><<<(uint32_t)((units + 255) / 256), 256, 0, st>>>(A.planes, A.tokens, A.n, A.pitch, (int)s.shares, A.bias, A.y, A.ld_y);
-    return launch_status();
+    A.sums = workspace;
+    A.tiling = tiles_of(A.tokens, A.n, A.k, MX);
+    const Tiling& s = A.tiling;
+    int rc;
+    if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 4 : 3>(A, st);
+    else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 5 : 3>(A, st);
+    else rc = launch_tile<XT, OUT, 128, 128, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3>(A, st);
+    if (rc != ECF8_OK || s.rest == 0) return rc;
+    return join_tiles<OUT>(A.sums, s, A.tokens, A.n, A.bias, A.y, A.ld_y, st);
 }
 
 }  // namespace
@@ -574,7 +542,9 @@ int run(const Args& A, const Shape& s, hipStream_t st)
 extern "C" uint64_t ecf8x_linear_bytes(uint64_t tokens, uint64_t out_features, uint64_t in_features, uint32_t x_type)
 {
     if (!sizes_ok(tokens, out_features, in_features)) return 0;
-    const uint64_t s = any_shape_of(tokens, out_features, in_features, x_type == ECF8X_MX4).shares;
+    const bool mx = x_type == ECF8X_MX4;
+    if (tokens > kFew) return sums_of(tiles_of(tokens, out_features, in_features, mx));
+    const uint64_t s = few_of(tokens, out_features, in_features, mx).shares;
     return s > 1 ? round_up(4 * s * tokens * round_up(out_features, 4), 256) : 0;
 }
 
@@ -593,7 +563,6 @@ extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_
     if ((!mx && (ld_x < in_features || ld_x > (1u << 22))) || ld_y < out_features || ld_y > (1ull << 40)) return ECF8_ERR_SIZE;
     const uint64_t need = ecf8x_linear_bytes(tokens, out_features, in_features, x_type);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ECF8_ERR_WORKSPACE;
-    const Shape s = any_shape_of(tokens, out_features, in_features, mx);
     Args A{};
     A.x = x;
     A.x_scales = x_scales;
@@ -603,15 +572,13 @@ extern "C" int ecf8x_linear(const void* x, const uint8_t* x_scales, uint64_t ld_
     A.bias = static_cast<const uint16_t*>(bias);
     A.y = static_cast<uint16_t*>(y);
     A.ld_y = (int64_t)ld_y;
-    A.planes = s.shares > 1 ? static_cast<float*>(workspace) : nullptr;
     A.tokens = (int64_t)tokens;
     A.n = (int)out_features;
     A.k = (int)in_features;
     A.kp = (int)padded(in_features);
-    A.pitch = (int)round_up(out_features, 4);
-    A.share = (int)round_up((in_features + s.shares - 1) / s.shares, tokens <= kFew ? 1024 : 256);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
     const bool b = y_type == ECF8A_BF16;
-    if (mx) return b ? run<kMx4, kBf16>(A, s, st) : run<kMx4, kFp16>(A, s, st);
-    return b ? run<kBf16, kBf16>(A, s, st) : run<kFp16, kFp16>(A, s, st);
+    float* ws = static_cast<float*>(workspace);
+    if (mx) return b ? run<kMx4, kBf16>(A, ws, st) : run<kMx4, kFp16>(A, ws, st);
+    return b ? run<kBf16, kBf16>(A, ws, st) : run<kFp16, kFp16>(A, ws, st);
 }

@@ -62,6 +62,39 @@ def test_products_in_shares(kind, T, N, K):
     product_is_right(kind, torch.randn(T, K, generator=gen(T, N)), w, wv)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "mx"])
+@pytest.mark.parametrize("T,N,K", [(1100, 15361, 2080), (1100, 15361, 4128)])
+def test_products_whose_last_tiles_go_in_shares(kind, T, N, K):
+    """More tiles than compute units, and a few left over; some tokens of each tile, all outputs."""
+    w, wv = weight(N, K)
+    dtype = FP if kind == "fp16" else BF
+    x = torch.randn(T, K, generator=gen(T, N)).to(dtype)
+    b = torch.randn(N, generator=gen(N)).to(dtype)
+    rows, given = x.double(), x.to(D)
+    if kind == "mx":
+        given = E.quantize_mxfp4(given)
+        rows = R.values(given.data, given.scales, K)
+    out = torch.full((T + 1, N + 3), 9.0, dtype=dtype, device=D)
+    E.linear_mxfp4(given, w, b.to(D), out=out[:T, 2:N + 2], **({"out_dtype": dtype} if kind == "mx" else {}))
+    some = list(range(0, T, 29)) + [T - 1]
+    R.check(out[some][:, 2:N + 2], *R.product(rows[some], wv, dtype, b.double()), (kind, K))
+    out[:T, 2:N + 2] = 9.0
+    assert bool((out == 9.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_input_grad_whose_last_tiles_go_in_shares(dtype):
+    T, N, K = 1100, 2001, 15392
+    w, wv = weight(N, K)
+    dy = torch.randn(T, 2008, generator=gen(T)).to(dtype)
+    out = torch.full((T + 1, K + 16), 9.0, dtype=dtype, device=D)
+    E.linear_mxfp4_input_grad(dy.to(D)[:, :N], w, out=out[:T, 8:K + 8])
+    some = list(range(0, T, 29)) + [T - 1]
+    R.check(out[some][:, 8:K + 8], *R.product(dy[some][:, :N].double(), wv.t().contiguous(), dtype), dtype)
+    out[:T, 8:K + 8] = 9.0
+    assert bool((out == 9.0).all())
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("T,N,K", [(1100, 333, 13024), (77, 5003, 288), (97, 2000, 1056), (20, 9000, 96)])
 def test_input_grad_in_large_tiles_and_shares(dtype, T, N, K):
