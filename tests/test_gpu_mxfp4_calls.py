@@ -103,6 +103,25 @@ def test_input_grad_in_large_tiles_and_shares(dtype, T, N, K):
     R.check(E.linear_mxfp4_input_grad(dy.to(D)[:, :N], w), *R.product(dy[:, :N].double(), wv.t().contiguous(), dtype), (T, N, K))
 
 
+def test_conversion_in_several_launches():
+    """More than 2^33 values, which are counted by eights and fours in 32 bits."""
+    rows, K = 270000, 32768
+    x = torch.zeros(rows, K, dtype=torch.uint8, device=D)
+    part = torch.randint(0, 256, (4, K), generator=gen(1)).to(torch.uint8)
+    part[(part & 127) == 127] = 5                                 # no NaN
+    at = [0, 262143, 262144, rows - 1]
+    x[at] = part.to(D)
+    q = E.quantize_mxfp4(x.view(torch.float8_e4m3fn))
+    want = R.store(*R.quantise(part.view(torch.float8_e4m3fn).float()))
+    assert torch.equal(q.data[at].cpu(), want[0]) and torch.equal(q.scales[at].cpu(), want[1])
+    del x
+    for dtype in (BF, torch.float32):
+        back = q.dequantize(dtype)
+        assert torch.equal(back[at].cpu().double(), R.values(*want, K))
+        assert not bool(back[1:262143:1000].any()) and not bool(back[262145:rows - 1:100].any())
+        del back
+
+
 @pytest.mark.parametrize("T", [3, 100])
 def test_smallest_numbers_count(T):
     """Subnormal bfloat16 and float16 values, under weights that bring the sum back into range."""
