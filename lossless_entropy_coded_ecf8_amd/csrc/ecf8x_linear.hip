@@ -45,6 +45,10 @@ __device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
 // ------------------------------------------------------------ few tokens
 
 // A share of the reduction is a multiple of 1024 values, so that it begins with a step.
+//
+// Up to about 16 tokens the stream of weights bounds it (28672 x 8192, 125 MB: one bfloat16 token 26 us, 4.8 TB/s; 16 of 4
+// bits 27), past them what each workgroup stages of the tokens beside its weights, 25 to 30 bytes a nanosecond and compute
+// unit together (45 float16 tokens 50 us, 40 of 4 bits 34).  Few rows (4096 x 4096: 6.6 us) are a chain of four steps.
 template <int XT, int OUT, int MF, int RG, int TR>
 __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 {
@@ -88,6 +92,11 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 //
 // Banks: place p of row r sits at p ^ turn(r); weight rows of 32 bytes lie as they
 // are.
+//
+// What bounds it: in the tiles of 256 x 256 the matrix instructions at the clock that the power limit leaves
+// (4096 x 28672 x 8192: bfloat16 1440 us, 1340 TFLOP/s; 4 bits 590, 3260); in float16 the scaling of each block's sums,
+// four multiply-adds for each product instruction (4096 x 13824 x 5120: 725 us, bfloat16 475); in tiles of
+// 128 x 256 of 4 bits the way from memory to LDS (331 x 13821 x 5120: 45 us, 25 KB in 1.1 us).
 //
 // Scales: a dword of every row comes with the step (16-bit x: the four blocks that two
 // steps share).  It asks the cache for as many lines as the codes do, so for the large
