@@ -192,28 +192,34 @@ struct Tile {
         }
     }
 
-    // One step's tiles, straight to LDS.
-    static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* buf)
+    // One step's tiles, straight to LDS, in kParts parts; scales that come with the step go with the first.
+    static constexpr int kParts = kUnitsA + kUnitsB;
+
+    static __device__ __forceinline__ void stage_part(const Args& A, const Places& at, int64_t t0, int n0, int k, int part, u32x4* buf)
     {
         u32x4 *la = buf, *lb = buf + kA;
         uint32_t* ls = reinterpret_cast<uint32_t*>(lb + kB);
-        const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
-        const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2));
         const int lane = threadIdx.x & 63, wave = wave_id();
         if constexpr (!GROUPED) {
-            if (MX && lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(ls + wave * kPartX), 4, at.sx, (k / 128) * 4, 0, 0);
-            if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(ls + kRowsX + wave * kPartW), 4, at.sw, (k / 128) * 4, 0, 0);
+            if (part == 0) {
+                if (MX && lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(ls + wave * kPartX), 4, at.sx, (k / 128) * 4, 0, 0);
+                if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(ls + kRowsX + wave * kPartW), 4, at.sw, (k / 128) * 4, 0, 0);
+            }
         }
-        if constexpr (kWaveB < 64) {
-            if (lane < kWaveB) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB), 16, at.b[0], k / 2, 0, 0);
+        if (part < kUnitsB) {
+            const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2));
+            if (kWaveB >= 64 || lane < kWaveB) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB + part * 64), 16, at.b[part], k / 2, 0, 0);
         } else {
-#pragma unroll
-            for (int i = 0; i < kUnitsB; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB + i * 64), 16, at.b[i], k / 2, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kUnitsA; ++i)
+            const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
+            const int i = part - kUnitsB;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + (wave * kUnitsA + i) * 64), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
+        }
+    }
+
+    static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n0, int k, u32x4* buf)
+    {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) stage_part(A, at, t0, n0, k, p, buf);
     }
 
     // The same where a reduction of 16-bit x ends inside the step: zeros past k1, a multiple of 32.  (Rows of 4 bits are
@@ -239,9 +245,16 @@ struct Tile {
     }
 
     // ls: the step's dword of the first row's scales, where they come in groups; odd: whether the step is the second of the
-    // two that share one (16-bit x).
-    static __device__ __forceinline__ void multiply(const u32x4* buf, const uint32_t* ls, int wm, int wn, int odd, f32x4 (*acc)[NF])
+    // two that share one (16-bit x).  between(p): what else there is to do, kParts parts of it spread over the products: a wave
+    // waits where it sends for more than the memory pipe has taken, and the pipe's time for a step is half of the step's.
+    template <class Between>
+    static __device__ __forceinline__ void multiply(const u32x4* buf, const uint32_t* ls, int wm, int wn, int odd, f32x4 (*acc)[NF], Between between)
     {
+        const auto spread = [&](int slot, int slots) {
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+                if (p * slots / kParts == slot) between(p);
+        };
         const u32x4 *la = buf, *lb = buf + kA;
         constexpr int EACH = GROUPED ? 4 : 1;                  // dwords from row to row
         if constexpr (!GROUPED) ls = reinterpret_cast<const uint32_t*>(lb + kB);
@@ -270,6 +283,7 @@ struct Tile {
             for (int m = 0; m < MF; m += 2) {
                 const int now = m / 2 & 1;
                 if (m + 2 < MF) read_a(m + 2, a[!now], sa[!now]);
+                spread(m / 2, MF / 2);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
@@ -317,6 +331,7 @@ struct Tile {
 #pragma unroll
                 for (int m = 0; m < MF + BLOCKS; ++m) {
                     if (m < MF) {
+                        spread(kk * MF + m, 2 * MF);
                         const int row = row0 + 16 * m;
                         const u32x4 a = la[row * AU + ((4 * kk + g) ^ turn(row))];
 #pragma unroll
@@ -342,10 +357,10 @@ struct Tile {
                                                               u32x4* __restrict__ to, u32x4* __restrict__ to_scales, const u32x4* __restrict__ from,
                                                               const uint32_t* __restrict__ ls, int wm, int wn, int odd, f32x4 (*acc)[NF])
     {
-        if constexpr (GROUPED) stage_group(A, at, dword, part, to_scales);
-        stage(A, at, t0, n0, later, to);
-        __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        multiply(from, ls, wm, wn, odd, acc);
+        multiply(from, ls, wm, wn, odd, acc, [&](int p) {
+            if (GROUPED && p == 0) stage_group(A, at, dword, part, to_scales);
+            stage_part(A, at, t0, n0, later, p, to);
+        });
     }
 
     // Where the dword of a group's first step lies.
@@ -414,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
             wait_and_meet<0>();
             S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
             wait_and_meet<0>();
-            S::multiply(lds, ls, wm, wn, steps & 1, acc);
+            S::multiply(lds, ls, wm, wn, steps & 1, acc, [](int) {});
         }
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
