@@ -98,17 +98,18 @@ struct Tile {
         return at;
     }
 
+    // Unit i of the kUnitsA that a wave sends for.
+    static __device__ __forceinline__ void stage_unit(const Args& A, const Places& at, int64_t t0, int n, int i, u32x4* la)
+    {
+        const int wave = wave_id();
+        if (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(A.dy + t0 * A.ld_dy), (LdsMem*)(la + wave * kWaveA + i * 64), 16, at.a[i], 2 * n, 0, 0);
+    }
+
     static __device__ __forceinline__ void stage(const Args& A, const Places& at, int64_t t0, int n, u32x4* la)
     {
-        const Rsrc ra = buffer_of(A.dy + t0 * A.ld_dy);
-        const int wave = wave_id();
-        if constexpr (kWaveA < 64) {
-            if ((int)(threadIdx.x & 63) < kWaveA) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + wave * kWaveA), 16, at.a[0], 2 * n, 0, 0);
-        } else {
 #pragma unroll
-            for (int i = 0; i < kUnitsA; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + wave * kWaveA + i * 64), 16, at.a[i], 2 * n, 0, 0);
-        }
+        for (int i = 0; i < kUnitsA; ++i) stage_unit(A, at, t0, n, i, la);
     }
 
     // What a thread loads early: a block of codes with its scale, and float16 dy.
@@ -237,9 +238,12 @@ struct Tile {
                                                 const u32x4* __restrict__ lb, int wm, int wn, int live, bool real, f32x4 (*acc)[NF])
     {
         fetch(A, at, t0, n + AHEAD * kStep, n1, whole, early);
-        if constexpr (!SPLIT) stage(A, at, t0, later, to_a);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
-        if (real) multiply(la, lb, wm, wn, live, acc, [&](int i) { store(i, at, n + kStep, n1, next, to_a, to_b); });
+        if (real)
+            multiply(la, lb, wm, wn, live, acc, [&](int i) {
+                if (!SPLIT && i < kUnitsA) stage_unit(A, at, t0, later, i, to_a);
+                store(i, at, n + kStep, n1, next, to_a, to_b);
+            });
     }
 };
 
@@ -329,7 +333,7 @@ constexpr Cost kCostsSplit[] = {{128, 256, 1.65, 0.0}, {128, 128, 1.3, 2.4}, {64
 
 Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
-    return split ? tiling_of(kCostsSplit, tokens, k, n, kStep, kStep, 256, 32) : tiling_of(kCosts, tokens, k, n, kStep, kStep, 256, 32);
+    return split ? tiling_of(kCostsSplit, 4, tokens, k, n, kStep, kStep, 256, 32) : tiling_of(kCosts, 5, tokens, k, n, kStep, kStep, 256, 32);
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)

@@ -83,7 +83,9 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 
 // One workgroup: BM tokens by BN outputs, eight waves in WM rows of WN, the
 // reduction in steps: 64 values of 16 bits (128 bytes of an x row, 32 of a weight
-// row), or 128 of 4 bits (64 bytes of each).
+// row), or of 4 bits 128 (64 bytes of each) or 256.  Runs of 64 bytes come to LDS at
+// 61 bytes a nanosecond and compute unit, of 128 at 100: the larger tiles take 256
+// (4096 x 28672 x 8192: 560 us in steps of 128 through four buffers, 527 so).
 //
 // Tiles go from memory to LDS without passing registers into STAGES buffers:
 // while step s is multiplied, step s + STAGES - 1 is sent for.  With 16-bit x lane group g takes units 2g and
@@ -94,21 +96,21 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // are.
 //
 // What bounds it: in the tiles of 256 x 256 the matrix instructions at the clock that the power limit leaves
-// (4096 x 28672 x 8192: bfloat16 1440 us, 1340 TFLOP/s; 4 bits 590, 3260); in float16 the scaling of each block's sums,
-// four multiply-adds for each product instruction (4096 x 13824 x 5120: 725 us, bfloat16 475); in tiles of
-// 128 x 256 of 4 bits the way from memory to LDS (331 x 13821 x 5120: 45 us, 25 KB in 1.1 us).
+// (4096 x 28672 x 8192: bfloat16 1360 us, 1415 TFLOP/s, 66% busy at 1.8 GHz; 4 bits 530, 3630, 43% at 1.9, beside as many cycles of LDS); in float16 the scaling of each block's sums,
+// four multiply-adds for each product instruction (4096 x 13824 x 5120: 695 us, bfloat16 450); where there are few
+// tiles, the units that have none (331 x 13821 x 5120 of 4 bits: 37 us, 162 tiles of 128 x 256).
 //
 // Scales: a dword of every row comes with the step (16-bit x: the four blocks that two
 // steps share).  It asks the cache for as many lines as the codes do, so for the large
 // tiles of 4-bit x they come in groups of 512 values instead, 16 bytes of a row, two
-// groups ahead: each step sends for some rows' next but one group (4096 x 28672 x 8192:
-// 631 -> 585 us; 512 x 4096 x 4096, in tiles of 128 x 128: 18 -> 21, so not there; 16-bit
+// groups ahead: each step sends for some rows' next but one group (4096 x 28672 x 8192
+// gained 7%; 512 x 4096 x 4096, in tiles of 128 x 128: 18 -> 21, so not there; 16-bit
 // x gained nothing).
-template <int XT, int BM, int BN, int WM, int WN, int STAGES>
+template <int XT, int BM, int BN, int WM, int WN, int STAGES, int LENGTH>
 struct Tile {
     static constexpr bool MX = XT == kMx4;
-    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = MX ? 128 : 64;
-    static constexpr int AU = MX ? 4 : 8, BU = MX ? 4 : 2;     // 16-byte units of a row's step: x, weight
+    static constexpr int MF = BM / WM / 16, NF = BN / WN / 16, STEP = LENGTH;
+    static constexpr int AU = MX ? STEP / 32 : 8, BU = MX ? AU : 2;     // 16-byte units of a row's step: x, weight
     static constexpr int kA = BM * AU, kB = BN * BU;            // 16-byte units of the two tiles
     static constexpr bool GROUPED = MX && BN == 256;
     static constexpr int GROUP = 512 / STEP;                   // steps of a group of scales
@@ -119,7 +121,7 @@ struct Tile {
     // Loads that may be under way at the end of a step, the same in every wave, some with part of its lanes: those of all
     // steps behind the next one; of groups of scales those sent for since its tiles, at least one step's.
     static constexpr int kTiles = kUnitsA + kUnitsB, kScales = 1 + MX;
-    static constexpr int kAhead = GROUPED ? (STAGES - 2) * kTiles + kScales : (STAGES - 2) * (kTiles + kScales);
+    static constexpr int kAhead = GROUPED ? (STAGES - 2) * kTiles + (STAGES > 2) * kScales : (STAGES - 2) * (kTiles + kScales);
     static_assert(STAGES >= 2 && (!GROUPED || STAGES <= GROUP + 2) && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
     static_assert(kA % kThreads == 0 && (kWaveB < 64 || kWaveB % 64 == 0), "waves stage alike");
     static_assert(GROUPED ? BN % (8 * GROUP) == 0 && kRowsX % (8 * GROUP) == 0 : BN <= 512 && kRowsX <= 512, "so for the scales");
@@ -129,7 +131,7 @@ struct Tile {
     // lane group g reads g and 4 + g, which the lanes of one cycle spread over all banks.
     static __device__ __forceinline__ int unit_at(int p) { return XT != kBf16 ? p : (p & 3) << 1 | p >> 2; }
 
-    static __device__ __forceinline__ int turn(int row) { return MX ? 0x78 >> (row >> 1 & 6) & 3 : row & 7; }
+    static __device__ __forceinline__ int turn(int row) { return AU == 4 ? 0x78 >> (row >> 1 & 6) & 3 : row & 7; }
 
     // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
     // no result that is stored.
@@ -154,7 +156,7 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kUnitsB; ++i) {
             const int u = kWaveB < 64 ? wave * kWaveB + lane % kWaveB : wave * kWaveB + i * 64 + lane, row = u / BU;
-            at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * (MX ? (u & 3) ^ turn(row) : u & 1);
+            at.b[i] = (uint32_t)min(row, A.n - 1 - n0) * pitch_w + 16 * (MX ? u % BU ^ turn(row) : u & 1);
         }
         const bool small = GROUPED && A.kp < 512;
         const uint32_t pitch = small ? 0 : A.kp / 32;
@@ -194,6 +196,11 @@ struct Tile {
 
     // One step's tiles, straight to LDS, in kParts parts; scales that come with the step go with the first.
     static constexpr int kParts = kUnitsA + kUnitsB;
+    static constexpr int kKeep = 0x386;                       // of the scheduler: vector and scalar arithmetic and LDS may pass, loads and products not
+
+    // Where step s of a share from k0 to k1 begins.  Rows of 4 bits are stored in whole 128 values: where half a step of 256 is
+    // left it begins earlier, and its first half is left out.
+    static __device__ __forceinline__ int start_of(int k0, int k1, int s) { return MX ? min(k0 + s * STEP, k1 - STEP) : k0 + s * STEP; }
 
     static __device__ __forceinline__ void stage_part(const Args& A, const Places& at, int64_t t0, int n0, int k, int part, u32x4* buf)
     {
@@ -247,7 +254,8 @@ struct Tile {
     // ls: the step's dword of the first row's scales, where they come in groups; odd: whether the step is the second of the
     // two that share one (16-bit x).  between(p): what else there is to do, kParts parts of it spread over the products: a wave
     // waits where it sends for more than the memory pipe has taken, and the pipe's time for a step is half of the step's.
-    template <class Between>
+    // FROM: 1 leaves the first half of a step of 256 values out.
+    template <int FROM, class Between>
     static __device__ __forceinline__ void multiply(const u32x4* buf, const uint32_t* ls, int wm, int wn, int odd, f32x4 (*acc)[NF], Between between)
     {
         const auto spread = [&](int slot, int slots) {
@@ -261,34 +269,44 @@ struct Tile {
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
         const int row0 = wm * (BM / WM) + c, col0 = wn * (BN / WN) + c;
         if constexpr (MX) {
-            // Token operands are read two fragments ahead of their use.
-            u32x4 a[2][2], b[NF];
-            uint32_t sa[2][2], sb[NF];
-            const auto read_a = [&](int m, u32x4* to, uint32_t* scale) {
+            // Token operands are read two fragments ahead of their use, weights a fragment a group before the half of the step
+            // that takes them.
+            constexpr int HALF = MF / 2, GROUPS = (STEP / 128 - FROM) * HALF;
+            u32x4 a[2][2], b[2][NF];
+            uint32_t sa[2][2], sb[2][NF];
+            // Sixteen rows on a unit's place is the same: one address, and constants from it.
+            const auto read_a = [&](int i) {
+                const int h = FROM + i / HALF, m = 2 * (i % HALF);
+                const u32x4* from = la + row0 * AU + ((4 * h + g) ^ turn(row0));
+                const uint32_t* scale = ls + EACH * row0 + h - FROM;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const int row = row0 + 16 * (m + p);
-                    to[p] = la[row * AU + (g ^ turn(row))];
-                    scale[p] = ls[EACH * row] >> (8 * g);
+                    a[i & 1][p] = from[16 * (m + p) * AU];
+                    sa[i & 1][p] = scale[EACH * 16 * (m + p)] >> (8 * g);
                 }
             };
+            const auto read_b = [&](int h, int n) {
+                b[h & 1][n] = (lb + col0 * BU + ((4 * h + g) ^ turn(col0)))[16 * n * BU];
+                sb[h & 1][n] = (ls + EACH * (BM + col0) + h - FROM)[EACH * 16 * n] >> (8 * g);
+            };
 #pragma unroll
-            for (int n = 0; n < NF; ++n) {
-                const int row = col0 + 16 * n;
-                b[n] = lb[row * BU + (g ^ turn(row))];
-                sb[n] = ls[EACH * (BM + row)] >> (8 * g);
-            }
-            read_a(0, a[0], sa[0]);
+            for (int n = 0; n < NF; ++n) read_b(FROM, n);
+            read_a(0);
 #pragma unroll
-            for (int m = 0; m < MF; m += 2) {
-                const int now = m / 2 & 1;
-                if (m + 2 < MF) read_a(m + 2, a[!now], sa[!now]);
-                spread(m / 2, MF / 2);
+            for (int i = 0; i < GROUPS; ++i) {
+                const int h = FROM + i / HALF, m = 2 * (i % HALF);
+                if (i + 1 < GROUPS) read_a(i + 1);
+                if (i + HALF < GROUPS) {
+#pragma unroll
+                    for (int n = 0; n < NF; ++n)
+                        if (n * HALF / NF == i % HALF) read_b(h + 1, n);
+                }
+                if (i < HALF) spread(i, HALF);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_mx4<0>(b[n], a[now][p], acc[m + p][n], sb[n], sa[now][p]);
+                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_mx4<0>(b[h & 1][n], a[i & 1][p], acc[m + p][n], sb[h & 1][n], sa[i & 1][p]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
@@ -316,6 +334,7 @@ struct Tile {
             for (int kk = 0; kk < 2; ++kk) {
                 u32x4 b[NF];
                 float by[BLOCKS ? NF : 1][4];
+                const u32x4* from_a = la + row0 * AU + ((4 * kk + g) ^ turn(row0));
 #pragma unroll
                 for (int n = 0; n < NF; ++n) {
                     if constexpr (BLOCKS) {
@@ -331,9 +350,10 @@ struct Tile {
 #pragma unroll
                 for (int m = 0; m < MF + BLOCKS; ++m) {
                     if (m < MF) {
+                        if constexpr (BLOCKS) __builtin_amdgcn_sched_barrier(kKeep);
                         spread(kk * MF + m, 2 * MF);
-                        const int row = row0 + 16 * m;
-                        const u32x4 a = la[row * AU + ((4 * kk + g) ^ turn(row))];
+                        if constexpr (BLOCKS) __builtin_amdgcn_sched_barrier(kKeep);
+                        const u32x4 a = from_a[16 * m * AU];
 #pragma unroll
                         for (int n = 0; n < NF; ++n) {
                             if constexpr (BLOCKS) sums[m & 1][n] = mfma_f16(b[n], a, f32x4{0, 0, 0, 0});
@@ -357,10 +377,17 @@ struct Tile {
                                                               u32x4* __restrict__ to, u32x4* __restrict__ to_scales, const u32x4* __restrict__ from,
                                                               const uint32_t* __restrict__ ls, int wm, int wn, int odd, f32x4 (*acc)[NF])
     {
-        multiply(from, ls, wm, wn, odd, acc, [&](int p) {
+        multiply<0>(from, ls, wm, wn, odd, acc, [&](int p) {
             if (GROUPED && p == 0) stage_group(A, at, dword, part, to_scales);
             stage_part(A, at, t0, n0, later, p, to);
         });
+        // The products belong here: without a use of their sums the compiler puts them behind the barrier that follows, where
+        // all waves multiply at once and none reads (4 bits: 571 us for 560, float16 gains 2%).  Of bfloat16 it moves the last
+        // few only, which is as well.
+#pragma unroll
+        for (int m = 0; m < (MX || XT == kFp16 ? MF : 0); ++m)
+#pragma unroll
+            for (int n = 0; n < NF; ++n) asm volatile("" : "+v"(acc[m][n]));
     }
 
     // Where the dword of a group's first step lies.
@@ -371,16 +398,17 @@ struct Tile {
     }
 };
 
-template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
+template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES, int LENGTH>
 __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 {
-    typedef Tile<XT, BM, BN, WM, WN, STAGES> S;
+    typedef Tile<XT, BM, BN, WM, WN, STAGES, LENGTH> S;
     extern __shared__ u32x4 lds[];
     const int wave = wave_id(), wm = wave / WN, wn = wave % WN;
     const Part part = part_of(A.tiling, blockIdx.x);
     const int64_t t0 = (int64_t)part.tm * BM;
     const int n0 = part.tn * BN;
     const int end = XT == kMx4 ? A.kp : A.k, k0 = part.share * A.tiling.length, k1 = part.at < 0 ? end : min(end, k0 + A.tiling.length), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
+    const int sent = steps + (S::MX && k0 + steps * S::STEP < k1);      // and half a step
     f32x4 acc[S::MF][S::NF] = {};
     const typename S::Places at = S::places(A, t0, n0);
     constexpr int kUnits = S::kStage / 16;
@@ -391,10 +419,10 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 #pragma unroll
             for (int i = 0; i < S::GROUP; ++i) S::stage_group(A, at, S::first_of(A, k0, 0), i, scales);
     }
-    if (steps > 0) {
+    if (sent > 0) {
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
-            S::stage(A, at, t0, n0, k0 + min(s, steps - 1) * S::STEP, lds + s * kUnits);
+            S::stage(A, at, t0, n0, S::start_of(k0, k1, min(s, sent - 1)), lds + s * kUnits);
             if (S::GROUPED && s == 0) {
 #pragma unroll
                 for (int i = 0; i < S::GROUP; ++i) S::stage_group(A, at, S::first_of(A, k0, 1), i, scales + S::kRows);
@@ -410,12 +438,12 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     u32x4* to_scales = scales + 2 * S::kRows;
     const uint32_t* ls = S::scales_of(A, k0, 0, scales);
     for (int s = 0; s < steps; ++s) {
-        S::stage_and_multiply(A, at, t0, n0, k0 + min(s + STAGES - 1, steps - 1) * S::STEP, dword, turn, lds + fill * kUnits, to_scales,
+        S::stage_and_multiply(A, at, t0, n0, S::start_of(k0, k1, min(s + STAGES - 1, sent - 1)), dword, turn, lds + fill * kUnits, to_scales,
                               lds + use * kUnits, ls, wm, wn, s & 1, acc);
         wait_and_meet<S::kAhead>();
         use = use == STAGES - 1 ? 0 : use + 1;
         fill = fill == STAGES - 1 ? 0 : fill + 1;
-        ++ls;
+        ls += S::MX ? S::STEP / 128 : 0;
         if (S::GROUPED && ++turn == S::GROUP) {
             turn = 0;
             ++group;
@@ -424,12 +452,15 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
             ls = S::scales_of(A, k0, group, scales);
         }
     }
-    if constexpr (XT != kMx4) {
+    if constexpr (S::MX) {
+        if constexpr (S::STEP > 128)
+            if (sent > steps) S::template multiply<1>(lds + use * kUnits, ls, wm, wn, 0, acc, [](int) {});
+    } else {
         if (k0 + steps * S::STEP < k1) {
             wait_and_meet<0>();
             S::stage_tail(A, t0, n0, k0 + steps * S::STEP, k1, lds);
             wait_and_meet<0>();
-            S::multiply(lds, ls, wm, wn, steps & 1, acc, [](int) {});
+            S::template multiply<0>(lds, ls, wm, wn, steps & 1, acc, [](int) {});
         }
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -460,11 +491,13 @@ constexpr uint64_t kFew = 64;
 // for a second one).  Shares cost their sums' traffic and the launch that joins them.  bfloat16's; float16 takes longer in
 // every tile and chooses as bfloat16 does.
 constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
-constexpr Cost kCostsMx[] = {{256, 256, 1.4, 0.0}, {128, 256, 1.1, 0.0}, {128, 128, 0.6, 1.2}};
+// (The first two take steps of 256 values: a stored row has to have as many.)
+constexpr Cost kCostsMx[] = {{256, 256, 1.2, 0.0}, {128, 256, 0.92, 0.0}, {128, 128, 0.6, 1.2}};
 
 Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
 {
-    return mx ? tiling_of(kCostsMx, tokens, n, k, 128, 256, 1024, 128) : tiling_of(kCosts16, tokens, n, k, 64, 256, 1024, 128);
+    if (!mx) return tiling_of(kCosts16, 3, tokens, n, k, 64, 256, 1024, 128);
+    return k > 128 ? tiling_of(kCostsMx, 3, tokens, n, k, 128, 256, 1024, 128) : tiling_of(kCostsMx + 2, 1, tokens, n, k, 128, 256, 1024, 128);
 }
 
 struct Few {
@@ -523,11 +556,11 @@ int run_few(const Args& A, const Few& s, hipStream_t st)
     return A.tokens <= 48 ? launch_few<XT, OUT, 3, 4>(A, s.shares, st) : launch_few<XT, OUT, 4, 4>(A, s.shares, st);
 }
 
-template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES>
+template <int XT, int OUT, int BM, int BN, int WM, int WN, int STAGES, int LENGTH>
 int launch_tile(const Args& A, hipStream_t st)
 {
-    constexpr int bytes = Tile<XT, BM, BN, WM, WN, STAGES>::kLds;
-    auto* kernel = tile_kernel<XT, OUT, BM, BN, WM, WN, STAGES>;
+    constexpr int bytes = Tile<XT, BM, BN, WM, WN, STAGES, LENGTH>::kLds;
+    auto* kernel = tile_kernel<XT, OUT, BM, BN, WM, WN, STAGES, LENGTH>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
@@ -554,9 +587,9 @@ int run(Args A, float* workspace, hipStream_t st)
     A.tiling = tiles_of(A.tokens, A.n, A.k, MX);
     const Tiling& s = A.tiling;
     int rc;
-    if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 4 : 3>(A, st);
-    else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 5 : 3>(A, st);
-    else rc = launch_tile<XT, OUT, 128, 128, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3>(A, st);
+    if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
+    else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
+    else rc = launch_tile<XT, OUT, 128, 128, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3, MX ? 128 : 64>(A, st);
     if (rc != ECF8_OK || s.rest == 0) return rc;
     return join_tiles<OUT>(A.sums, s, A.tokens, A.n, A.bias, A.y, A.ld_y, st);
 }

@@ -69,12 +69,12 @@ struct Cost {
 // The tiles, and the shares of those that are left, with the least time by the table: whole rounds of the compute units,
 // the last one's part, and for shares the traffic of their sums and the launch that joins them.  step: length of a step;
 // unit: what a share's length is a multiple of; least: its least length; small: the tile whose rows may be mostly padding.
-template <int COUNT>
-Tiling tiling_of(const Cost (&costs)[COUNT], uint64_t tokens, uint64_t cols, uint64_t length, int step, int unit, int least, int small)
+inline Tiling tiling_of(const Cost* costs, int count, uint64_t tokens, uint64_t cols, uint64_t length, int step, int unit, int least, int small)
 {
     Tiling best{};
     double shortest = -1.0;
-    for (const Cost& c : costs) {
+    for (int i = 0; i < count; ++i) {
+        const Cost& c = costs[i];
         if (c.bm > small && (uint64_t)c.bm / 2 >= tokens) continue;
         const uint64_t down = (tokens + c.bm - 1) / c.bm, across = (cols + c.bn - 1) / c.bn, tiles = down * across, slots = c.two > 0.0 ? 512 : 256;
         const double full = c.two > 0.0 ? c.two : c.one;
