@@ -328,8 +328,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 // 4096 in bfloat16 takes 24 + 5 us with 16 shares; 4096 x 13824 x 5120 530 us with all tiles in three shares, 455 with the 64
 // that are left of 320 in four.  float16 has twice the products, and no tiles of 256
 // tokens, whose two planes leave no room for a second buffer.
-constexpr Cost kCosts[] = {{256, 256, 1.62, 0.0}, {128, 256, 1.2, 0.0}, {128, 128, 0.7, 1.4}, {64, 256, 0.85, 0.0}, {32, 256, 0.65, 0.0}};
-constexpr Cost kCostsSplit[] = {{128, 256, 1.65, 0.0}, {128, 128, 1.3, 2.4}, {64, 256, 1.15, 0.0}, {32, 256, 0.85, 0.0}};
+constexpr Cost kCosts[] = {{256, 256, 1.55, 0.0}, {128, 256, 0.95, 0.0}, {128, 128, 0.68, 1.36}, {64, 256, 0.72, 0.0}, {32, 256, 0.61, 0.0}};
+constexpr Cost kCostsSplit[] = {{128, 256, 1.67, 0.0}, {128, 128, 1.19, 2.36}, {64, 256, 1.04, 0.0}, {32, 256, 0.81, 0.0}};
 
 Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {

@@ -487,16 +487,17 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 // and 12.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
 constexpr uint64_t kFew = 64;
 
-// Microseconds of a step of a workgroup, measured: of one alone on its compute unit and of two side by side (0: no LDS
-// for a second one).  Shares cost their sums' traffic and the launch that joins them.  bfloat16's; float16 takes longer in
-// every tile and chooses as bfloat16 does.
-constexpr Cost kCosts16[] = {{256, 256, 1.65, 0.0}, {128, 256, 1.0, 0.0}, {128, 128, 0.7, 1.1}};
-// (The first two take steps of 256 values: a stored row has to have as many.)
-constexpr Cost kCostsMx[] = {{256, 256, 1.2, 0.0}, {128, 256, 0.92, 0.0}, {128, 128, 0.6, 1.2}};
+// Microseconds of a step of a workgroup, measured over 8192 values (64 a step, of 4 bits 128): of one alone on its
+// compute unit and of two side by side (0: no LDS for a second one).
+constexpr Cost kCostsBf16[] = {{256, 256, 1.52, 0.0}, {128, 256, 0.92, 0.0}, {128, 128, 0.62, 1.10}};
+constexpr Cost kCostsFp16[] = {{256, 256, 2.36, 0.0}, {128, 256, 1.55, 0.0}, {128, 128, 1.26, 2.50}};
+// (The first two are of steps of 256 values: a stored row has to have as many.)
+constexpr Cost kCostsMx[] = {{256, 256, 1.16, 0.0}, {128, 256, 0.74, 0.0}, {128, 128, 0.62, 1.18}};
 
-Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool mx)
+template <int XT>
+Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k)
 {
-    if (!mx) return tiling_of(kCosts16, 3, tokens, n, k, 64, 256, 1024, 128);
+    if (XT != kMx4) return tiling_of(XT == kBf16 ? kCostsBf16 : kCostsFp16, 3, tokens, n, k, 64, 256, 1024, 128);
     return k > 128 ? tiling_of(kCostsMx, 3, tokens, n, k, 128, 256, 1024, 128) : tiling_of(kCostsMx + 2, 1, tokens, n, k, 128, 256, 1024, 128);
 }
 
@@ -584,7 +585,7 @@ int run(Args A, float* workspace, hipStream_t st)
         return launch_status();
     }
     A.sums = workspace;
-    A.tiling = tiles_of(A.tokens, A.n, A.k, MX);
+    A.tiling = tiles_of<XT>(A.tokens, A.n, A.k);
     const Tiling& s = A.tiling;
     int rc;
     if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
@@ -600,7 +601,9 @@ extern "C" uint64_t ecf8x_linear_bytes(uint64_t tokens, uint64_t out_features, u
 {
     if (!sizes_ok(tokens, out_features, in_features)) return 0;
     const bool mx = x_type == ECF8X_MX4;
-    if (tokens > kFew) return sums_of(tiles_of(tokens, out_features, in_features, mx));
+    if (tokens > kFew)
+        return sums_of(mx ? tiles_of<kMx4>(tokens, out_features, in_features)
+                          : x_type == ECF8A_FP16 ? tiles_of<kFp16>(tokens, out_features, in_features) : tiles_of<kBf16>(tokens, out_features, in_features));
     const uint64_t s = few_of(tokens, out_features, in_features, mx).shares;
     return s > 1 ? round_up(4 * s * tokens * round_up(out_features, 4), 256) : 0;
 }
