@@ -39,7 +39,7 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // once per workgroup.
 //
 // What bounds it: the matrix instructions, 1.5 us a step of 256 x 256 at the rate of a large library product, and beside them
-// 256 KB that go to and from LDS (4096 x 13824 x 5120: 450 us, 1290 TFLOP/s; float16, in tiles of 128 x 256 with twice the products and two planes of dy, 880), and with few
+// 256 KB that go to and from LDS (4096 x 13824 x 5120: 445 us, 1300 TFLOP/s; float16, in tiles of 128 x 256 with twice the products and two planes of dy, 880), and with few
 // tokens the start and end of short shares (77 x 14336 x 4096: 35 us in float16, 14 steps of 1.65 us).
 //
 // Banks.  Unit u (16 bytes) of dy's row r sits at u ^ (r & 7).  Unit u of the
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 // Measured on MI355X: microseconds of a step (64 rows of the weight) of a workgroup alone on its compute unit, and of two
 // side by side (0: no LDS for a second one).  Shares cost their sums' traffic and the launch that joins them: 77 x 14336 x
 // 4096 in bfloat16 takes 24 + 5 us with 16 shares; 4096 x 13824 x 5120 530 us with all tiles in three shares, 455 with the 64
-// that are left of 320 in four.  float16 has twice the products, and no tiles of 256
+// that are left of 320 in four (now 445).  float16 has twice the products, and no tiles of 256
 // tokens, whose two planes leave no room for a second buffer.
 constexpr Cost kCosts[] = {{256, 256, 1.55, 0.0}, {128, 256, 0.95, 0.0}, {128, 128, 0.68, 1.36}, {64, 256, 0.72, 0.0}, {32, 256, 0.61, 0.0}};
 constexpr Cost kCostsSplit[] = {{128, 256, 1.67, 0.0}, {128, 128, 1.19, 2.36}, {64, 256, 1.04, 0.0}, {32, 256, 0.81, 0.0}};

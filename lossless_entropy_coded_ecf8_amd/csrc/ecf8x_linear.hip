@@ -85,20 +85,23 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // reduction in steps: 64 values of 16 bits (128 bytes of an x row, 32 of a weight
 // row), or of 4 bits 128 (64 bytes of each) or 256.  Runs of 64 bytes come to LDS at
 // 61 bytes a nanosecond and compute unit, of 128 at 100: the larger tiles take 256
-// (4096 x 28672 x 8192: 560 us in steps of 128 through four buffers, 527 so).
+// (4096 x 28672 x 8192: 560 us in steps of 128 through four buffers, 530 so).
 //
 // Tiles go from memory to LDS without passing registers into STAGES buffers:
-// while step s is multiplied, step s + STAGES - 1 is sent for.  With 16-bit x lane group g takes units 2g and
-// 2g + 1 of an x row and the same values of a weight row, so that it meets 8
-// contiguous bytes of codes, under one scale; with 4-bit x unit g of either.
+// while step s is multiplied, step s + STAGES - 1 is sent for, between the products
+// (all ahead of them: bfloat16 1440 us for 1370).  With bfloat16 x lane group g takes
+// units 2g and 2g + 1 of an x row and the same values of a weight row, so that it meets
+// 8 contiguous bytes of codes, under one scale; with 4-bit x unit g of either; float16,
+// which takes one block at a time, unit g of its four.
 //
 // Banks: place p of row r sits at p ^ turn(r); weight rows of 32 bytes lie as they
 // are.
 //
-// What bounds it: in the tiles of 256 x 256 the matrix instructions at the clock that the power limit leaves
-// (4096 x 28672 x 8192: bfloat16 1360 us, 1415 TFLOP/s, 66% busy at 1.8 GHz; 4 bits 530, 3630, 43% at 1.9, beside as many cycles of LDS); in float16 the scaling of each block's sums,
-// four multiply-adds for each product instruction (4096 x 13824 x 5120: 695 us, bfloat16 450); where there are few
-// tiles, the units that have none (331 x 13821 x 5120 of 4 bits: 37 us, 162 tiles of 128 x 256).
+// What bounds it, in tiles of 256 x 256 (4096 x 28672 x 8192): bfloat16 1370 us, 1400 TFLOP/s, the matrix instructions,
+// 66% busy at the 1.8 GHz that the power limit leaves; 4 bits 530 us, 3630 TFLOP/s, 43% busy at 1.9, beside as many
+// cycles of LDS.  In float16 the scaling of each block's sums, four multiply-adds for each product instruction (4096 x
+// 13824 x 5120: 695 us, bfloat16 450).  Where there are few tiles, the units that have none (331 x 13821 x 5120 of 4 bits:
+// 37 us, 162 tiles of 128 x 256).
 //
 // Scales: a dword of every row comes with the step (16-bit x: the four blocks that two
 // steps share).  It asks the cache for as many lines as the codes do, so for the large
@@ -483,8 +486,8 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 // ------------------------------------------------------------ choice
 
 // Tokens of few_kernel, which widens each code for up to 64 tokens, and tiles of 128 for 128.  64 x 28672 x 8192 in
-// bfloat16, float16 and 4 bits: 48, 58 and 38 us, in tiles 72, 113 and 45; 64 x 4096 x 4096: 15, 16 and 14, in tiles 17, 28
-// and 12.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
+// bfloat16, float16 and 4 bits: 47, 58 and 38 us, in tiles 70, 110 and 44; 64 x 4096 x 4096: 15, 16 and 14, in tiles 17, 28
+// and 13.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
 constexpr uint64_t kFew = 64;
 
 // Microseconds of a step of a workgroup, measured over 8192 values (64 a step, of 4 bits 128): of one alone on its

@@ -7,7 +7,8 @@
 // shares, whose sums go to the workspace and are joined in order.  Few tiles are
 // all of them left ones.  (4096 x 13824 x 5120, input gradient: 320 tiles of
 // 256 x 256 on 256 compute units.  All of them in three shares 530 us, the 64 that
-// are left in four 455.  The product, 864 tiles: all whole 513, 96 in two 478.)
+// are left in four 455.  The product, 864 tiles: all whole 513, 96 in two 478.
+// Both by the step times of then; now 445 and 452.)
 #ifndef ECF8X_TILES_H
 #define ECF8X_TILES_H
 
