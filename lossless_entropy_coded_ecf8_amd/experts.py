@@ -157,6 +157,13 @@ class ECF8Experts(torch.nn.Module):
         self._whole: Optional[binding.DecodePlan] = None        # of the whole layer
         self._named: tuple = ((), None)                         # the experts last named, and their plan
 
+    def _apply(self, fn, *args, **kwargs):
+        """Module.to and its like: the scales stay float32, as the weights stay bytes, whatever type the module is brought to."""
+        scales = self.scales
+        super()._apply(fn, *args, **kwargs)
+        self.scales = scales.to(self.scales.device)
+        return self
+
     def compressed_bytes(self) -> int:
         return sum(e.compressed_bytes() for e in self.encs)
 

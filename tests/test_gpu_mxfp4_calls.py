@@ -277,3 +277,19 @@ def test_a_layer_with_four_bit_input_says_that_it_keeps_no_gradients(monkeypatch
     assert len(got) == 1 and "adapted" in str(got[0].message)
     layer4.adapted(x).float().sum().backward()
     assert x.grad is not None and layer4.half().scales.dtype == torch.uint8
+
+
+def test_modules_brought_to_another_type_keep_their_weights():
+    """Module.to changes a layer's bias, but neither the stored weights nor the experts' float32 scales."""
+    x = torch.randn(4, 64, generator=gen(6)).bfloat16().to(D)
+    linear = torch.nn.Linear(64, 40, device=D)
+    four = E.MXFP4Linear.from_linear(linear)
+    y = four(x)
+    assert torch.equal(four.to(BF)(x), y) and four.bias.dtype == BF
+    given, _ = layer(3, 32, 64, False)
+    scales = torch.rand(3, 3, generator=gen(7)) + 0.1
+    experts = E.ECF8Experts(*[[w[e].cpu() for e in range(3)] for w in given], scales, device=D)
+    ids, w = E.moe_route(torch.randn(4, 3, generator=gen(8)).to(D), 2)
+    y = experts(x, ids, w)
+    experts.to(BF)
+    assert torch.equal(experts.scales.cpu(), scales) and "scales" in dict(experts.named_buffers()) and torch.equal(experts(x, ids, w), y)
