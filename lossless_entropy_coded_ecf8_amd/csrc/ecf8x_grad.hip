@@ -47,17 +47,13 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // four rows in each lane group, and the 16 units that half a wave touches lie in
 // different banks; so do those that 16 lanes store, since lanes of the second
 // half of a row store their units in another order.
-// PART: fragments without tokens are left out.  For float16, whose products are twice as many, where at most three quarters of
-// one tile of 128 hold tokens: 77 x 14336 x 4096 takes 35 us and 37 without; 112 tokens 41 either way, and bfloat16
-// gains nothing at any number (28 us).  (Fragments given to the wave rows in turn, each left out by itself: 96 tokens 36 us
-// so, 39 then.)
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 struct Tile {
     static constexpr bool SPLIT = TYPE == kFp16;
     static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
     static constexpr int BU = BN / 8;                          // 16-byte units of a widened row
     static constexpr int kA = BM * 8, kB = kStep * BU;         // of a plane of dy's tile, of the widened tile
-    static constexpr int kWaveA = kA / 8, kUnitsA = kWaveA < 64 ? 1 : kWaveA / 64;    // a wave sends for the same number as any other
+    static constexpr int kWaveA = kA / 8, kUnitsA = (kWaveA + 63) / 64;    // a wave sends for the same number as any other, the last with part of its lanes
     static constexpr int kRaw = kStep * BN / 32;               // 16-byte units of codes
     static constexpr int kBuffers = SPLIT ? 4 : STAGES;        // split: two planes, two steps
     static constexpr int kLds = 16 * (kBuffers * kA + 2 * kB);
@@ -65,17 +61,14 @@ struct Tile {
     static constexpr int kAhead = (STAGES - 2) * (kUnitsA + 2);
     static_assert(STAGES >= 2 && kLds <= 160 * 1024 && kAhead < 64, "LDS and the load counter");
     static_assert(WM * WN == kThreads / 64 && MF >= 1 && NF >= 1 && kRaw <= kThreads && kRaw % 64 == 0, "eight waves");
-    static_assert(kUnitsA <= 4 && (MF < 2 || MF % 2 == 0), "quarters and groups");
-    static_assert(kWaveA < 64 || kWaveA % 64 == 0, "waves stage alike");
+    static_assert(kUnitsA <= 4 && kWaveA % 16 == 0, "quarters");
 
     static __device__ __forceinline__ int turn(int row) { return 2 * ((row & 3) | (row >> 1 & 4)) | (row >> 2 & 1); }
 
-    // Unit i that this lane sends for; lanes past a wave's share repeat others'.
-    static __device__ __forceinline__ int unit_a(int i)
-    {
-        const int lane = threadIdx.x & 63, wave = wave_id();
-        return kWaveA < 64 ? wave * kWaveA + lane % kWaveA : wave * kWaveA + i * 64 + lane;
-    }
+    // Unit i that this lane sends for; lanes past its share of a wave repeat others'.
+    static __device__ __forceinline__ int lanes_of(int i) { return kWaveA - 64 * i < 64 ? kWaveA - 64 * i : 64; }
+
+    static __device__ __forceinline__ int unit_a(int i) { return wave_id() * kWaveA + i * 64 + (int)(threadIdx.x & 63) % lanes_of(i); }
 
     struct Places {
         uint32_t a[kUnitsA];
@@ -102,7 +95,7 @@ struct Tile {
     static __device__ __forceinline__ void stage_unit(const Args& A, const Places& at, int64_t t0, int n, int i, u32x4* la)
     {
         const int wave = wave_id();
-        if (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA)
+        if (lanes_of(i) == 64 || (int)(threadIdx.x & 63) < lanes_of(i))
             __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(A.dy + t0 * A.ld_dy), (LdsMem*)(la + wave * kWaveA + i * 64), 16, at.a[i], 2 * n, 0, 0);
     }
 
@@ -155,7 +148,7 @@ struct Tile {
         if constexpr (SPLIT) {
 #pragma unroll
             for (int d = 0; d < kUnitsA; ++d)
-                if (d % 4 == i && (kWaveA >= 64 || (int)(threadIdx.x & 63) < kWaveA)) put_split(e.dy[d], unit_a(d), la);
+                if (d % 4 == i && (lanes_of(d) == 64 || (int)(threadIdx.x & 63) < lanes_of(d))) put_split(e.dy[d], unit_a(d), la);
         }
     }
 
@@ -177,11 +170,10 @@ struct Tile {
     // The products of a step, token fragments PER at a time: the operands of a group are read while the group before is
     // multiplied.  between(i): what else there is to do, a quarter before each of the first groups; its VALU and LDS work
     // then goes beside the other wave's products.  (All of it ahead of them: 2.0 us a step of 256 x 256; so: 1.6.)
-    // live: fragments that hold tokens.
     template <class Between>
-    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, int live, f32x4 (*acc)[NF], Between between)
+    static __device__ __forceinline__ void multiply(const u32x4* la, const u32x4* lb, int wm, int wn, f32x4 (*acc)[NF], Between between)
     {
-        constexpr int PER = MF < 2 ? 1 : 2, GROUPS = 2 * MF / PER;
+        constexpr int PER = MF % 2 ? 1 : 2, GROUPS = 2 * MF / PER;
         const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, row0 = wm * (BM / WM) + c;
         u32x4 a[2][PER], low[2][SPLIT ? PER : 1], b[2][NF];
         const auto read_b = [&](int kk) {
@@ -217,15 +209,13 @@ struct Tile {
                 for (int q = 0; q < (GROUPS >= 4 ? 1 : 4 / GROUPS); ++q) between(i * (GROUPS >= 4 ? 1 : 4 / GROUPS) + q);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (!PART || m < live) {
 #pragma unroll
-                for (int p = 0; p < PER; ++p) {
+            for (int p = 0; p < PER; ++p) {
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], a[i & 1][p], acc[m + p][n]);
-                    if constexpr (SPLIT) {
+                for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], a[i & 1][p], acc[m + p][n]);
+                if constexpr (SPLIT) {
 #pragma unroll
-                        for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], low[i & 1][p], acc[m + p][n]);
-                    }
+                    for (int n = 0; n < NF; ++n) acc[m + p][n] = mfma_bf16(b[kk][n], low[i & 1][p], acc[m + p][n]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -235,22 +225,22 @@ struct Tile {
     // The buffers are told apart by __restrict__: else every LDS read waits for the loads to LDS in flight.
     static __device__ __forceinline__ void step(const Args& A, const Places& at, int64_t t0, int n, int later, int n1, int whole, const Early& next,
                                                 Early& early, u32x4* __restrict__ to_a, u32x4* __restrict__ to_b, const u32x4* __restrict__ la,
-                                                const u32x4* __restrict__ lb, int wm, int wn, int live, bool real, f32x4 (*acc)[NF])
+                                                const u32x4* __restrict__ lb, int wm, int wn, bool real, f32x4 (*acc)[NF])
     {
         fetch(A, at, t0, n + AHEAD * kStep, n1, whole, early);
         __builtin_amdgcn_sched_barrier(0);                    // loads leave before the products that hide them
         if (real)
-            multiply(la, lb, wm, wn, live, acc, [&](int i) {
+            multiply(la, lb, wm, wn, acc, [&](int i) {
                 if (!SPLIT && i < kUnitsA) stage_unit(A, at, t0, later, i, to_a);
                 store(i, at, n + kStep, n1, next, to_a, to_b);
             });
     }
 };
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 {
-    typedef Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART> S;
+    typedef Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD> S;
     extern __shared__ u32x4 lds[];
     u32x4* const la = lds;
     u32x4* const lb = lds + S::kBuffers * S::kA;
@@ -261,7 +251,6 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
     const int n0 = part.share * A.tiling.length, n1 = part.at < 0 ? A.n : min(A.n, n0 + A.tiling.length), steps = n1 > n0 ? (n1 - n0) / kStep : 0;
     const int whole = steps > 0 ? n0 + (steps - 1) * kStep : -1;     // dy's last whole step
     f32x4 acc[S::MF][S::NF] = {};
-    const int live = (int)min((int64_t)S::MF, (A.tokens - t0 - wm * (BM / WM) + 15) / 16);      // this wave's fragments that hold tokens
     const typename S::Places at = S::places(A, t0, k0);
     typename S::Early early[AHEAD];                           // of step s at s % AHEAD
 #pragma unroll
@@ -286,7 +275,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
         for (int i = 0; i < AHEAD; ++i) {
             const int s = s0 + i;
             S::step(A, at, t0, n0 + s * kStep, n0 + min(s + STAGES - 1, steps - 1) * kStep, n1, whole, early[(i + 1) % AHEAD], early[i],
-                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, live, s < steps, acc);
+                    la + fill * kPlanes * S::kA, lb + (s + 1 & 1) * S::kB, la + use * kPlanes * S::kA, lb + (s & 1) * S::kB, wm, wn, s < steps, acc);
             if constexpr (S::SPLIT) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
@@ -305,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
         for (int i = 0; i < 4; ++i) S::store(i, at, n0 + steps * kStep, n1, early[0], la + (S::SPLIT ? 2 * S::kA : 0), lb);
         S::stage_tail(A, t0, n0 + steps * kStep, n1, la);     // (float16 dy: stale values went to the other buffer)
         wait_and_meet<0>();
-        S::multiply(la, lb, wm, wn, live, acc, [](int) {});
+        S::multiply(la, lb, wm, wn, acc, [](int) {});
     }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -326,14 +315,15 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
 // Measured on MI355X: microseconds of a step (64 rows of the weight) of a workgroup alone on its compute unit, and of two
 // side by side (0: no LDS for a second one).  Shares cost their sums' traffic and the launch that joins them: 77 x 14336 x
 // 4096 in bfloat16 takes 24 + 5 us with 16 shares; 4096 x 13824 x 5120 530 us with all tiles in three shares, 455 with the 64
-// that are left of 320 in four (now 445).  float16 has twice the products, and no tiles of 256
+// that are left of 320 in four (now 445).  96 rows: 77 tokens 28 us in tiles of 128, 26 so,
+// 192 tokens 42 and 38.  float16 has twice the products, and no tiles of 256
 // tokens, whose two planes leave no room for a second buffer.
-constexpr Cost kCosts[] = {{256, 256, 1.55, 0.0}, {128, 256, 0.95, 0.0}, {128, 128, 0.68, 1.36}, {64, 256, 0.72, 0.0}, {32, 256, 0.61, 0.0}};
-constexpr Cost kCostsSplit[] = {{128, 256, 1.67, 0.0}, {128, 128, 1.19, 2.36}, {64, 256, 1.04, 0.0}, {32, 256, 0.81, 0.0}};
+constexpr Cost kCosts[] = {{256, 256, 1.55, 0.0}, {128, 256, 0.95, 0.0}, {128, 128, 0.68, 1.36}, {96, 256, 0.85, 0.0}, {64, 256, 0.72, 0.0}, {32, 256, 0.61, 0.0}};
+constexpr Cost kCostsSplit[] = {{128, 256, 1.67, 0.0}, {128, 128, 1.19, 2.36}, {96, 256, 1.41, 0.0}, {64, 256, 1.04, 0.0}, {32, 256, 0.81, 0.0}};
 
 Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k, bool split)
 {
-    return split ? tiling_of(kCostsSplit, 4, tokens, k, n, kStep, kStep, 256, 32) : tiling_of(kCosts, 5, tokens, k, n, kStep, kStep, 256, 32);
+    return split ? tiling_of(kCostsSplit, 5, tokens, k, n, kStep, kStep, 256, 32) : tiling_of(kCosts, 6, tokens, k, n, kStep, kStep, 256, 32);
 }
 
 bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
@@ -342,11 +332,11 @@ bool sizes_ok(uint64_t tokens, uint64_t n, uint64_t k)
            k % ECF8X_BLOCK == 0;
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD, bool PART = false>
+template <int TYPE, int BM, int BN, int WM, int WN, int STAGES, int AHEAD>
 int launch(const Args& A, hipStream_t st)
 {
-    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>::kLds;
-    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD, PART>;
+    constexpr int bytes = Tile<TYPE, BM, BN, WM, WN, STAGES, AHEAD>::kLds;
+    auto* kernel = grad_kernel<TYPE, BM, BN, WM, WN, STAGES, AHEAD>;
     if (bytes > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
         return ECF8_ERR_HIP;
@@ -362,10 +352,9 @@ int run(const Args& A, hipStream_t st)
     if (s.bm == 256) {
         if constexpr (TYPE == kBf16) rc = launch<TYPE, 256, 256, 2, 4, 3, 2>(A, st);
         else rc = ECF8_ERR_UNSUPPORTED;                       // shape_of gives float16 none of these
-    } else if (s.bm == 128 && s.bn == 256) {
-        if (TYPE == kFp16 && A.tokens <= 96) rc = launch<TYPE, 128, 256, 2, 4, 5, 4, TYPE == kFp16>(A, st);
-        else rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, st);
-    } else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, st);
+    } else if (s.bm == 128 && s.bn == 256) rc = launch<TYPE, 128, 256, 2, 4, 5, 4>(A, st);
+    else if (s.bm == 96) rc = launch<TYPE, 96, 256, 2, 4, 5, 4>(A, st);
+    else if (s.bm == 128) rc = launch<TYPE, 128, 128, 4, 2, 3, 4>(A, st);
     else if (s.bm == 64) rc = launch<TYPE, 64, 256, 2, 4, 6, 4>(A, st);
     else rc = launch<TYPE, 32, 256, 2, 4, 6, 4>(A, st);
     if (rc != ECF8_OK || s.rest == 0) return rc;
