@@ -118,7 +118,7 @@ struct Tile {
     static constexpr bool GROUPED = MX && BN == 256;
     static constexpr int GROUP = 512 / STEP;                   // steps of a group of scales
     static constexpr int kRowsX = MX ? BM : 0, kRows = kRowsX + BN;    // rows of scales: tokens', then outputs'
-    static constexpr int kWaveB = kB / 8, kUnitsA = kA / kThreads, kUnitsB = kWaveB < 64 ? 1 : kB / kThreads;
+    static constexpr int kWaveA = kA / 8, kWaveB = kB / 8, kUnitsA = (kWaveA + 63) / 64, kUnitsB = kWaveB < 64 ? 1 : kB / kThreads;
     static constexpr int kStage = 16 * (kA + kB) + (GROUPED ? 0 : 4 * kRows);                    // bytes
     static constexpr int kLds = STAGES * kStage + (GROUPED ? 3 * 16 * kRows : 0);
     // Loads that may be under way at the end of a step, the same in every wave, some with part of its lanes: those of all
@@ -126,7 +126,7 @@ struct Tile {
     static constexpr int kTiles = kUnitsA + kUnitsB, kScales = 1 + MX;
     static constexpr int kAhead = GROUPED ? (STAGES - 2) * kTiles + (STAGES > 2) * kScales : (STAGES - 2) * (kTiles + kScales);
     static_assert(STAGES >= 2 && (!GROUPED || STAGES <= GROUP + 2) && kLds <= 160 * 1024 && kAhead < 64 && kStage % 16 == 0, "LDS and the load counter");
-    static_assert(kA % kThreads == 0 && (kWaveB < 64 || kWaveB % 64 == 0), "waves stage alike");
+    static_assert(kWaveA % 16 == 0 && (kWaveB < 64 || kWaveB % 64 == 0), "waves stage alike");
     static_assert(GROUPED ? BN % (8 * GROUP) == 0 && kRowsX % (8 * GROUP) == 0 : BN <= 512 && kRowsX <= 512, "so for the scales");
     static_assert(WM * WN == kWaves && (MX ? MF % 2 == 0 : MF >= 1) && NF >= 1, "eight waves");
 
@@ -146,6 +146,9 @@ struct Tile {
     };
     static constexpr int kPartX = kRowsX / (GROUPED ? 8 * GROUP : 8), kPartW = BN / (GROUPED ? 8 * GROUP : 8);    // rows of a wave
 
+    // Lanes of a wave that send for its unit i of x.
+    static __device__ __forceinline__ int lanes_of(int i) { return kWaveA - 64 * i < 64 ? kWaveA - 64 * i : 64; }
+
     static __device__ __forceinline__ Places places(const Args& A, int64_t t0, int n0)
     {
         Places at;
@@ -153,7 +156,7 @@ struct Tile {
         const int lane = threadIdx.x & 63, wave = wave_id();
 #pragma unroll
         for (int i = 0; i < kUnitsA; ++i) {
-            const int u = (wave * kUnitsA + i) * 64 + lane, row = u / AU;
+            const int u = wave * kWaveA + i * 64 + lane % lanes_of(i), row = u / AU;
             at.a[i] = (uint32_t)min((int64_t)row, A.tokens - 1 - t0) * pitch_x + 16 * unit_at((u % AU) ^ turn(row));
         }
 #pragma unroll
@@ -222,7 +225,8 @@ struct Tile {
         } else {
             const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
             const int i = part - kUnitsB;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + (wave * kUnitsA + i) * 64), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
+            if (lanes_of(i) == 64 || lane < lanes_of(i))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsMem*)(la + wave * kWaveA + i * 64), 16, at.a[i], MX ? k / 2 : 2 * k, 0, 0);
         }
     }
 
@@ -491,16 +495,17 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 constexpr uint64_t kFew = 64;
 
 // Microseconds of a step of a workgroup, measured over 8192 values (64 a step, of 4 bits 128): of one alone on its
-// compute unit and of two side by side (0: no LDS for a second one).
-constexpr Cost kCostsBf16[] = {{256, 256, 1.52, 0.0}, {128, 256, 0.92, 0.0}, {128, 128, 0.62, 1.10}};
-constexpr Cost kCostsFp16[] = {{256, 256, 2.36, 0.0}, {128, 256, 1.55, 0.0}, {128, 128, 1.26, 2.50}};
+// compute unit and of two side by side (0: no LDS for a second one, or no gain: two of 128 x 256 in bfloat16 1.54, as one of
+// 256 x 256).  Of 96 rows: 77 x 14336 x 4096 in bfloat16 26 us in tiles of 128, 25 so, 192 x 28672 x 8192 120 and 106.
+constexpr Cost kCostsBf16[] = {{256, 256, 1.52, 0.0}, {128, 256, 0.93, 0.0}, {128, 128, 0.62, 1.10}, {96, 256, 0.81, 0.0}};
+constexpr Cost kCostsFp16[] = {{256, 256, 2.36, 0.0}, {128, 256, 1.5, 0.0}, {128, 128, 1.26, 2.50}, {96, 256, 1.4, 0.0}};
 // (The first two are of steps of 256 values: a stored row has to have as many.)
 constexpr Cost kCostsMx[] = {{256, 256, 1.16, 0.0}, {128, 256, 0.74, 0.0}, {128, 128, 0.62, 1.18}};
 
 template <int XT>
 Tiling tiles_of(uint64_t tokens, uint64_t n, uint64_t k)
 {
-    if (XT != kMx4) return tiling_of(XT == kBf16 ? kCostsBf16 : kCostsFp16, 3, tokens, n, k, 64, 256, 1024, 128);
+    if (XT != kMx4) return tiling_of(XT == kBf16 ? kCostsBf16 : kCostsFp16, 4, tokens, n, k, 64, 256, 1024, 128);
     return k > 128 ? tiling_of(kCostsMx, 3, tokens, n, k, 128, 256, 1024, 128) : tiling_of(kCostsMx + 2, 1, tokens, n, k, 128, 256, 1024, 128);
 }
 
@@ -592,7 +597,8 @@ int run(Args A, float* workspace, hipStream_t st)
     const Tiling& s = A.tiling;
     int rc;
     if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
-    else if (s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
+    else if (s.bm == 128 && s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
+    else if (!MX && s.bm == 96) rc = launch_tile<MX ? kBf16 : XT, OUT, 96, 256, 2, 4, 3, 64>(A, st);
     else rc = launch_tile<XT, OUT, 128, 128, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3, MX ? 128 : 64>(A, st);
     if (rc != ECF8_OK || s.rest == 0) return rc;
     return join_tiles<OUT>(A.sums, s, A.tokens, A.n, A.bias, A.y, A.ld_y, st);

@@ -54,6 +54,13 @@ def test_products_in_large_tiles(T, K):
         R.check(y[:, 12000:], *R.product(rows, wv[:1001], dtype), (kind, T, K))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", [(65, 300, 96), (77, 5003, 288), (96, 14001, 1056), (97, 2000, 160), (192, 9001, 608), (285, 3000, 2080)])
+def test_products_in_tiles_of_96_tokens(kind, T, N, K):
+    w, wv = weight(N, K)
+    product_is_right(kind, torch.randn(T, K, generator=gen(T, N, K)), w, wv)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "mx"])
 @pytest.mark.parametrize("T,N,K", [(1, 1000, 8224), (4, 1000, 8224), (3, 4000, 4128), (8, 4000, 4128), (16, 130, 16416), (24, 4000, 4128),
                                    (40, 1000, 8224), (64, 3999, 4128), (70, 250, 16416), (200, 130, 6176)])
