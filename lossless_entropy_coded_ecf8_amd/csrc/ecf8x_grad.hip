@@ -39,8 +39,9 @@ typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 // once per workgroup.
 //
 // What bounds it: the matrix instructions, 1.5 us a step of 256 x 256 at the rate of a large library product, and beside them
-// 256 KB that go to and from LDS (4096 x 13824 x 5120: 445 us, 1300 TFLOP/s; float16, in tiles of 128 x 256 with twice the products and two planes of dy, 880), and with few
-// tokens the start and end of short shares (77 x 14336 x 4096: 35 us in float16, 14 steps of 1.65 us).
+// 256 KB that go to and from LDS (4096 x 13824 x 5120: 445 us, 1300 TFLOP/s; float16, in tiles of 128 x 256 with twice the
+// products and two planes of dy, 880).  With few tokens, the begin and end of short shares (77 x 14336 x 4096 in float16:
+// 33 us, 14 steps of 1.4 us in tiles of 96 x 256).
 //
 // Banks.  Unit u (16 bytes) of dy's row r sits at u ^ (r & 7).  Unit u of the
 // widened row r sits at u ^ turn(r): the transposing read takes two units of

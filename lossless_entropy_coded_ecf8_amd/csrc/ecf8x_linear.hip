@@ -221,7 +221,8 @@ struct Tile {
         }
         if (part < kUnitsB) {
             const Rsrc rb = buffer_of(A.w + (int64_t)n0 * (A.kp / 2));
-            if (kWaveB >= 64 || lane < kWaveB) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB + part * 64), 16, at.b[part], k / 2, 0, 0);
+            if (kWaveB >= 64 || lane < kWaveB)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsMem*)(lb + wave * kWaveB + part * 64), 16, at.b[part], k / 2, 0, 0);
         } else {
             const Rsrc ra = MX ? buffer_of(static_cast<const uint8_t*>(A.x) + t0 * (A.kp / 2)) : buffer_of(static_cast<const uint16_t*>(A.x) + t0 * A.ld_x);
             const int i = part - kUnitsB;
@@ -414,7 +415,8 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
     const Part part = part_of(A.tiling, blockIdx.x);
     const int64_t t0 = (int64_t)part.tm * BM;
     const int n0 = part.tn * BN;
-    const int end = XT == kMx4 ? A.kp : A.k, k0 = part.share * A.tiling.length, k1 = part.at < 0 ? end : min(end, k0 + A.tiling.length), steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
+    const int end = XT == kMx4 ? A.kp : A.k, k0 = part.share * A.tiling.length, k1 = part.at < 0 ? end : min(end, k0 + A.tiling.length);
+    const int steps = k1 > k0 ? (k1 - k0) / S::STEP : 0;
     const int sent = steps + (S::MX && k0 + steps * S::STEP < k1);      // and half a step
     f32x4 acc[S::MF][S::NF] = {};
     const typename S::Places at = S::places(A, t0, n0);
