@@ -58,12 +58,20 @@ __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Four rows' sums of one block, times the block's scales.
-__device__ __forceinline__ f32x4 add_scaled(f32x4 acc, f32x4 block, const float* scale)
+// The value of lane LANE of every 16.
+template <int LANE>
+__device__ __forceinline__ float of_lane(float v)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(block[i], scale[i], acc[i]);
-    return acc;
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + LANE, 0xF, 0xF, true));
+}
+
+// Four rows' sums of one block, times the block's scales, which lanes 4 N .. 4 N + 3 of every 16 hold: each lane then converts
+// one row's scale for the others, where it would convert those of all.
+template <int N>
+__device__ __forceinline__ f32x4 add_scaled(f32x4 acc, f32x4 block, float scale)
+{
+    return f32x4{__builtin_fmaf(of_lane<4 * N>(scale), block[0], acc[0]), __builtin_fmaf(of_lane<4 * N + 1>(scale), block[1], acc[1]),
+                 __builtin_fmaf(of_lane<4 * N + 2>(scale), block[2], acc[2]), __builtin_fmaf(of_lane<4 * N + 3>(scale), block[3], acc[3])};
 }
 
 // Eight E4M3 bytes as one operand of a 16-bit type.  Exact.

@@ -323,7 +323,6 @@ struct Tile {
             constexpr bool BLOCKS = XT == kFp16;
             uint32_t raw[NF][2];
             float scale[NF];
-            u32x4 rows[BLOCKS ? NF : 1];
             const int sh = 16 * odd + 8 * (g >> 1);
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
@@ -331,27 +330,24 @@ struct Tile {
                 if constexpr (BLOCKS) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) raw[n][kk] = reinterpret_cast<const uint32_t*>(lb)[row * 8 + 4 * kk + g];
-                    rows[n] = *reinterpret_cast<const u32x4*>(ls + wn * (BN / WN) + 16 * n + 4 * g);
                 } else {
                     const uint2 v = reinterpret_cast<const uint2*>(lb)[row * 4 + g];
                     raw[n][0] = v.x, raw[n][1] = v.y;
                     scale[n] = scale_of(ls[row] >> sh);
                 }
             }
+            // float16: lane 4 n + i of a group has the scales of row 4 g + i of fragment n.
+            static_assert(!BLOCKS || NF == 4, "sixteen rows of a group");
+            const uint32_t mine = BLOCKS ? ls[wn * (BN / WN) + 16 * (c >> 2) + 4 * g + (c & 3)] >> (16 * odd) : 0;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 u32x4 b[NF];
-                float by[BLOCKS ? NF : 1][4];
+                const float by = BLOCKS ? value_of(scale_of(mine >> (8 * kk))) : 0.0f;
                 const u32x4* from_a = la + row0 * AU + ((4 * kk + g) ^ turn(row0));
 #pragma unroll
                 for (int n = 0; n < NF; ++n) {
-                    if constexpr (BLOCKS) {
-                        b[n] = widen4_f16(raw[n][kk]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) by[n][i] = value_of(scale_of(rows[n][i] >> (16 * odd + 8 * kk)));
-                    } else {
-                        b[n] = widen4(raw[n][kk], scale[n]);
-                    }
+                    if constexpr (BLOCKS) b[n] = widen4_f16(raw[n][kk]);
+                    else b[n] = widen4(raw[n][kk], scale[n]);
                 }
                 // float16: the sums of one group of tokens are added while the next group's are made.
                 f32x4 sums[BLOCKS ? 2 : 1][NF];
@@ -371,8 +367,10 @@ struct Tile {
                     if constexpr (BLOCKS) {
                         __builtin_amdgcn_sched_barrier(0);
                         if (m > 0) {
-#pragma unroll
-                            for (int n = 0; n < NF; ++n) acc[m - 1][n] = add_scaled(acc[m - 1][n], sums[~m & 1][n], by[n]);
+                            acc[m - 1][0] = add_scaled<0>(acc[m - 1][0], sums[~m & 1][0], by);
+                            acc[m - 1][1] = add_scaled<1>(acc[m - 1][1], sums[~m & 1][1], by);
+                            acc[m - 1][2] = add_scaled<2>(acc[m - 1][2], sums[~m & 1][2], by);
+                            acc[m - 1][3] = add_scaled<3>(acc[m - 1][3], sums[~m & 1][3], by);
                         }
                     }
                 }

@@ -200,7 +200,7 @@ struct Stream {
         // block of 32 (lane group g its values 8 g ..), unscaled, and its result is scaled, exactly, as it is added.
         static constexpr bool BLOCKS = X == kFp16 && W == kMx4;
         u32x4 w[RF], x[MF][OPS], low[X == kPair ? MF : 1][X == kPair ? OPS : 1];
-        uint32_t sw[RF], sx[MF], rows[BLOCKS ? RF : 1][4];
+        uint32_t sw[RF], sx[MF];                       // BLOCKS: sw[0], of row 4 g + c % 4 of fragment c / 4 % 2
 
         __device__ __forceinline__ void read(const char* buf)
         {
@@ -211,8 +211,7 @@ struct Stream {
             for (int f = 0; f < RF; ++f) {
                 const int row = (rg * RF + f) * 16 + c;
                 if constexpr (BLOCKS) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rows[f][i] = ls[((rg * RF + f) * 16 + 4 * g + i) * KG + q];
+                    if (f == 0) sw[0] = ls[((rg * RF + (c >> 2 & 1)) * 16 + 4 * g + (c & 3)) * KG + q];
                 } else {
                     w[f] = lw[row * WU + ((4 * q + g) ^ turn<WU>(row))];
                     if constexpr (W == kMx4) sw[f] = ls[row * KG + q];
@@ -250,7 +249,8 @@ struct Stream {
             } else if constexpr (BLOCKS) {
                 // A block's sums are added while the next block's are made.
                 f32x4 sums[2][RF][MF];
-                float scale[2][RF][4];
+                float scale[2];
+                static_assert(RF == 2, "eight rows of a group");
 #pragma unroll
                 for (int j = 0; j < 5; ++j) {
                     if (j < 4) {
@@ -259,16 +259,16 @@ struct Stream {
                             const u32x4 wide = widen4_f16(w[f][j]);
 #pragma unroll
                             for (int m = 0; m < MF; ++m) sums[j & 1][f][m] = mfma_f16(wide, x[m][j], f32x4{0, 0, 0, 0});
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) scale[j & 1][f][i] = value_of(scale_at(rows[f][i], j));
                         }
+                        scale[j & 1] = value_of(scale_at(sw[0], j));
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     if (j > 0) {
 #pragma unroll
-                        for (int f = 0; f < RF; ++f)
-#pragma unroll
-                            for (int m = 0; m < MF; ++m) acc[f][m] = add_scaled(acc[f][m], sums[~j & 1][f][m], scale[~j & 1][f]);
+                        for (int m = 0; m < MF; ++m) {
+                            acc[0][m] = add_scaled<0>(acc[0][m], sums[~j & 1][0][m], scale[~j & 1]);
+                            acc[1][m] = add_scaled<1>(acc[1][m], sums[~j & 1][1][m], scale[~j & 1]);
+                        }
                     }
                 }
             } else {
