@@ -48,7 +48,7 @@ __device__ __forceinline__ void finish(const Args& A, int64_t t, int n, f32x4 v)
 //
 // Up to about 16 tokens the stream of weights bounds it (28672 x 8192, 125 MB: one bfloat16 token 26 us, 4.8 TB/s; 16 of 4
 // bits 27), past them what each workgroup stages of the tokens beside its weights, 25 to 30 bytes a nanosecond and compute
-// unit together (45 float16 tokens 50 us, 40 of 4 bits 34).  Few rows (4096 x 4096: 6.6 us) are a chain of four steps.
+// unit together (45 float16 tokens 46 us, 40 of 4 bits 34).  Few rows (4096 x 4096: 6.6 us) are a chain of four steps.
 template <int XT, int OUT, int MF, int RG, int TR>
 __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 {
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args A)
 // What bounds it, in tiles of 256 x 256 (4096 x 28672 x 8192): bfloat16 1370 us, 1400 TFLOP/s, the matrix instructions,
 // 66% busy at the 1.8 GHz that the power limit leaves; 4 bits 530 us, 3630 TFLOP/s, 43% busy at 1.9, beside as many
 // cycles of LDS.  In float16 the scaling of each block's sums, four multiply-adds for each product instruction (4096 x
-// 13824 x 5120: 695 us, bfloat16 450).  Where there are few tiles, the units that have none (331 x 13821 x 5120 of 4 bits:
+// 13824 x 5120: 628 us, bfloat16 450).  Where there are few tiles, the units that have none (331 x 13821 x 5120 of 4 bits:
 // 37 us, 162 tiles of 128 x 256).
 //
 // Scales: a dword of every row comes with the step (16-bit x: the four blocks that two
@@ -490,15 +490,17 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(Args A)
 // ------------------------------------------------------------ choice
 
 // Tokens of few_kernel, which widens each code for up to 64 tokens, and tiles of 128 for 128.  64 x 28672 x 8192 in
-// bfloat16, float16 and 4 bits: 47, 58 and 38 us, in tiles 70, 110 and 44; 64 x 4096 x 4096: 15, 16 and 14, in tiles 17, 28
+// bfloat16, float16 and 4 bits: 47, 53 and 38 us, in tiles 70, 88 and 44; 64 x 4096 x 4096: 15, 15 and 14, in tiles 17, 24
 // and 13.  (Past 64 an operand's accumulators leave no registers to read ahead with.)
 constexpr uint64_t kFew = 64;
 
 // Microseconds of a step of a workgroup, measured over 8192 values (64 a step, of 4 bits 128): of one alone on its
 // compute unit and of two side by side (0: no LDS for a second one, or no gain: two of 128 x 256 in bfloat16 1.54, as one of
 // 256 x 256).  Of 96 rows: 77 x 14336 x 4096 in bfloat16 26 us in tiles of 128, 25 so, 192 x 28672 x 8192 120 and 106.
+// Those of 128 x 128 hold where weights come from memory, in runs of 32 bytes; from a cache a step takes 0.57, in float16
+// 0.75, but choosing by that made 128 x 14336 x 4096 in float16 42 us for 37.
 constexpr Cost kCostsBf16[] = {{256, 256, 1.52, 0.0}, {128, 256, 0.93, 0.0}, {128, 128, 0.62, 1.10}, {96, 256, 0.81, 0.0}};
-constexpr Cost kCostsFp16[] = {{256, 256, 2.36, 0.0}, {128, 256, 1.5, 0.0}, {128, 128, 1.26, 2.50}, {96, 256, 1.4, 0.0}};
+constexpr Cost kCostsFp16[] = {{256, 256, 2.17, 0.0}, {128, 256, 1.37, 0.0}, {128, 128, 1.15, 2.28}, {96, 256, 1.28, 0.0}};
 // (The first two are of steps of 256 values: a stored row has to have as many.)
 constexpr Cost kCostsMx[] = {{256, 256, 1.16, 0.0}, {128, 256, 0.74, 0.0}, {128, 128, 0.62, 1.18}};
 
