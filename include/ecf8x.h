@@ -47,9 +47,8 @@
  *            a = gate_scale[e] * (gate[e] x[t]),  b = up_scale[e] * (up[e] x[t])
  *            h = a / (1 + exp(-a)) * b
  *            y[t] = sum over j of weights[t][j] * down_scale[e] * (down[e] h)
- *          Other ids add nothing.  h enters its product as two bfloat16, with
- *          16 significant bits: 2^-16 of each term, far below the rounding of
- *          y.  The same expert may be named twice.
+ *          Other ids add nothing.  h is a float32 and enters its product with
+ *          all of its 24 bits.  The same expert may be named twice.
  * The order of every sum is fixed: the same call gives the same bits.
  * ------------------------------------------------------------------------
  * Conventions as in ecf8a.h: ECF8_OK or a negative ECF8_ERR_*; the caller owns

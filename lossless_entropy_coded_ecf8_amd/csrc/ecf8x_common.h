@@ -74,6 +74,19 @@ __device__ __forceinline__ f32x4 add_scaled(f32x4 acc, f32x4 block, float scale)
                  __builtin_fmaf(of_lane<4 * N + 2>(scale), block[2], acc[2]), __builtin_fmaf(of_lane<4 * N + 3>(scale), block[3], acc[3])};
 }
 
+// Two float32 as the sums of three bfloat16, for the matrix instruction: hi is the value rounded, mid the rest rounded, low
+// what is left of 24 bits, eight of them: exact down to bfloat16's smallest step, 2^-133.  Where hi is infinite or NaN the
+// others are 0.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& low)
+{
+    hi = pack2<kBf16>(a, b);
+    const f32x2 h = unpack2<kBf16>(hi);
+    const float ra = __builtin_fabsf(a - h[0]) < 3.0e38f ? a - h[0] : 0.0f, rb = __builtin_fabsf(b - h[1]) < 3.0e38f ? b - h[1] : 0.0f;
+    mid = pack2<kBf16>(ra, rb);
+    const f32x2 m = unpack2<kBf16>(mid);
+    low = pack2<kBf16>(ra - m[0], rb - m[1]);
+}
+
 // Eight E4M3 bytes as one operand of a 16-bit type.  Exact.
 template <int TYPE>
 __device__ __forceinline__ u32x4 widen8(uint32_t a, uint32_t b)

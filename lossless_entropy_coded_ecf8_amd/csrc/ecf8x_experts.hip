@@ -5,10 +5,14 @@
 // kernels: gate and up with the activation (h of every pair of a token and an
 // expert), then down and the weighted sum over a token's experts.  Weights are
 // widened exactly; rows of the weight are operand A, the tokens of one expert
-// operand B of the matrix instruction.
+// operand B of the matrix instruction.  h keeps float32's 24 bits, as three
+// bfloat16 that add up to it; where an expert has four pairs at most, its parts
+// are columns of one operand, and the third costs no instruction.  (Two parts, 16
+// bits, took 5% less time with eight pairs an expert and more, and as long with fewer, but left
+// twice as many results a step off as sums of float32 do.)
 //
-// Measured: one token, 8 of 256 experts of 7168 x 2048 (352 MB of E4M3) 38 and 25 us,
-// 5.6 TB/s; 64 tokens, 8 of the 256 in 4 bits (5.2 GB) 1,050 us together, 4.9 TB/s.
+// Measured: one token, 8 of 256 experts of 7168 x 2048 (352 MB of E4M3) 39 and 25 us,
+// 5.5 TB/s; 64 tokens, 8 of the 256 in 4 bits (5.2 GB) 1,037 us together, 5.0 TB/s.
 #include "ecf8x_stream.h"
 
 namespace {
@@ -139,7 +143,7 @@ struct MoeArgs {
     Matrix gate, up, down;
     const int32_t* ids;
     const float* weights;
-    uint16_t* h;                // [pair][2][inner]: upper and lower bfloat16
+    uint16_t* h;                // [pair][3][inner]: three bfloat16, which add up to the float32 value
     uint16_t* y;
     int64_t ld_y;
     float* part;                // [pair][features]
@@ -224,12 +228,12 @@ __device__ __forceinline__ void gate_up(const MoeArgs& A, const Group& G, int e,
             const float v = acc[0][m][q] * fa;
             h[q] = v / (1.0f + expf(-v)) * (acc[1][m][q] * fb);
         }
-        uint32_t hi[2], lo[2];
-        split2(h[0], h[1], hi[0], lo[0]);
-        split2(h[2], h[3], hi[1], lo[1]);
-        uint16_t* out = A.h + (int64_t)G.pair[p] * 2 * A.inner + i;          // inner is a multiple of 16
-        *reinterpret_cast<uint2*>(out) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(out + A.inner) = make_uint2(lo[0], lo[1]);
+        uint32_t part[3][2];
+        split3(h[0], h[1], part[0][0], part[1][0], part[2][0]);
+        split3(h[2], h[3], part[0][1], part[1][1], part[2][1]);
+        uint16_t* out = A.h + (int64_t)G.pair[p] * 3 * A.inner + i;          // inner is a multiple of 16
+#pragma unroll
+        for (int j = 0; j < 3; ++j) *reinterpret_cast<uint2*>(out + j * A.inner) = make_uint2(part[j][0], part[j][1]);
     }
 }
 
@@ -278,7 +282,7 @@ __device__ __forceinline__ void down(const MoeArgs& A, const Group& G, Rsrc part
     const typename S::Rows rows{A.down.codes + row * row_bytes<W>(A.inner), A.down.scales + row * row_scales(A.inner), A.features - 1 - first};
     const float factor = A.down.factors ? A.down.factors[e] : 1.0f;
     const typename S::Places at = S::places(rows, row_bytes<W>(A.inner), row_scales(A.inner), A.h, nullptr, 2 * A.inner, [&](int i) {
-        return (uint32_t)G.pair[min(p0 + i, count - 1)] * 4 * (uint32_t)A.inner;
+        return (uint32_t)G.pair[min(p0 + i, count - 1)] * 6 * (uint32_t)A.inner;
     });
     f32x4 acc[S::RF][MF] = {};
     if (p0) __syncthreads();
@@ -300,7 +304,7 @@ __device__ __forceinline__ void down(const MoeArgs& A, const Group& G, Rsrc part
 template <int W, int TYPE, int MF, int RG>
 __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
 {
-    typedef Stream<W, kPair, MF ? MF : 1, RG> S;
+    typedef Stream<W, kThree, MF ? MF : 1, RG> S;
     __shared__ Group G;
     __shared__ uint32_t ended;
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -310,9 +314,10 @@ __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs A)
     if (e < 0 && (chosen || blockIdx.y)) return;              // where no token has an expert one workgroup clears y
     if (chosen) {
         if constexpr (MF == 0) {
-            if (count <= 4) down<Stream<W, kPair, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, part, e, 0, lds);
+            constexpr int TR = W == kMx4 && RG == 2 ? 4 : 8;   // (half of the LDS has no room for two stages of eight there)
+            if (count <= 4) down<Stream<W, kThree, 1, RG, 4, kHalf>, W, 1, RG, 4>(A, G, part, e, 0, lds);
             else
-                for (int p0 = 0; p0 < count; p0 += 8) down<Stream<W, kPair, 1, RG, 8, kHalf>, W, 1, RG, 8>(A, G, part, e, p0, lds);
+                for (int p0 = 0; p0 < count; p0 += TR) down<Stream<W, kThree, 1, RG, TR, kHalf>, W, 1, RG, TR>(A, G, part, e, p0, lds);
         } else {
             for (int p0 = 0; p0 < count; p0 += 16 * MF) down<S, W, MF, RG, 16 * MF>(A, G, part, e, p0, lds);
         }
@@ -363,7 +368,7 @@ int moe(MoeArgs A, hipStream_t st)
     constexpr int R = 32 * RG, rows = R / 2;                  // features of a workgroup of the second kernel, rows of gate of the first
     int first, second;                                        // LDS
     if constexpr (MF == 0) first = second = kHalf * 1024;
-    else first = Stream<W, TYPE, MF, RG>::kLds, second = Stream<W, kPair, MF, RG>::kLds;
+    else first = Stream<W, TYPE, MF, RG>::kLds, second = Stream<W, kThree, MF, RG>::kLds;
     const int most = A.pairs < A.experts ? A.pairs : A.experts;
     A.tiles = (A.features + R - 1) / R;
     if (allow(gate_up_kernel<W, TYPE, MF, RG>, first) != ECF8_OK || allow(down_kernel<W, TYPE, MF, RG>, second) != ECF8_OK) return ECF8_ERR_HIP;
@@ -379,11 +384,11 @@ int moe(const MoeArgs& A, hipStream_t st)
 {
     // Token rows of a stage, by how many an expert meets on average, up to the most that any can.  Microseconds of both
     // launches, experts x features x inner:
-    //   4 or 8 rows (two workgroups a compute unit) or 16: 128 x 4096 x 1024, 4 pairs an expert: 4-bit weights 218 and 284,
-    //     E4M3 301 and 288; 2 an expert: 188 and 257, 234 and 233; 8 an expert (64 x 2048 x 1408): 143 and 141, 164 and 125;
-    //   16 or 32: 64 x 2048 x 1408, 8 an expert: E4M3 125 and 138; 8 x 4096 x 2048, 16 an expert of 64 tokens: 79 and 56.
+    //   4 or 8 rows (two workgroups a compute unit) or 16: 128 x 4096 x 1024, 4 pairs an expert: 4-bit weights 226 and 298,
+    //     E4M3 297 and 297; 2 an expert: 182 and 255, 245 and 254; 8 an expert (64 x 2048 x 1408): 154 and 147, 178 and 131;
+    //   16 or 32: 64 x 2048 x 1408, 8 an expert: E4M3 131 and 144; 8 x 4096 x 2048, 16 an expert of 64 tokens: 99 and 62.
     // With so few chosen experts that 128 features a workgroup would not give every compute unit one, 64: 8 experts of
-    // 4096 x 1024 for one token 26 and 31 us (4 bits: 22 and 28); 32 of 2048 x 1408: 56 and 52.
+    // 4096 x 1024 for one token 31 and 33 us (4 bits: 24 and 29); 32 of 2048 x 1408: 57 and 51.
     const int most = A.pairs < A.experts ? A.pairs : A.experts;
     const bool small = (A.features + 127) / 128 * most <= 256;
     if (A.pairs <= (W == kMx4 || small ? 4 : 2) * A.experts) return small ? moe<W, TYPE, 0, 2>(A, st) : moe<W, TYPE, 0, 4>(A, st);
@@ -427,7 +432,7 @@ extern "C" uint64_t ecf8x_moe_bytes(uint64_t tokens, uint32_t top, const ecf8x_e
 {
     if (!layer || !layer_ok(*layer) || top > ECF8X_MAX_TOP || tokens > ECF8X_MAX_PAIRS || tokens * top > ECF8X_MAX_PAIRS) return 0;
     // h, the pairs' sums, the counters
-    return round_up(tokens * top * 4 * layer->inner, 256) + round_up(tokens * top * 4 * layer->features, 256) +
+    return round_up(tokens * top * 6 * layer->inner, 256) + round_up(tokens * top * 4 * layer->features, 256) +
            round_up(4 * ((layer->features + kLeastRows - 1) / kLeastRows), 256);
 }
 
@@ -456,7 +461,7 @@ extern "C" int ecf8x_moe(const void* x, uint64_t ld_x, uint32_t type, uint64_t t
     A.ids = ids;
     A.weights = weights;
     A.h = static_cast<uint16_t*>(workspace);
-    A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * top * 4 * layer->inner, 256));
+    A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(tokens * top * 6 * layer->inner, 256));
     A.counters = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(A.part) + round_up(tokens * top * 4 * layer->features, 256));
     A.y = static_cast<uint16_t*>(y);
     A.ld_y = (int64_t)ld_y;

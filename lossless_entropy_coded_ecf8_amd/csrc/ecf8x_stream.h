@@ -21,7 +21,7 @@
 
 namespace ecf8x {
 
-constexpr int kPair = 6;                  // x as two bfloat16 rows, the upper and the lower halves of its values
+constexpr int kThree = 6;                 // x as three bfloat16 rows, which add up to its float32 values
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void LdsMem;
@@ -35,6 +35,13 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes = ~0u)
 // The wave's number, known to be the same in all of its lanes.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// The value of the lane N on, of every 16 (0 past the last).
+template <int N>
+__device__ __forceinline__ float lane_on(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x100 + N, 0xF, 0xF, true));
+}
+
 // All but the newest LOADS loads have arrived, and every LDS access is done, in
 // every wave of the workgroup.
 template <int LOADS>
@@ -46,7 +53,8 @@ __device__ __forceinline__ void wait_and_meet()
 }
 
 // TR: rows of tokens that a stage holds, 16 MF, or 4 or 8 where there are no more (lanes then share them).
-// ROOM: KB of LDS for the stages; 0: half of a compute unit's, for two workgroups, where three stages fit in it, else all.
+// ROOM: KB of LDS for the stages; 0: half of a compute unit's, for two workgroups, where three stages fit in it (of tokens in three
+// parts two: 128 experts of 4096 x 1024, 64 tokens, 313 us, and in all of it 348), else all.
 template <int W, int X, int MF, int RG, int TR = 16 * MF, int ROOM = 0>
 struct Stream {
     static constexpr int RF = 2, NW = 8, KG = NW / RG, kThreads = 64 * NW;
@@ -54,21 +62,28 @@ struct Stream {
     static constexpr int VALUES = W == kMx4 ? 32 : 16;         // of a 16-byte unit of weights
     static constexpr int STEP = 4 * KG * VALUES;               // values of a step
     static constexpr int WU = 4 * KG;                          // units of a weight row's step
-    static constexpr int XU = X == kMx4 ? 4 * KG : X == kPair ? STEP / 4 : STEP / 8;   // of a token's
+    static constexpr int XU = X == kMx4 ? 4 * KG : (X == kThree ? 3 : 1) * STEP / 8;   // of a token's
+    static constexpr int PLANE = X == kThree ? XU / 3 : XU;    // of one of its rows
+    // Four token rows of three parts: columns 4 p .. 4 p + 3 of operand B hold part p of the rows, so that one instruction takes
+    // all of a row's parts (the last four columns repeat the last part and are not used).
+    static constexpr bool PACKED = X == kThree && TR == 4;
     static constexpr int kW = R * WU, kX = TR * XU;       // units of a stage
     static constexpr int kS = W == kMx4 ? R * KG : 0, kXS = X == kMx4 ? TR * KG : 0;   // dwords of scales
     static constexpr int kStage = 16 * (kW + kX) + 4 * (kS + kXS);
     // 8 KB of a workgroup's share are left to the callers.
     static constexpr int kFit = 72 * 1024 / kStage, kMost = 152 * 1024 / kStage,
-                         kRoom = ROOM ? ROOM * 1024 / kStage : kFit >= 3 ? kFit : kMost,
+                         kRoom = ROOM ? ROOM * 1024 / kStage : kFit >= (X == kThree ? 2 : 3) ? kFit : kMost,
                          STAGES = kRoom < 8 ? kRoom : 8;
     static constexpr int kSums = 16 * 64 * NW * RF * MF, kLds = STAGES * kStage > kSums ? STAGES * kStage : kSums;
     // Loads of a wave and a stage: the same in every wave, some with part of its lanes.
-    static constexpr int kEachX = kX / NW < 64 ? 1 : kX / kThreads;
+    static constexpr int kWaveX = kX / NW, kEachX = (kWaveX + 63) / 64;
     static constexpr int kLoads = kW / kThreads + (kS > 0) + kEachX + (kXS > 0);
     static constexpr int kAhead = (STAGES - 2) * kLoads;
     static_assert(RG * KG == NW && kW == 128 * NW && STAGES >= 2 && (TR == 16 * MF || (TR < 16 && MF == 1)) && kLds <= 152 * 1024 && kAhead < 64, "LDS and the load counter");
-    static_assert(kX % NW == 0 && (kX / NW < 64 || kX % kThreads == 0) && kXS / NW <= 64 && kS / NW <= 64 && kStage % 16 == 0, "waves stage alike");
+    static_assert(kX % NW == 0 && kXS / NW <= 64 && kS / NW <= 64 && kStage % 16 == 0, "waves stage alike");
+
+    // Lanes of a wave that send for its token unit i.
+    static __device__ __forceinline__ int lanes_of(int i) { return kWaveX - 64 * i < 64 ? kWaveX - 64 * i : 64; }
 
     // Where unit u of a row of `units` lies, so that 16 rows' units of one number fall in different banks.
     template <int UNITS>
@@ -78,9 +93,12 @@ struct Stream {
         return UNITS == 8 ? row >> 1 & 7 : row & 15;
     }
 
+    // The same for a token row, which place p of it says to which part it belongs.
+    static __device__ __forceinline__ int turn_x(int row, int p) { return PACKED ? row | p / PLANE << 2 : turn<XU>(row); }
+
     // The unit of a token row that lies at place p: where a lane group has four neighbouring units, places are numbered
     // so that the groups' places of one read are neighbours, which the lanes of one cycle spread over all banks.
-    static constexpr bool FOURS = W == kMx4 && (X == kBf16 || X == kPair);
+    static constexpr bool FOURS = W == kMx4 && (X == kBf16 || X == kThree);
     static __device__ __forceinline__ int token_unit(int p) { return FOURS ? (p & ~15) | (p & 3) << 2 | (p >> 2 & 3) : p; }
 
     // The rows that this wave sends for, 16 RF / KG of them: its fragment's first row, and the last that exists
@@ -98,10 +116,11 @@ struct Stream {
         uint32_t at_w[2], at_s, at_x[kEachX], at_xs;
     };
 
-    // token(i): byte offset of token row i (0 .. TR - 1) from x, for kMx4 its number.
+    // token(i): byte offset of token row i (0 .. TR - 1) from x, for kMx4 its number.  plane: bytes from one of its three rows
+    // to the next.
     template <class Token>
     static __device__ __forceinline__ Places places(const Rows& rows, uint32_t row_bytes, uint32_t row_scales, const void* x, const void* x_scales,
-                                                    uint32_t low, Token token)
+                                                    uint32_t plane, Token token)
     {
         const int lane = threadIdx.x & 63, wave = wave_id();
         Places p;
@@ -121,11 +140,10 @@ struct Stream {
         }
 #pragma unroll
         for (int i = 0; i < kEachX; ++i) {
-            const int u = kX / NW < 64 ? wave * (kX / NW) + lane % (kX / NW) : wave * (kX / NW) + i * 64 + lane, row = u / XU;
-            const int unit = token_unit((u % XU) ^ turn<XU>(row));
+            const int u = wave * kWaveX + i * 64 + lane % lanes_of(i), row = u / XU;
+            const int unit = token_unit((u % XU) ^ turn_x(row, u % XU));
             if constexpr (X == kMx4) p.at_x[i] = (uint32_t)token(row) * row_bytes + 16 * unit;
-            else if constexpr (X == kPair) p.at_x[i] = (uint32_t)token(row) + (unit < XU / 2 ? 16 * unit : low + 16 * (unit - XU / 2));
-            else p.at_x[i] = (uint32_t)token(row) + 16 * unit;
+            else p.at_x[i] = (uint32_t)token(row) + unit / PLANE * plane + 16 * (unit % PLANE);
         }
         if constexpr (X == kMx4) {
             const int d = wave * (kXS / NW) + lane % (kXS / NW);
@@ -146,13 +164,10 @@ struct Stream {
             if (lane < 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.s, (LdsMem*)(ls + wave * 32), 4, p.at_s, step * 4 * KG, 0, 0);
         }
         const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;      // of a token's plane
-        if constexpr (kX / NW < 64) {
-            if (lane < kX / NW) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / NW)), 16, p.at_x[0], step * bytes, 0, 0);
-        } else {
 #pragma unroll
-            for (int i = 0; i < kEachX; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * (kX / NW) + i * 64), 16, p.at_x[i], step * bytes, 0, 0);
-        }
+        for (int i = 0; i < kEachX; ++i)
+            if (lanes_of(i) == 64 || lane < lanes_of(i))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(p.x, (LdsMem*)(lx + wave * kWaveX + i * 64), 16, p.at_x[i], step * bytes, 0, 0);
         if constexpr (X == kMx4) {
             if (lane < kXS / NW) __builtin_amdgcn_raw_ptr_buffer_load_lds(p.xs, (LdsMem*)(lxs + wave * (kXS / NW)), 4, p.at_xs, step * 4 * KG, 0, 0);
         }
@@ -180,8 +195,8 @@ struct Stream {
         const int bytes = X == kMx4 ? 16 * WU : 2 * STEP;
 #pragma unroll
         for (int i = 0; i < kEachX; ++i) {
-            const int u = wave * (kX / NW) + i * 64 + lane, unit = token_unit((u % XU) ^ turn<XU>(u / XU)) % (X == kPair ? XU / 2 : XU);
-            if (kX / NW < 64 && lane >= kX / NW) break;
+            const int u = wave * kWaveX + i * 64 + lane, unit = token_unit((u % XU) ^ turn_x(u / XU, u % XU)) % PLANE;
+            if (lane >= lanes_of(i)) break;
             u32x4 v{0, 0, 0, 0};
             if (unit * (X == kMx4 ? 32 : 8) < left) v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(x) + p.at_x[i] + step * bytes);
             lx[u] = v;
@@ -199,7 +214,8 @@ struct Stream {
         // float16 tokens and 4-bit weights: a block's power of two need not fit float16, so each instruction takes one
         // block of 32 (lane group g its values 8 g ..), unscaled, and its result is scaled, exactly, as it is added.
         static constexpr bool BLOCKS = X == kFp16 && W == kMx4;
-        u32x4 w[RF], x[MF][OPS], low[X == kPair ? MF : 1][X == kPair ? OPS : 1];
+        static constexpr int PLANES = PACKED ? 1 : XU / PLANE;     // of an operand's column
+        u32x4 w[RF], x[MF][OPS][PLANES];
         uint32_t sw[RF], sx[MF];                       // BLOCKS: sw[0], of row 4 g + c % 4 of fragment c / 4 % 2
 
         __device__ __forceinline__ void read(const char* buf)
@@ -230,8 +246,11 @@ struct Stream {
 #pragma unroll
                 for (int m = 0; m < MF; ++m) {
                     const int row = (16 * m + c) % TR, unit = BLOCKS || FOURS ? (4 * q + j) * 4 + g : (4 * q + g) * OPS + j;
-                    x[m][j] = lx[row * XU + (unit ^ turn<XU>(row))];
-                    if constexpr (X == kPair) low[m][j] = lx[row * XU + ((XU / 2 + unit) ^ turn<XU>(row))];
+#pragma unroll
+                    for (int p = 0; p < PLANES; ++p) {
+                        const int place = (PACKED ? min(c >> 2, 2) : p) * PLANE + unit;
+                        x[m][j][p] = lx[row * XU + (place ^ turn_x(row, place))];
+                    }
                     if constexpr (X == kMx4) sx[m] = lxs[row * KG + q];
                 }
             }
@@ -245,7 +264,7 @@ struct Stream {
 #pragma unroll
                 for (int m = 0; m < MF; ++m)
 #pragma unroll
-                    for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0], acc[f][m], sw[f] >> (8 * g), sx[m] >> (8 * g));
+                    for (int f = 0; f < RF; ++f) acc[f][m] = mfma_mx4<0>(w[f], x[m][0][0], acc[f][m], sw[f] >> (8 * g), sx[m] >> (8 * g));
             } else if constexpr (BLOCKS) {
                 // A block's sums are added while the next block's are made.
                 f32x4 sums[2][RF][MF];
@@ -258,7 +277,7 @@ struct Stream {
                         for (int f = 0; f < RF; ++f) {
                             const u32x4 wide = widen4_f16(w[f][j]);
 #pragma unroll
-                            for (int m = 0; m < MF; ++m) sums[j & 1][f][m] = mfma_f16(wide, x[m][j], f32x4{0, 0, 0, 0});
+                            for (int m = 0; m < MF; ++m) sums[j & 1][f][m] = mfma_f16(wide, x[m][j][0], f32x4{0, 0, 0, 0});
                         }
                         scale[j & 1] = value_of(scale_at(sw[0], j));
                         __builtin_amdgcn_sched_barrier(0);
@@ -285,15 +304,11 @@ struct Stream {
                         else wide[f] = widen8<TYPE>(w[f][2 * j], w[f][2 * j + 1]);
                     }
 #pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        const u32x4 hi = x[m][j];
+                    for (int m = 0; m < MF; ++m)
 #pragma unroll
-                        for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], hi, acc[f][m]);
-                        if constexpr (X == kPair) {
+                        for (int p = 0; p < PLANES; ++p)
 #pragma unroll
-                            for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], low[m][j], acc[f][m]);
-                        }
-                    }
+                            for (int f = 0; f < RF; ++f) acc[f][m] = mfma<TYPE>(wide[f], x[m][j][p], acc[f][m]);
                 }
             }
         }
@@ -354,6 +369,14 @@ struct Stream {
                 for (int m = 0; m < MF; ++m)
 #pragma unroll
                     for (int q = 1; q < KG; ++q) acc[f][m] += sums[(((q * RG + wave) * RF + f) * MF + m) * 64 + lane];
+            if constexpr (PACKED) {
+#pragma unroll
+                for (int f = 0; f < RF; ++f) {
+                    const f32x4 v = acc[f][0];
+                    acc[f][0] = f32x4{v[0] + (lane_on<4>(v[0]) + lane_on<8>(v[0])), v[1] + (lane_on<4>(v[1]) + lane_on<8>(v[1])),
+                                      v[2] + (lane_on<4>(v[2]) + lane_on<8>(v[2])), v[3] + (lane_on<4>(v[3]) + lane_on<8>(v[3]))};
+                }
+            }
         }
     }
 };
