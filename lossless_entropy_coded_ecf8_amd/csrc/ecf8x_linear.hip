@@ -7,6 +7,7 @@
 // with float16 x an instruction takes one block of 32 unscaled, and its float32
 // result is scaled as it is added.  Four-bit x: the scaled matrix instruction takes
 // codes and scale bytes as they are stored.
+#include "ecf8x_offsets.h"
 #include "ecf8x_stream.h"
 #include "ecf8x_tiles.h"
 
@@ -136,15 +137,15 @@ struct Tile {
 
     static __device__ __forceinline__ int turn(int row) { return AU == 4 ? 0x78 >> (row >> 1 & 6) & 3 : row & 7; }
 
+    // Parts in which the rows' scales are sent for, and the rows of a wave and part.
+    static constexpr int PARTS = GROUPED ? GROUP : 1, kPartX = kRowsX / (8 * PARTS), kPartW = BN / (8 * PARTS);
+
     // Byte offsets from the tile's corner of what a lane sends for.  Rows past the last read the last one's; they reach
     // no result that is stored.
-    // Of scales: the byte offset of a lane's row, in groups that of the first of GROUP parts.  Rows past the last are past
-    // the end of the buffer, whose loads give 0.
     struct Places {
-        uint32_t a[kUnitsA], b[kUnitsB], sx, sw;
+        uint32_t a[kUnitsA], b[kUnitsB], sx[PARTS], sw[PARTS];
         Rsrc x_scales, w_scales;
     };
-    static constexpr int kPartX = kRowsX / (GROUPED ? 8 * GROUP : 8), kPartW = BN / (GROUPED ? 8 * GROUP : 8);    // rows of a wave
 
     // Lanes of a wave that send for its unit i of x.
     static __device__ __forceinline__ int lanes_of(int i) { return kWaveA - 64 * i < 64 ? kWaveA - 64 * i : 64; }
@@ -166,10 +167,13 @@ struct Tile {
         }
         const bool small = GROUPED && A.kp < 512;
         const uint32_t pitch = small ? 0 : A.kp / 32;
-        at.sx = (wave * kPartX + lane) * pitch;
-        at.sw = (wave * kPartW + lane) * pitch;
-        at.w_scales = buffer_of(small ? A.w : A.w_scales + (int64_t)n0 * (A.kp / 32), small ? 16 : (uint32_t)min(BN, A.n - n0) * pitch);
-        if constexpr (MX) at.x_scales = buffer_of(small ? A.w : A.x_scales + t0 * (A.kp / 32), small ? 16 : (uint32_t)min((int64_t)BM, A.tokens - t0) * pitch);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            at.sx[p] = MX ? scale_offset(p, wave, lane, kPartX, A.tokens - t0, pitch) : 0;
+            at.sw[p] = scale_offset(p, wave, lane, kPartW, A.n - n0, pitch);
+        }
+        at.w_scales = buffer_of(small ? A.w : A.w_scales + (int64_t)n0 * (A.kp / 32));
+        if constexpr (MX) at.x_scales = buffer_of(small ? A.w : A.x_scales + t0 * (A.kp / 32));
         return at;
     }
 
@@ -181,12 +185,13 @@ struct Tile {
     // send for; the same loads then read codes, which nobody looks at.
     static __device__ __forceinline__ void stage_group(const Args& A, const Places& at, int dword, int part, u32x4* to)
     {
-        const int lane = threadIdx.x & 63, wave = wave_id(), pitch = A.kp < 512 ? 0 : A.kp / 32, from = A.kp < 512 ? 0 : 4 * dword;
-        if (lane < kPartX)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(to + (part * 8 + wave) * kPartX), 16, at.sx, from + part * 8 * kPartX * pitch, 0, 0);
-        if (lane < kPartW)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(to + kRowsX + (part * 8 + wave) * kPartW), 16, at.sw,
-                                                     from + part * 8 * kPartW * pitch, 0, 0);
+        const int lane = threadIdx.x & 63, wave = wave_id(), from = A.kp < 512 ? 0 : 4 * dword;
+        uint32_t x = at.sx[0], w = at.sw[0];
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p)
+            if (part == p) x = at.sx[p], w = at.sw[p];
+        if (lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(to + scale_row(part, wave, 0, kPartX)), 16, x, from, 0, 0);
+        if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(to + kRowsX + scale_row(part, wave, 0, kPartW)), 16, w, from, 0, 0);
     }
 
     // Rows of fewer than 16 bytes of scales: all of them, as group 0.
@@ -215,8 +220,8 @@ struct Tile {
         const int lane = threadIdx.x & 63, wave = wave_id();
         if constexpr (!GROUPED) {
             if (part == 0) {
-                if (MX && lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(ls + wave * kPartX), 4, at.sx, (k / 128) * 4, 0, 0);
-                if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(ls + kRowsX + wave * kPartW), 4, at.sw, (k / 128) * 4, 0, 0);
+                if (MX && lane < kPartX) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.x_scales, (LdsMem*)(ls + wave * kPartX), 4, at.sx[0], (k / 128) * 4, 0, 0);
+                if (lane < kPartW) __builtin_amdgcn_raw_ptr_buffer_load_lds(at.w_scales, (LdsMem*)(ls + kRowsX + wave * kPartW), 4, at.sw[0], (k / 128) * 4, 0, 0);
             }
         }
         if (part < kUnitsB) {

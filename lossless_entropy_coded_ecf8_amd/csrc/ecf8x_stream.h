@@ -26,11 +26,8 @@ constexpr int kThree = 6;                 // x as three bfloat16 rows, which add
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void LdsMem;
 
-// bytes: the range, past which loads give 0; left open where every offset is inside the operand.
-__device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes = ~0u)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
-}
+// Every offset is inside the operand: the range is left open.
+__device__ __forceinline__ Rsrc buffer_of(const void* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, ~0, 0x00020000); }
 
 // The wave's number, known to be the same in all of its lanes.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
