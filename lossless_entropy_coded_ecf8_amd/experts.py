@@ -156,6 +156,7 @@ class ECF8Experts(torch.nn.Module):
         self._pool: Optional[torch.Tensor] = None
         self._whole: Optional[binding.DecodePlan] = None        # of the whole layer
         self._named: tuple = ((), None)                         # the experts last named, and their plan
+        self._captured: dict = {}                               # plans of named experts that a capture used, whose graphs read them
 
     def _apply(self, fn, *args, **kwargs):
         """Module.to and its like: the scales stay float32, as the weights stay bytes, whatever type the module is brought to."""
@@ -172,6 +173,8 @@ class ECF8Experts(torch.nn.Module):
             return self._whole
         if experts is not None and self._named[0] == experts:
             return self._named[1]
+        if experts in self._captured:
+            return self._captured[experts]
         if _capturing(stream):
             raise RuntimeError("a plan cannot be made while its stream is captured: decode the same experts once before")
         if self._pool is None:
@@ -189,13 +192,17 @@ class ECF8Experts(torch.nn.Module):
     def decode(self, experts: Optional[Sequence[int]] = None, stream=None):
         """Decodes the layer, or the experts named, into the layer's pool; returns gate, up and down as moe_few takes them.
         Other experts' places are left as they are.  The plan of the whole layer is kept, and that of the experts last named:
-        naming others costs their plan, which is made on the host.  All calls write the one pool: on several streams the
-        caller orders them, and what reads it."""
+        naming others costs their plan, which is made on the host.  A plan that was run in a capture is kept with the layer,
+        which has to live as long as the graph.  All calls write the one pool: on several streams the caller orders them, and
+        what reads it."""
         if experts is not None:
             experts = tuple(sorted({int(e) for e in experts}))
             if not experts or experts[0] < 0 or experts[-1] >= self.experts:
                 raise ValueError("experts must be some of 0 .. %d" % (self.experts - 1))
-        self._plan(experts, stream).run(stream)
+        plan = self._plan(experts, stream)
+        if experts is not None and _capturing(stream):
+            self._captured[experts] = plan
+        plan.run(stream)
         size = self.experts * self.inner * self.features
         return tuple(self._pool[m * size:(m + 1) * size].view(self.experts, *self.shapes[m]) for m in range(3))
 
