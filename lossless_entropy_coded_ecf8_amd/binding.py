@@ -575,6 +575,9 @@ class DecodePlan:
         s = _torch_stream(stream)
         if s.cuda_stream not in self._synced:
             s.wait_event(self._ready)
+            # freed while that stream runs the plan, its memory must not go to later work of the prepare stream
+            self.workspace.record_stream(s)
+            self.out.record_stream(s)
             self._synced.add(s.cuda_stream)
         return ctypes.c_void_p(s.cuda_stream)
 

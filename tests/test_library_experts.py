@@ -1,4 +1,4 @@
-"""The plans of a compressed expert layer without a GPU: which are kept."""
+"""The plans of a compressed expert layer without a GPU: which are kept, and which streams use their memory."""
 import gc
 import types
 import weakref
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import lossless_entropy_coded_ecf8_amd as E
+from lossless_entropy_coded_ecf8_amd import binding
 from lossless_entropy_coded_ecf8_amd import experts as X
 
 
@@ -70,3 +71,30 @@ def test_a_plan_that_no_capture_used_goes_when_others_are_named(layer):
     layer.decode()                                                # the whole layer's plan stays anyway
     with pytest.raises(RuntimeError):
         layer.decode([0, 3])
+
+
+class Memory:
+    def __init__(self):
+        self.users = []
+
+    def record_stream(self, stream):
+        self.users.append(stream)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream, self.waits = handle, []
+
+    def wait_event(self, event):
+        self.waits.append(event)
+
+
+@pytest.mark.parametrize("kind", [binding.DecodePlan, binding.DecodePlanV])
+def test_a_plans_memory_is_known_to_be_used_on_the_streams_that_run_it(kind):
+    """Freed while such a stream still runs it, the memory goes to no other work of the stream that prepared it before that run ends."""
+    plan = object.__new__(kind)
+    maker, side = Stream(5), Stream(6)
+    plan.workspace, plan.out, plan._ready, plan._synced = Memory(), Memory(), "event", {maker.cuda_stream}
+    for _ in range(2):
+        assert plan._launch_stream(maker).value == 5 and plan._launch_stream(side).value == 6
+    assert plan.workspace.users == [side] and plan.out.users == [side] and side.waits == ["event"] and maker.waits == []
