@@ -152,6 +152,7 @@ class ECF8Experts(torch.nn.Module):
         scales = torch.as_tensor(scales, dtype=torch.float32, device=self.device)
         if scales.shape != (3, self.experts):
             raise ValueError("scales must be (3, %d), got %s" % (self.experts, tuple(scales.shape)))
+        self.device = scales.device                             # with its number
         self.register_buffer("scales", scales.contiguous())
         self._pool: Optional[torch.Tensor] = None
         self._whole: Optional[binding.DecodePlan] = None        # of the whole layer
@@ -199,10 +200,11 @@ class ECF8Experts(torch.nn.Module):
             experts = tuple(sorted({int(e) for e in experts}))
             if not experts or experts[0] < 0 or experts[-1] >= self.experts:
                 raise ValueError("experts must be some of 0 .. %d" % (self.experts - 1))
-        plan = self._plan(experts, stream)
-        if experts is not None and _capturing(stream):
-            self._captured[experts] = plan
-        plan.run(stream)
+        with _Launch(self.device, stream):               # also where another device is current
+            plan = self._plan(experts, stream)
+            if experts is not None and _capturing(stream):
+                self._captured[experts] = plan
+            plan.run(stream)
         size = self.experts * self.inner * self.features
         return tuple(self._pool[m * size:(m + 1) * size].view(self.experts, *self.shapes[m]) for m in range(3))
 

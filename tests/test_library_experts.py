@@ -1,4 +1,5 @@
-"""The plans of a compressed expert layer without a GPU: which are kept, and which streams use their memory."""
+"""The plans of a compressed expert layer without a GPU: which are kept, which streams use their memory, on which device they run."""
+import contextlib
 import gc
 import types
 import weakref
@@ -25,11 +26,17 @@ class Plan:
 @pytest.fixture
 def layer(monkeypatch):
     """A layer of five experts whose plans are stand-ins, on the CPU; layer.state.capturing: whether the launch stream is captured."""
-    state = types.SimpleNamespace(capturing=False)
+    state = types.SimpleNamespace(capturing=False, launches=[])
+
+    @contextlib.contextmanager
+    def launch(device, stream):
+        state.launches.append((device, stream))
+        yield 0
 
     monkeypatch.setattr(X.binding, "DecodePlan", Plan)
     monkeypatch.setattr(X, "_capturing", lambda stream: state.capturing)
     monkeypatch.setattr(X, "_empty", lambda n, dtype, device, stream: torch.empty(n, dtype=dtype))
+    monkeypatch.setattr(X, "_Launch", launch)
     g = torch.Generator().manual_seed(1)
     stack = [torch.randint(0, 100, (16, 16), generator=g, dtype=torch.uint8) for _ in range(5)]
     made = E.ECF8Experts(stack, stack, stack, torch.ones(3, 5), device="cpu")
@@ -71,6 +78,14 @@ def test_a_plan_that_no_capture_used_goes_when_others_are_named(layer):
     layer.decode()                                                # the whole layer's plan stays anyway
     with pytest.raises(RuntimeError):
         layer.decode([0, 3])
+
+
+def test_decoding_runs_on_the_layers_device(layer):
+    """Whichever device is current: the launch is made as the products are."""
+    side = object()
+    layer.decode([1], stream=side)
+    layer.decode()
+    assert layer.state.launches == [(layer.device, side), (layer.device, None)] and layer.device == layer.scales.device
 
 
 class Memory:
