@@ -81,7 +81,7 @@ def moe_few(x: torch.Tensor, gate, up, down, ids: torch.Tensor, weights: torch.T
     chosen expert's weights are read once, which is what bounds few tokens.  Returns (T, K) in x's type.  Serving only: no
     gradients (it warns once where an operand requires them).
     """
-    _no_graph("moe_few", x, weights)
+    _no_graph("moe_few", x, weights, gate_scale, up_scale, down_scale)
     _on_gpu(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be (T, K), got %s" % (tuple(x.shape),))

@@ -123,7 +123,7 @@ def _no_graph(name: str, *operands):
     if name not in _warned and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in operands):
         _warned.add(name)
         warnings.warn("%s keeps no gradients%s; when serving, torch.no_grad() or requires_grad_(False) says that none are wanted"
-                      % (name, ": MXFP4Linear.adapted is the differentiable layer" if "linear" in name else ""), stacklevel=3)
+                      % (name, ": MXFP4Linear.adapted is the differentiable layer" if "mxfp4" in name else ""), stacklevel=3)
 
 
 def _on_gpu(t, what: str):
@@ -137,8 +137,14 @@ def quantize_mxfp4(x: torch.Tensor, x_scale: Optional[torch.Tensor] = None, *, o
     holds an infinity or NaN is all NaN.
 
     x: bfloat16, float16, float32, or float8_e4m3fn with a float32 x_scale (default 1); a matrix's rows may lie apart, a
-    tensor of more dimensions must be contiguous.  out: an MXFP4 of x's shape to write into.
+    tensor of more dimensions must be contiguous.  out: an MXFP4 of x's shape to write into.  Not differentiable (it warns
+    once where an operand requires gradients).
     """
+    _no_graph("quantize_mxfp4", x, x_scale)
+    return _quantize(x, x_scale, out, stream)
+
+
+def _quantize(x, x_scale=None, out=None, stream=None) -> MXFP4:
     _on_gpu(x, "x")
     if x.dtype not in _TYPES:
         raise ValueError("x must be bfloat16, float16, float32 or float8_e4m3fn, got %s" % x.dtype)
@@ -232,8 +238,10 @@ def linear_mxfp4_input_grad(dy: torch.Tensor, w: MXFP4, *, out: Optional[torch.T
                             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dx = dy w: the gradient that linear_mxfp4's frozen weight passes to its input (ecf8x_input_grad).
 
-    dy: (T, N) bfloat16 or float16, rows on 16-byte borders.  Returns (T, K) in dy's type.
+    dy: (T, N) bfloat16 or float16, rows on 16-byte borders.  Returns (T, K) in dy's type.  Not differentiable itself (it
+    warns once where dy requires gradients).
     """
+    _no_graph("linear_mxfp4_input_grad", dy)
     N, K = _weight_ok(w)
     if dy.dim() != 2:
         raise ValueError("dy must be (T, N), got %s" % (tuple(dy.shape),))
@@ -302,7 +310,7 @@ class MXFP4Linear(torch.nn.Module):
             raise ValueError("adapters need the index of each token's adapter")
         if self.four_bit_input:
             _no_graph("linear_mxfp4", x)
-            y = linear_mxfp4(quantize_mxfp4(x), self.weight, self._bias(x.dtype), out_dtype=x.dtype)
+            y = linear_mxfp4(_quantize(x), self.weight, self._bias(x.dtype), out_dtype=x.dtype)
         else:
             y = linear_mxfp4(x, self.weight, self._bias(x.dtype))
         return y if adapters is None else adapters.add_(y, x, index)
