@@ -34,7 +34,10 @@
  * Products are exact, sums are held in float32, and each result is rounded
  * once.  Widened weights are exact in bfloat16.  A block's power of two need not fit
  * float16: with float16 x the sums of one block at a time are scaled, in float32,
- * as they are added, and float16 dy enters as two bfloat16, exactly.
+ * as they are added, and float16 dy enters as two bfloat16, exactly.  Magnitudes of
+ * 2^128 and more, which quantisation never stores, are infinite in bfloat16: beside
+ * bfloat16 x or dy, and in an expert layer, the results that they reach are infinite
+ * or NaN.  (Beside float16 dy they count as they are.)
  *
  *   route: the `top` largest of a token's E logits, largest first, of equal
  *          ones the lowest expert (NaN counts as the largest); an expert with

@@ -7,6 +7,13 @@
 // per workgroup, on their way to LDS, and the operands are turned there by the
 // transposing LDS read.  Widened values are exact bfloat16; float16 dy is split
 // into two bfloat16 (exact).  Sums in float32, rounded once.
+//
+// Magnitudes of 2^128 and more, which quantisation never stores, widen to
+// infinity.  A lower half of 0, or of the other sign, would make a NaN of that
+// one, so that beside float16 dy weights are widened with an eighth of their
+// scale, and the sums taken eight times.  (The scales of 2^-124 and less, which
+// have no eighth, stay 2^-127 times eight: what they add to a sum, under 2^-80, is
+// far below float16's smallest step.)
 #include "ecf8x_stream.h"
 #include "ecf8x_tiles.h"
 
@@ -129,6 +136,13 @@ struct Tile {
         }
     }
 
+    // The scale byte that a block is widened with; `in`: 0 for rows past the last, which are zero.
+    static __device__ __forceinline__ uint32_t scale_byte(uint32_t scale, uint32_t in)
+    {
+        if constexpr (SPLIT) scale = scale == 255 ? 255 : max(scale, 3u) - 3;
+        return scale & in;
+    }
+
     static __device__ __forceinline__ void put_split(u32x4 v, int u, u32x4* la)
     {
         u32x4 hi, lo;
@@ -144,7 +158,7 @@ struct Tile {
             const int j = threadIdx.x % (BN / 32), swap = j >> 2 & 1;
             // Masks: no branch between the products, no register chosen by a number that only the lane knows.
             const uint32_t in = n + at.row < n1 ? ~0u : 0, other = -(uint32_t)swap;
-            lb[at.row * BU + ((4 * j + (i ^ swap)) ^ turn(at.row))] = widen4(((e.codes[i ^ 1] & other) | (e.codes[i] & ~other)) & in, scale_of(e.scale & in));
+            lb[at.row * BU + ((4 * j + (i ^ swap)) ^ turn(at.row))] = widen4(((e.codes[i ^ 1] & other) | (e.codes[i] & ~other)) & in, scale_of(scale_byte(e.scale, in)));
         }
         if constexpr (SPLIT) {
 #pragma unroll
@@ -306,6 +320,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args A)
         for (int n = 0; n < S::NF; ++n) {
             const int col = k0 + wn * (BN / WN) + n * 16 + 4 * g;   // K is a multiple of 32: an operand's columns are in or out
             if (col >= A.k) continue;
+            if constexpr (S::SPLIT) acc[m][n] *= 8.0f;
             if (part.at >= 0) *reinterpret_cast<f32x4*>(A.sums + ((int64_t)part.at * BM + (t - t0)) * BN + (col - k0)) = acc[m][n];
             else store4<TYPE>(A.dx + t * A.ld_dx + col, acc[m][n], 4);
         }
