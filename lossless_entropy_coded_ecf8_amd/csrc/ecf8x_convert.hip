@@ -49,9 +49,10 @@ struct Unit {
         }
     }
 
-    // mask: 0 makes them zeros.
+    // mask: 0 makes them zeros, whatever the factor is.
     __device__ __forceinline__ void widen(uint32_t mask, float factor, float v[8]) const
     {
+        factor = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, factor) & mask);
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
             const uint32_t d = raw[i] & mask;
