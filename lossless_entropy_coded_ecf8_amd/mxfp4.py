@@ -140,7 +140,8 @@ def quantize_mxfp4(x: torch.Tensor, x_scale: Optional[torch.Tensor] = None, *, o
     tensor of more dimensions must be contiguous.  out: an MXFP4 of x's shape to write into.  Not differentiable (it warns
     once where an operand requires gradients).
     """
-    _no_graph("quantize_mxfp4", x, x_scale)
+    if x.requires_grad or (x_scale is not None and x_scale.requires_grad):
+        _no_graph("quantize_mxfp4", x, x_scale)
     return _quantize(x, x_scale, out, stream)
 
 
@@ -241,7 +242,8 @@ def linear_mxfp4_input_grad(dy: torch.Tensor, w: MXFP4, *, out: Optional[torch.T
     dy: (T, N) bfloat16 or float16, rows on 16-byte borders.  Returns (T, K) in dy's type.  Not differentiable itself (it
     warns once where dy requires gradients).
     """
-    _no_graph("linear_mxfp4_input_grad", dy)
+    if dy.requires_grad:
+        _no_graph("linear_mxfp4_input_grad", dy)
     N, K = _weight_ok(w)
     if dy.dim() != 2:
         raise ValueError("dy must be (T, N), got %s" % (tuple(dy.shape),))
