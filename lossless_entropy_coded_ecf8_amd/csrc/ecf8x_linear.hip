@@ -584,6 +584,23 @@ int launch_tile(const Args& A, hipStream_t st)
     return launch_status();
 }
 
+// The tiles that tiles_of chose.
+template <int XT, int OUT>
+int run_tiles(const Args& A, hipStream_t st)
+{
+    const int bm = A.tiling.bm, bn = A.tiling.bn;
+    if constexpr (XT == kMx4) {
+        if (bm == 256) return launch_tile<XT, OUT, 256, 256, 2, 4, 2, 256>(A, st);
+        if (bn == 256) return launch_tile<XT, OUT, 128, 256, 2, 4, 2, 256>(A, st);
+        return launch_tile<XT, OUT, 128, 128, 2, 4, 4, 128>(A, st);
+    } else {
+        if (bm == 256) return launch_tile<XT, OUT, 256, 256, 2, 4, 3, 64>(A, st);
+        if (bm == 96) return launch_tile<XT, OUT, 96, 256, 2, 4, 3, 64>(A, st);
+        if (bn == 256) return launch_tile<XT, OUT, 128, 256, 2, 4, 3, 64>(A, st);
+        return launch_tile<XT, OUT, 128, 128, 4, 2, 3, 64>(A, st);
+    }
+}
+
 template <int XT, int OUT>
 int run(Args A, float* workspace, hipStream_t st)
 {
@@ -602,11 +619,7 @@ int run(Args A, float* workspace, hipStream_t st)
     A.sums = workspace;
     A.tiling = tiles_of<XT>(A.tokens, A.n, A.k);
     const Tiling& s = A.tiling;
-    int rc;
-    if (s.bm == 256) rc = launch_tile<XT, OUT, 256, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
-    else if (s.bm == 128 && s.bn == 256) rc = launch_tile<XT, OUT, 128, 256, 2, 4, MX ? 2 : 3, MX ? 256 : 64>(A, st);
-    else if (!MX && s.bm == 96) rc = launch_tile<MX ? kBf16 : XT, OUT, 96, 256, 2, 4, 3, 64>(A, st);
-    else rc = launch_tile<XT, OUT, 128, 128, MX ? 2 : 4, MX ? 4 : 2, MX ? 4 : 3, MX ? 128 : 64>(A, st);
+    const int rc = run_tiles<XT, OUT>(A, st);
     if (rc != ECF8_OK || s.rest == 0) return rc;
     return join_tiles<OUT>(A.sums, s, A.tokens, A.n, A.bias, A.y, A.ld_y, st);
 }
