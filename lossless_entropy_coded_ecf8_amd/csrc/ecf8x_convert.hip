@@ -9,7 +9,7 @@
 // row, took as long (28672 x 8192 bfloat16: 107 us and 106).
 //
 // Measured: 28672 x 8192 bfloat16 quantised in 104 us, 595 MB read and written at
-// 5.7 TB/s; E4M3 of the same size in 72, and back to bfloat16 in 84.
+// 5.7 TB/s; E4M3 of the same size in 63, and back to bfloat16 in 84.
 #include "ecf8x_common.h"
 
 namespace {

@@ -1,7 +1,11 @@
 // ecf8x_experts.hip -- a mixture-of-experts layer for a few tokens: the choice
 // of experts, and the gated products of those that were chosen.
 //
-// What bounds the products is reading the chosen experts' weights, once.  Two
+// What bounds the products is reading the chosen experts' weights: once for every 8
+// of an expert's pairs, or 16 or 32, as the pairs an expert of the whole batch has on
+// average (the second product of small 4-bit layers: 4).  Batches that are far from
+// even read them more often than that average needs: 8 of 256 experts, the same for all
+// tokens, E4M3: 8 tokens 68 us, 16 127, 64 496.  Two
 // kernels: gate and up with the activation (h of every pair of a token and an
 // expert), then down and the weighted sum over a token's experts.  Weights are
 // widened exactly; rows of the weight are operand A, the tokens of one expert
@@ -11,8 +15,8 @@
 // bits, took 5% less time with eight pairs an expert and more, and as long with fewer, but left
 // twice as many results a step off as sums of float32 do.)
 //
-// Measured: one token, 8 of 256 experts of 7168 x 2048 (352 MB of E4M3) 39 and 25 us,
-// 5.5 TB/s; 64 tokens, 8 of the 256 in 4 bits (5.2 GB) 1,037 us together, 5.0 TB/s.
+// Measured: one token, 8 of 256 experts of 7168 x 2048 (352 MB of E4M3) 38 and 24 us,
+// 5.6 TB/s; 64 tokens, 8 of the 256 in 4 bits (5.2 GB) 1,040 us together, 5.0 TB/s.
 #include "ecf8x_stream.h"
 
 namespace {

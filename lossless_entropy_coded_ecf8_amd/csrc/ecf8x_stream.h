@@ -1,4 +1,4 @@
-// ecf8x_stream.h -- the product of a few tokens with a weight that is read once.
+// ecf8x_stream.h -- the product of a few tokens with a weight that streams past them.
 //
 // What bounds it is the stream of weights from memory.  A workgroup takes
 // R rows of the weight; both operands go from memory to LDS without

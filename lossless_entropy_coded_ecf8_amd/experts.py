@@ -77,9 +77,10 @@ def moe_few(x: torch.Tensor, gate, up, down, ids: torch.Tensor, weights: torch.T
 
     x: (T, K) bfloat16 or float16, rows on 16-byte borders.  gate, up: (E, I, K), down: (E, K, I), all three MXFP4, or
     all three uint8 E4M3 bytes (K and I multiples of 16) with a float32 scale for each expert (default 1).  ids: (T, top)
-    int32, a value outside [0, E) adds nothing; weights: (T, top) float32; both contiguous.  T * top is at most 512: each
-    chosen expert's weights are read once, which is what bounds few tokens.  Returns (T, K) in x's type.  Serving only: no
-    gradients (it warns once where an operand requires them).
+    int32, a value outside [0, E) adds nothing; weights: (T, top) float32; both contiguous.  T * top is at most 512.  A chosen
+    expert's weights are read once for every 8, 16 or 32 of its pairs, as the pairs an expert has on average; that reading
+    is what bounds few tokens, so that batches far from even routing take longer.  Returns (T, K) in x's type.  Serving
+    only: no gradients (it warns once where an operand requires them).
     """
     _no_graph("moe_few", x, weights, gate_scale, up_scale, down_scale)
     _on_gpu(x, "x")
