@@ -11,9 +11,9 @@
 // Magnitudes of 2^128 and more, which quantisation never stores, widen to
 // infinity.  A lower half of 0, or of the other sign, would make a NaN of that
 // one, so that beside float16 dy weights are widened with an eighth of their
-// scale, and the sums taken eight times.  (The scales of 2^-124 and less, which
-// have no eighth, stay 2^-127 times eight: what they add to a sum, under 2^-80, is
-// far below float16's smallest step.)
+// scale, and the sums taken eight times.  (Scales of 2^-125 and less, which have no
+// eighth, count as 2^-124 there: what they add to a sum, under 2^-80, is far below
+// float16's smallest step.)
 #include "ecf8x_stream.h"
 #include "ecf8x_tiles.h"
 

@@ -174,3 +174,33 @@ def test_results_of_experts_past_the_types_range_have_their_sign(T, n, top, four
         assert bool((ref[2] < -3.5e38).all())
     ref = torch.where(ref.abs() >= most, torch.copysign(torch.full_like(ref, float("inf")), ref), ref)
     check(E.moe_few(x.to(D), *given, ids.to(D), w.to(D)), ref, tol.nan_to_num(0.0, posinf=0.0), (T, n, top))
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 40, 64, 65, 150, 400])
+@pytest.mark.parametrize("N,K", [(70, 288), (300, 1056)])
+def test_products_under_the_largest_and_smallest_scales(T, N, K):
+    """float16 activations, and both operands in 4 bits: zeros stay zeros, what passes the type's range has its sign, what is too small vanishes."""
+    g = gen(T, N, K, 4)
+    data, scales = R.random_stored((N,), K, g)
+    data &= 0x77                                                  # no negative weights, so that no sum cancels
+    data |= 0x22
+    kind = torch.randint(0, 3, (N, 1), generator=g)
+    scales[:, : K // 32] = torch.where(kind == 0, 254, torch.where(kind == 1, 0, scales[:, : K // 32])).to(torch.uint8)
+    w, wv = E.MXFP4(data.to(D), scales.to(D), K), R.values(data, scales, K)
+    x = (torch.rand(T, K, generator=g) + 0.5).to(FP)
+    x[::3] *= -1
+    if T > 1:
+        x[1::4] = 0
+    ref, tol = R.product(x.double(), wv, FP)
+    check(E.linear_mxfp4(x.to(D), w), as_float16(ref), tol.nan_to_num(0.0, posinf=0.0), (T, N, K))
+    xd, xs = R.random_stored((T,), K, g)
+    xd = (xd & 0x77) | 0x22
+    sign = torch.randint(0, 2, (T, 1), generator=g).to(torch.uint8)
+    xd |= sign * 0x88
+    xs[:, : K // 32] = torch.where(torch.randint(0, 2, (T, 1), generator=g) == 0, 254, 0).to(torch.uint8)
+    if T > 1:
+        xd[1::4] = 0
+    ref, tol = R.product(R.values(xd, xs, K), wv, BF)
+    ref = torch.where(ref.abs() >= 3.4e38, torch.copysign(torch.full_like(ref, float("inf")), ref), ref)
+    got = E.linear_mxfp4(E.MXFP4(xd.to(D), xs.to(D), K), w)
+    check(got, ref, torch.where(torch.isinf(ref), 0.0, tol), (T, N, K))
